@@ -1,6 +1,7 @@
-"""Python binding of the block-scaled GEMM C ABI (libbsg.so, include/bsg.h).
+"""Python binding of the C ABI of libbsg.so: the block-scaled GEMM (include/bsg.h) and the paged NVFP4
+key/value cache with its attention (include/bsg_kv.h).
 
-Argument marshalling only: every step of the GEMM runs in the HIP library.  Tensors are passed as
+Argument marshalling only: every step runs in the HIP library.  Tensors are passed as
 device pointers (anything with .data_ptr(), or a plain int); streams as hipStream_t handles (an
 object with .cuda_stream, an int, or None for torch's current stream).  PyTorch is only used, when
 present, to find the current stream.
@@ -14,7 +15,8 @@ import os
 
 __all__ = ["Plan", "BsgError", "LibraryNotBuilt", "load_library", "bench_loop", "null_loop", "run_noalloc", "NOALLOC_SCRATCH_BYTES", "decode_nvfp4_f16",
            "FORMATS", "OUT_DTYPES", "SCALE_LAYOUTS", "abi_version", "packed_strides", "Problem", "PROBLEM_V1_SIZE", "PROBLEM_V2_SIZE",
-           "pack_scales", "scales_ktile_bytes"]
+           "pack_scales", "scales_ktile_bytes",
+           "KVPlan", "KVBatch", "kv_page_bytes", "rope_table"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libbsg.so")
@@ -71,6 +73,30 @@ def packed_strides(fmt: str, M: int, N: int, K: int, scale_layout: str = "linear
     return dict(a=int(M * lda * elem), b=int(N * ldb * elem), sa=sa, sb=sb, bias=0, d=2 * M * ldd)
 
 
+class Heads(ctypes.Structure):  # bsg_heads
+    _fields_ = [("ptr", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class KVProblem(ctypes.Structure):  # bsg_kv_problem
+    _fields_ = [("struct_size", ctypes.c_uint32), ("dtype", ctypes.c_int32), ("q_heads", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_tokens", ctypes.c_int32),
+                ("num_pages", ctypes.c_int64), ("page_stride", ctypes.c_int64), ("max_tokens", ctypes.c_int64),
+                ("flags", ctypes.c_uint32), ("rope_dim", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("k_scale", ctypes.c_float),
+                ("v_scale", ctypes.c_float), ("device", ctypes.c_int32)]
+
+
+class KVBatchArgs(ctypes.Structure):  # bsg_kv_batch
+    _fields_ = [("struct_size", ctypes.c_uint32), ("num_seqs", ctypes.c_int32), ("num_tokens", ctypes.c_int64),
+                ("max_q", ctypes.c_int32), ("max_kv", ctypes.c_int32), ("q_start", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("pages", ctypes.c_void_p), ("pages_stride", ctypes.c_int64)]
+
+
+class KVPlanInfo(ctypes.Structure):  # bsg_kv_plan_info
+    _fields_ = [("struct_size", ctypes.c_uint32), ("reserved", ctypes.c_int32), ("page_bytes", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("workspace_bytes", ctypes.c_uint64)]
+
+
 class PlanInfo(ctypes.Structure):
     _fields_ = [("struct_size", ctypes.c_uint32), ("variant", ctypes.c_char * 64), ("tile_m", ctypes.c_int32),
                 ("tile_n", ctypes.c_int32), ("tile_k", ctypes.c_int32), ("grid_x", ctypes.c_uint32),
@@ -99,6 +125,13 @@ _SIGNATURES = {
                                       ctypes.c_int, _VP, ctypes.POINTER(ctypes.c_double),
                                       ctypes.POINTER(ctypes.c_double)]),
     "bsg_run_noalloc": (ctypes.c_int, [ctypes.POINTER(Problem), _VP, _VP, _VP, _VP, _VP, ctypes.c_float, _VP, _VP]),
+    "bsg_kv_plan_create": (ctypes.c_int, [ctypes.POINTER(KVProblem), ctypes.POINTER(_VP)]),
+    "bsg_kv_plan_destroy": (ctypes.c_int, [_VP]),
+    "bsg_kv_plan_query": (ctypes.c_int, [_VP, ctypes.POINTER(KVPlanInfo)]),
+    "bsg_kv_page_bytes": (ctypes.c_int64, [ctypes.c_int32] * 3),
+    "bsg_kv_append": (ctypes.c_int, [_VP] * 7 + [ctypes.c_int64, _VP, _VP]),
+    "bsg_kv_attend": (ctypes.c_int, [_VP] * 7),
+    "bsg_kv_read": (ctypes.c_int, [_VP] * 6),
     "bsg_bench_null_loop": (ctypes.c_int, [ctypes.c_int, _VP, ctypes.POINTER(ctypes.c_double),
                                            ctypes.POINTER(ctypes.c_double)]),
 }
@@ -138,15 +171,21 @@ def _ptr(x) -> int | None:
     return x.data_ptr()
 
 
+_torch_cuda = None  # torch.cuda once a GPU was seen through it
+
+
 def _stream(s) -> int | None:
+    global _torch_cuda
     if s is None:
-        try:
-            import torch
-            if torch.cuda.is_available():
-                return torch.cuda.current_stream().cuda_stream
-        except ImportError:
-            pass
-        return None
+        if _torch_cuda is None:
+            try:
+                import torch
+            except ImportError:
+                return None
+            if not torch.cuda.is_available():
+                return None
+            _torch_cuda = torch.cuda
+        return _torch_cuda.current_stream().cuda_stream
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -272,3 +311,150 @@ def pack_scales(src, dst, rows: int, codes_per_row: int, stream=None) -> None:
     """dst (scales_ktile_bytes(rows, codes_per_row) bytes, device) = the K-tile-major layout of the
     row-major scale codes src [rows][codes_per_row] (device); enqueued on `stream`."""
     _check(load_library().bsg_pack_scales(_ptr(src), _ptr(dst), rows, codes_per_row, _stream(stream)))
+
+
+KV_ROPE_INTERLEAVED, KV_NONCAUSAL = 1, 2
+ROPE_LAYOUTS = ("half", "interleaved")
+
+
+def kv_page_bytes(kv_heads: int, head_dim: int, page_tokens: int) -> int:
+    """Bytes of one packed page of a paged NVFP4 cache (0 for a geometry without kernels)."""
+    return load_library().bsg_kv_page_bytes(kv_heads, head_dim, page_tokens)
+
+
+class KVBatch:
+    """The new tokens of a call and where their sequences' positions live (bsg_kv_batch).
+
+    q_start [seqs + 1], kv_len [seqs] and pages [seqs][entries]: int32 device tensors (kept alive here);
+    num_tokens = q_start[-1]; max_q and max_kv bound every sequence's new tokens and context.
+    """
+
+    def __init__(self, q_start, kv_len, pages, num_tokens: int, max_q: int, max_kv: int):
+        seqs = kv_len.shape[0]
+        if q_start.shape[0] != seqs + 1 or pages.dim() != 2 or pages.shape[0] != seqs:
+            raise ValueError("q_start needs one entry more than kv_len, and pages one row for each of its entries")
+        for t in (q_start, kv_len, pages):
+            if t.element_size() != 4 or t.is_floating_point() or (t.numel() and t.stride(-1) != 1):
+                raise ValueError("q_start, kv_len and pages must be int32 with contiguous rows")
+        self.num_tokens, self._held = num_tokens, (q_start, kv_len, pages)
+        stride = pages.stride(0) if seqs > 1 else pages.shape[1]
+        self._args = KVBatchArgs(ctypes.sizeof(KVBatchArgs), seqs, num_tokens, max_q, max_kv, q_start.data_ptr(),
+                                 kv_len.data_ptr(), pages.data_ptr(), stride)
+        self._ref = ctypes.byref(self._args)
+
+
+class KVPlan:
+    """A plan of the paged NVFP4 cache and its attention for one geometry (bsg_kv.h): append, attend, read.
+
+    The cache is a uint8 device tensor of num_pages * page_bytes bytes (or with page_stride between pages).
+    q, k, v and outputs: 16-bit tensors [tokens][heads][head_dim] of `dtype`, any token and head strides that
+    are multiples of 8 elements.  window > 0: causal attention to the last `window` positions only.
+    """
+
+    def __init__(self, q_heads: int, kv_heads: int, head_dim: int, page_tokens: int, num_pages: int, max_tokens: int,
+                 dtype: str = "bf16", scale: float = 0.0, causal: bool = True, window: int = 0, softcap: float = 0.0,
+                 k_scale: float = 1.0, v_scale: float = 1.0, rope_dim: int = 0, rope_layout: str = "half",
+                 page_stride: int = 0, device: int = -1):
+        if rope_layout not in ROPE_LAYOUTS:
+            raise ValueError(f"rope_layout must be one of {ROPE_LAYOUTS}")
+        self._h = None
+        self._lib = lib = load_library()
+        self.q_heads, self.kv_heads, self.head_dim, self.rope_dim = q_heads, kv_heads, head_dim, rope_dim
+        prob = KVProblem(ctypes.sizeof(KVProblem), OUT_DTYPES[dtype], q_heads, kv_heads, head_dim, page_tokens, num_pages,
+                         page_stride, max_tokens, (KV_ROPE_INTERLEAVED if rope_layout == "interleaved" else 0)
+                         | (0 if causal else KV_NONCAUSAL), rope_dim, window, scale, softcap, k_scale, v_scale, device)
+        h = _VP()
+        _check(lib.bsg_kv_plan_create(ctypes.byref(prob), ctypes.byref(h)))
+        self._h = h
+        self.page_bytes = self.info()["page_stride"]
+
+    def _heads(self, t, tokens: int, heads: int):
+        if t.shape != (tokens, heads, self.head_dim) or t.element_size() != 2 or t.stride(2) != 1:
+            raise ValueError(f"expected a 16-bit tensor [{tokens}][{heads}][{self.head_dim}] with contiguous rows, got "
+                             f"{tuple(t.shape)} with strides {t.stride()}")
+        return ctypes.byref(Heads(t.data_ptr(), t.stride(0), t.stride(1)))
+
+    def append(self, batch: KVBatch, k, v, cache, q=None, q_out=None, rope=None, stream=None) -> None:
+        """Store the batch's keys (rotated) and values; with q, write rotated queries to q_out (q: in place).
+        rope: float32 table [rows][2][rope_dim / 2] (rope_table makes one)."""
+        n = batch.num_tokens
+        if rope is not None and (rope.shape[1:] != (2, self.rope_dim // 2) or rope.element_size() != 4
+                                 or not rope.is_contiguous()):
+            raise ValueError(f"rope must be a contiguous float32 tensor [rows][2][{self.rope_dim // 2}]")
+        _check(self._lib.bsg_kv_append(
+            self._h, batch._ref, None if q is None else self._heads(q, n, self.q_heads),
+            self._heads(k, n, self.kv_heads), self._heads(v, n, self.kv_heads),
+            None if q_out is None else self._heads(q_out, n, self.q_heads), _ptr(rope),
+            0 if rope is None else rope.shape[0], _ptr(cache), _stream(stream)))
+
+    def attend(self, batch: KVBatch, q, cache, out, lse=None, stream=None) -> None:
+        """out = attention of the batch's queries over the cache; lse: float32 [tokens][q_heads] or None."""
+        n = batch.num_tokens
+        if lse is not None and (lse.shape != (n, self.q_heads) or lse.element_size() != 4 or not lse.is_contiguous()):
+            raise ValueError(f"lse must be a contiguous float32 tensor [{n}][{self.q_heads}]")
+        _check(self._lib.bsg_kv_attend(self._h, batch._ref, self._heads(q, n, self.q_heads), _ptr(cache),
+                                       self._heads(out, n, self.q_heads), _ptr(lse), _stream(stream)))
+
+    def read(self, batch: KVBatch, cache, k, v, stream=None) -> None:
+        """k, v = the values that the cache holds at the positions of the batch's new tokens."""
+        n = batch.num_tokens
+        _check(self._lib.bsg_kv_read(self._h, batch._ref, _ptr(cache), self._heads(k, n, self.kv_heads),
+                                     self._heads(v, n, self.kv_heads), _stream(stream)))
+
+    def info(self) -> dict:
+        inf = KVPlanInfo()
+        inf.struct_size = ctypes.sizeof(KVPlanInfo)
+        _check(self._lib.bsg_kv_plan_query(self._h, ctypes.byref(inf)))
+        return dict(page_bytes=inf.page_bytes, page_stride=inf.page_stride, workspace_bytes=inf.workspace_bytes)
+
+    def close(self) -> None:
+        if self._h is not None and self._h.value:
+            _check(self._lib.bsg_kv_plan_destroy(self._h))
+        self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+
+def rope_table(rows: int, rope_dim: int, base: float = 10000.0, scaling: tuple | None = None):
+    """The rotation table of positions 0 .. rows - 1: float32 array [rows][2][rope_dim / 2], cosines then sines.
+
+    Pair i turns by position * base^(-2 i / rope_dim).  scaling, for contexts longer than a model was trained on:
+      ("linear", f)        positions divided by f;
+      ("base", f)          base multiplied by f^(R / (R - 2)): the slowest pair slows down by f, the fastest not at all;
+      ("parts", f, n)      pairs that turn more than 32 times in the trained n positions stay, pairs that turn less than
+                           once slow down by f, those between go linearly from one to the other; cosines and sines are
+                           multiplied by 1 + 0.1 ln f.
+    Angles are formed in 64 bits (in 32, position 100000 would be off by 0.004 rad)."""
+    import numpy as np
+
+    if rope_dim < 2 or rope_dim % 2 or rows < 1:
+        raise ValueError("rope_dim must be even and positive, rows positive")
+    half = rope_dim // 2
+    kind = scaling[0] if scaling else None
+    if kind not in (None, "linear", "base", "parts"):
+        raise ValueError('scaling must be None, ("linear", f), ("base", f) or ("parts", f, n)')
+    if kind == "base":
+        base = base * scaling[1] ** (rope_dim / max(rope_dim - 2, 1))
+    freq = base ** (-np.arange(half, dtype=np.float64) / half)
+    gain = 1.0
+    if kind == "linear":
+        freq = freq / scaling[1]
+    elif kind == "parts":
+        turns = freq * scaling[2] / (2.0 * np.pi)
+        first = half * np.log(scaling[2] / (32 * 2.0 * np.pi)) / np.log(base)  # pair that turns 32 times
+        last = half * np.log(scaling[2] / (2.0 * np.pi)) / np.log(base)        # pair that turns once
+        slow = np.clip((np.arange(half) - first) / max(last - first, 1e-3), 0.0, 1.0)
+        freq = np.where(turns >= 32, freq, np.where(turns <= 1, freq / scaling[1], freq * (1 - slow) + freq / scaling[1] * slow))
+        gain = 1.0 + 0.1 * np.log(scaling[1])
+    angle = np.arange(rows, dtype=np.float64)[:, None] * freq
+    return np.stack((np.cos(angle) * gain, np.sin(angle) * gain), 1).astype(np.float32)

@@ -35,6 +35,50 @@ void set_error(const char* fmt, ...) {
   va_end(ap);
 }
 
+// hipMalloc / hipFree on `dev`, restoring the caller's current device.
+bsg_status device_alloc(int dev, size_t bytes, void** out) {
+  int cur = -1;
+  if (hipGetDevice(&cur) != hipSuccess) cur = -1;
+  if (cur != dev && hipSetDevice(dev) != hipSuccess) {
+    set_error("hipSetDevice(%d) failed", dev);
+    return BSG_ERR_HIP;
+  }
+  const hipError_t e = hipMalloc(out, bytes);
+  if (cur >= 0 && cur != dev) (void)hipSetDevice(cur);
+  if (e != hipSuccess) {
+    *out = nullptr;
+    set_error("hipMalloc(%zu) of a plan's workspace failed: %s", bytes, hipGetErrorString(e));
+    return BSG_ERR_HIP;
+  }
+  return BSG_OK;
+}
+
+void device_free(int dev, void* p) {
+  if (!p) return;
+  int cur = -1;
+  if (hipGetDevice(&cur) != hipSuccess) cur = -1;
+  if (cur != dev) (void)hipSetDevice(dev);
+  (void)hipFree(p);
+  if (cur >= 0 && cur != dev) (void)hipSetDevice(cur);
+}
+
+bsg_status device_clear(int dev, void* p, size_t bytes) {
+  int cur = -1;
+  if (hipGetDevice(&cur) != hipSuccess) cur = -1;
+  if (cur != dev && hipSetDevice(dev) != hipSuccess) {
+    set_error("hipSetDevice(%d) failed", dev);
+    return BSG_ERR_HIP;
+  }
+  hipError_t e = hipMemset(p, 0, bytes);
+  if (e == hipSuccess) e = hipStreamSynchronize(nullptr);
+  if (cur >= 0 && cur != dev) (void)hipSetDevice(cur);
+  if (e != hipSuccess) {
+    set_error("clearing a plan's workspace failed: %s", hipGetErrorString(e));
+    return BSG_ERR_HIP;
+  }
+  return BSG_OK;
+}
+
 }  // namespace bsg
 
 namespace {
@@ -125,32 +169,8 @@ int choose_splits(const bsg::KernelVariant& v, int64_t tiles, int64_t K, double 
   return best;
 }
 
-// hipMalloc / hipFree on `dev`, restoring the caller's current device.
-bsg_status device_alloc(int dev, size_t bytes, void** out) {
-  int cur = -1;
-  if (hipGetDevice(&cur) != hipSuccess) cur = -1;
-  if (cur != dev && hipSetDevice(dev) != hipSuccess) {
-    set_error("hipSetDevice(%d) failed", dev);
-    return BSG_ERR_HIP;
-  }
-  const hipError_t e = hipMalloc(out, bytes);
-  if (cur >= 0 && cur != dev) (void)hipSetDevice(cur);
-  if (e != hipSuccess) {
-    *out = nullptr;
-    set_error("hipMalloc(%zu) of the split-K workspace failed: %s", bytes, hipGetErrorString(e));
-    return BSG_ERR_HIP;
-  }
-  return BSG_OK;
-}
-
-void device_free(int dev, void* p) {
-  if (!p) return;
-  int cur = -1;
-  if (hipGetDevice(&cur) != hipSuccess) cur = -1;
-  if (cur != dev) (void)hipSetDevice(dev);
-  (void)hipFree(p);
-  if (cur >= 0 && cur != dev) (void)hipSetDevice(cur);
-}
+using bsg::device_alloc;
+using bsg::device_free;
 
 static_assert(offsetof(bsg_problem, batch) == 44 && offsetof(bsg_problem, stride_a) == BSG_PROBLEM_V1_SIZE,
               "the batch fields extend the ABI-1 layout (batch sits in its tail padding)");
@@ -276,6 +296,24 @@ const char* bsg_status_string(bsg_status s) {
 
 namespace bsg {
 
+bsg_status resolve_device(int requested, int* out_dev, int* out_cus) {
+  bsg_status st = check_forced_arch();
+  if (st != BSG_OK) return st;
+  int dev = requested;
+  if (dev < 0) {
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) {
+      set_error("no current HIP device: %s", hipGetErrorString(e));
+      return BSG_ERR_DEVICE;
+    }
+  }
+  st = check_device(dev);
+  if (st != BSG_OK) return st;
+  *out_dev = dev;
+  *out_cus = g_dev_cus[dev];
+  return BSG_OK;
+}
+
 // Everything bsg_plan_create does except allocating: validation, variant choice, launch shape and the
 // argument template, written into *plan (caller-owned storage).  The split-K workspace size is
 // plan->workspace_bytes; plan->args.ws is left null for the caller to point at a workspace.
@@ -290,17 +328,8 @@ bsg_status build_plan(const bsg_problem* problem, bsg_plan_s* plan) {
   problem = &prob;
   st = validate(problem);
   if (st != BSG_OK) return st;
-  st = check_forced_arch();
-  if (st != BSG_OK) return st;
-  int dev = problem->device;
-  if (dev < 0) {
-    hipError_t e = hipGetDevice(&dev);
-    if (e != hipSuccess) {
-      set_error("no current HIP device: %s", hipGetErrorString(e));
-      return BSG_ERR_DEVICE;
-    }
-  }
-  st = check_device(dev);
+  int dev = -1, cus = 0;
+  st = resolve_device(problem->device, &dev, &cus);
   if (st != BSG_OK) return st;
 
   const bool bias = problem->flags & BSG_EPI_BIAS, silu = problem->flags & BSG_EPI_SILU;
@@ -337,7 +366,7 @@ bsg_status build_plan(const bsg_problem* problem, bsg_plan_s* plan) {
   a.tiles_n = (int)((problem->N + v.tile_n - 1) / v.tile_n);
   a.scale_ktile = (problem->flags & BSG_SCALES_KTILE) ? 1 : 0;
   a.splits = choose_splits(v, (int64_t)a.tiles_m * a.tiles_n * problem->batch, problem->K,
-                           4.0 * (double)problem->batch * (double)problem->M * (double)problem->N, g_dev_cus[dev]);
+                           4.0 * (double)problem->batch * (double)problem->M * (double)problem->N, cus);
   a.stride_a = problem->stride_a;
   a.stride_b = problem->stride_b;
   a.stride_sa = problem->stride_sa;
@@ -360,8 +389,7 @@ bsg_status build_plan(const bsg_problem* problem, bsg_plan_s* plan) {
   plan->block = dim3((unsigned)v.block_threads, 1, 1);
   // A persistent kernel takes at most one workgroup per CU; a multiple of 8 keeps each workgroup's
   // tiles on one XCD (workgroups go to the XCDs round-robin).
-  if (v.persistent && g_dev_cus[dev] > 0 && g_dev_cus[dev] % 8 == 0 && plan->grid.x > (unsigned)g_dev_cus[dev])
-    plan->grid.x = (unsigned)g_dev_cus[dev];
+  if (v.persistent && cus > 0 && cus % 8 == 0 && plan->grid.x > (unsigned)cus) plan->grid.x = (unsigned)cus;
   plan->log_level = env_log_level();
   if (plan->log_level >= 1)
     fprintf(stderr,

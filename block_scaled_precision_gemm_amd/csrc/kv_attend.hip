@@ -1,0 +1,576 @@
+// Attention over the paged NVFP4 cache for few query rows per key/value head.
+//
+// A unit of work is a block of R = 16 RT query rows (new tokens x the query heads that share a
+// key/value head) of one sequence and key/value head, over that sequence's positions.  Positions are
+// cut into tiles of 64; the tiles of all units form one line, and each workgroup takes an equal run of
+// it, whatever the contexts' lengths.  A unit whose tiles lie in several workgroups is joined by the
+// last of them to finish, in the workgroups' order, from partial results (output, maximum, sum) that
+// the others left in the plan's workspace.  So one launch balances any mixture of lengths, and the
+// order of every sum is fixed.
+//
+// Inside a workgroup the four waves take consecutive quarters of a run and are joined through LDS.  A
+// wave handles 64 positions at a time, everything in registers:
+// * S^T = K Q^T on v_mfma_f32_16x16x32_f16: a lane loads D/4 consecutive dims of one position (16
+//   bytes for D = 128) -- the k order of the product is free, so those are its k values.  K is decoded
+//   exactly (codec.h); Q is exact in fp16 once each row is scaled by a power of two (bf16 rows).
+// * The result has position 4g + i (g = lane / 16) of each 16 in element i and the row in lane % 16,
+//   which is the layout in which P^T enters O^T += V^T P^T as the second operand: softmax needs no
+//   data movement but the maximum over g.
+// * For that product a lane needs 8 positions of one dim.  It loads 4 bytes (D = 128: 8 dims) of each
+//   of 8 positions, interleaves the nibbles of two positions (4 operations for 16 values), and decodes
+//   each byte to the pair (position j, position j + 1), which one packed multiply scales by the pair of
+//   scales, stored with the position fastest for this purpose.
+// Softmax: running maximum m and sum l per row, in fp32 and base 2; accumulators are rescaled only when
+// some row's maximum grew.  P is rounded to fp16 for its product, offset by 2^14 so that weights down to
+// 2^-38 of the largest are kept (fp16 steps are 2^-24); l sums the unrounded values.
+//
+// Bound: bytes of the cache (D 9/8 bytes per position and head).
+#include "kv.h"
+
+namespace bsg {
+namespace {
+
+typedef float v2f __attribute__((ext_vector_type(2)));
+
+constexpr int kThreads = 256;
+constexpr int kTile = 64;       // positions of a tile, and of a wave's step
+constexpr int kMinTiles = 4;    // a workgroup's run is at least one tile per wave
+constexpr int kWgPerCu = 2;
+constexpr float kPBias = 14.0f; // P is held as 2^14 P
+constexpr float kNegInf = -__builtin_inff();
+
+// Combine the four lanes of one row (lane % 16): each swap gives every lane its own value and its partner's.
+__device__ __forceinline__ void swap32(float x, float& a, float& b) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  const uint32_t r0 = r[0], r1 = r[1];
+  a = __builtin_bit_cast(float, r0);
+  b = __builtin_bit_cast(float, r1);
+}
+__device__ __forceinline__ void swap16(float x, float& a, float& b) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  const uint32_t r0 = r[0], r1 = r[1];
+  a = __builtin_bit_cast(float, r0);
+  b = __builtin_bit_cast(float, r1);
+}
+__device__ __forceinline__ float max_over_g(float x) {
+  float a, b;
+  swap32(x, a, b);
+  swap16(__builtin_fmaxf(a, b), a, b);
+  return __builtin_fmaxf(a, b);
+}
+__device__ __forceinline__ float sum_over_g(float x) {
+  float a, b;
+  swap32(x, a, b);
+  swap16(a + b, a, b);
+  return a + b;
+}
+
+// Two non-negative E4M3 codes (bytes SEL picks) -> fp16 pair, times 2^-8; 0x7F -> NaN (0x3F80 + 0x80
+// carries into the bit that makes it one).
+template <uint32_t SEL>
+__device__ __forceinline__ uint32_t scale_pair(uint32_t w) {
+  const uint32_t t = __builtin_amdgcn_perm(0u, w, SEL) >> 1;
+  return t | ((t + 0x00800080u) & 0x40004000u);
+}
+constexpr uint32_t kLow = 0x010C000Cu, kHigh = 0x030C020Cu;  // bytes 0, 1 and bytes 2, 3
+
+__device__ __forceinline__ v2h fp4_pair(uint32_t w, int b) {
+  // the byte is an immediate of the instruction
+  switch (b) {
+    case 0: return __builtin_bit_cast(v2h, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0));
+    case 1: return __builtin_bit_cast(v2h, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1));
+    case 2: return __builtin_bit_cast(v2h, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2));
+    default: return __builtin_bit_cast(v2h, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3));
+  }
+}
+
+// What a unit covers.
+struct Span {
+  int q_len, len;  // new tokens and context of the sequence
+  int lo, tiles;   // first position read (a multiple of 16), and tiles of each of its units
+};
+
+__device__ __forceinline__ Span span_of(const KvArgs& p, int b) {
+  Span s;
+  s.len = seq_len(p, b);
+  s.q_len = p.one_each ? 1 : min(max(seq_start(p, b + 1) - seq_start(p, b), 0), p.max_q);
+  s.lo = p.window > 0 ? max(0, s.len - s.q_len - p.window + 1) & ~15 : 0;
+  s.tiles = max(1, (s.len - s.lo + kTile - 1) / kTile);
+  return s;
+}
+
+template <Out O>
+__device__ __forceinline__ uint16_t out_bits(float y) {
+  if constexpr (O == Out::BF16) return __builtin_bit_cast(uint16_t, (__bf16)y);
+  else return __builtin_bit_cast(uint16_t, (_Float16)y);
+}
+
+template <Out O, int D, int RT>
+__global__ __launch_bounds__(kThreads) void few_kernel(KvArgs p) {
+  constexpr int R = 16 * RT;
+  constexpr int NJ = D / 32;       // k steps of Q K^T; dwords of K codes a lane loads per position
+  constexpr int E = D / 16;        // dims of a lane in V; output tiles
+  constexpr int OS = D + 4;        // LDS row of the joining buffer (padded)
+  constexpr int SLOT = R * (D + 2);  // floats of a partial: R x D outputs, R maxima, R sums
+  using L = PageLayout<D>;
+  __shared__ float sh_o[4][R][OS];
+  __shared__ float sh_m[4][R], sh_l[4][R];
+  __shared__ int sh_sum[4], sh_at[3], sh_last;
+
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int c = lane & 15, g = lane >> 4;
+  const int H = p.kv_heads, G = p.group;
+  const int P = 1 << p.page_shift;
+
+  // ---- this workgroup's run of the line of tiles
+  const int per_thread = (p.num_seqs + kThreads - 1) / kThreads;
+  int mine = 0;
+  for (int i = 0; i < per_thread; ++i) {
+    const int b = tid * per_thread + i;
+    if (b < p.num_seqs) {
+      const Span s = span_of(p, b);
+      mine += (s.q_len * G + R - 1) / R * H * s.tiles;
+    }
+  }
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int y = __shfl_up(incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 63) sh_sum[wave] = incl;
+  __syncthreads();
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    if (w < wave) incl += sh_sum[w];
+    total += sh_sum[w];
+  }
+  const int per = max(kMinTiles, (total + (int)gridDim.x - 1) / (int)gridDim.x);
+  const int run0 = blockIdx.x * per;
+  if (run0 >= total) return;
+  const int run1 = min(run0 + per, total);
+  if (incl - mine <= run0 && run0 < incl) {  // the one thread whose sequences hold the run's start
+    int at = incl - mine, b = tid * per_thread;
+    for (;; ++b) {
+      const Span s = span_of(p, b);
+      const int n = (s.q_len * G + R - 1) / R * H * s.tiles;
+      if (run0 < at + n) break;
+      at += n;
+    }
+    sh_at[0] = b;
+    sh_at[1] = at;
+  }
+  __syncthreads();
+  int b = __builtin_amdgcn_readfirstlane(sh_at[0]);
+  int seq0 = __builtin_amdgcn_readfirstlane(sh_at[1]);  // line position of sequence b's first tile
+
+  for (int x = run0; x < run1;) {
+    Span s = span_of(p, b);
+    int blocks = (s.q_len * G + R - 1) / R;
+    while (x >= seq0 + blocks * H * s.tiles) {
+      seq0 += blocks * H * s.tiles;
+      ++b;
+      s = span_of(p, b);
+      blocks = (s.q_len * G + R - 1) / R;
+    }
+    const int unit = (x - seq0) / s.tiles;
+    const int u0 = seq0 + unit * s.tiles, u1 = u0 + s.tiles;  // the unit's tiles on the line
+    const int rb = unit / H, h = unit - rb * H;
+    const int x1 = min(run1, u1);
+    const int first_token = p.one_each ? b : seq_start(p, b);
+    const int rows = min(R, s.q_len * G - rb * R);
+    const bool causal = !(p.flags & BSG_KV_NONCAUSAL);
+    const int pos0 = s.len - s.q_len;  // position of the sequence's first new token
+    // positions seen by some row of the block
+    const int i_first = rb * R / G, i_last = (rb * R + rows - 1) / G;
+    const int lo = p.window > 0 ? max(0, pos0 + i_first - p.window + 1) : 0;
+    const int hi = causal ? max(0, pos0 + i_last + 1) : s.len;
+    const int s0 = max(s.lo + (x - u0) * kTile, lo & ~15), s1 = min(s.lo + (x1 - u0) * kTile, hi);
+
+    // ---- queries
+    v8h q[RT][NJ];
+    float mul[RT];   // base-2 score of one accumulator unit
+    int pos[RT];     // the row's position: it sees (pos - window, pos]
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      const int r = 16 * t + c;
+      const bool ok = r < rows;
+      const int i = (rb * R + (ok ? r : 0)) / G, hq = (rb * R + (ok ? r : 0)) - i * G;
+      const uint16_t* src = (const uint16_t*)p.q.ptr + (int64_t)(first_token + i) * p.q.token_stride +
+                            (int64_t)(h * G + hq) * p.q.head_stride + g * (D / 4);
+      pos[t] = causal ? pos0 + i : s.len - 1;
+      mul[t] = p.score_mul * (1.44269504088896341f * 256.0f);
+      v4i w[NJ];
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) w[j] = *(const v4i*)(src + 8 * j);
+      if constexpr (O == Out::F16) {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) q[t][j] = __builtin_bit_cast(v8h, w[j]);
+      } else {
+        // scale the row so that its largest magnitude lies in [2^14, 2^15): exact in fp16 down to
+        // 2^-39 of it
+        float f[NJ][8], most = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            f[j][2 * k] = __builtin_bit_cast(float, (uint32_t)w[j][k] << 16);
+            f[j][2 * k + 1] = __builtin_bit_cast(float, (uint32_t)w[j][k] & 0xFFFF0000u);
+            most = __builtin_fmaxf(most, __builtin_fmaxf(__builtin_fabsf(f[j][2 * k]), __builtin_fabsf(f[j][2 * k + 1])));
+          }
+        most = max_over_g(most);
+        const int e = (int)(__builtin_bit_cast(uint32_t, most) >> 23) - 127;  // -127 for zero and subnormals
+        const int up = e > 127 ? 0 : max(14 - e, -110);                       // inf or NaN: as it is
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) q[t][j][k] = (_Float16)__builtin_amdgcn_ldexpf(f[j][k], up);
+        mul[t] = __builtin_amdgcn_ldexpf(mul[t], -up);
+      }
+    }
+
+    v4f o[RT][E];
+    float m[RT], l[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      m[t] = kNegInf;
+      l[t] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[t][e] = v4f{0, 0, 0, 0};
+    }
+
+    // ---- this wave's positions
+    const int steps = s1 > s0 ? (s1 - s0 + kTile - 1) / kTile : 0;
+    const int per_wave = (steps + 3) / 4;
+    const int w0 = s0 + wave * per_wave * kTile, w1 = min(s1, w0 + per_wave * kTile);
+    if (w0 < w1) {
+      const int* table = p.pages + (int64_t)b * p.pages_stride;
+      const int last_pos = hi - 1;
+      int page_base = w0 >> p.page_shift;
+      int page_ids = clamp_page(p, table[min(page_base + lane, last_pos >> p.page_shift)]);
+      const int chunk = L::chunk(P);
+      // chunk of the 16 positions at t (clamped into the context), and their first slot
+      auto group_at = [&](int t, int& slot) -> const uint8_t* {
+        t = min(t, last_pos & ~15);
+        const int page = t >> p.page_shift;
+        if (page - page_base >= 64) {
+          page_base = page;
+          page_ids = clamp_page(p, table[min(page_base + lane, last_pos >> p.page_shift)]);
+        }
+        slot = t & (P - 1);
+        return p.cache + (int64_t)__builtin_amdgcn_readlane(page_ids, page - page_base) * p.page_stride +
+               (int64_t)h * chunk;
+      };
+      uint32_t kq[4][NJ], ks[4], vq[4][4], vs[4];
+      auto load_k = [&](int gr, const uint8_t* base, int slot) {
+        const uint8_t* kp = base + (slot + c) * L::kRow + g * (4 * NJ);
+        if constexpr (D == 128) {
+          const v4i w = *(const v4i*)kp;
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) kq[gr][j] = (uint32_t)w[j];
+          ks[gr] = *(const uint16_t*)(base + L::k_scales(P) + (slot + c) * L::kBlocks + 2 * g);
+        } else {
+          const uint2 w = *(const uint2*)kp;
+          kq[gr][0] = w.x;
+          kq[gr][1] = w.y;
+          ks[gr] = base[L::k_scales(P) + (slot + c) * L::kBlocks + g];
+        }
+      };
+      auto load_v = [&](int gr, const uint8_t* base, int slot) {
+        const uint8_t* vp = base + L::v_codes(P) + (slot + 4 * g) * L::kRow + c * (E / 2);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          vq[gr][j] = E == 8 ? *(const uint32_t*)(vp + j * L::kRow) : *(const uint16_t*)(vp + j * L::kRow);
+        vs[gr] = *(const uint32_t*)(base + L::v_scales(P) + (c * E / 16) * P + slot + 4 * g);
+      };
+      const uint8_t* base[4];
+      int slot[4];
+#pragma unroll
+      for (int gr = 0; gr < 4; ++gr) {
+        base[gr] = group_at(w0 + 16 * gr, slot[gr]);
+        load_k(gr, base[gr], slot[gr]);
+        load_v(gr, base[gr], slot[gr]);
+      }
+      for (int t0 = w0; t0 < w1; t0 += kTile) {
+        const bool more = t0 + kTile < w1;
+        // -- scores
+        v4f sc[RT][4];
+#pragma unroll
+        for (int gr = 0; gr < 4; ++gr) {
+          const uint32_t sp = scale_pair<kLow>(ks[gr]);
+          const uint32_t sp0 = f16x2_splat_lo(sp), sp1 = f16x2_splat_hi(sp);
+#pragma unroll
+          for (int t = 0; t < RT; ++t) sc[t][gr] = v4f{0, 0, 0, 0};
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            const v8h a = __builtin_bit_cast(v8h, e2m1x8_scaled_f16x8(kq[gr][j], j < 2 ? sp0 : sp1));
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+              sc[t][gr] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, q[t][j], sc[t][gr], 0, 0, 0);
+          }
+        }
+        if (more) {
+#pragma unroll
+          for (int gr = 0; gr < 4; ++gr) {
+            base[gr] = group_at(t0 + kTile + 16 * gr, slot[gr]);
+            load_k(gr, base[gr], slot[gr]);
+          }
+        }
+        // -- masks: only where a row does not see the whole tile
+        const int first_pos = causal ? pos0 + i_first : s.len - 1;
+        const int last_row_pos = causal ? pos0 + i_last : s.len - 1;
+        const bool edge = t0 + kTile - 1 > min(first_pos, w1 - 1) || (p.window > 0 && t0 <= last_row_pos - p.window);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+#pragma unroll
+          for (int gr = 0; gr < 4; ++gr) sc[t][gr] = sc[t][gr] * mul[t];
+          if (p.softcap > 0.0f) {
+            const float cap = p.softcap * 1.44269504088896341f, inv = 2.0f / p.softcap;  // tanh(y) = 1 - 2 / (e^2y + 1)
+#pragma unroll
+            for (int gr = 0; gr < 4; ++gr)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                sc[t][gr][i] = cap - 2.0f * cap * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(sc[t][gr][i] * inv) + 1.0f);
+          }
+          if (edge) {
+            const int top = min(pos[t], w1 - 1), bottom = p.window > 0 ? pos[t] - p.window : -1;
+#pragma unroll
+            for (int gr = 0; gr < 4; ++gr)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int at = t0 + 16 * gr + 4 * g + i;
+                sc[t][gr][i] = at <= top && at > bottom ? sc[t][gr][i] : kNegInf;
+              }
+          }
+        }
+        uint32_t nan_codes = 0;
+        if (edge) {
+          // positions that no row sees count as zero, whatever their slots hold; NaN blocks seen by
+          // some rows only are taken out here and given to those rows below
+          const int from = max(lo, w0), to = w1;
+#pragma unroll
+          for (int gr = 0; gr < 4; ++gr) {
+            uint32_t keep = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int at = t0 + 16 * gr + 4 * g + i;
+              if (at >= from && at < to) keep |= 0xFFu << (8 * i);
+            }
+            vs[gr] &= keep;
+            const uint32_t bad = ((vs[gr] + 0x01010101u) & 0x80808080u) >> 7;  // 1 in each byte that is 0x7F
+            nan_codes |= bad;
+            vs[gr] &= ~(bad * 0x7Fu);
+          }
+        }
+        // -- softmax
+        v8h pt[RT][2];
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+          float top = sc[t][0][0];
+#pragma unroll
+          for (int gr = 0; gr < 4; ++gr)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = __builtin_fmaxf(top, sc[t][gr][i]);
+          if (__any(top > m[t])) {
+            const float grown = __builtin_fmaxf(m[t], max_over_g(top));
+            const float f = grown == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m[t] - grown);
+            m[t] = grown;
+            l[t] *= f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[t][e] *= f;
+          }
+          const float off = m[t] == kNegInf ? 0.0f : m[t] - kPBias;
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              float e4[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                e4[i] = __builtin_amdgcn_exp2f(sc[t][2 * k + half][i] - off);
+                l[t] += e4[i];
+              }
+              const v2h a = __builtin_convertvector((v2f{e4[0], e4[1]}), v2h), bb = __builtin_convertvector((v2f{e4[2], e4[3]}), v2h);
+              pt[t][k][4 * half] = a[0];
+              pt[t][k][4 * half + 1] = a[1];
+              pt[t][k][4 * half + 2] = bb[0];
+              pt[t][k][4 * half + 3] = bb[1];
+            }
+        }
+        // -- O^T += V^T P^T
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          v4i frag[E];
+#pragma unroll
+          for (int jj = 0; jj < 4; ++jj) {  // pairs of positions: two of each 16
+            const int gr = 2 * k + jj / 2, j = (jj & 1) * 2;
+            const v2h s2 = __builtin_bit_cast(v2h, (jj & 1) ? scale_pair<kHigh>(vs[gr]) : scale_pair<kLow>(vs[gr]));
+            const uint32_t a = vq[gr][j], bb = vq[gr][j + 1], mask = 0x0F0F0F0Fu;
+            const uint32_t even = (a & mask) | ((bb << 4) & ~mask), odd = ((a >> 4) & mask) | (bb & ~mask);
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+              frag[e][jj] = __builtin_bit_cast(int, fp4_pair(even, e / 2) * s2);
+              frag[e + 1][jj] = __builtin_bit_cast(int, fp4_pair(odd, e / 2) * s2);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+              o[t][e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, frag[e]), pt[t][k], o[t][e], 0, 0, 0);
+        }
+        if (__any(nan_codes)) {
+          // rare: a NaN block among positions that not every row sees.  Output element i of tile e is
+          // dim E (4g + i) + e, so element i lies in block E (4g + i) / 16.
+          for (int at = max(t0, max(lo, w0)); at < min(t0 + kTile, w1); ++at) {
+            const int page = clamp_page(p, table[at >> p.page_shift]), sl = at & (P - 1);
+            const uint8_t* codes = p.cache + (int64_t)page * p.page_stride + (int64_t)h * chunk + L::v_scales(P) + sl;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const bool bad = codes[E * (4 * g + i) / 16 * P] == 0x7F;
+#pragma unroll
+              for (int t = 0; t < RT; ++t)
+                if (bad && at <= pos[t] && (p.window <= 0 || at > pos[t] - p.window))
+#pragma unroll
+                  for (int e = 0; e < E; ++e) o[t][e][i] = __builtin_nanf("");
+            }
+          }
+        }
+        if (more) {
+#pragma unroll
+          for (int gr = 0; gr < 4; ++gr) load_v(gr, base[gr], slot[gr]);
+        }
+      }
+    }
+
+    // ---- join the waves
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      const float sum = sum_over_g(l[t]);
+      const int r = 16 * t + c;
+      if (g == 0) {
+        sh_m[wave][r] = m[t];
+        sh_l[wave][r] = sum;
+      }
+      if (sum != 0.0f) {  // a NaN row counts
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < E; e += 4)
+            *(v4f*)&sh_o[wave][r][E * (4 * g + i) + e] = v4f{o[t][e][i], o[t][e + 1][i], o[t][e + 2][i], o[t][e + 3][i]};
+      }
+    }
+    __syncthreads();
+    const bool whole = x <= u0 && x1 >= u1;
+    float* slot0 = p.part;
+    const int wg0 = u0 / per;  // the first workgroup of the unit
+    if (!whole) slot0 += (size_t)(2 * blockIdx.x + (u0 >= run0 ? 1 : 0)) * SLOT;
+    // element (row r, dims d .. d+3)
+    auto store_out = [&](int r, int d, v4f y, float top, float sum) {
+      const int i = (rb * R + r) / G, hq = rb * R + r - i * G;
+      const float f = sum > 0.0f ? p.v_scale * 256.0f / sum : sum;  // an empty row: zeros; a NaN stays one
+      uint16_t* dst = (uint16_t*)p.out.ptr + (int64_t)(first_token + i) * p.out.token_stride +
+                      (int64_t)(h * G + hq) * p.out.head_stride + d;
+      const uint32_t a = out_bits<O>(sum == 0.0f ? 0.0f : y[0] * f), bq = out_bits<O>(sum == 0.0f ? 0.0f : y[1] * f);
+      const uint32_t cc = out_bits<O>(sum == 0.0f ? 0.0f : y[2] * f), dd = out_bits<O>(sum == 0.0f ? 0.0f : y[3] * f);
+      *(uint2*)dst = make_uint2(a | bq << 16, cc | dd << 16);
+      if (p.lse && d == 0)
+        p.lse[(int64_t)(first_token + i) * p.q_heads + h * G + hq] =
+            sum == 0.0f ? kNegInf : (top - kPBias + __builtin_amdgcn_logf(sum)) * 0.693147180559945309f;
+    };
+    for (int k = tid; k < rows * (D / 4); k += kThreads) {
+      const int r = k / (D / 4), d = k % (D / 4) * 4;
+      float top = kNegInf, sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) top = __builtin_fmaxf(top, sh_m[w][r]);
+      v4f y = {0, 0, 0, 0};
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        if (sh_l[w][r] != 0.0f) {
+          const float f = sh_m[w][r] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(sh_m[w][r] - top);
+          sum += f * sh_l[w][r];
+          y += f * *(const v4f*)&sh_o[w][r][d];
+        }
+      if (whole) {
+        store_out(r, d, y, top, sum);
+      } else {
+        *(v4f*)&slot0[r * D + d] = y;
+        if (d == 0) {
+          slot0[R * D + r] = top;
+          slot0[R * D + R + r] = sum;
+        }
+      }
+    }
+    if (!whole) {
+      // ---- the last workgroup of the unit joins the partials
+      const int wgs = (u1 - 1) / per - wg0 + 1;
+      __threadfence();
+      __syncthreads();
+      int* counter = p.arrived + ((int64_t)first_token * G + (int64_t)rb * R) * H + h;
+      if (tid == 0) {
+        const int before = __hip_atomic_fetch_add(counter, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+        sh_last = before == wgs - 1;
+        if (before == wgs - 1) __hip_atomic_store(counter, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+      __syncthreads();
+      if (sh_last) {
+        __threadfence();
+        // workgroup wg0 + k left its part in slot 2 (wg0 + k), the unit's first one in 2 wg0 + 1 (the
+        // unit starts inside it) or 2 wg0 (it starts with the run)
+        auto part_of = [&](int k) -> const float* {
+          const int wg = wg0 + k;
+          return p.part + (size_t)(2 * wg + (u0 >= wg * per ? 1 : 0)) * SLOT;
+        };
+        for (int k = tid; k < rows * (D / 4); k += kThreads) {
+          const int r = k / (D / 4), d = k % (D / 4) * 4;
+          float top = kNegInf, sum = 0.0f;
+          for (int w = 0; w < wgs; ++w) top = __builtin_fmaxf(top, part_of(w)[R * D + r]);
+          v4f y = {0, 0, 0, 0};
+          for (int w = 0; w < wgs; ++w) {
+            const float* s = part_of(w);
+            const float mw = s[R * D + r];
+            const float f = mw == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mw - top);
+            sum += f * s[R * D + R + r];
+            y += f * *(const v4f*)&s[r * D + d];
+          }
+          store_out(r, d, y, top, sum);
+        }
+      }
+    }
+    __syncthreads();  // the joining buffers are free again
+    x = x1;
+  }
+}
+
+template <Out O, int D>
+hipError_t launch(const KvArgs& a, int cus, hipStream_t stream) {
+  KvArgs args = a;
+  void* argv[] = {&args};
+  const int64_t rows = (int64_t)a.max_q * a.group;
+  const int R = rows <= 16 ? 16 : 32;
+  const int64_t context = a.window > 0 ? (int64_t)a.window + a.max_q + 16 : a.max_kv;
+  const int64_t tiles = ((context < a.max_kv ? context : a.max_kv) + kTile - 1) / kTile + 1;
+  // units: sum over sequences of ceil(tokens * group / R), at most one partial block each
+  const int64_t units = ((int64_t)a.num_tokens * a.group / R + a.num_seqs) * a.kv_heads;
+  const int64_t want = (units * tiles + kMinTiles - 1) / kMinTiles, most = (int64_t)cus * kWgPerCu;
+  const dim3 grid((unsigned)(want < most ? want : most));
+  const void* fn = R == 16 ? (const void*)&few_kernel<O, D, 1> : (const void*)&few_kernel<O, D, 2>;
+  return hipLaunchKernel(fn, grid, dim3(kThreads), argv, 0, stream);
+}
+
+}  // namespace
+
+hipError_t kv_attend_launch(const KvArgs& a, int dtype, int head_dim, int cus, hipStream_t stream) {
+  if (head_dim == 64) return dtype ? launch<Out::F16, 64>(a, cus, stream) : launch<Out::BF16, 64>(a, cus, stream);
+  return dtype ? launch<Out::F16, 128>(a, cus, stream) : launch<Out::BF16, 128>(a, cus, stream);
+}
+
+void kv_workspace(const bsg_kv_problem& p, int cus, size_t* part_floats, size_t* counters) {
+  *part_floats = (size_t)cus * kWgPerCu * 2 * 32 * (p.head_dim + 2);
+  *counters = (size_t)p.max_tokens * p.q_heads;
+}
+
+}  // namespace bsg

@@ -35,4 +35,12 @@ bsg_status launch_plan(const bsg_plan_s* plan, const void* A, const void* B, con
 
 void set_error(const char* fmt, ...);
 
+// The device a plan is for (`requested` < 0: the current one), checked to be gfx950, and its compute units.
+bsg_status resolve_device(int requested, int* dev, int* cus);
+
+// hipMalloc / hipFree / zero-fill (finished on return) on `dev`, leaving the caller's current device current.
+bsg_status device_alloc(int dev, size_t bytes, void** out);
+void device_free(int dev, void* p);
+bsg_status device_clear(int dev, void* p, size_t bytes);
+
 }  // namespace bsg
