@@ -1,5 +1,6 @@
-"""Python binding of the C ABI of libbsg.so: the block-scaled GEMM (include/bsg.h) and the paged NVFP4
-key/value cache with its attention (include/bsg_kv.h).
+"""Python binding of the C ABI of libbsg.so: the block-scaled GEMM (include/bsg.h), the paged NVFP4
+key/value cache with its attention (include/bsg_kv.h) and the mixture-of-experts layer for few tokens
+(include/bsg_moe.h).
 
 Argument marshalling only: every step runs in the HIP library.  Tensors are passed as
 device pointers (anything with .data_ptr(), or a plain int); streams as hipStream_t handles (an
@@ -16,7 +17,7 @@ import os
 __all__ = ["Plan", "BsgError", "LibraryNotBuilt", "load_library", "bench_loop", "null_loop", "run_noalloc", "NOALLOC_SCRATCH_BYTES", "decode_nvfp4_f16",
            "FORMATS", "OUT_DTYPES", "SCALE_LAYOUTS", "abi_version", "packed_strides", "Problem", "PROBLEM_V1_SIZE", "PROBLEM_V2_SIZE",
            "pack_scales", "scales_ktile_bytes",
-           "KVPlan", "KVBatch", "kv_page_bytes", "rope_table"]
+           "KVPlan", "KVBatch", "kv_page_bytes", "rope_table", "MoEPlan"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libbsg.so")
@@ -97,6 +98,19 @@ class KVPlanInfo(ctypes.Structure):  # bsg_kv_plan_info
                 ("page_stride", ctypes.c_int64), ("workspace_bytes", ctypes.c_uint64)]
 
 
+class MoEProblem(ctypes.Structure):  # bsg_moe_problem
+    _fields_ = [("struct_size", ctypes.c_uint32), ("format", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("flags", ctypes.c_uint32), ("experts", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("hidden", ctypes.c_int64), ("inter", ctypes.c_int64), ("max_tokens", ctypes.c_int64),
+                ("device", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class MoEWeights(ctypes.Structure):  # bsg_moe_weights
+    _fields_ = [("struct_size", ctypes.c_uint32), ("reserved", ctypes.c_uint32), ("router", ctypes.c_void_p),
+                ("w13", ctypes.c_void_p), ("s13", ctypes.c_void_p), ("w2", ctypes.c_void_p), ("s2", ctypes.c_void_p),
+                ("alpha13", ctypes.c_void_p), ("alpha2", ctypes.c_void_p)]
+
+
 class PlanInfo(ctypes.Structure):
     _fields_ = [("struct_size", ctypes.c_uint32), ("variant", ctypes.c_char * 64), ("tile_m", ctypes.c_int32),
                 ("tile_n", ctypes.c_int32), ("tile_k", ctypes.c_int32), ("grid_x", ctypes.c_uint32),
@@ -132,6 +146,9 @@ _SIGNATURES = {
     "bsg_kv_append": (ctypes.c_int, [_VP] * 7 + [ctypes.c_int64, _VP, _VP]),
     "bsg_kv_attend": (ctypes.c_int, [_VP] * 7),
     "bsg_kv_read": (ctypes.c_int, [_VP] * 6),
+    "bsg_moe_plan_create": (ctypes.c_int, [ctypes.POINTER(MoEProblem), ctypes.POINTER(_VP)]),
+    "bsg_moe_plan_destroy": (ctypes.c_int, [_VP]),
+    "bsg_moe_run": (ctypes.c_int, [_VP, ctypes.c_int64, _VP, ctypes.c_int64, _VP, _VP, ctypes.c_int64, _VP, _VP, _VP]),
     "bsg_bench_null_loop": (ctypes.c_int, [ctypes.c_int, _VP, ctypes.POINTER(ctypes.c_double),
                                            ctypes.POINTER(ctypes.c_double)]),
 }
@@ -410,6 +427,70 @@ class KVPlan:
     def close(self) -> None:
         if self._h is not None and self._h.value:
             _check(self._lib.bsg_kv_plan_destroy(self._h))
+        self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+
+MOE_KEEP_PROBABILITIES = 1
+
+
+class MoEPlan:
+    """A plan of a mixture-of-experts layer for up to max_tokens (at most 64) tokens (bsg_moe.h).
+
+    fmt: format of the experts' weights; dtype: of x, router and out.  renormalize: the chosen experts' weights
+    are divided by their sum.
+    """
+
+    def __init__(self, fmt: str, experts: int, top_k: int, hidden: int, inter: int, max_tokens: int, dtype: str = "bf16",
+                 renormalize: bool = True, device: int = -1):
+        self._h = None
+        self._lib = lib = load_library()
+        self.fmt, self.experts, self.top_k, self.hidden, self.inter = fmt, experts, top_k, hidden, inter
+        prob = MoEProblem(ctypes.sizeof(MoEProblem), FORMATS[fmt], OUT_DTYPES[dtype],
+                          0 if renormalize else MOE_KEEP_PROBABILITIES, experts, top_k, hidden, inter, max_tokens, device, 0)
+        h = _VP()
+        _check(lib.bsg_moe_plan_create(ctypes.byref(prob), ctypes.byref(h)))
+        self._h = h
+        per = 2 if fmt == "nvfp4" else 1
+        self._sizes = {"w13": 2 * inter * hidden // per, "s13": 2 * inter * hidden // SCALE_BLOCK[fmt],
+                       "w2": inter * hidden // per, "s2": inter * hidden // SCALE_BLOCK[fmt]}
+
+    def run(self, x, router, w13, s13, w2, s2, out, alpha13=None, alpha2=None, ids=None, weights=None, stream=None) -> None:
+        """out = the layer applied to x [tokens][hidden] (row-strided views are fine).  w13, s13, w2, s2: uint8 codes
+        and row-major scale codes of every expert; alpha13, alpha2: float32 [experts] or None; ids (int32) and weights
+        (float32) [tokens][top_k]: the routing, or None."""
+        tokens = x.shape[0]
+        for t in (x, out):
+            if t.shape != (tokens, self.hidden) or t.element_size() != 2 or t.stride(1) != 1:
+                raise ValueError(f"expected 16-bit rows [{tokens}][{self.hidden}], got {tuple(t.shape)} with strides {t.stride()}")
+        if router.shape != (self.experts, self.hidden) or router.element_size() != 2 or not router.is_contiguous():
+            raise ValueError(f"router must be a contiguous 16-bit tensor [{self.experts}][{self.hidden}]")
+        for name, t in (("w13", w13), ("s13", s13), ("w2", w2), ("s2", s2)):
+            if t.numel() != self.experts * self._sizes[name] or t.element_size() != 1 or not t.is_contiguous():
+                raise ValueError(f"{name} must hold {self.experts} x {self._sizes[name]} contiguous bytes")
+        for t, n in ((alpha13, self.experts), (alpha2, self.experts), (ids, tokens * self.top_k), (weights, tokens * self.top_k)):
+            if t is not None and (t.numel() != n or t.element_size() != 4 or not t.is_contiguous()):
+                raise ValueError("alpha13 and alpha2 have one 32-bit value per expert, ids and weights [tokens][top_k]")
+        w = MoEWeights(ctypes.sizeof(MoEWeights), 0, router.data_ptr(), w13.data_ptr(), s13.data_ptr(), w2.data_ptr(),
+                       s2.data_ptr(), _ptr(alpha13), _ptr(alpha2))
+        _check(self._lib.bsg_moe_run(self._h, tokens, x.data_ptr(), x.stride(0) if tokens > 1 else self.hidden,
+                                     ctypes.byref(w), out.data_ptr(), out.stride(0) if tokens > 1 else self.hidden,
+                                     _ptr(ids), _ptr(weights), _stream(stream)))
+
+    def close(self) -> None:
+        if self._h is not None and self._h.value:
+            _check(self._lib.bsg_moe_plan_destroy(self._h))
         self._h = None
 
     def __del__(self):
