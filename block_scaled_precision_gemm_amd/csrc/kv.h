@@ -36,8 +36,8 @@ struct KvArgs {
   float* lse;
   // workspace of the attention kernels
   float* part;       // partial outputs and their softmax statistics
-  int* arrived;      // arrival counter of each unit, zero between calls
-  int splits;        // KV splits of the row-tile kernel
+  int* group_arrived;  // arrival counters of groups of parts, and of units; zero between calls
+  int* arrived;
 };
 
 // Byte offsets inside the chunk of one head of a page (P = page tokens, D = head dim).
@@ -67,8 +67,8 @@ hipError_t kv_append_launch(const KvArgs& a, int dtype, int head_dim, bool with_
 hipError_t kv_read_launch(const KvArgs& a, int dtype, int head_dim, hipStream_t stream);
 hipError_t kv_attend_launch(const KvArgs& a, int dtype, int head_dim, int cus, hipStream_t stream);
 
-// Workspace of the attention kernels for calls of up to max_tokens tokens: floats of partials, and
-// counters (the counters follow the partials).
-void kv_workspace(const bsg_kv_problem& p, int cus, size_t* part_floats, size_t* counters);
+// Workspace of the attention kernels for calls of up to max_tokens tokens: floats of partials, then
+// counters, the first of them those of groups.
+void kv_workspace(const bsg_kv_problem& p, int cus, size_t* part_floats, size_t* counters, size_t* group_counters);
 
 }  // namespace bsg

@@ -244,14 +244,15 @@ bsg_status bsg_kv_plan_create(const bsg_kv_problem* problem, bsg_kv_plan* out_pl
   a.v_scale = p.v_scale;
   a.k_inv = 1.0f / p.k_scale;
   a.v_inv = 1.0f / p.v_scale;
-  size_t part = 0, counters = 0;
-  bsg::kv_workspace(p, cus, &part, &counters);
+  size_t part = 0, counters = 0, groups = 0;
+  bsg::kv_workspace(p, cus, &part, &counters, &groups);
   plan->workspace_bytes = (part + counters) * 4;
   st = bsg::device_alloc(dev, plan->workspace_bytes, &plan->workspace);
   if (st == BSG_OK) {
     a.part = (float*)plan->workspace;
-    a.arrived = (int*)(a.part + part);
-    st = bsg::device_clear(dev, a.arrived, counters * 4);
+    a.group_arrived = (int*)(a.part + part);
+    a.arrived = a.group_arrived + groups;
+    st = bsg::device_clear(dev, a.group_arrived, counters * 4);
     if (st != BSG_OK) bsg::device_free(dev, plan->workspace);
   }
   if (st != BSG_OK) {

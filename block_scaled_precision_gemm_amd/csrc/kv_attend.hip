@@ -25,6 +25,7 @@
 // 2^-38 of the largest are kept (fp16 steps are 2^-24); l sums the unrounded values.
 //
 // Bound: bytes of the cache (D 9/8 bytes per position and head).
+#include "handoff.h"
 #include "kv.h"
 
 namespace bsg {
@@ -37,6 +38,7 @@ constexpr int kTile = 64;       // positions of a tile, and of a wave's step
 constexpr int kMinTiles = 4;    // a workgroup's run is at least one tile per wave
 constexpr int kWgPerCu = 2;
 constexpr float kPBias = 14.0f; // P is held as 2^14 P
+constexpr int kJoin = 16;       // parts joined at a time
 constexpr float kNegInf = -__builtin_inff();
 
 // Combine the four lanes of one row (lane % 16): each swap gives every lane its own value and its partner's.
@@ -113,11 +115,11 @@ __global__ __launch_bounds__(kThreads) void few_kernel(KvArgs p) {
   constexpr int NJ = D / 32;       // k steps of Q K^T; dwords of K codes a lane loads per position
   constexpr int E = D / 16;        // dims of a lane in V; output tiles
   constexpr int OS = D + 4;        // LDS row of the joining buffer (padded)
-  constexpr int SLOT = R * (D + 2);  // floats of a partial: R x D outputs, R maxima, R sums
+  constexpr int SLOT = R * (D + 4);  // floats of a part
   using L = PageLayout<D>;
   __shared__ float sh_o[4][R][OS];
   __shared__ float sh_m[4][R], sh_l[4][R];
-  __shared__ int sh_sum[4], sh_at[3], sh_last;
+  __shared__ int sh_sum[4], sh_at[2], sh_last;
 
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int c = lane & 15, g = lane >> 4;
@@ -465,21 +467,29 @@ __global__ __launch_bounds__(kThreads) void few_kernel(KvArgs p) {
     }
     __syncthreads();
     const bool whole = x <= u0 && x1 >= u1;
-    float* slot0 = p.part;
-    const int wg0 = u0 / per;  // the first workgroup of the unit
-    if (!whole) slot0 += (size_t)(2 * blockIdx.x + (u0 >= run0 ? 1 : 0)) * SLOT;
+    const int wg0 = u0 / per, wgs = (u1 - 1) / per - wg0 + 1;  // the workgroups that share the unit
+    // Slot of the part that workgroup wg0 + k left: 2 (wg0 + k), or one more where the unit starts inside
+    // that workgroup's run.
+    auto slot_of = [&](int k) { return 2 * (wg0 + k) + (u0 >= (wg0 + k) * per ? 1 : 0); };
+    const __amdgpu_buffer_rsrc_t parts = handoff_buffer(p.part, 2u * gridDim.x * SLOT * 4u);
     // element (row r, dims d .. d+3)
     auto store_out = [&](int r, int d, v4f y, float top, float sum) {
       const int i = (rb * R + r) / G, hq = rb * R + r - i * G;
-      const float f = sum > 0.0f ? p.v_scale * 256.0f / sum : sum;  // an empty row: zeros; a NaN stays one
+      const float f = p.v_scale * 256.0f / sum;
+      const bool none = sum == 0.0f;  // an empty row gives zeros
       uint16_t* dst = (uint16_t*)p.out.ptr + (int64_t)(first_token + i) * p.out.token_stride +
                       (int64_t)(h * G + hq) * p.out.head_stride + d;
-      const uint32_t a = out_bits<O>(sum == 0.0f ? 0.0f : y[0] * f), bq = out_bits<O>(sum == 0.0f ? 0.0f : y[1] * f);
-      const uint32_t cc = out_bits<O>(sum == 0.0f ? 0.0f : y[2] * f), dd = out_bits<O>(sum == 0.0f ? 0.0f : y[3] * f);
+      const uint32_t a = out_bits<O>(none ? 0.0f : y[0] * f), bq = out_bits<O>(none ? 0.0f : y[1] * f);
+      const uint32_t cc = out_bits<O>(none ? 0.0f : y[2] * f), dd = out_bits<O>(none ? 0.0f : y[3] * f);
       *(uint2*)dst = make_uint2(a | bq << 16, cc | dd << 16);
       if (p.lse && d == 0)
         p.lse[(int64_t)(first_token + i) * p.q_heads + h * G + hq] =
-            sum == 0.0f ? kNegInf : (top - kPBias + __builtin_amdgcn_logf(sum)) * 0.693147180559945309f;
+            none ? kNegInf : (top - kPBias + __builtin_amdgcn_logf(sum)) * 0.693147180559945309f;
+    };
+    // part: R rows of D outputs, then (maximum, sum) of each row in a group of four floats
+    auto store_part = [&](int slot, int r, int d, v4f y, float top, float sum) {
+      handoff_store4(parts, slot * SLOT + r * D + d, y);
+      if (d == 0) handoff_store4(parts, slot * SLOT + R * D + 4 * r, v4f{top, sum, 0.0f, 0.0f});
     };
     for (int k = tid; k < rows * (D / 4); k += kThreads) {
       const int r = k / (D / 4), d = k % (D / 4) * 4;
@@ -494,49 +504,53 @@ __global__ __launch_bounds__(kThreads) void few_kernel(KvArgs p) {
           sum += f * sh_l[w][r];
           y += f * *(const v4f*)&sh_o[w][r][d];
         }
-      if (whole) {
-        store_out(r, d, y, top, sum);
-      } else {
-        *(v4f*)&slot0[r * D + d] = y;
-        if (d == 0) {
-          slot0[R * D + r] = top;
-          slot0[R * D + R + r] = sum;
-        }
-      }
+      if (whole) store_out(r, d, y, top, sum);
+      else store_part(slot_of(blockIdx.x - wg0), r, d, y, top, sum);
     }
     if (!whole) {
-      // ---- the last workgroup of the unit joins the partials
-      const int wgs = (u1 - 1) / per - wg0 + 1;
-      __threadfence();
-      __syncthreads();
-      int* counter = p.arrived + ((int64_t)first_token * G + (int64_t)rb * R) * H + h;
-      if (tid == 0) {
-        const int before = __hip_atomic_fetch_add(counter, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
-        sh_last = before == wgs - 1;
-        if (before == wgs - 1) __hip_atomic_store(counter, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      }
-      __syncthreads();
-      if (sh_last) {
-        __threadfence();
-        // workgroup wg0 + k left its part in slot 2 (wg0 + k), the unit's first one in 2 wg0 + 1 (the
-        // unit starts inside it) or 2 wg0 (it starts with the run)
-        auto part_of = [&](int k) -> const float* {
-          const int wg = wg0 + k;
-          return p.part + (size_t)(2 * wg + (u0 >= wg * per ? 1 : 0)) * SLOT;
-        };
+      // ---- the last workgroup of the unit joins the parts: in groups of kJoin, each joined by its own
+      // last one, where there are many
+      // joined part of workgroups wg0 + first + step * i, i < n, for this thread's elements
+      auto join = [&](int first, int step, int n, bool final, int slot) {
         for (int k = tid; k < rows * (D / 4); k += kThreads) {
           const int r = k / (D / 4), d = k % (D / 4) * 4;
           float top = kNegInf, sum = 0.0f;
-          for (int w = 0; w < wgs; ++w) top = __builtin_fmaxf(top, part_of(w)[R * D + r]);
           v4f y = {0, 0, 0, 0};
-          for (int w = 0; w < wgs; ++w) {
-            const float* s = part_of(w);
-            const float mw = s[R * D + r];
-            const float f = mw == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mw - top);
-            sum += f * s[R * D + R + r];
-            y += f * *(const v4f*)&s[r * D + d];
+          for (int i0 = 0; i0 < n; i0 += kJoin) {
+            v4f ms[kJoin], ys[kJoin];
+#pragma unroll
+            for (int i = 0; i < kJoin; ++i) {  // all loads in flight at once; a repeated last part counts nothing
+              const uint32_t at = slot_of(first + step * min(i0 + i, n - 1)) * SLOT;
+              ms[i] = handoff_load4(parts, at + R * D + 4 * r);
+              ys[i] = handoff_load4(parts, at + r * D + d);
+            }
+            float grown = top;
+#pragma unroll
+            for (int i = 0; i < kJoin; ++i) grown = __builtin_fmaxf(grown, ms[i][0]);
+            const float f0 = top == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(top - grown);
+            y *= f0;
+            sum *= f0;
+#pragma unroll
+            for (int i = 0; i < kJoin; ++i)
+              if (i0 + i < n) {
+                const float f = ms[i][0] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(ms[i][0] - grown);
+                sum += f * ms[i][1];
+                y += f * ys[i];
+              }
+            top = grown;
           }
-          store_out(r, d, y, top, sum);
+          if (final) store_out(r, d, y, top, sum);
+          else store_part(slot, r, d, y, top, sum);
+        }
+      };
+      int* unit_counter = p.arrived + ((int64_t)first_token * G + (int64_t)rb * R) * H + h;
+      if (wgs <= kJoin) {
+        if (last_arrival(unit_counter, wgs, &sh_last)) join(0, 1, wgs, true, 0);
+      } else {
+        const int k0 = (blockIdx.x - wg0) / kJoin * kJoin, n = min(kJoin, wgs - k0);
+        if (last_arrival(p.group_arrived + slot_of(k0), n, &sh_last)) {
+          join(k0, 1, n, false, slot_of(k0));
+          if (last_arrival(unit_counter, (wgs + kJoin - 1) / kJoin, &sh_last)) join(0, kJoin, (wgs + kJoin - 1) / kJoin, true, 0);
         }
       }
     }
@@ -568,9 +582,11 @@ hipError_t kv_attend_launch(const KvArgs& a, int dtype, int head_dim, int cus, h
   return dtype ? launch<Out::F16, 128>(a, cus, stream) : launch<Out::BF16, 128>(a, cus, stream);
 }
 
-void kv_workspace(const bsg_kv_problem& p, int cus, size_t* part_floats, size_t* counters) {
-  *part_floats = (size_t)cus * kWgPerCu * 2 * 32 * (p.head_dim + 2);
-  *counters = (size_t)p.max_tokens * p.q_heads;
+void kv_workspace(const bsg_kv_problem& p, int cus, size_t* part_floats, size_t* counters, size_t* group_counters) {
+  const size_t slots = (size_t)cus * kWgPerCu * 2;
+  *part_floats = slots * 32 * (p.head_dim + 4);
+  *counters = slots + (size_t)p.max_tokens * p.q_heads;
+  *group_counters = slots;
 }
 
 }  // namespace bsg

@@ -15,6 +15,7 @@
 //
 // Three launches: the router must know every token's choice before weights can be read, and the second
 // product needs all of an expert's SiLU(gate) up.
+#include "handoff.h"
 #include "moe.h"
 
 namespace bsg {
@@ -35,21 +36,6 @@ __device__ __forceinline__ v4f mfma(v4i a, v4i b, v4f c) {
 __device__ __forceinline__ uint16_t bf16_bits(float x) { return __builtin_bit_cast(uint16_t, (__bf16)x); }
 __device__ __forceinline__ float bf16_value(uint16_t b) { return __builtin_bit_cast(float, (uint32_t)b << 16); }
 
-// Whether every lane's stores before this call are seen by the workgroup that arrives last, and whether
-// this is that one (the counter is then zero again).  Called by all threads.
-__device__ __forceinline__ bool last_arrival(int* counter, int expected, int* shared) {
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    const int before = __hip_atomic_fetch_add(counter, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
-    *shared = before == expected - 1;
-    if (before == expected - 1) __hip_atomic_store(counter, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  }
-  __syncthreads();
-  if (*shared) __threadfence();
-  return *shared;
-}
-
 // ------------------------------------------------------------------------------------------- router
 constexpr int kRouterThreads = 512;
 constexpr int kKeys = 8192;  // logits held in LDS at a time while they are ranked
@@ -68,7 +54,7 @@ __device__ void choose(const MoeArgs& p, uint32_t* keys, int* chosen, int* sums)
   for (int t0 = 0; t0 < T; t0 += step) {
     const int n = min(step, T - t0) * E;
     __syncthreads();
-    for (int i = tid; i < n; i += kRouterThreads) keys[i] = order_key(p.logits[(size_t)t0 * E + i]);
+    for (int i = tid; i < n; i += kRouterThreads) keys[i] = order_key(handoff_load(p.logits + (size_t)t0 * E + i));
     __syncthreads();
     for (int i = tid; i < n; i += kRouterThreads) {
       const int t = i / E, e = i - t * E;
@@ -114,15 +100,15 @@ __device__ void choose(const MoeArgs& p, uint32_t* keys, int* chosen, int* sums)
   __syncthreads();
   for (int t = tid; t < T; t += kRouterThreads) {
     const float* l = p.logits + (size_t)t * E;
-    const float top = l[chosen[t * K]];
+    const float top = handoff_load(l + chosen[t * K]);
     float sum = 0.0f;
     if (p.keep)
-      for (int e = 0; e < E; ++e) sum += __builtin_amdgcn_exp2f((l[e] - top) * 1.44269504088896341f);
+      for (int e = 0; e < E; ++e) sum += __builtin_amdgcn_exp2f((handoff_load(l + e) - top) * 1.44269504088896341f);
     else
-      for (int j = 0; j < K; ++j) sum += __builtin_amdgcn_exp2f((l[chosen[t * K + j]] - top) * 1.44269504088896341f);
+      for (int j = 0; j < K; ++j) sum += __builtin_amdgcn_exp2f((handoff_load(l + chosen[t * K + j]) - top) * 1.44269504088896341f);
     for (int j = 0; j < K; ++j) {
       const int i = t * K + j;
-      const float w = __builtin_amdgcn_exp2f((l[chosen[i]] - top) * 1.44269504088896341f) / sum;
+      const float w = __builtin_amdgcn_exp2f((handoff_load(l + chosen[i]) - top) * 1.44269504088896341f) / sum;
       p.row_weight[p.row_of[i]] = w;
       if (p.ids) p.ids[i] = chosen[i];
       if (p.weights) p.weights[i] = w;
@@ -182,7 +168,8 @@ __global__ __launch_bounds__(kRouterThreads) void router_kernel(MoeArgs p) {
     for (int w = 1; w < 8; ++w) s += *(v4f*)sh.part[w][lane];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (t0 + c < p.tokens && e0 + 4 * g + i < p.experts) p.logits[(size_t)(t0 + c) * p.experts + e0 + 4 * g + i] = s[i];
+      if (t0 + c < p.tokens && e0 + 4 * g + i < p.experts) 
+        handoff_store(p.logits + (size_t)(t0 + c) * p.experts + e0 + 4 * g + i, s[i]);
   }
   if (last_arrival(p.arrived, gridDim.x * gridDim.y, &last)) choose(p, sh.keys, chosen, sums);
 }
@@ -368,20 +355,22 @@ __global__ __launch_bounds__(kThreads) void down_kernel(MoeArgs p) {
     for (int n = 0; n < NT; ++n) sh[wave][m][n][lane] = acc[m][n];
   __syncthreads();
   const float alpha = p.alpha2 ? p.alpha2[e] : 1.0f;
+  // (a few tokens' rows: far below 2^31 bytes)
+  const __amdgpu_buffer_rsrc_t ybuf = handoff_buffer(p.y, (uint32_t)(p.tokens * p.top_k) * (uint32_t)p.hidden * 4u);
   for (int k = tid; k < TILES * nts * 64; k += kThreads) {
     const int l = k & 63, m = (k >> 6) % TILES, n = (k >> 6) / TILES, col = 16 * n + (l & 15), d = d0 + 16 * m + 4 * (l >> 4);
     v4f y = sh[0][m][n][l];
 #pragma unroll
     for (int w = 1; w < 4; ++w) y += sh[w][m][n][l];
     if (col >= count || d >= p.hidden) continue;
-    *(v4f*)(p.y + (start + col) * (int64_t)p.hidden + d) = y * (alpha * p.row_weight[start + col]);
+    handoff_store4(ybuf, (uint32_t)(start + col) * p.hidden + d, y * (alpha * p.row_weight[start + col]));
   }
   if (!last_arrival(p.arrived + 1 + blockIdx.x, active, &last)) return;
   for (int k = tid; k < p.tokens * 16; k += kThreads) {
     const int t = k >> 4, d = d0 + 4 * (k & 15);
     if (d >= p.hidden) continue;
     v4f y = {0, 0, 0, 0};
-    for (int j = 0; j < p.top_k; ++j) y += *(const v4f*)(p.y + (int64_t)p.row_of[t * p.top_k + j] * p.hidden + d);
+    for (int j = 0; j < p.top_k; ++j) y += handoff_load4(ybuf, (uint32_t)p.row_of[t * p.top_k + j] * p.hidden + d);
     uint32_t b[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) b[r] = F16 ? __builtin_bit_cast(uint16_t, (_Float16)y[r]) : bf16_bits(y[r]);
