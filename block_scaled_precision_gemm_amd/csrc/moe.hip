@@ -8,13 +8,17 @@
 // same order, 64 contiguous bytes per lane.  A workgroup's waves take alternate slabs of 128 k and are
 // summed through LDS.
 //
-// Operands are bf16: E2M1 * E4M3 has at most 6 significant bits and E4M3 * 2^e has 4, so decoded
-// weights are exact and keep fp32's range.  16-bit activations are exact as bf16 x, or as the sum of
-// two bf16 parts for fp16 x; SiLU(gate) up is held as two bf16 parts (16 significant bits, so its
-// rounding is far below the output's).  Each part is one more product per weight fragment.
+// Decoded weights are exact: E2M1 * E4M3 has at most 6 significant bits, E4M3 * 2^e has 4.  MXFP8
+// weights decode to bf16, whose exponents hold any E8M0 scale.  NVFP4 weights decode to fp16 for the
+// first product (one conversion and one packed multiply for two values) and x enters it in fp16, bf16
+// rows scaled by a power of two each; for the second product, whose activations have no known range
+// before all of them are there, they decode to bf16.  SiLU(gate) up is held as two bf16 parts (16
+// significant bits, so its rounding is far below the output's), as is fp16 x beside MXFP8 weights; each
+// part is one more product per weight fragment.
 //
 // Three launches: the router must know every token's choice before weights can be read, and the second
 // product needs all of an expert's SiLU(gate) up.
+#include "codec.h"
 #include "handoff.h"
 #include "moe.h"
 
@@ -22,23 +26,27 @@ namespace bsg {
 namespace {
 
 typedef __bf16 v8b __attribute__((ext_vector_type(8)));
-typedef _Float16 v8h __attribute__((ext_vector_type(8)));
-typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 typedef float v2f __attribute__((ext_vector_type(2)));
 typedef __bf16 v2b __attribute__((ext_vector_type(2)));
 
 constexpr int kSlab = 128;
 
+template <bool F16>
 __device__ __forceinline__ v4f mfma(v4i a, v4i b, v4f c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8b, a), __builtin_bit_cast(v8b, b), c, 0, 0, 0);
+  if constexpr (F16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8b, a), __builtin_bit_cast(v8b, b), c, 0, 0, 0);
 }
 
 __device__ __forceinline__ uint16_t bf16_bits(float x) { return __builtin_bit_cast(uint16_t, (__bf16)x); }
 __device__ __forceinline__ float bf16_value(uint16_t b) { return __builtin_bit_cast(float, (uint32_t)b << 16); }
 
 // ------------------------------------------------------------------------------------------- router
-constexpr int kRouterThreads = 512;
+constexpr int kRouterThreads = 1024, kRouterWaves = kRouterThreads / 64;
 constexpr int kKeys = 8192;  // logits held in LDS at a time while they are ranked
+constexpr int kMaxChoices = BSG_MOE_MAX_TOKENS * BSG_MOE_MAX_TOP_K;
+constexpr float kLog2e = 1.44269504088896341f;
 
 // Order of floats as unsigned: larger float, larger key; NaN above all; -0 as 0.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -46,279 +54,449 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   const uint32_t u = __builtin_bit_cast(uint32_t, x + 0.0f);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __builtin_bit_cast(float, k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
+}
 
-// Top k of every token and the tokens of every expert; one workgroup.
-__device__ void choose(const MoeArgs& p, uint32_t* keys, int* chosen, int* sums) {
-  const int tid = threadIdx.x, E = p.experts, K = p.top_k, T = p.tokens;
-  const int step = kKeys / E;  // tokens at a time
+struct Choice {  // in LDS
+  uint4 keys[kKeys / 4];  // rows of E keys, padded to a multiple of 4 with 0 (below every logit's)
+  unsigned long long tokens_of[BSG_MOE_MAX_EXPERTS];  // bit t: token t chose the expert
+  int first_row[BSG_MOE_MAX_EXPERTS];
+  int chosen[kMaxChoices];  // expert and logit of each choice: tokens in order, ranks in order
+  float logit[kMaxChoices];
+  int sums[2 * kRouterWaves];
+};
+static_assert(BSG_MOE_MAX_TOKENS <= 64, "a bit for each token");
+
+// Top k of every token and the tokens of every expert; one workgroup.  A logit's rank is the number of
+// larger ones (or equal ones of lower experts), counted by one thread per logit: ranks are a
+// permutation, so each place is filled exactly once, and no step waits for another.  A choice's row
+// follows from the bits of the tokens that chose its expert.
+__device__ void choose(const MoeArgs& p, Choice& sh) {
+  const int tid = threadIdx.x, E = p.experts, K = p.top_k, T = p.tokens, choices = T * K;
+  const int quads = (E + 3) / 4, step = kKeys / 4 / quads;  // tokens at a time
+  for (int e = tid; e < E; e += kRouterThreads) sh.tokens_of[e] = 0;
   for (int t0 = 0; t0 < T; t0 += step) {
-    const int n = min(step, T - t0) * E;
-    __syncthreads();
-    for (int i = tid; i < n; i += kRouterThreads) keys[i] = order_key(handoff_load(p.logits + (size_t)t0 * E + i));
+    const int tokens = min(step, T - t0), n = tokens * quads * 4;
     __syncthreads();
     for (int i = tid; i < n; i += kRouterThreads) {
-      const int t = i / E, e = i - t * E;
-      const uint32_t mine = keys[i];
+      const int t = i / (quads * 4), e = i - t * quads * 4;
+      ((uint32_t*)sh.keys)[i] = e < E ? order_key(handoff_load(p.logits + (size_t)(t0 + t) * E + e)) : 0u;
+    }
+    __syncthreads();
+    for (int i = tid; i < n; i += kRouterThreads) {
+      const int t = i / (quads * 4), e = i - t * quads * 4;
+      const uint32_t mine = ((const uint32_t*)sh.keys)[i];
+      const uint4* row = sh.keys + t * quads;
       int rank = 0;
-      for (int j = 0; j < E; ++j) {
-        const uint32_t other = keys[t * E + j];
-        rank += other > mine || (other == mine && j < e);
+#pragma unroll 8
+      for (int j = 0; j < quads; ++j) {
+        const uint4 k = row[j];  // equal keys of lower experts count: key > mine - 1
+        rank += (k.x > mine - (4 * j < e)) + (k.y > mine - (4 * j + 1 < e)) + (k.z > mine - (4 * j + 2 < e)) +
+                (k.w > mine - (4 * j + 3 < e));
       }
-      if (rank < K) chosen[(t0 + t) * K + rank] = e;  // ranks are a permutation: each place is filled once
+      if (e < E && rank < K) {
+        sh.chosen[(t0 + t) * K + rank] = e;
+        sh.logit[(t0 + t) * K + rank] = key_value(mine);
+        atomicOr(&sh.tokens_of[e], 1ull << (t0 + t));
+      }
+    }
+    if (p.keep) {  // the sum over all experts, kept with the token's first key
+      __syncthreads();
+      for (int t = tid; t < tokens; t += kRouterThreads) {
+        const uint32_t* row = (const uint32_t*)(sh.keys + t * quads);
+        const float top = sh.logit[(t0 + t) * K];
+        float sum = 0.0f;
+        for (int e = 0; e < E; ++e) sum += __builtin_amdgcn_exp2f((key_value(row[e]) - top) * kLog2e);
+        p.row_weight[t0 + t] = sum;
+      }
     }
   }
   __syncthreads();
-  // rows of each expert: thread e counts its tokens, places by a scan
-  int count = 0;
-  if (tid < E)
-    for (int i = 0; i < T * K; ++i) count += chosen[i] == tid;
-  int rows = count, slots = count > 0;
+  // rows of each expert, and its slots of up to slot_rows rows: a scan over the experts
+  const int count = tid < E ? __popcll(sh.tokens_of[tid]) : 0, mine = (count + p.slot_rows - 1) / p.slot_rows;
+  int rows = count, slots = mine;
   const int lane = tid & 63, wave = tid >> 6;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
     const int a = __shfl_up(rows, o), b = __shfl_up(slots, o);
     if (lane >= o) rows += a, slots += b;
   }
-  if (lane == 63) sums[wave] = rows, sums[8 + wave] = slots;
+  if (lane == 63) sh.sums[wave] = rows, sh.sums[kRouterWaves + wave] = slots;
   __syncthreads();
-  for (int w = 0; w < wave; ++w) rows += sums[w], slots += sums[8 + w];
-  if (tid < E && count) {
-    int row = rows - count;
-    p.slot_expert[slots - 1] = tid;
-    p.slot_start[slots - 1] = row;
-    for (int i = 0; i < T * K; ++i)
-      if (chosen[i] == tid) {
-        p.row_token[row] = i / K;
-        p.row_of[i] = row++;
-      }
+#pragma unroll
+  for (int w = 0; w < kRouterWaves; ++w)
+    if (w < wave) rows += sh.sums[w], slots += sh.sums[kRouterWaves + w];
+  if (tid < E) {
+    sh.first_row[tid] = rows - count;
+    for (int k = 0; k < mine; ++k)
+      p.slots[slots - mine + k] = int4{tid, rows - count + k * p.slot_rows, min(count - k * p.slot_rows, p.slot_rows), 0};
   }
-  if (tid == kRouterThreads - 1) {
-    *p.active = slots;
-    p.slot_start[slots] = rows;
-  }
-  __threadfence_block();
+  if (tid == kRouterThreads - 1) *p.active = slots;
   __syncthreads();
-  for (int t = tid; t < T; t += kRouterThreads) {
-    const float* l = p.logits + (size_t)t * E;
-    const float top = handoff_load(l + chosen[t * K]);
+  const int c = tid;  // one thread per choice
+  static_assert(kMaxChoices <= kRouterThreads, "one thread per choice");
+  float w = 0.0f;
+  int row = 0;
+  if (c < choices) {
+    const int t = c / K, e = sh.chosen[c];
+    const float* l = sh.logit + t * K;
+    const float top = l[0];
     float sum = 0.0f;
-    if (p.keep)
-      for (int e = 0; e < E; ++e) sum += __builtin_amdgcn_exp2f((handoff_load(l + e) - top) * 1.44269504088896341f);
-    else
-      for (int j = 0; j < K; ++j) sum += __builtin_amdgcn_exp2f((handoff_load(l + chosen[t * K + j]) - top) * 1.44269504088896341f);
-    for (int j = 0; j < K; ++j) {
-      const int i = t * K + j;
-      const float w = __builtin_amdgcn_exp2f((handoff_load(l + chosen[i]) - top) * 1.44269504088896341f) / sum;
-      p.row_weight[p.row_of[i]] = w;
-      if (p.ids) p.ids[i] = chosen[i];
-      if (p.weights) p.weights[i] = w;
+    if (p.keep) {
+      sum = p.row_weight[t];
+    } else {
+#pragma unroll 4
+      for (int k = 0; k < K; ++k) sum += __builtin_amdgcn_exp2f((l[k] - top) * kLog2e);
     }
+    w = __builtin_amdgcn_exp2f((sh.logit[c] - top) * kLog2e) / sum;
+    row = sh.first_row[e] + __popcll(sh.tokens_of[e] & ((1ull << t) - 1));
+    p.row_token[row] = t;
+    p.row_of[c] = row;
+    if (p.ids) p.ids[c] = e;
+    if (p.weights) p.weights[c] = w;
+  }
+  __syncthreads();  // the sums of p.row_weight were read
+  if (c < choices) p.row_weight[row] = w;
+}
+
+// The form in which the first product takes x: as it is, bf16 rows as fp16 scaled by a power of two each
+// (NVFP4 weights decode to fp16 in half the operations of bf16), or fp16 rows as two bf16 parts (MXFP8
+// weights need bf16's range).
+enum class Prep { kNone, kScaled, kParts };
+template <bool NV, bool F16>
+constexpr Prep kPrep = NV ? (F16 ? Prep::kNone : Prep::kScaled) : (F16 ? Prep::kParts : Prep::kNone);
+
+template <Prep PREP>
+__device__ __forceinline__ void prepare_row(const MoeArgs& p, int t, int lane) {
+  const uint16_t* x = p.x + t * p.x_stride;
+  uint16_t* dst = p.xs + (int64_t)t * p.hidden;
+  int up = 0;
+  if constexpr (PREP == Prep::kScaled) {
+    uint32_t most = 0;  // largest magnitude, as bits
+    for (int i = 8 * lane; i < p.hidden; i += 512) {
+      const v4i w = *(const v4i*)(x + i);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) most = max(most, max((uint32_t)w[k] & 0x7FFFu, ((uint32_t)w[k] >> 16) & 0x7FFFu));
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) most = max(most, (uint32_t)__shfl_xor((int)most, o));
+    // largest magnitude to [2^7, 2^8): exact in fp16 down to 2^-32 of it, and products with decoded
+    // weights (below 2^4) stay far inside fp32; rows with an infinity or a NaN are left as they are
+    const int e = (int)(most >> 7) - 127;
+    up = e > 127 ? 0 : max(7 - e, -110);
+    if (lane == 0) p.x_exp[t] = up;
+  }
+  for (int i = 8 * lane; i < p.hidden; i += 512) {
+    const v4i w = *(const v4i*)(x + i);
+    v4i hi, lo;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (PREP == Prep::kScaled) {
+        const float f0 = __builtin_bit_cast(float, (uint32_t)w[k] << 16), f1 = __builtin_bit_cast(float, (uint32_t)w[k] & 0xFFFF0000u);
+        const v2f f = {__builtin_amdgcn_ldexpf(f0, up), __builtin_amdgcn_ldexpf(f1, up)};
+        hi[k] = __builtin_bit_cast(int, __builtin_convertvector(f, v2h));
+      } else {
+        const uint32_t u = (uint32_t)w[k];
+        const v2h v = __builtin_bit_cast(v2h, u);
+        const float f0 = (float)v[0], f1 = (float)v[1];
+        const uint16_t h0 = bf16_bits(f0), h1 = bf16_bits(f1);
+        const bool fin0 = __builtin_fabsf(f0) < 65536.0f, fin1 = __builtin_fabsf(f1) < 65536.0f;  // else no low part
+        hi[k] = h0 | h1 << 16;
+        lo[k] = (fin0 ? bf16_bits(f0 - bf16_value(h0)) : 0) | (fin1 ? bf16_bits(f1 - bf16_value(h1)) : 0) << 16;
+      }
+    }
+    *(v4i*)(dst + i) = hi;
+    if constexpr (PREP == Prep::kParts) *(v4i*)(dst + (int64_t)p.tokens * p.hidden + i) = lo;
   }
 }
 
-// Workgroup (x, y): logits of experts 16x .. 16x+15 for tokens 16y .. 16y+15, its 8 waves taking
-// alternate steps of 32 k; the last workgroup to finish chooses.
-template <bool F16>
+// Workgroup (x, y): logits of experts 16x .. 16x+15 for tokens 16y .. 16y+15, its waves taking
+// alternate steps of 32 k, kBatch of them in flight; the last workgroup to finish chooses.
+template <bool NV, bool F16>
 __global__ __launch_bounds__(kRouterThreads) void router_kernel(MoeArgs p) {
   __shared__ union {
-    float part[8][64][4];
-    uint32_t keys[kKeys];
+    float part[kRouterWaves][64][4];
+    Choice choice;
   } sh;
-  __shared__ int chosen[BSG_MOE_MAX_TOKENS * BSG_MOE_MAX_TOP_K];
-  __shared__ int sums[16], last;
+  __shared__ int last;
+  constexpr int kBatch = 8;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, c = lane & 15, g = lane >> 4;
   const int e0 = blockIdx.x * 16, t0 = blockIdx.y * 16;
   const uint16_t* a = p.router + (size_t)min(e0 + c, p.experts - 1) * p.hidden + 8 * g;
   const uint16_t* b = p.x + (int64_t)min(t0 + c, p.tokens - 1) * p.x_stride + 8 * g;
   v4f acc = {0, 0, 0, 0};
   const int steps = p.hidden / 32;
-  for (int s = wave; s < steps; s += 8) {
-    const v4i aw = *(const v4i*)(a + 32 * s), bw = *(const v4i*)(b + 32 * s);
-    if constexpr (F16)
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, aw), __builtin_bit_cast(v8h, bw), acc, 0, 0, 0);
-    else
-      acc = mfma(aw, bw, acc);
-  }
-  *(v4f*)sh.part[wave][lane] = acc;
-  if constexpr (F16) {
-    // x as two bf16 parts: each workgroup of the row of tokens writes its share of the columns
-    const int share = (p.hidden / 8 + gridDim.x - 1) / gridDim.x;
-    const int first = blockIdx.x * share, n = min(share, p.hidden / 8 - first);
-    const int rows = min(16, p.tokens - t0);
-    for (int i = tid; i < rows * n; i += kRouterThreads) {
-      const int r = t0 + i / n, col = 8 * (first + i % n);
-      const v8h v = *(const v8h*)(p.x + (int64_t)r * p.x_stride + col);
-      v4i hi, lo;
+  for (int s0 = wave; s0 < steps; s0 += kRouterWaves * kBatch) {
+    v4i aw[kBatch], bw[kBatch];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float f0 = (float)v[2 * k], f1 = (float)v[2 * k + 1];
-        const uint16_t h0 = bf16_bits(f0), h1 = bf16_bits(f1);
-        const bool fin0 = __builtin_fabsf(f0) < 65536.0f, fin1 = __builtin_fabsf(f1) < 65536.0f;  // else no low part
-        hi[k] = h0 | h1 << 16;
-        lo[k] = (fin0 ? bf16_bits(f0 - bf16_value(h0)) : 0) | (fin1 ? bf16_bits(f1 - bf16_value(h1)) : 0) << 16;
-      }
-      *(v4i*)(p.xs + (size_t)r * p.hidden + col) = hi;
-      *(v4i*)(p.xs + (size_t)(p.tokens + r) * p.hidden + col) = lo;
+    for (int k = 0; k < kBatch; ++k) {
+      const int s = min(s0 + k * kRouterWaves, steps - 1);
+      aw[k] = *(const v4i*)(a + 32 * s);
+      bw[k] = *(const v4i*)(b + 32 * s);
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const bool in = s0 + k * kRouterWaves < steps;  // repeated steps count as zero
+      aw[k] = in ? aw[k] : v4i{0, 0, 0, 0};
+      bw[k] = in ? bw[k] : v4i{0, 0, 0, 0};
+      acc = mfma<F16>(aw[k], bw[k], acc);
     }
   }
+  *(v4f*)sh.part[wave][lane] = acc;
+  // the activations' form for the first product, a wave per token (the tiles of experts share the tokens)
+  if (kPrep<NV, F16> != Prep::kNone && wave < 16 && wave % gridDim.x == blockIdx.x && t0 + wave < p.tokens)
+    prepare_row<kPrep<NV, F16>>(p, t0 + wave, lane);
   __syncthreads();
   if (wave == 0) {
     v4f s = *(v4f*)sh.part[0][lane];
 #pragma unroll
-    for (int w = 1; w < 8; ++w) s += *(v4f*)sh.part[w][lane];
+    for (int w = 1; w < kRouterWaves; ++w) s += *(v4f*)sh.part[w][lane];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (t0 + c < p.tokens && e0 + 4 * g + i < p.experts) 
+      if (t0 + c < p.tokens && e0 + 4 * g + i < p.experts)
         handoff_store(p.logits + (size_t)(t0 + c) * p.experts + e0 + 4 * g + i, s[i]);
   }
-  if (last_arrival(p.arrived, gridDim.x * gridDim.y, &last)) choose(p, sh.keys, chosen, sums);
+  if (last_arrival(p.arrived, gridDim.x * gridDim.y, &last)) choose(p, sh.choice);
 }
 
 // ------------------------------------------------------------------------------------------- weights
-// One row's 32 codes from k0 on, and their scales, decoded to four bf16 fragments.
-template <bool NV>
-struct Row;
+constexpr int kThreads = 256;
 
-template <>
-struct Row<true> {  // NVFP4: two scales
-  v4i q;
-  uint32_t s;
-  __device__ __forceinline__ void load(const uint8_t* w, const uint8_t* sc, int64_t row, int K, int k0) {
-    q = *(const v4i*)(w + row * (K / 2) + k0 / 2);
-    s = *(const uint16_t*)(sc + row * (K / 16) + k0 / 16);
-  }
-  __device__ __forceinline__ void clear() {
-    q = v4i{0, 0, 0, 0};
-    s = 0;
-  }
-  __device__ __forceinline__ v4i fragment(int j) const {
-    const float f = j < 2 ? __builtin_amdgcn_cvt_f32_fp8((int)s, 0) : __builtin_amdgcn_cvt_f32_fp8((int)s, 1);
-    const uint32_t w = (uint32_t)q[j];
-    const v2f a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
-    const v2f c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
-    // products of at most 6 significant bits: their upper halves are the bf16 values
-    auto pair = [&](float x, float y) {
-      return (int)__builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, y * f), __builtin_bit_cast(uint32_t, x * f), 0x07060302u);
-    };
-    const float a0 = a[0], a1 = a[1], b0 = b[0], b1 = b[1], c0 = c[0], c1 = c[1], d0 = d[0], d1 = d[1];
-    return v4i{pair(a0, a1), pair(b0, b1), pair(c0, c1), pair(d0, d1)};
-  }
+// How codes become fragments of a product.
+enum class Dec { kNvF16, kNvBf16, kMxBf16 };
+
+template <Dec DEC>
+struct Codes {
+  static constexpr bool NV = DEC != Dec::kMxBf16, F16 = DEC == Dec::kNvF16;
+  static constexpr int kBlock = NV ? 16 : 32;                   // elements per scale
+  static constexpr int kSlabBytes = NV ? kSlab / 2 : kSlab;     // code bytes of a slab of a row
+  static constexpr int kSlabScales = kSlab / kBlock;
+  static constexpr int kRegs = NV ? 4 : 8;
+  static constexpr int kDepth = 2;                              // slabs of weights in flight
 };
 
-template <>
-struct Row<false> {  // MXFP8: one scale
-  v4i q0, q1;
-  uint32_t s;
-  __device__ __forceinline__ void load(const uint8_t* w, const uint8_t* sc, int64_t row, int K, int k0) {
-    q0 = *(const v4i*)(w + row * K + k0);
-    q1 = *(const v4i*)(w + row * K + k0 + 16);
-    s = sc[row * (K / 32) + k0 / 32];
-  }
-  __device__ __forceinline__ void clear() {
-    q0 = q1 = v4i{0, 0, 0, 0};
-    s = 0;
-  }
-  __device__ __forceinline__ v4i fragment(int j) const {
-    const float f = __builtin_bit_cast(float, s << 23);
-    const v4i q = j < 2 ? q0 : q1;
-    const int lo = q[2 * (j & 1)], hi = q[2 * (j & 1) + 1];
-    return v4i{__builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, f, false)),
-               __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, f, true)),
-               __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, f, false)),
-               __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, f, true))};
-  }
-};
-
-// acc[tile][nt] += rows x columns over the slabs wave, wave + 4, ...: rows of tile m are w's rows
-// row[m] + lane % 16, columns the activations at b + column[nt] (element offsets), PARTS parts `part`
-// elements apart.
-template <bool NV, int TILES, int NT, int PARTS>
-__device__ __forceinline__ void products(const uint8_t* w, const uint8_t* sc, const int64_t row[TILES], int K, int wave,
-                                         int g, const uint16_t* b, const int64_t column[NT], int64_t part, int nts,
-                                         v4f acc[TILES][NT]) {
-  const int slabs = (K + kSlab - 1) / kSlab;
-  Row<NV> cur[TILES], next[TILES];
-  auto fetch = [&](Row<NV>* r, int s) {
-    const int k0 = s * kSlab + 32 * g;
-    if (k0 < K) {
+// A lane's 32 codes of one row.
+template <Dec DEC>
+struct Row {
+  using C = Codes<DEC>;
+  uint32_t q[C::kRegs];
+  __device__ __forceinline__ void load(const uint8_t* w) {
+    const v4i a = *(const v4i*)w;
 #pragma unroll
-      for (int m = 0; m < TILES; ++m) r[m].load(w, sc, row[m], K, k0);
-    } else {
+    for (int i = 0; i < 4; ++i) q[i] = (uint32_t)a[i];
+    if constexpr (!C::NV) {
+      const v4i b = *(const v4i*)(w + 16);
 #pragma unroll
-      for (int m = 0; m < TILES; ++m) r[m].clear();
+      for (int i = 0; i < 4; ++i) q[4 + i] = (uint32_t)b[i];
     }
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < C::kRegs; ++i) q[i] = 0;
+  }
+  // Fragment j of four; `s`: the two scale codes of the 32 elements (NVFP4), or the one.
+  __device__ __forceinline__ v4i fragment(int j, uint32_t s) const {
+    if constexpr (DEC == Dec::kNvF16) {  // times 2^-8 (codec.h)
+      const uint32_t s2 = e4m3x2_scale_f16x2(s);
+      return e2m1x8_scaled_f16x8(q[j], j < 2 ? f16x2_splat_lo(s2) : f16x2_splat_hi(s2));
+    } else if constexpr (DEC == Dec::kNvBf16) {
+      const float f = j < 2 ? __builtin_amdgcn_cvt_f32_fp8((int)s, 0) : __builtin_amdgcn_cvt_f32_fp8((int)s, 1);
+      const v2f a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[j], 1.0f, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[j], 1.0f, 1);
+      const v2f c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[j], 1.0f, 2), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[j], 1.0f, 3);
+      // products of at most 6 significant bits: their upper halves are the bf16 values
+      auto pair = [&](float x, float y) {
+        return (int)__builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, y * f), __builtin_bit_cast(uint32_t, x * f), 0x07060302u);
+      };
+      const float a0 = a[0], a1 = a[1], b0 = b[0], b1 = b[1], c0 = c[0], c1 = c[1], d0 = d[0], d1 = d[1];
+      return v4i{pair(a0, a1), pair(b0, b1), pair(c0, c1), pair(d0, d1)};
+    } else {
+      const float f = __builtin_bit_cast(float, s << 23);
+      const int lo = (int)q[2 * j], hi = (int)q[2 * j + 1];
+      return v4i{__builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, f, false)),
+                 __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, f, true)),
+                 __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, f, false)),
+                 __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, f, true))};
+    }
+  }
+};
+
+// Scale codes of a workgroup's rows for kChunk k at a time, in LDS: read from memory a row's codes are
+// a few bytes per slab in 16 rows at once, and those reads cost more than the codes' (gate/up of 33
+// tokens, 64 experts of 4096 x 2048 in NVFP4: 191 us with them, 155 us with constant scales).  Rows are
+// padded so that the 16 rows of a tile lie in different banks.
+constexpr int kChunk = 4096;
+template <Dec DEC, int TILES>
+struct Scales {
+  static constexpr int kRowBytes = kChunk / Codes<DEC>::kBlock, kPitch = kRowBytes + (Codes<DEC>::NV ? 8 : 4);
+  uint8_t rows[TILES * 16][kPitch];
+};
+
+// Copy the codes of chunk k0 .. k0 + n - 1 of tiles whose first rows start at sc[m].
+template <Dec DEC, int TILES>
+__device__ __forceinline__ void stage_scales(Scales<DEC, TILES>& sh, const uint8_t* const sc[TILES], int K, int k0, int n, int tid) {
+  const int row_bytes = K / Codes<DEC>::kBlock, first = k0 / Codes<DEC>::kBlock, bytes = n / Codes<DEC>::kBlock;
+  auto copy = [&](auto unit) {
+    using U = decltype(unit);
+    const int per_row = bytes / (int)sizeof(U);
+#pragma unroll
+    for (int m = 0; m < TILES; ++m)
+#pragma unroll 2
+      for (int i = tid; i < 16 * per_row; i += kThreads) {
+        const int r = i / per_row, at = (i - r * per_row) * (int)sizeof(U);
+        const U v = *(const U*)(sc[m] + r * row_bytes + first + at);
+        __builtin_memcpy(&sh.rows[16 * m + r][at], &v, sizeof(U));
+      }
   };
-  if (wave < slabs) fetch(cur, wave);
-  for (int s = wave; s < slabs; s += 4) {
-    if (s + 4 < slabs) fetch(next, s + 4);
-    const int k0 = s * kSlab + 32 * g;
-    v4i x[PARTS][NT][4];
+  if (row_bytes % 8 == 0) copy(uint2{});  // (chunks start at multiples of 8 codes; scales are 4-byte aligned at least)
+  else if constexpr (Codes<DEC>::NV) copy(uint16_t{});
+  else copy(uint8_t{});
+}
+
+// acc[tile][nt] += rows x columns: tile m's 16 rows start at w[m] (codes) and sc[m] (scales), the lane's
+// column is at b[nt], PARTS parts `part` elements apart.  Slabs of 128 k go to the four waves in turn.
+template <Dec DEC, int TILES, int NT, int PARTS>
+__device__ __forceinline__ void products(Scales<DEC, TILES>& sh, const uint8_t* const w[TILES], const uint8_t* const sc[TILES],
+                                         int K, int tid, int wave, const uint16_t* const b[NT], int64_t part, int nts,
+                                         v4f acc[TILES][NT]) {
+  using C = Codes<DEC>;
+  constexpr int DEPTH = C::kDepth;
+  static_assert(DEPTH % 2 == 0, "the activations' buffers alternate");
+  const int lane = tid & 63, c = lane & 15, g = lane >> 4;
+  const int row_bytes = C::NV ? K / 2 : K;
+  const uint32_t at0 = c * row_bytes + g * (C::kSlabBytes / 4);
+  Row<DEC> buf[DEPTH][TILES];
+  v4i x[2][PARTS][NT][4];
+  auto fetch = [&](Row<DEC>* r, int s) {
+#pragma unroll
+    for (int m = 0; m < TILES; ++m) r[m].load(w[m] + (at0 + (uint32_t)s * C::kSlabBytes));
+  };
+  auto fetch_x = [&](v4i (*v)[NT][4], int s) {
 #pragma unroll
     for (int q = 0; q < PARTS; ++q)
 #pragma unroll
       for (int n = 0; n < NT; ++n)
         if (n < nts) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            x[q][n][j] = k0 < K ? *(const v4i*)(b + q * part + column[n] + k0 + 8 * j) : v4i{0, 0, 0, 0};
+          for (int j = 0; j < 4; ++j) v[q][n][j] = *(const v4i*)(b[n] + q * part + s * kSlab + 32 * g + 8 * j);
         }
+  };
+  auto multiply = [&](const Row<DEC>* r, const v4i (*v)[NT][4], int chunk_slab) {
 #pragma unroll
-    for (int m = 0; m < TILES; ++m)
+    for (int m = 0; m < TILES; ++m) {
+      const uint8_t* codes = &sh.rows[16 * m + c][chunk_slab * C::kSlabScales + g * (C::kSlabScales / 4)];
+      const uint32_t s = C::NV ? (uint32_t)*(const uint16_t*)codes : (uint32_t)*codes;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const v4i a = cur[m].fragment(j);
+        const v4i a = r[m].fragment(j, s);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
           if (n < nts) {
 #pragma unroll
-            for (int q = 0; q < PARTS; ++q) acc[m][n] = mfma(a, x[q][n][j], acc[m][n]);
+            for (int q = 0; q < PARTS; ++q) acc[m][n] = mfma<C::F16>(a, v[q][n][j], acc[m][n]);
           }
       }
+    }
+  };
+  for (int k0 = 0; k0 < K; k0 += kChunk) {
+    const int n = min(kChunk, K - k0), first = k0 / kSlab, full = first + n / kSlab;
+    const int s1 = first + wave;
 #pragma unroll
-    for (int m = 0; m < TILES; ++m) cur[m] = next[m];
+    for (int d = 0; d < DEPTH; ++d)
+      if (s1 + 4 * d < full) fetch(buf[d], s1 + 4 * d);
+    if (s1 < full) fetch_x(x[0], s1);
+    if (k0) __syncthreads();
+    stage_scales<DEC, TILES>(sh, sc, K, k0, n, tid);
+    __syncthreads();
+    for (int s0 = s1; s0 < full; s0 += 4 * DEPTH) {
+#pragma unroll
+      for (int d = 0; d < DEPTH; ++d) {
+        const int s = s0 + 4 * d;
+        if (s < full) {
+          if (s + 4 < full) fetch_x(x[(d + 1) & 1], s + 4);
+          multiply(buf[d], x[d & 1], s - first);
+          if (s + 4 * DEPTH < full) fetch(buf[d], s + 4 * DEPTH);
+        }
+      }
+    }
+    if (n % kSlab && wave == full % 4) {  // the rest: lanes past the end count as zero
+      const bool in = full * kSlab + 32 * g < K;
+#pragma unroll
+      for (int m = 0; m < TILES; ++m) buf[0][m].clear();
+#pragma unroll
+      for (int q = 0; q < PARTS; ++q)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[0][q][nt][j] = v4i{0, 0, 0, 0};
+      if (in) {
+        fetch_x(x[0], full);
+        fetch(buf[0], full);
+      } else {
+        // their scales are whatever LDS holds: zero them, so that no NaN comes of it
+#pragma unroll
+        for (int m = 0; m < TILES; ++m)
+#pragma unroll
+          for (int i = 0; i < C::kSlabScales / 4; ++i)
+            sh.rows[16 * m + c][(full - first) * C::kSlabScales + g * (C::kSlabScales / 4) + i] = 0;
+      }
+      multiply(buf[0], x[0], full - first);
+    }
   }
 }
 
-constexpr int kThreads = 256;
-
 // Workgroup (x, slot): SiLU(gate) up of dims 32x .. 32x+31 for the tokens of the slot's expert.
-template <bool NV, int NT, int PARTS>
+template <bool NV, bool F16, int NT>
 __global__ __launch_bounds__(kThreads) void gate_up_kernel(MoeArgs p) {
   constexpr int TILES = 4;  // gate rows 0..15, 16..31, up rows 0..15, 16..31
-  __shared__ v4f sh[4][TILES][NT][64];
+  constexpr Dec DEC = NV ? Dec::kNvF16 : Dec::kMxBf16;
+  constexpr Prep PREP = kPrep<NV, F16>;
+  constexpr int PARTS = PREP == Prep::kParts ? 2 : 1;
+  __shared__ union {
+    Scales<DEC, TILES> scales;
+    v4f acc[4][TILES][NT][64];
+  } sh;
+  const int4 slot = p.slots[blockIdx.y];
   if ((int)blockIdx.y >= *p.active) return;
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, c = lane & 15, g = lane >> 4;
-  const int e = p.slot_expert[blockIdx.y], start = p.slot_start[blockIdx.y], count = p.slot_start[blockIdx.y + 1] - start;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, c = lane & 15;
+  const int e = __builtin_amdgcn_readfirstlane(slot.x), start = __builtin_amdgcn_readfirstlane(slot.y);
+  const int count = __builtin_amdgcn_readfirstlane(slot.z);
   const int nts = (count + 15) / 16, i0 = blockIdx.x * 32;
-  int64_t row[TILES], column[NT];
+  const uint8_t *w[TILES], *sc[TILES];
 #pragma unroll
   for (int m = 0; m < TILES; ++m) {
-    const int i = min(i0 + (m & 1) * 16 + c, p.inter - 1);
-    row[m] = (int64_t)e * 2 * p.inter + (m < 2 ? 0 : p.inter) + i;
+    const int64_t row = (int64_t)e * 2 * p.inter + (m < 2 ? 0 : p.inter) + i0 + (m & 1) * 16;
+    w[m] = p.w13 + row * (NV ? p.hidden / 2 : p.hidden);
+    sc[m] = p.s13 + row * (NV ? p.hidden / 16 : p.hidden / 32);
   }
-  const uint16_t* b = PARTS == 1 ? p.x : p.xs;
-  const int64_t stride = PARTS == 1 ? p.x_stride : p.hidden;
+  const uint16_t* b[NT];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) column[n] = p.row_token[start + min(16 * n + c, count - 1)] * stride;
+  for (int n = 0; n < NT; ++n) {
+    const int t = p.row_token[start + min(16 * n + c, count - 1)];
+    b[n] = PREP == Prep::kNone ? p.x + t * p.x_stride : p.xs + (int64_t)t * p.hidden;
+  }
   v4f acc[TILES][NT] = {};
-  products<NV, TILES, NT, PARTS>(p.w13, p.s13, row, p.hidden, wave, g, b, column, (int64_t)p.tokens * p.hidden, nts, acc);
+  products<DEC, TILES, NT, PARTS>(sh.scales, w, sc, p.hidden, tid, wave, b, (int64_t)p.tokens * p.hidden, nts, acc);
+  __syncthreads();  // the scales are done with
 #pragma unroll
   for (int m = 0; m < TILES; ++m)
 #pragma unroll
-    for (int n = 0; n < NT; ++n) sh[wave][m][n][lane] = acc[m][n];
+    for (int n = 0; n < NT; ++n) sh.acc[wave][m][n][lane] = acc[m][n];
   __syncthreads();
   const float alpha = p.alpha13 ? p.alpha13[e] : 1.0f;
   const int64_t rows = (int64_t)p.tokens * p.top_k;
   for (int k = tid; k < 2 * nts * 64; k += kThreads) {
     const int l = k & 63, m = (k >> 6) & 1, n = k >> 7, col = 16 * n + (l & 15), i = i0 + 16 * m + 4 * (l >> 4);
-    v4f gate = sh[0][m][n][l], up = sh[0][m + 2][n][l];
+    v4f gate = sh.acc[0][m][n][l], up = sh.acc[0][m + 2][n][l];
 #pragma unroll
-    for (int w = 1; w < 4; ++w) gate += sh[w][m][n][l], up += sh[w][m + 2][n][l];
+    for (int w = 1; w < 4; ++w) gate += sh.acc[w][m][n][l], up += sh.acc[w][m + 2][n][l];
     if (col >= count || i >= p.inter) continue;
+    // powers of two that the operands carry: decoded weights 2^-8, scaled rows of x 2^x_exp
+    const int back = (NV ? 8 : 0) - (PREP == Prep::kScaled ? p.x_exp[p.row_token[start + col]] : 0);
     uint16_t hi[4], lo[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const float x = alpha * gate[r], u = alpha * up[r];
+      const float x = alpha * __builtin_amdgcn_ldexpf(gate[r], back), u = alpha * __builtin_amdgcn_ldexpf(up[r], back);
       const float v = x / (1.0f + __builtin_amdgcn_exp2f(x * -1.44269504088896341f)) * u;
       hi[r] = bf16_bits(v);
       const float rest = v - bf16_value(hi[r]);
@@ -335,33 +513,45 @@ __global__ __launch_bounds__(kThreads) void gate_up_kernel(MoeArgs p) {
 template <bool NV, bool F16, int NT>
 __global__ __launch_bounds__(kThreads) void down_kernel(MoeArgs p) {
   constexpr int TILES = 4;
-  __shared__ v4f sh[4][TILES][NT][64];
+  constexpr Dec DEC = NV ? Dec::kNvBf16 : Dec::kMxBf16;
+  __shared__ union {
+    Scales<DEC, TILES> scales;
+    v4f acc[4][TILES][NT][64];
+  } sh;
   __shared__ int last;
   const int active = *p.active;
+  const int4 slot = p.slots[blockIdx.y];
   if ((int)blockIdx.y >= active) return;
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, c = lane & 15, g = lane >> 4;
-  const int e = p.slot_expert[blockIdx.y], start = p.slot_start[blockIdx.y], count = p.slot_start[blockIdx.y + 1] - start;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, c = lane & 15;
+  const int e = __builtin_amdgcn_readfirstlane(slot.x), start = __builtin_amdgcn_readfirstlane(slot.y);
+  const int count = __builtin_amdgcn_readfirstlane(slot.z);
   const int nts = (count + 15) / 16, d0 = blockIdx.x * 64;
-  int64_t row[TILES], column[NT];
+  const uint8_t *w[TILES], *sc[TILES];
 #pragma unroll
-  for (int m = 0; m < TILES; ++m) row[m] = (int64_t)e * p.hidden + min(d0 + 16 * m + c, p.hidden - 1);
+  for (int m = 0; m < TILES; ++m) {
+    const int64_t row = (int64_t)e * p.hidden + min(d0 + 16 * m, p.hidden - 16);  // (tiles past the end repeat the last)
+    w[m] = p.w2 + row * (NV ? p.inter / 2 : p.inter);
+    sc[m] = p.s2 + row * (NV ? p.inter / 16 : p.inter / 32);
+  }
+  const uint16_t* b[NT];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) column[n] = (int64_t)(start + min(16 * n + c, count - 1)) * p.inter;
+  for (int n = 0; n < NT; ++n) b[n] = p.h + (int64_t)(start + min(16 * n + c, count - 1)) * p.inter;
   v4f acc[TILES][NT] = {};
-  products<NV, TILES, NT, 2>(p.w2, p.s2, row, p.inter, wave, g, p.h, column, (int64_t)p.tokens * p.top_k * p.inter, nts, acc);
+  products<DEC, TILES, NT, 2>(sh.scales, w, sc, p.inter, tid, wave, b, (int64_t)p.tokens * p.top_k * p.inter, nts, acc);
+  __syncthreads();  // the scales are done with
 #pragma unroll
   for (int m = 0; m < TILES; ++m)
 #pragma unroll
-    for (int n = 0; n < NT; ++n) sh[wave][m][n][lane] = acc[m][n];
+    for (int n = 0; n < NT; ++n) sh.acc[wave][m][n][lane] = acc[m][n];
   __syncthreads();
   const float alpha = p.alpha2 ? p.alpha2[e] : 1.0f;
   // (a few tokens' rows: far below 2^31 bytes)
   const __amdgpu_buffer_rsrc_t ybuf = handoff_buffer(p.y, (uint32_t)(p.tokens * p.top_k) * (uint32_t)p.hidden * 4u);
   for (int k = tid; k < TILES * nts * 64; k += kThreads) {
     const int l = k & 63, m = (k >> 6) % TILES, n = (k >> 6) / TILES, col = 16 * n + (l & 15), d = d0 + 16 * m + 4 * (l >> 4);
-    v4f y = sh[0][m][n][l];
+    v4f y = sh.acc[0][m][n][l];
 #pragma unroll
-    for (int w = 1; w < 4; ++w) y += sh[w][m][n][l];
+    for (int w = 1; w < 4; ++w) y += sh.acc[w][m][n][l];
     if (col >= count || d >= p.hidden) continue;
     handoff_store4(ybuf, (uint32_t)(start + col) * p.hidden + d, y * (alpha * p.row_weight[start + col]));
   }
@@ -370,7 +560,15 @@ __global__ __launch_bounds__(kThreads) void down_kernel(MoeArgs p) {
     const int t = k >> 4, d = d0 + 4 * (k & 15);
     if (d >= p.hidden) continue;
     v4f y = {0, 0, 0, 0};
-    for (int j = 0; j < p.top_k; ++j) y += handoff_load4(ybuf, (uint32_t)p.row_of[t * p.top_k + j] * p.hidden + d);
+    for (int j0 = 0; j0 < p.top_k; j0 += 8) {
+      v4f v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)  // all in flight
+        v[j] = handoff_load4(ybuf, (uint32_t)p.row_of[t * p.top_k + min(j0 + j, p.top_k - 1)] * p.hidden + d);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j0 + j < p.top_k) y += v[j];
+    }
     uint32_t b[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) b[r] = F16 ? __builtin_bit_cast(uint16_t, (_Float16)y[r]) : bf16_bits(y[r]);
@@ -382,11 +580,13 @@ template <bool NV, bool F16, int NT>
 hipError_t launch(const MoeArgs& a, hipStream_t stream) {
   MoeArgs args = a;
   void* argv[] = {&args};
-  hipError_t e = hipLaunchKernel((const void*)&router_kernel<F16>, dim3((a.experts + 15) / 16, (a.tokens + 15) / 16),
+  hipError_t e = hipLaunchKernel((const void*)&router_kernel<NV, F16>, dim3((a.experts + 15) / 16, (a.tokens + 15) / 16),
                                  dim3(kRouterThreads), argv, 0, stream);
   if (e != hipSuccess) return e;
-  const unsigned slots = a.tokens * a.top_k < a.experts ? a.tokens * a.top_k : a.experts;
-  e = hipLaunchKernel((const void*)&gate_up_kernel<NV, NT, F16 ? 2 : 1>, dim3((a.inter + 31) / 32, slots), dim3(kThreads),
+  // at most one slot per choice, and one per expert and slot_rows choices
+  const int choices = a.tokens * a.top_k, bound = a.experts + choices / a.slot_rows;
+  const unsigned slots = choices < bound ? choices : bound;
+  e = hipLaunchKernel((const void*)&gate_up_kernel<NV, F16, NT>, dim3((a.inter + 31) / 32, slots), dim3(kThreads),
                       argv, 0, stream);
   if (e != hipSuccess) return e;
   return hipLaunchKernel((const void*)&down_kernel<NV, F16, NT>, dim3((a.hidden + 63) / 64, slots), dim3(kThreads), argv, 0,
@@ -395,10 +595,7 @@ hipError_t launch(const MoeArgs& a, hipStream_t stream) {
 
 template <bool NV, bool F16>
 hipError_t launch_nt(const MoeArgs& a, hipStream_t stream) {
-  // an expert may get every token
-  if (a.tokens <= 16) return launch<NV, F16, 1>(a, stream);
-  if (a.tokens <= 32) return launch<NV, F16, 2>(a, stream);
-  return launch<NV, F16, 4>(a, stream);
+  return a.slot_rows == 16 ? launch<NV, F16, 1>(a, stream) : launch<NV, F16, 2>(a, stream);
 }
 
 }  // namespace
@@ -417,12 +614,12 @@ size_t moe_workspace(const bsg_moe_problem& p, uint8_t* base, MoeArgs* a, size_t
     return base ? base + here : nullptr;
   };
   a->logits = (float*)take(T * p.experts * 4);
-  a->xs = (uint16_t*)take(p.dtype == BSG_OUT_F16 ? 2 * T * p.hidden * 2 : 0);
+  a->xs = (uint16_t*)take(2 * T * p.hidden * 2);
+  a->x_exp = (int*)take(T * 4);
   a->h = (uint16_t*)take(2 * rows * p.inter * 2);
   a->y = (float*)take(rows * p.hidden * 4);
   a->active = (int*)take(4);
-  a->slot_expert = (int*)take((size_t)p.experts * 4);
-  a->slot_start = (int*)take(((size_t)p.experts + 1) * 4);
+  a->slots = (int4*)take((p.experts + rows / 16 + 1) * sizeof(int4));
   a->row_token = (int*)take(rows * 4);
   a->row_weight = (float*)take(rows * 4);
   a->row_of = (int*)take(rows * 4);

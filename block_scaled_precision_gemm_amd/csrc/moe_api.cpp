@@ -165,6 +165,7 @@ bsg_status bsg_moe_run(bsg_moe_plan plan, int64_t tokens, const void* x, int64_t
   }
   bsg::MoeArgs a = plan->args;
   a.tokens = (int)tokens;
+  a.slot_rows = tokens <= 16 ? 16 : 32;  // up to 16 tokens fill one column tile of a product
   a.x = (const uint16_t*)x;
   a.router = (const uint16_t*)w->router;
   a.w13 = (const uint8_t*)w->w13;
