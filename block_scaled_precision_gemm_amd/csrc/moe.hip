@@ -44,11 +44,10 @@ __device__ __forceinline__ float bf16_value(uint16_t b) { return __builtin_bit_c
 
 // ------------------------------------------------------------------------------------------- router
 constexpr int kRouterThreads = 1024, kRouterWaves = kRouterThreads / 64;
-constexpr int kKeys = 8192;  // logits held in LDS at a time while they are ranked
 constexpr int kMaxChoices = BSG_MOE_MAX_TOKENS * BSG_MOE_MAX_TOP_K;
 constexpr float kLog2e = 1.44269504088896341f;
 
-// Order of floats as unsigned: larger float, larger key; NaN above all; -0 as 0.
+// Order of floats as unsigned: larger float, larger key; NaN above all; -0 as 0.  No logit's key is 0.
 __device__ __forceinline__ uint32_t order_key(float x) {
   if (x != x) return 0xFFFFFFFFu;
   const uint32_t u = __builtin_bit_cast(uint32_t, x + 0.0f);
@@ -58,65 +57,101 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __builtin_bit_cast(float, k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
 }
 
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ uint32_t dpp(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROW_MASK, 0xF, false);
+}
+// Largest of the wave's keys, in every lane (lanes without a source see 0).
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+  x = max(x, dpp<0x111, 0xF>(x));  // shift right within rows of 16 lanes by 1, 2, 4, 8
+  x = max(x, dpp<0x112, 0xF>(x));
+  x = max(x, dpp<0x114, 0xF>(x));
+  x = max(x, dpp<0x118, 0xF>(x));
+  x = max(x, dpp<0x142, 0xA>(x));  // lane 15 of rows 0 and 2 to rows 1 and 3
+  x = max(x, dpp<0x143, 0xC>(x));  // lane 31 to rows 2 and 3
+  return (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
+}
+__device__ __forceinline__ float wave_sum(float x) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o);
+  return x;
+}
+
 struct Choice {  // in LDS
-  uint4 keys[kKeys / 4];  // rows of E keys, padded to a multiple of 4 with 0 (below every logit's)
   unsigned long long tokens_of[BSG_MOE_MAX_EXPERTS];  // bit t: token t chose the expert
   int first_row[BSG_MOE_MAX_EXPERTS];
-  int chosen[kMaxChoices];  // expert and logit of each choice: tokens in order, ranks in order
-  float logit[kMaxChoices];
+  int chosen[kMaxChoices];  // expert and weight of each choice: tokens in order, ranks in order
+  float weight[kMaxChoices];
   int sums[2 * kRouterWaves];
 };
 static_assert(BSG_MOE_MAX_TOKENS <= 64, "a bit for each token");
+static_assert(kMaxChoices <= kRouterThreads && BSG_MOE_MAX_EXPERTS <= kRouterThreads, "one thread for each");
+static_assert(BSG_MOE_MAX_TOP_K <= 64, "a lane for each of a token's choices");
 
-// Top k of every token and the tokens of every expert; one workgroup.  A logit's rank is the number of
-// larger ones (or equal ones of lower experts), counted by one thread per logit: ranks are a
-// permutation, so each place is filled exactly once, and no step waits for another.  A choice's row
-// follows from the bits of the tokens that chose its expert.
+// Top k of every token and the tokens of every expert; one workgroup.  A wave takes a token: lane i
+// holds the logits of experts R i .. R i + R - 1, and k times the largest is found and taken out (of
+// equal ones the lowest lane's and its lowest).  A choice's row follows from the bits of the tokens that
+// chose its expert.
+template <int R>
 __device__ void choose(const MoeArgs& p, Choice& sh) {
-  const int tid = threadIdx.x, E = p.experts, K = p.top_k, T = p.tokens, choices = T * K;
-  const int quads = (E + 3) / 4, step = kKeys / 4 / quads;  // tokens at a time
-  for (int e = tid; e < E; e += kRouterThreads) sh.tokens_of[e] = 0;
-  for (int t0 = 0; t0 < T; t0 += step) {
-    const int tokens = min(step, T - t0), n = tokens * quads * 4;
-    __syncthreads();
-    for (int i = tid; i < n; i += kRouterThreads) {
-      const int t = i / (quads * 4), e = i - t * quads * 4;
-      ((uint32_t*)sh.keys)[i] = e < E ? order_key(handoff_load(p.logits + (size_t)(t0 + t) * E + e)) : 0u;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int E = p.experts, K = p.top_k, T = p.tokens, choices = T * K;
+  if (tid < E) sh.tokens_of[tid] = 0;
+  __syncthreads();
+  for (int t = wave; t < T; t += kRouterWaves) {
+    uint32_t key[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int e = lane * R + r;
+      const float x = handoff_load(p.logits + (size_t)t * E + min(e, E - 1));
+      key[r] = e < E ? order_key(x) : 0u;
     }
-    __syncthreads();
-    for (int i = tid; i < n; i += kRouterThreads) {
-      const int t = i / (quads * 4), e = i - t * quads * 4;
-      const uint32_t mine = ((const uint32_t*)sh.keys)[i];
-      const uint4* row = sh.keys + t * quads;
-      int rank = 0;
-#pragma unroll 8
-      for (int j = 0; j < quads; ++j) {
-        const uint4 k = row[j];  // equal keys of lower experts count: key > mine - 1
-        rank += (k.x > mine - (4 * j < e)) + (k.y > mine - (4 * j + 1 < e)) + (k.z > mine - (4 * j + 2 < e)) +
-                (k.w > mine - (4 * j + 3 < e));
+    float all = 0.0f, mine = 0.0f;
+    uint32_t top = 0;
+    int expert = 0;
+    for (int k = 0; k < K; ++k) {
+      uint32_t best = key[0];
+#pragma unroll
+      for (int r = 1; r < R; ++r) best = max(best, key[r]);
+      const uint32_t most = wave_max(best);
+      const int owner = __builtin_ctzll(__ballot(best == most));
+      if (k == 0) {
+        top = most;
+        if (p.keep) {  // the sum over all experts, before any is taken out
+          float s = 0.0f;
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+            if (key[r]) s += __builtin_amdgcn_exp2f((key_value(key[r]) - key_value(top)) * kLog2e);
+          all = wave_sum(s);
+        }
       }
-      if (e < E && rank < K) {
-        sh.chosen[(t0 + t) * K + rank] = e;
-        sh.logit[(t0 + t) * K + rank] = key_value(mine);
-        atomicOr(&sh.tokens_of[e], 1ull << (t0 + t));
+      int place = 0;
+      bool taken = lane != owner;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const bool hit = !taken && key[r] == most;
+        place = hit ? r : place;
+        key[r] = hit ? 0u : key[r];
+        taken |= hit;
+      }
+      const int e = owner * R + __builtin_amdgcn_readlane(place, owner);
+      if (lane == k) {
+        expert = e;
+        mine = __builtin_amdgcn_exp2f((key_value(most) - key_value(top)) * kLog2e);
       }
     }
-    if (p.keep) {  // the sum over all experts, kept with the token's first key
-      __syncthreads();
-      for (int t = tid; t < tokens; t += kRouterThreads) {
-        const uint32_t* row = (const uint32_t*)(sh.keys + t * quads);
-        const float top = sh.logit[(t0 + t) * K];
-        float sum = 0.0f;
-        for (int e = 0; e < E; ++e) sum += __builtin_amdgcn_exp2f((key_value(row[e]) - top) * kLog2e);
-        p.row_weight[t0 + t] = sum;
-      }
+    const float sum = p.keep ? all : wave_sum(mine);
+    if (lane < K) {
+      const int c = t * K + lane;
+      sh.chosen[c] = expert;
+      sh.weight[c] = mine / sum;
+      atomicOr(&sh.tokens_of[expert], 1ull << t);
     }
   }
   __syncthreads();
   // rows of each expert, and its slots of up to slot_rows rows: a scan over the experts
   const int count = tid < E ? __popcll(sh.tokens_of[tid]) : 0, mine = (count + p.slot_rows - 1) / p.slot_rows;
   int rows = count, slots = mine;
-  const int lane = tid & 63, wave = tid >> 6;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
     const int a = __shfl_up(rows, o), b = __shfl_up(slots, o);
@@ -134,30 +169,16 @@ __device__ void choose(const MoeArgs& p, Choice& sh) {
   }
   if (tid == kRouterThreads - 1) *p.active = slots;
   __syncthreads();
-  const int c = tid;  // one thread per choice
-  static_assert(kMaxChoices <= kRouterThreads, "one thread per choice");
-  float w = 0.0f;
-  int row = 0;
-  if (c < choices) {
-    const int t = c / K, e = sh.chosen[c];
-    const float* l = sh.logit + t * K;
-    const float top = l[0];
-    float sum = 0.0f;
-    if (p.keep) {
-      sum = p.row_weight[t];
-    } else {
-#pragma unroll 4
-      for (int k = 0; k < K; ++k) sum += __builtin_amdgcn_exp2f((l[k] - top) * kLog2e);
-    }
-    w = __builtin_amdgcn_exp2f((sh.logit[c] - top) * kLog2e) / sum;
-    row = sh.first_row[e] + __popcll(sh.tokens_of[e] & ((1ull << t) - 1));
+  if (tid < choices) {
+    const int t = tid / K, e = sh.chosen[tid];
+    const float w = sh.weight[tid];
+    const int row = sh.first_row[e] + __popcll(sh.tokens_of[e] & ((1ull << t) - 1));
     p.row_token[row] = t;
-    p.row_of[c] = row;
-    if (p.ids) p.ids[c] = e;
-    if (p.weights) p.weights[c] = w;
+    p.row_weight[row] = w;
+    p.row_of[tid] = row;
+    if (p.ids) p.ids[tid] = e;
+    if (p.weights) p.weights[tid] = w;
   }
-  __syncthreads();  // the sums of p.row_weight were read
-  if (c < choices) p.row_weight[row] = w;
 }
 
 // The form in which the first product takes x: as it is, bf16 rows as fp16 scaled by a power of two each
@@ -167,37 +188,43 @@ enum class Prep { kNone, kScaled, kParts };
 template <bool NV, bool F16>
 constexpr Prep kPrep = NV ? (F16 ? Prep::kNone : Prep::kScaled) : (F16 ? Prep::kParts : Prep::kNone);
 
+// One token's row, by a whole workgroup.
 template <Prep PREP>
-__device__ __forceinline__ void prepare_row(const MoeArgs& p, int t, int lane) {
+__device__ __forceinline__ void prepare_row(const MoeArgs& p, int t, uint32_t* shared) {
+  const int tid = threadIdx.x;
   const uint16_t* x = p.x + t * p.x_stride;
   uint16_t* dst = p.xs + (int64_t)t * p.hidden;
-  int up = 0;
+  float scale = 1.0f;
+  v4i w = {0, 0, 0, 0};
   if constexpr (PREP == Prep::kScaled) {
     uint32_t most = 0;  // largest magnitude, as bits
-    for (int i = 8 * lane; i < p.hidden; i += 512) {
-      const v4i w = *(const v4i*)(x + i);
+    for (int i = 8 * tid; i < p.hidden; i += 8 * kRouterThreads) {
+      w = *(const v4i*)(x + i);
 #pragma unroll
       for (int k = 0; k < 4; ++k) most = max(most, max((uint32_t)w[k] & 0x7FFFu, ((uint32_t)w[k] >> 16) & 0x7FFFu));
     }
+    most = wave_max(most);
+    if ((tid & 63) == 0) shared[tid >> 6] = most;
+    __syncthreads();
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) most = max(most, (uint32_t)__shfl_xor((int)most, o));
+    for (int k = 0; k < kRouterWaves; ++k) most = max(most, shared[k]);
     // largest magnitude to [2^7, 2^8): exact in fp16 down to 2^-32 of it, and products with decoded
     // weights (below 2^4) stay far inside fp32; rows with an infinity or a NaN are left as they are
-    const int e = (int)(most >> 7) - 127;
-    up = e > 127 ? 0 : max(7 - e, -110);
-    if (lane == 0) p.x_exp[t] = up;
+    const int e = (int)(most >> 7) - 127, up = e > 127 ? 0 : max(7 - e, -110);
+    if (tid == 0) p.x_exp[t] = up;
+    scale = __builtin_amdgcn_ldexpf(1.0f, min(up, 127));  // (rows of bf16 subnormals: short of it, still exact)
+    if (up > 127 && tid == 0) p.x_exp[t] = 127;
   }
-  for (int i = 8 * lane; i < p.hidden; i += 512) {
-    const v4i w = *(const v4i*)(x + i);
+  for (int i = 8 * tid; i < p.hidden; i += 8 * kRouterThreads) {
+    if (PREP != Prep::kScaled || p.hidden > 8 * kRouterThreads) w = *(const v4i*)(x + i);  // else still held
     v4i hi, lo;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
+      const uint32_t u = (uint32_t)w[k];
       if constexpr (PREP == Prep::kScaled) {
-        const float f0 = __builtin_bit_cast(float, (uint32_t)w[k] << 16), f1 = __builtin_bit_cast(float, (uint32_t)w[k] & 0xFFFF0000u);
-        const v2f f = {__builtin_amdgcn_ldexpf(f0, up), __builtin_amdgcn_ldexpf(f1, up)};
+        const v2f f = {__builtin_bit_cast(float, u << 16) * scale, __builtin_bit_cast(float, u & 0xFFFF0000u) * scale};
         hi[k] = __builtin_bit_cast(int, __builtin_convertvector(f, v2h));
       } else {
-        const uint32_t u = (uint32_t)w[k];
         const v2h v = __builtin_bit_cast(v2h, u);
         const float f0 = (float)v[0], f1 = (float)v[1];
         const uint16_t h0 = bf16_bits(f0), h1 = bf16_bits(f1);
@@ -211,18 +238,25 @@ __device__ __forceinline__ void prepare_row(const MoeArgs& p, int t, int lane) {
   }
 }
 
-// Workgroup (x, y): logits of experts 16x .. 16x+15 for tokens 16y .. 16y+15, its waves taking
-// alternate steps of 32 k, kBatch of them in flight; the last workgroup to finish chooses.
+// Workgroups 0 .. tiles - 1: the logits of one tile of 16 experts and 16 tokens, the waves taking
+// alternate steps of 32 k, kBatch of them in flight; the last of these workgroups to finish chooses.  The
+// others prepare one token's row each.
 template <bool NV, bool F16>
 __global__ __launch_bounds__(kRouterThreads) void router_kernel(MoeArgs p) {
   __shared__ union {
     float part[kRouterWaves][64][4];
     Choice choice;
+    uint32_t most[kRouterWaves];
   } sh;
   __shared__ int last;
   constexpr int kBatch = 8;
+  const int tiles_e = (p.experts + 15) / 16, tiles = tiles_e * ((p.tokens + 15) / 16);
+  if ((int)blockIdx.x >= tiles) {
+    if constexpr (kPrep<NV, F16> != Prep::kNone) prepare_row<kPrep<NV, F16>>(p, blockIdx.x - tiles, sh.most);
+    return;
+  }
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, c = lane & 15, g = lane >> 4;
-  const int e0 = blockIdx.x * 16, t0 = blockIdx.y * 16;
+  const int e0 = blockIdx.x % tiles_e * 16, t0 = blockIdx.x / tiles_e * 16;
   const uint16_t* a = p.router + (size_t)min(e0 + c, p.experts - 1) * p.hidden + 8 * g;
   const uint16_t* b = p.x + (int64_t)min(t0 + c, p.tokens - 1) * p.x_stride + 8 * g;
   v4f acc = {0, 0, 0, 0};
@@ -244,9 +278,6 @@ __global__ __launch_bounds__(kRouterThreads) void router_kernel(MoeArgs p) {
     }
   }
   *(v4f*)sh.part[wave][lane] = acc;
-  // the activations' form for the first product, a wave per token (the tiles of experts share the tokens)
-  if (kPrep<NV, F16> != Prep::kNone && wave < 16 && wave % gridDim.x == blockIdx.x && t0 + wave < p.tokens)
-    prepare_row<kPrep<NV, F16>>(p, t0 + wave, lane);
   __syncthreads();
   if (wave == 0) {
     v4f s = *(v4f*)sh.part[0][lane];
@@ -257,7 +288,10 @@ __global__ __launch_bounds__(kRouterThreads) void router_kernel(MoeArgs p) {
       if (t0 + c < p.tokens && e0 + 4 * g + i < p.experts)
         handoff_store(p.logits + (size_t)(t0 + c) * p.experts + e0 + 4 * g + i, s[i]);
   }
-  if (last_arrival(p.arrived, gridDim.x * gridDim.y, &last)) choose(p, sh.choice);
+  if (!last_arrival(p.arrived, tiles, &last)) return;
+  if (p.experts <= 64) choose<1>(p, sh.choice);
+  else if (p.experts <= 128) choose<2>(p, sh.choice);
+  else choose<BSG_MOE_MAX_EXPERTS / 64>(p, sh.choice);
 }
 
 // ------------------------------------------------------------------------------------------- weights
@@ -447,7 +481,7 @@ __device__ __forceinline__ void products(Scales<DEC, TILES>& sh, const uint8_t* 
 
 // Workgroup (x, slot): SiLU(gate) up of dims 32x .. 32x+31 for the tokens of the slot's expert.
 template <bool NV, bool F16, int NT>
-__global__ __launch_bounds__(kThreads) void gate_up_kernel(MoeArgs p) {
+__global__ __launch_bounds__(kThreads, NT > 1 ? 1 : NV ? 3 : 2) void gate_up_kernel(MoeArgs p) {
   constexpr int TILES = 4;  // gate rows 0..15, 16..31, up rows 0..15, 16..31
   constexpr Dec DEC = NV ? Dec::kNvF16 : Dec::kMxBf16;
   constexpr Prep PREP = kPrep<NV, F16>;
@@ -511,7 +545,7 @@ __global__ __launch_bounds__(kThreads) void gate_up_kernel(MoeArgs p) {
 // Workgroup (x, slot): output dims 64x .. 64x+63 of the slot's tokens, times their weights; the last
 // slot of a row of workgroups to finish adds each token's choices in the order of their rank.
 template <bool NV, bool F16, int NT>
-__global__ __launch_bounds__(kThreads) void down_kernel(MoeArgs p) {
+__global__ __launch_bounds__(kThreads, NT > 1 ? 1 : NV ? 3 : 2) void down_kernel(MoeArgs p) {
   constexpr int TILES = 4;
   constexpr Dec DEC = NV ? Dec::kNvBf16 : Dec::kMxBf16;
   __shared__ union {
@@ -580,8 +614,10 @@ template <bool NV, bool F16, int NT>
 hipError_t launch(const MoeArgs& a, hipStream_t stream) {
   MoeArgs args = a;
   void* argv[] = {&args};
-  hipError_t e = hipLaunchKernel((const void*)&router_kernel<NV, F16>, dim3((a.experts + 15) / 16, (a.tokens + 15) / 16),
-                                 dim3(kRouterThreads), argv, 0, stream);
+  const unsigned tiles = (a.experts + 15) / 16 * ((a.tokens + 15) / 16);
+  hipError_t e = hipLaunchKernel((const void*)&router_kernel<NV, F16>,
+                                 dim3(tiles + (kPrep<NV, F16> != Prep::kNone ? a.tokens : 0)), dim3(kRouterThreads), argv, 0,
+                                 stream);
   if (e != hipSuccess) return e;
   // at most one slot per choice, and one per expert and slot_rows choices
   const int choices = a.tokens * a.top_k, bound = a.experts + choices / a.slot_rows;
