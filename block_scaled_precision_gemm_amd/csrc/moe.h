@@ -11,7 +11,6 @@ struct MoeArgs {
   int experts, top_k, hidden, inter, keep;
   // call
   int tokens;
-  int slot_rows;     // 16 or 32: rows of a slot
   const uint16_t* x;
   const uint16_t* router;
   const uint8_t *w13, *s13, *w2, *s2;
@@ -22,12 +21,12 @@ struct MoeArgs {
   int64_t x_stride, out_stride;
   // workspace
   float* logits;     // [tokens][experts]
-  uint16_t* xs;      // x as the first product takes it: [tokens][hidden] scaled fp16, or [2] bf16 parts of it
+  uint16_t* xs;      // x as the first product takes it: [tokens][hidden], or [2][tokens][hidden] bf16 parts of it
   int* x_exp;        // [tokens] powers of two of scaled rows
   uint16_t* h;       // [2][tokens * top_k][inter] bf16 parts of SiLU(gate) up, rows grouped by expert
   float* y;          // [tokens * top_k][hidden] weighted outputs, rows grouped by expert
   int* active;       // number of slots
-  int4* slots;       // (expert, first row, rows, 0): up to slot_rows rows of one expert
+  int4* slots;       // (expert, first row, rows, 0): up to 16 rows of one expert
   int* row_token;    // [tokens * top_k]
   float* row_weight; // [tokens * top_k]
   int* row_of;       // [tokens][top_k] row of a token's choice

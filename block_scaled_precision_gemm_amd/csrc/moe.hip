@@ -2,10 +2,8 @@
 //
 // Few tokens read many weights, so the layer is bound by the bytes of the chosen experts' weights,
 // and every kernel streams weight rows through registers into v_mfma_f32_16x16x32: rows of weights are
-// the product's first operand (16 rows), tokens the second (16 columns, unused ones repeat the first
-// token).  A lane loads the codes of 32 consecutive k of one row (16 bytes of E2M1, 32 of E4M3) and
-// uses them in four products; the k order of a product is free, so the tokens' operand is read in the
-// same order, 64 contiguous bytes per lane.  A workgroup's waves take alternate slabs of 128 k and are
+// the product's first operand (16 rows), tokens the second (16 columns, unused ones zero).  A lane loads the codes of 32 consecutive k of one row (16 bytes of E2M1, 32 of E4M3) and
+// uses them in four products; the k order of a product is free, and the tokens' operand follows it.  A workgroup's waves take alternate slabs of 128 k and are
 // summed through LDS.
 //
 // Decoded weights are exact: E2M1 * E4M3 has at most 6 significant bits, E4M3 * 2^e has 4.  MXFP8
@@ -30,6 +28,7 @@ typedef float v2f __attribute__((ext_vector_type(2)));
 typedef __bf16 v2b __attribute__((ext_vector_type(2)));
 
 constexpr int kSlab = 128;
+constexpr int kSlotRows = 16;  // rows of a slot: the columns of a product
 
 template <bool F16>
 __device__ __forceinline__ v4f mfma(v4i a, v4i b, v4f c) {
@@ -88,10 +87,57 @@ static_assert(BSG_MOE_MAX_TOKENS <= 64, "a bit for each token");
 static_assert(kMaxChoices <= kRouterThreads && BSG_MOE_MAX_EXPERTS <= kRouterThreads, "one thread for each");
 static_assert(BSG_MOE_MAX_TOP_K <= 64, "a lane for each of a token's choices");
 
-// Top k of every token and the tokens of every expert; one workgroup.  A wave takes a token: lane i
-// holds the logits of experts R i .. R i + R - 1, and k times the largest is found and taken out (of
-// equal ones the lowest lane's and its lowest).  A choice's row follows from the bits of the tokens that
-// chose its expert.
+// The top k of one token, by a wave: lane i holds the logits of experts R i .. R i + R - 1, and k times
+// the largest is found and taken out (of equal ones the lowest lane's, and its lowest).  Lane i ends with
+// the expert of rank i and its weight (i < K); the last rank looked for is `last`.
+template <int R, class Load>
+__device__ __forceinline__ void top_k(int E, int last, bool keep, int lane, Load load, int& expert, float& weight) {
+  uint32_t key[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int e = lane * R + r;
+    const float x = load(min(e, E - 1));
+    key[r] = e < E ? order_key(x) : 0u;
+  }
+  float all = 0.0f, mine = 0.0f;
+  uint32_t top = 0;
+  expert = 0;
+  for (int k = 0; k <= last; ++k) {
+    uint32_t best = key[0];
+#pragma unroll
+    for (int r = 1; r < R; ++r) best = max(best, key[r]);
+    const uint32_t most = wave_max(best);
+    const int owner = __builtin_ctzll(__ballot(best == most));
+    if (k == 0) {
+      top = most;
+      if (keep) {  // the sum over all experts, before any is taken out
+        float s = 0.0f;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          if (key[r]) s += __builtin_amdgcn_exp2f((key_value(key[r]) - key_value(top)) * kLog2e);
+        all = wave_sum(s);
+      }
+    }
+    int place = 0;
+    bool taken = lane != owner;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const bool hit = !taken && key[r] == most;
+      place = hit ? r : place;
+      key[r] = hit ? 0u : key[r];
+      taken |= hit;
+    }
+    const int e = owner * R + __builtin_amdgcn_readlane(place, owner);
+    if (lane == k) {
+      expert = e;
+      mine = __builtin_amdgcn_exp2f((key_value(most) - key_value(top)) * kLog2e);
+    }
+  }
+  weight = mine / (keep ? all : wave_sum(mine));
+}
+
+// Top k of every token and the tokens of every expert; one workgroup, a wave for each token.  A choice's
+// row follows from the bits of the tokens that chose its expert.
 template <int R>
 __device__ void choose(const MoeArgs& p, Choice& sh) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -99,58 +145,19 @@ __device__ void choose(const MoeArgs& p, Choice& sh) {
   if (tid < E) sh.tokens_of[tid] = 0;
   __syncthreads();
   for (int t = wave; t < T; t += kRouterWaves) {
-    uint32_t key[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int e = lane * R + r;
-      const float x = handoff_load(p.logits + (size_t)t * E + min(e, E - 1));
-      key[r] = e < E ? order_key(x) : 0u;
-    }
-    float all = 0.0f, mine = 0.0f;
-    uint32_t top = 0;
-    int expert = 0;
-    for (int k = 0; k < K; ++k) {
-      uint32_t best = key[0];
-#pragma unroll
-      for (int r = 1; r < R; ++r) best = max(best, key[r]);
-      const uint32_t most = wave_max(best);
-      const int owner = __builtin_ctzll(__ballot(best == most));
-      if (k == 0) {
-        top = most;
-        if (p.keep) {  // the sum over all experts, before any is taken out
-          float s = 0.0f;
-#pragma unroll
-          for (int r = 0; r < R; ++r)
-            if (key[r]) s += __builtin_amdgcn_exp2f((key_value(key[r]) - key_value(top)) * kLog2e);
-          all = wave_sum(s);
-        }
-      }
-      int place = 0;
-      bool taken = lane != owner;
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const bool hit = !taken && key[r] == most;
-        place = hit ? r : place;
-        key[r] = hit ? 0u : key[r];
-        taken |= hit;
-      }
-      const int e = owner * R + __builtin_amdgcn_readlane(place, owner);
-      if (lane == k) {
-        expert = e;
-        mine = __builtin_amdgcn_exp2f((key_value(most) - key_value(top)) * kLog2e);
-      }
-    }
-    const float sum = p.keep ? all : wave_sum(mine);
+    int expert;
+    float weight;
+    top_k<R>(E, K - 1, p.keep, lane, [&](int e) { return handoff_load(p.logits + (size_t)t * E + e); }, expert, weight);
     if (lane < K) {
       const int c = t * K + lane;
       sh.chosen[c] = expert;
-      sh.weight[c] = mine / sum;
+      sh.weight[c] = weight;
       atomicOr(&sh.tokens_of[expert], 1ull << t);
     }
   }
   __syncthreads();
-  // rows of each expert, and its slots of up to slot_rows rows: a scan over the experts
-  const int count = tid < E ? __popcll(sh.tokens_of[tid]) : 0, mine = (count + p.slot_rows - 1) / p.slot_rows;
+  // rows of each expert, and its slots of up to kSlotRows rows: a scan over the experts
+  const int count = tid < E ? __popcll(sh.tokens_of[tid]) : 0, mine = (count + kSlotRows - 1) / kSlotRows;
   int rows = count, slots = mine;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
@@ -165,7 +172,7 @@ __device__ void choose(const MoeArgs& p, Choice& sh) {
   if (tid < E) {
     sh.first_row[tid] = rows - count;
     for (int k = 0; k < mine; ++k)
-      p.slots[slots - mine + k] = int4{tid, rows - count + k * p.slot_rows, min(count - k * p.slot_rows, p.slot_rows), 0};
+      p.slots[slots - mine + k] = int4{tid, rows - count + k * kSlotRows, min(count - k * kSlotRows, kSlotRows), 0};
   }
   if (tid == kRouterThreads - 1) *p.active = slots;
   __syncthreads();
@@ -181,12 +188,12 @@ __device__ void choose(const MoeArgs& p, Choice& sh) {
   }
 }
 
-// The form in which the first product takes x: as it is, bf16 rows as fp16 scaled by a power of two each
-// (NVFP4 weights decode to fp16 in half the operations of bf16), or fp16 rows as two bf16 parts (MXFP8
-// weights need bf16's range).
-enum class Prep { kNone, kScaled, kParts };
+// The form in which the first product takes x, in rows without gaps: as it is, bf16 rows as fp16 scaled
+// by a power of two each (NVFP4 weights decode to fp16 in half the operations of bf16), or fp16 rows as
+// two bf16 parts (MXFP8 weights need bf16's range).
+enum class Prep { kAsIs, kScaled, kParts };
 template <bool NV, bool F16>
-constexpr Prep kPrep = NV ? (F16 ? Prep::kNone : Prep::kScaled) : (F16 ? Prep::kParts : Prep::kNone);
+constexpr Prep kPrep = NV ? (F16 ? Prep::kAsIs : Prep::kScaled) : (F16 ? Prep::kParts : Prep::kAsIs);
 
 // One token's row, by a whole workgroup.
 template <Prep PREP>
@@ -224,6 +231,8 @@ __device__ __forceinline__ void prepare_row(const MoeArgs& p, int t, uint32_t* s
       if constexpr (PREP == Prep::kScaled) {
         const v2f f = {__builtin_bit_cast(float, u << 16) * scale, __builtin_bit_cast(float, u & 0xFFFF0000u) * scale};
         hi[k] = __builtin_bit_cast(int, __builtin_convertvector(f, v2h));
+      } else if constexpr (PREP == Prep::kAsIs) {
+        hi[k] = (int)u;
       } else {
         const v2h v = __builtin_bit_cast(v2h, u);
         const float f0 = (float)v[0], f1 = (float)v[1];
@@ -252,7 +261,7 @@ __global__ __launch_bounds__(kRouterThreads) void router_kernel(MoeArgs p) {
   constexpr int kBatch = 8;
   const int tiles_e = (p.experts + 15) / 16, tiles = tiles_e * ((p.tokens + 15) / 16);
   if ((int)blockIdx.x >= tiles) {
-    if constexpr (kPrep<NV, F16> != Prep::kNone) prepare_row<kPrep<NV, F16>>(p, blockIdx.x - tiles, sh.most);
+    prepare_row<kPrep<NV, F16>>(p, blockIdx.x - tiles, sh.most);
     return;
   }
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, c = lane & 15, g = lane >> 4;
@@ -288,7 +297,7 @@ __global__ __launch_bounds__(kRouterThreads) void router_kernel(MoeArgs p) {
       if (t0 + c < p.tokens && e0 + 4 * g + i < p.experts)
         handoff_store(p.logits + (size_t)(t0 + c) * p.experts + e0 + 4 * g + i, s[i]);
   }
-  if (!last_arrival(p.arrived, tiles, &last)) return;
+  if (p.tokens == 1 || !last_arrival(p.arrived, tiles, &last)) return;  // (one token: gate_up_kernel chooses)
   if (p.experts <= 64) choose<1>(p, sh.choice);
   else if (p.experts <= 128) choose<2>(p, sh.choice);
   else choose<BSG_MOE_MAX_EXPERTS / 64>(p, sh.choice);
@@ -366,136 +375,178 @@ struct Scales {
   uint8_t rows[TILES * 16][kPitch];
 };
 
-// Copy the codes of chunk k0 .. k0 + n - 1 of tiles whose first rows start at sc[m].
+// Copy the codes of chunk k0 .. k0 + n - 1 of tiles whose first rows start at sc[m]: 16 threads a row.
 template <Dec DEC, int TILES>
 __device__ __forceinline__ void stage_scales(Scales<DEC, TILES>& sh, const uint8_t* const sc[TILES], int K, int k0, int n, int tid) {
-  const int row_bytes = K / Codes<DEC>::kBlock, first = k0 / Codes<DEC>::kBlock, bytes = n / Codes<DEC>::kBlock;
+  const int row_bytes = K / Codes<DEC>::kBlock, bytes = n / Codes<DEC>::kBlock, r = tid >> 4;
+  const uint32_t first = r * row_bytes + k0 / Codes<DEC>::kBlock;
   auto copy = [&](auto unit) {
     using U = decltype(unit);
-    const int per_row = bytes / (int)sizeof(U);
+    for (int at = (tid & 15) * (int)sizeof(U); at < bytes; at += 16 * (int)sizeof(U)) {
+      U v[TILES];
 #pragma unroll
-    for (int m = 0; m < TILES; ++m)
-#pragma unroll 2
-      for (int i = tid; i < 16 * per_row; i += kThreads) {
-        const int r = i / per_row, at = (i - r * per_row) * (int)sizeof(U);
-        const U v = *(const U*)(sc[m] + r * row_bytes + first + at);
-        __builtin_memcpy(&sh.rows[16 * m + r][at], &v, sizeof(U));
-      }
+      for (int m = 0; m < TILES; ++m) v[m] = *(const U*)(sc[m] + first + at);
+#pragma unroll
+      for (int m = 0; m < TILES; ++m) __builtin_memcpy(&sh.rows[16 * m + r][at], &v[m], sizeof(U));
+    }
   };
-  if (row_bytes % 8 == 0) copy(uint2{});  // (chunks start at multiples of 8 codes; scales are 4-byte aligned at least)
+  // whole rows of 8 codes keep every row at 4 bytes or better (scales are 4-byte aligned), chunks start
+  // at multiples of 8 codes
+  if (row_bytes % 8 == 0) copy(uint2{});
   else if constexpr (Codes<DEC>::NV) copy(uint16_t{});
   else copy(uint8_t{});
 }
 
-// acc[tile][nt] += rows x columns: tile m's 16 rows start at w[m] (codes) and sc[m] (scales), the lane's
-// column is at b[nt], PARTS parts `part` elements apart.  Slabs of 128 k go to the four waves in turn.
-template <Dec DEC, int TILES, int NT, int PARTS>
-__device__ __forceinline__ void products(Scales<DEC, TILES>& sh, const uint8_t* const w[TILES], const uint8_t* const sc[TILES],
-                                         int K, int tid, int wave, const uint16_t* const b[NT], int64_t part, int nts,
-                                         v4f acc[TILES][NT]) {
+// A wave's slab of the activations in LDS: 16 columns of 128 k, padded so that the 16 lanes of a fragment
+// read lie in different banks.  Read straight from memory in fragment order each lane would touch a
+// line of its own four times over (64 lines in each of four loads, against 64 of all the weights').
+constexpr int kXPitch = 2 * kSlab + 16;
+template <int PARTS>
+struct Slab {
+  uint8_t at[4][PARTS][16 * kXPitch];  // [wave][part]
+};
+
+// acc[tile] += rows x columns: tile m's 16 rows start at w[m] (codes) and sc[m] (scales); the columns are
+// rows of `x` (bf16 or fp16, K long), column i's at byte column[i] (of the lane's columns 4 i + lane / 16;
+// kNoColumn: none, zeros), part q `part` bytes further.  Slabs of 128 k go to the four waves in turn.
+constexpr uint32_t kNoColumn = 0x80000000u;
+template <Dec DEC, int TILES, int PARTS>
+__device__ __forceinline__ void products(Scales<DEC, TILES>& sh, Slab<PARTS>& slab, const uint8_t* const w[TILES],
+                                         const uint8_t* const sc[TILES], int K, int tid, int wave, const void* x,
+                                         uint32_t x_bytes, const uint32_t column[4], uint32_t part, v4f acc[TILES]) {
   using C = Codes<DEC>;
   constexpr int DEPTH = C::kDepth;
-  static_assert(DEPTH % 2 == 0, "the activations' buffers alternate");
   const int lane = tid & 63, c = lane & 15, g = lane >> 4;
-  const int row_bytes = C::NV ? K / 2 : K;
-  const uint32_t at0 = c * row_bytes + g * (C::kSlabBytes / 4);
+  const uint32_t at0 = c * (C::NV ? K / 2 : K) + g * (C::kSlabBytes / 4);
+  const __amdgpu_buffer_rsrc_t xbuf = handoff_buffer(x, x_bytes);
   Row<DEC> buf[DEPTH][TILES];
-  v4i x[2][PARTS][NT][4];
+  v4u_t raw[PARTS][4];
   auto fetch = [&](Row<DEC>* r, int s) {
 #pragma unroll
     for (int m = 0; m < TILES; ++m) r[m].load(w[m] + (at0 + (uint32_t)s * C::kSlabBytes));
   };
-  auto fetch_x = [&](v4i (*v)[NT][4], int s) {
+  auto fetch_x = [&](int s) {
+    const uint32_t k = s * kSlab + 8 * c;  // the lane's 8 k of each of its columns
 #pragma unroll
     for (int q = 0; q < PARTS; ++q)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-        if (n < nts) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) v[q][n][j] = *(const v4i*)(b[n] + q * part + s * kSlab + 32 * g + 8 * j);
-        }
+      for (int i = 0; i < 4; ++i)  // beyond the buffer: zeros, and no memory access
+        raw[q][i] = __builtin_amdgcn_raw_buffer_load_b128(xbuf, (int)(k < (uint32_t)K ? column[i] + 2 * k + q * part : kNoColumn), 0, 0);
   };
-  auto multiply = [&](const Row<DEC>* r, const v4i (*v)[NT][4], int chunk_slab) {
+  auto multiply = [&](const Row<DEC>* r, int chunk_slab, int next) {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+    for (int q = 0; q < PARTS; ++q)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) *(v4u_t*)&slab.at[wave][q][(4 * i + g) * kXPitch + 16 * c] = raw[q][i];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();  // (one wave's LDS accesses are in order)
+    fetch_x(next);
+    v4i v[PARTS][4];
+#pragma unroll
+    for (int q = 0; q < PARTS; ++q)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[q][j] = *(const v4i*)&slab.at[wave][q][c * kXPitch + 64 * g + 16 * j];
+    uint32_t s[TILES];
 #pragma unroll
     for (int m = 0; m < TILES; ++m) {
       const uint8_t* codes = &sh.rows[16 * m + c][chunk_slab * C::kSlabScales + g * (C::kSlabScales / 4)];
-      const uint32_t s = C::NV ? (uint32_t)*(const uint16_t*)codes : (uint32_t)*codes;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const v4i a = r[m].fragment(j, s);
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-          if (n < nts) {
-#pragma unroll
-            for (int q = 0; q < PARTS; ++q) acc[m][n] = mfma<C::F16>(a, v[q][n][j], acc[m][n]);
-          }
-      }
+      s[m] = C::NV ? (uint32_t)*(const uint16_t*)codes : (uint32_t)*codes;
     }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int m = 0; m < TILES; ++m) {
+        const v4i a = r[m].fragment(j, s[m]);
+#pragma unroll
+        for (int q = 0; q < PARTS; ++q) acc[m] = mfma<C::F16>(a, v[q][j], acc[m]);
+      }
   };
   for (int k0 = 0; k0 < K; k0 += kChunk) {
     const int n = min(kChunk, K - k0), first = k0 / kSlab, full = first + n / kSlab;
     const int s1 = first + wave;
+    // slabs past the last are read again as the last and not used
+    const int mine = s1 < full ? (full - s1 + 3) / 4 : 0, last = s1 + 4 * (mine - 1);
+    if (mine) {
 #pragma unroll
-    for (int d = 0; d < DEPTH; ++d)
-      if (s1 + 4 * d < full) fetch(buf[d], s1 + 4 * d);
-    if (s1 < full) fetch_x(x[0], s1);
+      for (int d = 0; d < DEPTH; ++d) fetch(buf[d], min(s1 + 4 * d, last));
+      fetch_x(s1);
+    }
     if (k0) __syncthreads();
     stage_scales<DEC, TILES>(sh, sc, K, k0, n, tid);
     __syncthreads();
-    for (int s0 = s1; s0 < full; s0 += 4 * DEPTH) {
+    int i = 0;
+    for (; i + DEPTH <= mine; i += DEPTH) {
 #pragma unroll
       for (int d = 0; d < DEPTH; ++d) {
-        const int s = s0 + 4 * d;
-        if (s < full) {
-          if (s + 4 < full) fetch_x(x[(d + 1) & 1], s + 4);
-          multiply(buf[d], x[d & 1], s - first);
-          if (s + 4 * DEPTH < full) fetch(buf[d], s + 4 * DEPTH);
-        }
+        const int s = s1 + 4 * (i + d);
+        multiply(buf[d], s - first, min(s + 4, last));
+        fetch(buf[d], min(s + 4 * DEPTH, last));
       }
     }
+#pragma unroll
+    for (int d = 0; d < DEPTH - 1; ++d)
+      if (i + d < mine) multiply(buf[d], s1 + 4 * (i + d) - first, min(s1 + 4 * (i + d + 1), last));
     if (n % kSlab && wave == full % 4) {  // the rest: lanes past the end count as zero
-      const bool in = full * kSlab + 32 * g < K;
-#pragma unroll
-      for (int m = 0; m < TILES; ++m) buf[0][m].clear();
-#pragma unroll
-      for (int q = 0; q < PARTS; ++q)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) x[0][q][nt][j] = v4i{0, 0, 0, 0};
-      if (in) {
-        fetch_x(x[0], full);
+      fetch_x(full);
+      if (full * kSlab + 32 * g < K) {
         fetch(buf[0], full);
       } else {
-        // their scales are whatever LDS holds: zero them, so that no NaN comes of it
+        // their scales are whatever LDS holds: zero them too, so that no NaN comes of it
 #pragma unroll
-        for (int m = 0; m < TILES; ++m)
+        for (int m = 0; m < TILES; ++m) {
+          buf[0][m].clear();
 #pragma unroll
-          for (int i = 0; i < C::kSlabScales / 4; ++i)
-            sh.rows[16 * m + c][(full - first) * C::kSlabScales + g * (C::kSlabScales / 4) + i] = 0;
+          for (int b = 0; b < C::kSlabScales / 4; ++b)
+            sh.rows[16 * m + c][(full - first) * C::kSlabScales + g * (C::kSlabScales / 4) + b] = 0;
+        }
       }
-      multiply(buf[0], x[0], full - first);
+      multiply(buf[0], full - first, full);
     }
   }
 }
 
 // Workgroup (x, slot): SiLU(gate) up of dims 32x .. 32x+31 for the tokens of the slot's expert.
-template <bool NV, bool F16, int NT>
-__global__ __launch_bounds__(kThreads, NT > 1 ? 1 : NV ? 3 : 2) void gate_up_kernel(MoeArgs p) {
+template <bool NV, bool F16, bool ONE>
+__global__ __launch_bounds__(kThreads, NV ? 3 : 2) void gate_up_kernel(MoeArgs p) {
   constexpr int TILES = 4;  // gate rows 0..15, 16..31, up rows 0..15, 16..31
   constexpr Dec DEC = NV ? Dec::kNvF16 : Dec::kMxBf16;
   constexpr Prep PREP = kPrep<NV, F16>;
   constexpr int PARTS = PREP == Prep::kParts ? 2 : 1;
   __shared__ union {
-    Scales<DEC, TILES> scales;
-    v4f acc[4][TILES][NT][64];
+    struct {
+      Scales<DEC, TILES> scales;
+      Slab<PARTS> slab;
+    };
+    v4f acc[4][TILES][64];
   } sh;
-  const int4 slot = p.slots[blockIdx.y];
-  if ((int)blockIdx.y >= *p.active) return;
+  int4 slot;
+  if (ONE) {
+    // one token: slot y is its choice of rank y, found by each workgroup for itself while it would wait
+    // for the router's last workgroup otherwise; the first workgroup of a slot keeps it for the next kernel
+    const int lane = threadIdx.x & 63, y = blockIdx.y, last = blockIdx.x ? y : p.top_k - 1;
+    int expert;
+    float weight;
+    auto load = [&](int e) { return p.logits[e]; };
+    if (p.experts <= 64) top_k<1>(p.experts, last, p.keep, lane, load, expert, weight);
+    else top_k<BSG_MOE_MAX_EXPERTS / 64>(p.experts, last, p.keep, lane, load, expert, weight);
+    slot = int4{__builtin_amdgcn_readlane(expert, y), y, 1, 0};
+    if (blockIdx.x == 0 && (int)threadIdx.x == y) {
+      p.slots[y] = slot;
+      p.row_weight[y] = weight;
+      p.row_of[y] = y;
+      if (y == 0) *p.active = p.top_k;
+      if (p.ids) p.ids[y] = expert;
+      if (p.weights) p.weights[y] = weight;
+    }
+  } else {
+    slot = p.slots[blockIdx.y];
+    if ((int)blockIdx.y >= *p.active) return;
+  }
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, c = lane & 15;
   const int e = __builtin_amdgcn_readfirstlane(slot.x), start = __builtin_amdgcn_readfirstlane(slot.y);
   const int count = __builtin_amdgcn_readfirstlane(slot.z);
-  const int nts = (count + 15) / 16, i0 = blockIdx.x * 32;
+  const int i0 = blockIdx.x * 32;
   const uint8_t *w[TILES], *sc[TILES];
 #pragma unroll
   for (int m = 0; m < TILES; ++m) {
@@ -503,35 +554,34 @@ __global__ __launch_bounds__(kThreads, NT > 1 ? 1 : NV ? 3 : 2) void gate_up_ker
     w[m] = p.w13 + row * (NV ? p.hidden / 2 : p.hidden);
     sc[m] = p.s13 + row * (NV ? p.hidden / 16 : p.hidden / 32);
   }
-  const uint16_t* b[NT];
+  uint32_t column[4];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int t = p.row_token[start + min(16 * n + c, count - 1)];
-    b[n] = PREP == Prep::kNone ? p.x + t * p.x_stride : p.xs + (int64_t)t * p.hidden;
+  for (int i = 0; i < 4; ++i) {
+    const int col = 4 * i + (lane >> 4), t = ONE ? 0 : p.row_token[start + min(col, count - 1)];
+    column[i] = col < count ? (uint32_t)t * p.hidden * 2 : kNoColumn;
   }
-  v4f acc[TILES][NT] = {};
-  products<DEC, TILES, NT, PARTS>(sh.scales, w, sc, p.hidden, tid, wave, b, (int64_t)p.tokens * p.hidden, nts, acc);
-  __syncthreads();  // the scales are done with
+  v4f acc[TILES] = {};
+  const uint32_t part = (uint32_t)p.tokens * p.hidden * 2;
+  products<DEC, TILES, PARTS>(sh.scales, sh.slab, w, sc, p.hidden, tid, wave, p.xs, PARTS * part, column, part, acc);
+  __syncthreads();  // the scales and the slabs are done with
 #pragma unroll
-  for (int m = 0; m < TILES; ++m)
-#pragma unroll
-    for (int n = 0; n < NT; ++n) sh.acc[wave][m][n][lane] = acc[m][n];
+  for (int m = 0; m < TILES; ++m) sh.acc[wave][m][lane] = acc[m];
   __syncthreads();
   const float alpha = p.alpha13 ? p.alpha13[e] : 1.0f;
   const int64_t rows = (int64_t)p.tokens * p.top_k;
-  for (int k = tid; k < 2 * nts * 64; k += kThreads) {
-    const int l = k & 63, m = (k >> 6) & 1, n = k >> 7, col = 16 * n + (l & 15), i = i0 + 16 * m + 4 * (l >> 4);
-    v4f gate = sh.acc[0][m][n][l], up = sh.acc[0][m + 2][n][l];
+  if (tid < 128) {
+    const int m = tid >> 6, col = c, i = i0 + 16 * m + 4 * (lane >> 4);
+    v4f gate = sh.acc[0][m][lane], up = sh.acc[0][m + 2][lane];
 #pragma unroll
-    for (int w = 1; w < 4; ++w) gate += sh.acc[w][m][n][l], up += sh.acc[w][m + 2][n][l];
-    if (col >= count || i >= p.inter) continue;
+    for (int w = 1; w < 4; ++w) gate += sh.acc[w][m][lane], up += sh.acc[w][m + 2][lane];
+    if (col >= count || i >= p.inter) return;
     // powers of two that the operands carry: decoded weights 2^-8, scaled rows of x 2^x_exp
-    const int back = (NV ? 8 : 0) - (PREP == Prep::kScaled ? p.x_exp[p.row_token[start + col]] : 0);
+    const int back = (NV ? 8 : 0) - (PREP == Prep::kScaled ? p.x_exp[ONE ? 0 : p.row_token[start + col]] : 0);
     uint16_t hi[4], lo[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const float x = alpha * __builtin_amdgcn_ldexpf(gate[r], back), u = alpha * __builtin_amdgcn_ldexpf(up[r], back);
-      const float v = x / (1.0f + __builtin_amdgcn_exp2f(x * -1.44269504088896341f)) * u;
+      const float v = x / (1.0f + __builtin_amdgcn_exp2f(-x * kLog2e)) * u;
       hi[r] = bf16_bits(v);
       const float rest = v - bf16_value(hi[r]);
       lo[r] = rest - rest == 0.0f ? bf16_bits(rest) : 0;  // an infinite high part has no low part
@@ -544,13 +594,16 @@ __global__ __launch_bounds__(kThreads, NT > 1 ? 1 : NV ? 3 : 2) void gate_up_ker
 
 // Workgroup (x, slot): output dims 64x .. 64x+63 of the slot's tokens, times their weights; the last
 // slot of a row of workgroups to finish adds each token's choices in the order of their rank.
-template <bool NV, bool F16, int NT>
-__global__ __launch_bounds__(kThreads, NT > 1 ? 1 : NV ? 3 : 2) void down_kernel(MoeArgs p) {
+template <bool NV, bool F16>
+__global__ __launch_bounds__(kThreads, NV ? 3 : 2) void down_kernel(MoeArgs p) {
   constexpr int TILES = 4;
   constexpr Dec DEC = NV ? Dec::kNvBf16 : Dec::kMxBf16;
   __shared__ union {
-    Scales<DEC, TILES> scales;
-    v4f acc[4][TILES][NT][64];
+    struct {
+      Scales<DEC, TILES> scales;
+      Slab<2> slab;
+    };
+    v4f acc[4][TILES][64];
   } sh;
   __shared__ int last;
   const int active = *p.active;
@@ -559,7 +612,7 @@ __global__ __launch_bounds__(kThreads, NT > 1 ? 1 : NV ? 3 : 2) void down_kernel
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, c = lane & 15;
   const int e = __builtin_amdgcn_readfirstlane(slot.x), start = __builtin_amdgcn_readfirstlane(slot.y);
   const int count = __builtin_amdgcn_readfirstlane(slot.z);
-  const int nts = (count + 15) / 16, d0 = blockIdx.x * 64;
+  const int d0 = blockIdx.x * 64;
   const uint8_t *w[TILES], *sc[TILES];
 #pragma unroll
   for (int m = 0; m < TILES; ++m) {
@@ -567,27 +620,28 @@ __global__ __launch_bounds__(kThreads, NT > 1 ? 1 : NV ? 3 : 2) void down_kernel
     w[m] = p.w2 + row * (NV ? p.inter / 2 : p.inter);
     sc[m] = p.s2 + row * (NV ? p.inter / 16 : p.inter / 32);
   }
-  const uint16_t* b[NT];
+  uint32_t column[4];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) b[n] = p.h + (int64_t)(start + min(16 * n + c, count - 1)) * p.inter;
-  v4f acc[TILES][NT] = {};
-  products<DEC, TILES, NT, 2>(sh.scales, w, sc, p.inter, tid, wave, b, (int64_t)p.tokens * p.top_k * p.inter, nts, acc);
-  __syncthreads();  // the scales are done with
+  for (int i = 0; i < 4; ++i) {
+    const int col = 4 * i + (lane >> 4);
+    column[i] = col < count ? (uint32_t)(start + col) * p.inter * 2 : kNoColumn;
+  }
+  v4f acc[TILES] = {};
+  const uint32_t part = (uint32_t)(p.tokens * p.top_k) * p.inter * 2;
+  products<DEC, TILES, 2>(sh.scales, sh.slab, w, sc, p.inter, tid, wave, p.h, 2 * part, column, part, acc);
+  __syncthreads();  // the scales and the slabs are done with
 #pragma unroll
-  for (int m = 0; m < TILES; ++m)
-#pragma unroll
-    for (int n = 0; n < NT; ++n) sh.acc[wave][m][n][lane] = acc[m][n];
+  for (int m = 0; m < TILES; ++m) sh.acc[wave][m][lane] = acc[m];
   __syncthreads();
   const float alpha = p.alpha2 ? p.alpha2[e] : 1.0f;
-  // (a few tokens' rows: far below 2^31 bytes)
   const __amdgpu_buffer_rsrc_t ybuf = handoff_buffer(p.y, (uint32_t)(p.tokens * p.top_k) * (uint32_t)p.hidden * 4u);
-  for (int k = tid; k < TILES * nts * 64; k += kThreads) {
-    const int l = k & 63, m = (k >> 6) % TILES, n = (k >> 6) / TILES, col = 16 * n + (l & 15), d = d0 + 16 * m + 4 * (l >> 4);
-    v4f y = sh.acc[0][m][n][l];
+  {
+    const int m = wave, col = c, d = d0 + 16 * m + 4 * (lane >> 4);
+    v4f y = sh.acc[0][m][lane];
 #pragma unroll
-    for (int w = 1; w < 4; ++w) y += sh.acc[w][m][n][l];
-    if (col >= count || d >= p.hidden) continue;
-    handoff_store4(ybuf, (uint32_t)(start + col) * p.hidden + d, y * (alpha * p.row_weight[start + col]));
+    for (int w = 1; w < 4; ++w) y += sh.acc[w][m][lane];
+    if (col < count && d < p.hidden)
+      handoff_store4(ybuf, (uint32_t)(start + col) * p.hidden + d, y * (alpha * p.row_weight[start + col]));
   }
   if (!last_arrival(p.arrived + 1 + blockIdx.x, active, &last)) return;
   for (int k = tid; k < p.tokens * 16; k += kThreads) {
@@ -610,35 +664,29 @@ __global__ __launch_bounds__(kThreads, NT > 1 ? 1 : NV ? 3 : 2) void down_kernel
   }
 }
 
-template <bool NV, bool F16, int NT>
+template <bool NV, bool F16>
 hipError_t launch(const MoeArgs& a, hipStream_t stream) {
   MoeArgs args = a;
   void* argv[] = {&args};
   const unsigned tiles = (a.experts + 15) / 16 * ((a.tokens + 15) / 16);
   hipError_t e = hipLaunchKernel((const void*)&router_kernel<NV, F16>,
-                                 dim3(tiles + (kPrep<NV, F16> != Prep::kNone ? a.tokens : 0)), dim3(kRouterThreads), argv, 0,
+                                 dim3(tiles + a.tokens), dim3(kRouterThreads), argv, 0,
                                  stream);
   if (e != hipSuccess) return e;
-  // at most one slot per choice, and one per expert and slot_rows choices
-  const int choices = a.tokens * a.top_k, bound = a.experts + choices / a.slot_rows;
+  // at most one slot per choice, and one per expert and kSlotRows choices
+  const int choices = a.tokens * a.top_k, bound = a.experts + choices / kSlotRows;
   const unsigned slots = choices < bound ? choices : bound;
-  e = hipLaunchKernel((const void*)&gate_up_kernel<NV, F16, NT>, dim3((a.inter + 31) / 32, slots), dim3(kThreads),
-                      argv, 0, stream);
+  const void* gate_up = a.tokens == 1 ? (const void*)&gate_up_kernel<NV, F16, true> : (const void*)&gate_up_kernel<NV, F16, false>;
+  e = hipLaunchKernel(gate_up, dim3((a.inter + 31) / 32, slots), dim3(kThreads), argv, 0, stream);
   if (e != hipSuccess) return e;
-  return hipLaunchKernel((const void*)&down_kernel<NV, F16, NT>, dim3((a.hidden + 63) / 64, slots), dim3(kThreads), argv, 0,
-                         stream);
-}
-
-template <bool NV, bool F16>
-hipError_t launch_nt(const MoeArgs& a, hipStream_t stream) {
-  return a.slot_rows == 16 ? launch<NV, F16, 1>(a, stream) : launch<NV, F16, 2>(a, stream);
+  return hipLaunchKernel((const void*)&down_kernel<NV, F16>, dim3((a.hidden + 63) / 64, slots), dim3(kThreads), argv, 0, stream);
 }
 
 }  // namespace
 
 hipError_t moe_launch(const MoeArgs& a, int format, int dtype, hipStream_t stream) {
-  if (format) return dtype ? launch_nt<true, true>(a, stream) : launch_nt<true, false>(a, stream);
-  return dtype ? launch_nt<false, true>(a, stream) : launch_nt<false, false>(a, stream);
+  if (format) return dtype ? launch<true, true>(a, stream) : launch<true, false>(a, stream);
+  return dtype ? launch<false, true>(a, stream) : launch<false, false>(a, stream);
 }
 
 size_t moe_workspace(const bsg_moe_problem& p, uint8_t* base, MoeArgs* a, size_t* counters_at, size_t* counters_bytes) {

@@ -165,9 +165,6 @@ bsg_status bsg_moe_run(bsg_moe_plan plan, int64_t tokens, const void* x, int64_t
   }
   bsg::MoeArgs a = plan->args;
   a.tokens = (int)tokens;
-  // Rows of a slot: one column tile of a product (16), or two where many experts would need two slots and
-  // read their weights twice.
-  a.slot_rows = tokens * a.top_k <= 8 * a.experts || tokens <= 16 ? 16 : 32;
   a.x = (const uint16_t*)x;
   a.router = (const uint16_t*)w->router;
   a.w13 = (const uint8_t*)w->w13;
