@@ -38,6 +38,7 @@ struct KvArgs {
   float* part;       // partial outputs and their softmax statistics
   int* group_arrived;  // arrival counters of groups of parts, and of units; zero between calls
   int* arrived;
+  int splits;        // position splits of the many-row kernel
 };
 
 // Byte offsets inside the chunk of one head of a page (P = page tokens, D = head dim).

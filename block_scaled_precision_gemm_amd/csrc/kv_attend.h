@@ -1,0 +1,111 @@
+// What the attention kernels share: layouts of fragments, decoding, query rows.
+#pragma once
+
+#include "kv.h"
+
+namespace bsg {
+
+typedef float v2f __attribute__((ext_vector_type(2)));
+
+constexpr int kTile = 64;       // positions of a tile
+constexpr float kPBias = 14.0f; // P is held as 2^14 P
+constexpr int kJoin = 16;       // parts joined at a time
+constexpr float kNegInf = -__builtin_inff();
+constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
+
+// Combine the four lanes of one row (lane % 16): each swap gives every lane its own value and its partner's.
+__device__ __forceinline__ void swap32(float x, float& a, float& b) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  const uint32_t r0 = r[0], r1 = r[1];
+  a = __builtin_bit_cast(float, r0);
+  b = __builtin_bit_cast(float, r1);
+}
+__device__ __forceinline__ void swap16(float x, float& a, float& b) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  const uint32_t r0 = r[0], r1 = r[1];
+  a = __builtin_bit_cast(float, r0);
+  b = __builtin_bit_cast(float, r1);
+}
+__device__ __forceinline__ float max_over_g(float x) {
+  float a, b;
+  swap32(x, a, b);
+  swap16(__builtin_fmaxf(a, b), a, b);
+  return __builtin_fmaxf(a, b);
+}
+__device__ __forceinline__ float sum_over_g(float x) {
+  float a, b;
+  swap32(x, a, b);
+  swap16(a + b, a, b);
+  return a + b;
+}
+
+// Two non-negative E4M3 codes (bytes SEL picks) -> fp16 pair, times 2^-8; 0x7F -> NaN (0x3F80 + 0x80
+// carries into the bit that makes it one).
+template <uint32_t SEL>
+__device__ __forceinline__ uint32_t scale_pair(uint32_t w) {
+  const uint32_t t = __builtin_amdgcn_perm(0u, w, SEL) >> 1;
+  return t | ((t + 0x00800080u) & 0x40004000u);
+}
+constexpr uint32_t kLow = 0x010C000Cu, kHigh = 0x030C020Cu;  // bytes 0, 1 and bytes 2, 3
+
+__device__ __forceinline__ v2h fp4_pair(uint32_t w, int b) {
+  // the byte is an immediate of the instruction
+  switch (b) {
+    case 0: return __builtin_bit_cast(v2h, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0));
+    case 1: return __builtin_bit_cast(v2h, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1));
+    case 2: return __builtin_bit_cast(v2h, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2));
+    default: return __builtin_bit_cast(v2h, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3));
+  }
+}
+
+template <Out O>
+__device__ __forceinline__ uint16_t out_bits(float y) {
+  if constexpr (O == Out::BF16) return __builtin_bit_cast(uint16_t, (__bf16)y);
+  else return __builtin_bit_cast(uint16_t, (_Float16)y);
+}
+
+// Query row `row` (token first_token + row / group, head h * group + row % group) in the lanes of its
+// column (lane / 16 = g holds dims g D/4 .. (g+1) D/4 - 1) as fp16, and the base-2 score of one unit of
+// q . k as the products give it: keys decode times 2^-8, and bf16 rows are scaled so that their largest
+// magnitude lies in [2^14, 2^15), exact in fp16 down to 2^-39 of it.
+template <Out O, int D>
+__device__ __forceinline__ void load_query(const KvArgs& p, int first_token, int h, int row, int g, v8h q[D / 32], float& mul) {
+  constexpr int NJ = D / 32;
+  const int i = row / p.group, hq = row - i * p.group;
+  const uint16_t* src = (const uint16_t*)p.q.ptr + (int64_t)(first_token + i) * p.q.token_stride +
+                        (int64_t)(h * p.group + hq) * p.q.head_stride + g * (D / 4);
+  mul = p.score_mul * (kLog2e * 256.0f);
+  v4i w[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) w[j] = *(const v4i*)(src + 8 * j);
+  if constexpr (O == Out::F16) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) q[j] = __builtin_bit_cast(v8h, w[j]);
+  } else {
+    float f[NJ][8], most = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        f[j][2 * k] = __builtin_bit_cast(float, (uint32_t)w[j][k] << 16);
+        f[j][2 * k + 1] = __builtin_bit_cast(float, (uint32_t)w[j][k] & 0xFFFF0000u);
+        most = __builtin_fmaxf(most, __builtin_fmaxf(__builtin_fabsf(f[j][2 * k]), __builtin_fabsf(f[j][2 * k + 1])));
+      }
+    most = max_over_g(most);
+    const int e = (int)(__builtin_bit_cast(uint32_t, most) >> 23) - 127;  // -127 for zero and subnormals
+    const int up = e > 127 ? 0 : max(14 - e, -110);                       // inf or NaN: as it is
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) q[j][k] = (_Float16)__builtin_amdgcn_ldexpf(f[j][k], up);
+    mul = __builtin_amdgcn_ldexpf(mul, -up);
+  }
+}
+
+hipError_t kv_attend_rows_launch(const KvArgs& a, int dtype, int head_dim, int cus, hipStream_t stream);
+// Floats of parts that kv_attend_rows_launch may use.
+size_t kv_rows_part_floats(const bsg_kv_problem& p, int cus);
+
+}  // namespace bsg

@@ -26,67 +26,14 @@
 //
 // Bound: bytes of the cache (D 9/8 bytes per position and head).
 #include "handoff.h"
-#include "kv.h"
+#include "kv_attend.h"
 
 namespace bsg {
 namespace {
 
-typedef float v2f __attribute__((ext_vector_type(2)));
-
 constexpr int kThreads = 256;
-constexpr int kTile = 64;       // positions of a tile, and of a wave's step
 constexpr int kMinTiles = 4;    // a workgroup's run is at least one tile per wave
 constexpr int kWgPerCu = 2;
-constexpr float kPBias = 14.0f; // P is held as 2^14 P
-constexpr int kJoin = 16;       // parts joined at a time
-constexpr float kNegInf = -__builtin_inff();
-
-// Combine the four lanes of one row (lane % 16): each swap gives every lane its own value and its partner's.
-__device__ __forceinline__ void swap32(float x, float& a, float& b) {
-  const uint32_t u = __builtin_bit_cast(uint32_t, x);
-  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-  const uint32_t r0 = r[0], r1 = r[1];
-  a = __builtin_bit_cast(float, r0);
-  b = __builtin_bit_cast(float, r1);
-}
-__device__ __forceinline__ void swap16(float x, float& a, float& b) {
-  const uint32_t u = __builtin_bit_cast(uint32_t, x);
-  const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-  const uint32_t r0 = r[0], r1 = r[1];
-  a = __builtin_bit_cast(float, r0);
-  b = __builtin_bit_cast(float, r1);
-}
-__device__ __forceinline__ float max_over_g(float x) {
-  float a, b;
-  swap32(x, a, b);
-  swap16(__builtin_fmaxf(a, b), a, b);
-  return __builtin_fmaxf(a, b);
-}
-__device__ __forceinline__ float sum_over_g(float x) {
-  float a, b;
-  swap32(x, a, b);
-  swap16(a + b, a, b);
-  return a + b;
-}
-
-// Two non-negative E4M3 codes (bytes SEL picks) -> fp16 pair, times 2^-8; 0x7F -> NaN (0x3F80 + 0x80
-// carries into the bit that makes it one).
-template <uint32_t SEL>
-__device__ __forceinline__ uint32_t scale_pair(uint32_t w) {
-  const uint32_t t = __builtin_amdgcn_perm(0u, w, SEL) >> 1;
-  return t | ((t + 0x00800080u) & 0x40004000u);
-}
-constexpr uint32_t kLow = 0x010C000Cu, kHigh = 0x030C020Cu;  // bytes 0, 1 and bytes 2, 3
-
-__device__ __forceinline__ v2h fp4_pair(uint32_t w, int b) {
-  // the byte is an immediate of the instruction
-  switch (b) {
-    case 0: return __builtin_bit_cast(v2h, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0));
-    case 1: return __builtin_bit_cast(v2h, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1));
-    case 2: return __builtin_bit_cast(v2h, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2));
-    default: return __builtin_bit_cast(v2h, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3));
-  }
-}
 
 // What a unit covers.
 struct Span {
@@ -101,12 +48,6 @@ __device__ __forceinline__ Span span_of(const KvArgs& p, int b) {
   s.lo = p.window > 0 ? max(0, s.len - s.q_len - p.window + 1) & ~15 : 0;
   s.tiles = max(1, (s.len - s.lo + kTile - 1) / kTile);
   return s;
-}
-
-template <Out O>
-__device__ __forceinline__ uint16_t out_bits(float y) {
-  if constexpr (O == Out::BF16) return __builtin_bit_cast(uint16_t, (__bf16)y);
-  else return __builtin_bit_cast(uint16_t, (_Float16)y);
 }
 
 template <Out O, int D, int RT>
@@ -198,40 +139,9 @@ __global__ __launch_bounds__(kThreads) void few_kernel(KvArgs p) {
     int pos[RT];     // the row's position: it sees (pos - window, pos]
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-      const int r = 16 * t + c;
-      const bool ok = r < rows;
-      const int i = (rb * R + (ok ? r : 0)) / G, hq = (rb * R + (ok ? r : 0)) - i * G;
-      const uint16_t* src = (const uint16_t*)p.q.ptr + (int64_t)(first_token + i) * p.q.token_stride +
-                            (int64_t)(h * G + hq) * p.q.head_stride + g * (D / 4);
-      pos[t] = causal ? pos0 + i : s.len - 1;
-      mul[t] = p.score_mul * (1.44269504088896341f * 256.0f);
-      v4i w[NJ];
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) w[j] = *(const v4i*)(src + 8 * j);
-      if constexpr (O == Out::F16) {
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) q[t][j] = __builtin_bit_cast(v8h, w[j]);
-      } else {
-        // scale the row so that its largest magnitude lies in [2^14, 2^15): exact in fp16 down to
-        // 2^-39 of it
-        float f[NJ][8], most = 0.0f;
-#pragma unroll
-        for (int j = 0; j < NJ; ++j)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            f[j][2 * k] = __builtin_bit_cast(float, (uint32_t)w[j][k] << 16);
-            f[j][2 * k + 1] = __builtin_bit_cast(float, (uint32_t)w[j][k] & 0xFFFF0000u);
-            most = __builtin_fmaxf(most, __builtin_fmaxf(__builtin_fabsf(f[j][2 * k]), __builtin_fabsf(f[j][2 * k + 1])));
-          }
-        most = max_over_g(most);
-        const int e = (int)(__builtin_bit_cast(uint32_t, most) >> 23) - 127;  // -127 for zero and subnormals
-        const int up = e > 127 ? 0 : max(14 - e, -110);                       // inf or NaN: as it is
-#pragma unroll
-        for (int j = 0; j < NJ; ++j)
-#pragma unroll
-          for (int k = 0; k < 8; ++k) q[t][j][k] = (_Float16)__builtin_amdgcn_ldexpf(f[j][k], up);
-        mul[t] = __builtin_amdgcn_ldexpf(mul[t], -up);
-      }
+      const int r = 16 * t + c, row = rb * R + (r < rows ? r : 0);
+      load_query<O, D>(p, first_token, h, row, g, q[t], mul[t]);
+      pos[t] = causal ? pos0 + row / G : s.len - 1;
     }
 
     v4f o[RT][E];
@@ -578,13 +488,16 @@ hipError_t launch(const KvArgs& a, int cus, hipStream_t stream) {
 }  // namespace
 
 hipError_t kv_attend_launch(const KvArgs& a, int dtype, int head_dim, int cus, hipStream_t stream) {
+  if ((int64_t)a.max_q * a.group > 32) return kv_attend_rows_launch(a, dtype, head_dim, cus, stream);
   if (head_dim == 64) return dtype ? launch<Out::F16, 64>(a, cus, stream) : launch<Out::BF16, 64>(a, cus, stream);
   return dtype ? launch<Out::F16, 128>(a, cus, stream) : launch<Out::BF16, 128>(a, cus, stream);
 }
 
 void kv_workspace(const bsg_kv_problem& p, int cus, size_t* part_floats, size_t* counters, size_t* group_counters) {
   const size_t slots = (size_t)cus * kWgPerCu * 2;
+  const size_t rows = kv_rows_part_floats(p, cus);
   *part_floats = slots * 32 * (p.head_dim + 4);
+  if (*part_floats < rows) *part_floats = rows;
   *counters = slots + (size_t)p.max_tokens * p.q_heads;
   *group_counters = slots;
 }

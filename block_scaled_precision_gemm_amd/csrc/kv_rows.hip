@@ -1,0 +1,403 @@
+// Attention over the paged NVFP4 cache for many query rows per key/value head: prompt chunks.
+//
+// A workgroup holds R = 32 WAVES query rows (new tokens x the heads that share a key/value head) of one
+// sequence and walks the positions that they see in tiles of 64.  Each tile is decoded once by the
+// workgroup, from packed codes in registers to fp16 fragments in LDS, while the previous tile is
+// multiplied (two buffers, one barrier per tile).  Fragments are stored in the order in which the lanes
+// of a product read them, so every LDS access is 1 KB in a row:
+// * keys: 16 positions x 32 dims per fragment, S^T = K Q^T;
+// * values: 16 dims x 32 positions, O^T += V^T P^T, with P^T straight from S^T's registers.
+// The lane layouts, the softmax and the decoding are those of the few-row kernel (kv_attend.hip).  Each
+// wave keeps 32 rows, so a fragment read from LDS feeds two products.
+//
+// Workgroups that share a sequence and head follow each other at a distance of (sequences x heads), a
+// multiple of 8 for 8 heads, so that they run on one XCD and share its L2; the longest run first.  Where
+// the rows alone give too few workgroups, positions are split and the last workgroup of a row block
+// joins the parts.
+//
+// Bound: matrix products and the softmax's and decoding's vector operations, at similar rates.
+#include "handoff.h"
+#include "kv_attend.h"
+
+namespace bsg {
+namespace {
+
+template <Out O, int D, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
+  constexpr int RT = 2, R = 32 * WAVES;
+  constexpr int NJ = D / 32, E = D / 16;
+  constexpr int SLOT = R * (D + 4);
+  using L = PageLayout<D>;
+  struct Buffer {
+    v4i k[4][NJ][64];  // [16 positions][32 dims][lane]
+    v4i v[2][E][64];   // [32 positions][dims E m + e][lane]
+  };
+  __shared__ Buffer sh[2];
+  __shared__ int sh_nan[2], sh_last;  // sh_nan: the buffer's tile, if it has such a NaN block (below)
+
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int c = lane & 15, g = lane >> 4;
+  const int H = p.kv_heads, G = p.group, P = 1 << p.page_shift;
+  const bool causal = !(p.flags & BSG_KV_NONCAUSAL);
+
+  // ---- unit and split: x = ((block from the last) * splits + split) * sequences * heads + (sequence, head)
+  const int bh = blockIdx.x % (p.num_seqs * H), rest = blockIdx.x / (p.num_seqs * H);
+  const int b = bh / H, h = bh - b * H, split = rest % p.splits;
+  const int first_token = p.one_each ? b : seq_start(p, b);
+  const int len = seq_len(p, b);
+  const int q_len = p.one_each ? 1 : min(max(seq_start(p, b + 1) - first_token, 0), p.max_q);
+  const int blocks = (q_len * G + R - 1) / R, rb = blocks - 1 - rest / p.splits;
+  if (rb < 0) return;
+  const int rows = min(R, q_len * G - rb * R), pos0 = len - q_len;
+  const int i_first = rb * R / G, i_last = (rb * R + rows - 1) / G;
+  const int lo = p.window > 0 ? max(0, pos0 + i_first - p.window + 1) : 0;
+  const int hi = causal ? max(0, pos0 + i_last + 1) : len;
+  const int base = lo & ~15, all = hi > base ? (hi - base + kTile - 1) / kTile : 0;
+  const int per = (all + p.splits - 1) / p.splits;
+  const int t_begin = base + split * per * kTile, t_end = min(hi, t_begin + per * kTile);
+
+  // ---- queries
+  const int w_row = 32 * wave;  // the wave's first row
+  const bool busy = w_row < rows;
+  v8h q[RT][NJ];
+  float mul[RT];
+  int pos[RT];
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    const int r = w_row + 16 * t + c, row = rb * R + (r < rows ? r : 0);
+    load_query<O, D>(p, first_token, h, row, g, q[t], mul[t]);
+    pos[t] = causal ? pos0 + row / G : len - 1;
+  }
+  // positions that all, and any, of the wave's rows see up to
+  const int w_first = causal ? pos0 + (rb * R + min(w_row, rows - 1)) / G : len - 1;
+  const int w_last = causal ? pos0 + (rb * R + min(w_row + 31, rows - 1)) / G : len - 1;
+  // a scaled score is mul * s with mul > 0: the maximum is taken over the products themselves
+  const bool negative = p.score_mul < 0.0f;
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    if (negative)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) q[t][j] = -q[t][j];
+    mul[t] = __builtin_fmaxf(__builtin_fabsf(mul[t]), 1.17549435e-38f);
+  }
+
+  v4f o[RT][E];
+  float m[RT], l[RT];
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    m[t] = kNegInf;
+    l[t] = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[t][e] = v4f{0, 0, 0, 0};
+  }
+
+  if (t_begin < t_end) {
+    const int* table = p.pages + (int64_t)b * p.pages_stride;
+    const int last_pos = hi - 1, chunk = L::chunk(P);
+    // The tile's work is cut in 8 tasks: 0 .. 3 decode the values of positions 32 (task / 2) .. + 31 for
+    // even or odd dims, 4 .. 7 the keys of 16 positions each.  Wave w takes tasks w, w + WAVES, ...
+    constexpr bool kBoth = WAVES == 4;
+    const bool do_v = kBoth || wave < 4, do_k = kBoth || wave >= 4;
+    const int vt = wave & 3, kt = wave & 3;
+    uint32_t kq[NJ], ks = 0, vq[2][4], vs[2];
+    auto group_at = [&](int t, int& slot) -> const uint8_t* {
+      t = min(t, last_pos & ~15);
+      slot = t & (P - 1);
+      const int page = __builtin_amdgcn_readfirstlane(clamp_page(p, table[t >> p.page_shift]));
+      return p.cache + (int64_t)page * p.page_stride + (int64_t)h * chunk;
+    };
+    auto load = [&](int t0) {
+      if (do_v) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          int slot;
+          const uint8_t* at = group_at(t0 + 32 * (vt >> 1) + 16 * u, slot);
+          const uint8_t* vp = at + L::v_codes(P) + (slot + 4 * g) * L::kRow + c * (E / 2);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            vq[u][j] = E == 8 ? *(const uint32_t*)(vp + j * L::kRow) : *(const uint16_t*)(vp + j * L::kRow);
+          vs[u] = *(const uint32_t*)(at + L::v_scales(P) + (c * E / 16) * P + slot + 4 * g);
+        }
+      }
+      if (do_k) {
+        int slot;
+        const uint8_t* at = group_at(t0 + 16 * kt, slot);
+        const uint8_t* kp = at + (slot + c) * L::kRow + g * (4 * NJ);
+        if constexpr (D == 128) {
+          const v4i w = *(const v4i*)kp;
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) kq[j] = (uint32_t)w[j];
+          ks = *(const uint16_t*)(at + L::k_scales(P) + (slot + c) * L::kBlocks + 2 * g);
+        } else {
+          const uint2 w = *(const uint2*)kp;
+          kq[0] = w.x;
+          kq[1] = w.y;
+          ks = at[L::k_scales(P) + (slot + c) * L::kBlocks + g];
+        }
+      }
+    };
+    // some row of the workgroup does not see all of the tile at t0
+    const int all_first = causal ? pos0 + i_first : len - 1, any_last = causal ? pos0 + i_last : len - 1;
+    auto partly_hidden = [&](int t0) {
+      return t0 + kTile - 1 > min(all_first, t_end - 1) || (p.window > 0 && t0 <= any_last - p.window);
+    };
+    auto decode = [&](int t0, int buf) {
+      if (do_v) {
+        if (partly_hidden(t0)) {
+          // positions outside the workgroup's count as zero, whatever their slots hold; NaN blocks that
+          // only some rows see are taken out and given to those rows by the waves
+          uint32_t bad = 0;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            uint32_t keep = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int at = t0 + 32 * (vt >> 1) + 16 * u + 4 * g + i;
+              if (at >= lo && at < t_end) keep |= 0xFFu << (8 * i);
+            }
+            vs[u] &= keep;
+            const uint32_t hit = ((vs[u] + 0x01010101u) & 0x80808080u) >> 7;
+            bad |= hit;
+            vs[u] &= ~(hit * 0x7Fu);
+          }
+          if (__any(bad) && lane == 0) sh_nan[buf] = t0;
+        }
+        const int odd = vt & 1;
+        v4i frag[E / 2];
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj) {
+          const int u = jj / 2, j = (jj & 1) * 2;
+          const v2h s2 = __builtin_bit_cast(v2h, (jj & 1) ? scale_pair<kHigh>(vs[u]) : scale_pair<kLow>(vs[u]));
+          const uint32_t a = vq[u][j], bb = vq[u][j + 1], mask = 0x0F0F0F0Fu;
+          const uint32_t pairs = odd ? ((a >> 4) & mask) | (bb & ~mask) : (a & mask) | ((bb << 4) & ~mask);
+#pragma unroll
+          for (int e = 0; e < E / 2; ++e) frag[e][jj] = __builtin_bit_cast(int, fp4_pair(pairs, e) * s2);
+        }
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) sh[buf].v[vt >> 1][2 * e + odd][lane] = frag[e];
+      }
+      if (do_k) {
+        const uint32_t sp = scale_pair<kLow>(ks), sp0 = f16x2_splat_lo(sp), sp1 = f16x2_splat_hi(sp);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) sh[buf].k[kt][j][lane] = e2m1x8_scaled_f16x8(kq[j], j < 2 ? sp0 : sp1);
+      }
+    };
+    if (tid < 2) sh_nan[tid] = -1;
+    load(t_begin);
+    __syncthreads();
+    decode(t_begin, 0);
+    load(t_begin + kTile);  // (clamped into the context)
+    __syncthreads();
+    int buf = 0;
+    for (int t0 = t_begin; t0 < t_end; t0 += kTile, buf ^= 1) {
+      const bool mine = busy && t0 <= w_last && !(p.window > 0 && t0 + kTile - 1 <= w_first - p.window);
+      v4f sc[RT][4];
+      if (mine) {
+#pragma unroll
+        for (int gr = 0; gr < 4; ++gr)
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            const v8h a = __builtin_bit_cast(v8h, sh[buf].k[gr][j][lane]);
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+              sc[t][gr] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, q[t][j], j ? sc[t][gr] : v4f{0, 0, 0, 0}, 0, 0, 0);
+          }
+      }
+      if (t0 + kTile < t_end) {
+        decode(t0 + kTile, buf ^ 1);
+        if (t0 + 2 * kTile < t_end) load(t0 + 2 * kTile);
+      }
+      if (mine) {
+        const bool edge = t0 + kTile - 1 > min(w_first, t_end - 1) || (p.window > 0 && t0 <= w_last - p.window);
+        v8h pt[RT][2];
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+          float scale = mul[t];
+          if (p.softcap > 0.0f) {
+            const float cap = p.softcap * kLog2e, inv = 2.0f / p.softcap * mul[t];  // tanh(y) = 1 - 2 / (e^2y + 1)
+            scale = 1.0f;
+#pragma unroll
+            for (int gr = 0; gr < 4; ++gr)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                sc[t][gr][i] = cap - 2.0f * cap * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(sc[t][gr][i] * inv) + 1.0f);
+          }
+          if (edge) {
+            const int top = min(pos[t], t_end - 1), bottom = p.window > 0 ? pos[t] - p.window : -1;
+#pragma unroll
+            for (int gr = 0; gr < 4; ++gr)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int at = t0 + 16 * gr + 4 * g + i;
+                sc[t][gr][i] = at <= top && at > bottom ? sc[t][gr][i] : kNegInf;
+              }
+          }
+          float top = sc[t][0][0];
+#pragma unroll
+          for (int gr = 0; gr < 4; ++gr)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = __builtin_fmaxf(top, sc[t][gr][i]);
+          if (__any(top > m[t])) {  // m: maximum of the products
+            const float grown = __builtin_fmaxf(m[t], max_over_g(top));
+            const float f = grown == kNegInf ? 1.0f : __builtin_amdgcn_exp2f((m[t] - grown) * scale);
+            m[t] = grown;
+            l[t] *= f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[t][e] *= f;
+          }
+          const float off = m[t] == kNegInf ? 0.0f : kPBias - m[t] * scale;
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              float e4[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                e4[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][2 * k + half][i], scale, off));
+                l[t] += e4[i];
+              }
+              const v2h x = __builtin_convertvector((v2f{e4[0], e4[1]}), v2h), y = __builtin_convertvector((v2f{e4[2], e4[3]}), v2h);
+              pt[t][k][4 * half] = x[0];
+              pt[t][k][4 * half + 1] = x[1];
+              pt[t][k][4 * half + 2] = y[0];
+              pt[t][k][4 * half + 3] = y[1];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const v8h a = __builtin_bit_cast(v8h, sh[buf].v[k][e][lane]);
+#pragma unroll
+            for (int t = 0; t < RT; ++t) o[t][e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pt[t][k], o[t][e], 0, 0, 0);
+          }
+        if (__builtin_amdgcn_readfirstlane(sh_nan[buf]) == t0) {
+          // rare: a NaN block among positions that not every row sees.  Output element i of tile e is
+          // dim E (4g + i) + e, so element i lies in block E (4g + i) / 16.
+          for (int at = max(t0, lo); at < min(t0 + kTile, t_end); ++at) {
+            const int page = clamp_page(p, table[at >> p.page_shift]), sl = at & (P - 1);
+            const uint8_t* codes = p.cache + (int64_t)page * p.page_stride + (int64_t)h * chunk + L::v_scales(P) + sl;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const bool bad = codes[E * (4 * g + i) / 16 * P] == 0x7F;
+#pragma unroll
+              for (int t = 0; t < RT; ++t)
+                if (bad && at <= pos[t] && (p.window <= 0 || at > pos[t] - p.window))
+#pragma unroll
+                  for (int e = 0; e < E; ++e) o[t][e][i] = __builtin_nanf("");
+            }
+          }
+        }
+      }
+      __syncthreads();
+    }
+  }
+
+  // ---- results
+  const __amdgpu_buffer_rsrc_t parts = handoff_buffer(p.part, (uint32_t)gridDim.x * SLOT * 4u);
+  auto store_lse = [&](int row, float top, float sum) {
+    const int i = (rb * R + row) / G, hq = rb * R + row - i * G;
+    p.lse[(int64_t)(first_token + i) * p.q_heads + h * G + hq] =
+        sum == 0.0f ? kNegInf : (top - kPBias + __builtin_amdgcn_logf(sum)) * kLn2;
+  };
+  auto out_at = [&](int row, int d) {
+    const int i = (rb * R + row) / G, hq = rb * R + row - i * G;
+    return (uint16_t*)p.out.ptr + (int64_t)(first_token + i) * p.out.token_stride + (int64_t)(h * G + hq) * p.out.head_stride + d;
+  };
+  auto pack4 = [&](v4f y, float f, bool none) {
+    uint32_t bits[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bits[i] = out_bits<O>(none ? 0.0f : y[i] * f);
+    return make_uint2(bits[0] | bits[1] << 16, bits[2] | bits[3] << 16);
+  };
+  const uint32_t slot0 = (uint32_t)(blockIdx.x) * SLOT;  // of this split; the next one's is sequences * heads slots on
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    const int r = w_row + 16 * t + c;
+    const float sum = sum_over_g(l[t]), top = m[t] == kNegInf ? kNegInf : p.softcap > 0.0f ? m[t] : m[t] * mul[t];
+    if (r >= rows) continue;
+    if (p.splits == 1) {
+      const float f = p.v_scale * 256.0f / sum;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint16_t* dst = out_at(r, E * (4 * g + i));
+#pragma unroll
+        for (int e = 0; e < E; e += 4)
+          *(uint2*)(dst + e) = pack4(v4f{o[t][e][i], o[t][e + 1][i], o[t][e + 2][i], o[t][e + 3][i]}, f, sum == 0.0f);
+      }
+      if (p.lse && g == 0) store_lse(r, top, sum);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < E; e += 4)
+          handoff_store4(parts, slot0 + r * D + E * (4 * g + i) + e, v4f{o[t][e][i], o[t][e + 1][i], o[t][e + 2][i], o[t][e + 3][i]});
+      if (g == 0) handoff_store4(parts, slot0 + R * D + 4 * r, v4f{top, sum, 0.0f, 0.0f});
+    }
+  }
+  if (p.splits == 1) return;
+  int* counter = p.arrived + ((int64_t)first_token * G + (int64_t)rb * R) * H + h;
+  if (!last_arrival(counter, p.splits, &sh_last)) return;
+  const uint32_t first_slot = (uint32_t)(blockIdx.x - split * p.num_seqs * H);
+  for (int k = tid; k < rows * (D / 4); k += 64 * WAVES) {
+    const int r = k / (D / 4), d = k % (D / 4) * 4;
+    v4f ms[kJoin], ys[kJoin];
+#pragma unroll
+    for (int i = 0; i < kJoin; ++i) {  // all in flight; splits past the last repeat it and count nothing
+      const uint32_t at = (first_slot + (uint32_t)(min(i, p.splits - 1) * p.num_seqs * H)) * SLOT;
+      ms[i] = handoff_load4(parts, at + R * D + 4 * r);
+      ys[i] = handoff_load4(parts, at + r * D + d);
+    }
+    float top = kNegInf, sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kJoin; ++i) top = __builtin_fmaxf(top, ms[i][0]);
+    v4f y = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < kJoin; ++i)
+      if (i < p.splits) {
+        const float f = ms[i][0] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(ms[i][0] - top);
+        sum += f * ms[i][1];
+        y += f * ys[i];
+      }
+    *(uint2*)out_at(r, d) = pack4(y, p.v_scale * 256.0f / sum, sum == 0.0f);
+    if (p.lse && d == 0) store_lse(r, top, sum);
+  }
+}
+
+// Rows of a workgroup: 8 waves halve the decoding per row; 4 where no sequence fills more.
+int rows_waves(int64_t max_rows) { return max_rows > 128 ? 8 : 4; }
+
+template <Out O, int D>
+hipError_t launch(const KvArgs& a, int cus, hipStream_t stream) {
+  KvArgs args = a;
+  const int waves = rows_waves((int64_t)a.max_q * a.group), R = 32 * waves;
+  const int64_t blocks = ((int64_t)a.max_q * a.group + R - 1) / R, groups = (int64_t)a.num_seqs * a.kv_heads;
+  // units that exist, at most: ragged sequences leave some of the grid's without rows
+  int64_t units = ((int64_t)a.num_tokens * a.group / R + a.num_seqs) * a.kv_heads;
+  if (units > blocks * groups) units = blocks * groups;
+  const int64_t fill = (int64_t)cus * (8 / waves);  // workgroups that run at once
+  const int64_t tiles = ((int64_t)(a.window > 0 && a.window + a.max_q < a.max_kv ? a.window + a.max_q : a.max_kv) + kTile - 1) / kTile;
+  int64_t splits = (fill + units - 1) / units;
+  if (splits > tiles / 4) splits = tiles / 4;  // at least four tiles each
+  if (splits > kJoin) splits = kJoin;
+  if (splits < 1) splits = 1;
+  while (splits > 1 && blocks * groups * splits > 2 * fill) --splits;  // (the workspace's slots)
+  args.splits = (int)splits;
+  void* argv[] = {&args};
+  const void* fn = waves == 8 ? (const void*)&rows_kernel<O, D, 8> : (const void*)&rows_kernel<O, D, 4>;
+  return hipLaunchKernel(fn, dim3((unsigned)(blocks * groups * splits)), dim3(64 * waves), argv, 0, stream);
+}
+
+}  // namespace
+
+hipError_t kv_attend_rows_launch(const KvArgs& a, int dtype, int head_dim, int cus, hipStream_t stream) {
+  if (head_dim == 64) return dtype ? launch<Out::F16, 64>(a, cus, stream) : launch<Out::BF16, 64>(a, cus, stream);
+  return dtype ? launch<Out::F16, 128>(a, cus, stream) : launch<Out::BF16, 128>(a, cus, stream);
+}
+
+size_t kv_rows_part_floats(const bsg_kv_problem& p, int cus) {
+  if (p.max_tokens * (p.q_heads / p.kv_heads) <= 32) return 0;
+  return (size_t)2 * cus * 256 * (p.head_dim + 4);  // 2 x 8 waves per CU, 32 rows each
+}
+
+}  // namespace bsg
