@@ -51,7 +51,7 @@ __device__ __forceinline__ Span span_of(const KvArgs& p, int b) {
 }
 
 template <Out O, int D, int RT>
-__global__ __launch_bounds__(kThreads) void few_kernel(KvArgs p) {
+__global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
   constexpr int R = 16 * RT;
   constexpr int NJ = D / 32;       // k steps of Q K^T; dwords of K codes a lane loads per position
   constexpr int E = D / 16;        // dims of a lane in V; output tiles
