@@ -1,15 +1,16 @@
 // Attention over the paged NVFP4 cache for few query rows per key/value head.
 //
 // A unit of work is a block of R = 16 RT query rows (new tokens x the query heads that share a
-// key/value head) of one sequence and key/value head, over that sequence's positions.  Positions are
-// cut into tiles of 64; the tiles of all units form one line, and each workgroup takes an equal run of
-// it, whatever the contexts' lengths.  A unit whose tiles lie in several workgroups is joined by the
-// last of them to finish, in the workgroups' order, from partial results (output, maximum, sum) that
-// the others left in the plan's workspace.  So one launch balances any mixture of lengths, and the
-// order of every sum is fixed.
+// key/value head) of one sequence and key/value head, over that sequence's positions, which are cut into
+// tiles of 64.  Where there are few units each is cut into pieces, one per workgroup, all about as long;
+// where there are many, the tiles of all units, and a fixed cost for each unit, form one line, and each
+// workgroup takes an equal run of it.  Either way one launch balances any mixture of lengths.  A unit
+// that lies in several workgroups is joined by the last of them to finish, in the workgroups' order, from
+// the parts (output, maximum, sum) that the others left in the plan's workspace, so the order of every
+// sum is fixed.
 //
 // Inside a workgroup the four waves take consecutive quarters of a run and are joined through LDS.  A
-// wave handles 64 positions at a time, everything in registers:
+// wave handles 32 positions at a time, everything in registers, while the next two steps' codes arrive:
 // * S^T = K Q^T on v_mfma_f32_16x16x32_f16: a lane loads D/4 consecutive dims of one position (16
 //   bytes for D = 128) -- the k order of the product is free, so those are its k values.  K is decoded
 //   exactly (codec.h); Q is exact in fp16 once each row is scaled by a power of two (bf16 rows).
@@ -32,7 +33,10 @@ namespace bsg {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMinTiles = 4;    // a workgroup's run is at least one tile per wave
+constexpr int kMinTiles = 2;    // a piece is at least a step of each wave
+// What a unit costs a workgroup besides its tiles, in tiles: queries, the pipeline's filling, joining the
+// waves (measured with 64 contexts up to 16384: 10 us for each further unit of a run, 0.7 us per tile).
+constexpr int kUnitCost = 12;
 constexpr int kWgPerCu = 2;
 
 // What a unit covers.
@@ -53,6 +57,8 @@ __device__ __forceinline__ Span span_of(const KvArgs& p, int b) {
 template <Out O, int D, int RT>
 __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
   constexpr int R = 16 * RT;
+  constexpr int NG = 2, DEPTH = 2;   // groups of 16 positions in a wave's step, steps in flight
+  constexpr int kStep = 16 * NG;
   constexpr int NJ = D / 32;       // k steps of Q K^T; dwords of K codes a lane loads per position
   constexpr int E = D / 16;        // dims of a lane in V; output tiles
   constexpr int OS = D + 4;        // LDS row of the joining buffer (padded)
@@ -60,46 +66,71 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
   using L = PageLayout<D>;
   __shared__ float sh_o[4][R][OS];
   __shared__ float sh_m[4][R], sh_l[4][R];
-  __shared__ int sh_sum[4], sh_at[2], sh_last;
+  __shared__ int sh_sum[2][4], sh_at[2], sh_last;
 
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int c = lane & 15, g = lane >> 4;
   const int H = p.kv_heads, G = p.group;
   const int P = 1 << p.page_shift;
 
-  // ---- this workgroup's run of the line of tiles
+  // ---- how the work is divided: all threads look at the sequences together
   const int per_thread = (p.num_seqs + kThreads - 1) / kThreads;
+  auto block_sums = [&](int a, int b2, int& sum_a, int& sum_b, int& before) {  // and a's sum over earlier threads
+    int incl = a;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int y = __shfl_up(incl, o), z = __shfl_xor(b2, o);
+      if (lane >= o) incl += y;
+      b2 += z;
+    }
+    if (lane == 63) sh_sum[0][wave] = incl, sh_sum[1][wave] = b2;
+    __syncthreads();
+    sum_a = sum_b = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      if (w < wave) incl += sh_sum[0][w];
+      sum_a += sh_sum[0][w];
+      sum_b += sh_sum[1][w];
+    }
+    before = incl - a;
+    __syncthreads();
+  };
+  int tiles = 0, units = 0;
+  for (int i = 0; i < per_thread; ++i) {
+    const int b = tid * per_thread + i;
+    if (b < p.num_seqs) {
+      const Span s = span_of(p, b);
+      const int n = (s.q_len * G + R - 1) / R * H;
+      tiles += n * s.tiles;
+      units += n;
+    }
+  }
+  int all_tiles, all_units, before;
+  block_sums(tiles, units, all_tiles, all_units, before);
+  // Few units: each is cut in pieces of about `piece` tiles, one piece per workgroup.  Many: their tiles
+  // and kUnitCost more for each form one line, of which every workgroup takes an equal run.
+  const bool pieces = 2 * all_units <= (int)gridDim.x;
+  const int piece = pieces ? max(kMinTiles, (all_tiles + (int)gridDim.x - all_units - 1) / ((int)gridDim.x - all_units)) : 1;
+  auto items = [&](const Span& s) { return pieces ? (s.tiles + piece - 1) / piece : s.tiles + kUnitCost; };
   int mine = 0;
   for (int i = 0; i < per_thread; ++i) {
     const int b = tid * per_thread + i;
     if (b < p.num_seqs) {
       const Span s = span_of(p, b);
-      mine += (s.q_len * G + R - 1) / R * H * s.tiles;
+      mine += (s.q_len * G + R - 1) / R * H * items(s);
     }
   }
-  int incl = mine;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int y = __shfl_up(incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 63) sh_sum[wave] = incl;
-  __syncthreads();
-  int total = 0;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    if (w < wave) incl += sh_sum[w];
-    total += sh_sum[w];
-  }
-  const int per = max(kMinTiles, (total + (int)gridDim.x - 1) / (int)gridDim.x);
+  int total, unused;
+  block_sums(mine, 0, total, unused, before);
+  const int per = pieces ? 1 : (total + (int)gridDim.x - 1) / (int)gridDim.x;
   const int run0 = blockIdx.x * per;
   if (run0 >= total) return;
   const int run1 = min(run0 + per, total);
-  if (incl - mine <= run0 && run0 < incl) {  // the one thread whose sequences hold the run's start
-    int at = incl - mine, b = tid * per_thread;
+  if (before <= run0 && run0 < before + mine) {  // the one thread whose sequences hold the run's start
+    int at = before, b = tid * per_thread;
     for (;; ++b) {
       const Span s = span_of(p, b);
-      const int n = (s.q_len * G + R - 1) / R * H * s.tiles;
+      const int n = (s.q_len * G + R - 1) / R * H * items(s);
       if (run0 < at + n) break;
       at += n;
     }
@@ -108,21 +139,30 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
   }
   __syncthreads();
   int b = __builtin_amdgcn_readfirstlane(sh_at[0]);
-  int seq0 = __builtin_amdgcn_readfirstlane(sh_at[1]);  // line position of sequence b's first tile
+  int seq0 = __builtin_amdgcn_readfirstlane(sh_at[1]);  // line position of sequence b's first item
 
   for (int x = run0; x < run1;) {
     Span s = span_of(p, b);
-    int blocks = (s.q_len * G + R - 1) / R;
-    while (x >= seq0 + blocks * H * s.tiles) {
-      seq0 += blocks * H * s.tiles;
+    int blocks = (s.q_len * G + R - 1) / R, len = items(s);
+    while (x >= seq0 + blocks * H * len) {
+      seq0 += blocks * H * len;
       ++b;
       s = span_of(p, b);
       blocks = (s.q_len * G + R - 1) / R;
+      len = items(s);
     }
-    const int unit = (x - seq0) / s.tiles;
-    const int u0 = seq0 + unit * s.tiles, u1 = u0 + s.tiles;  // the unit's tiles on the line
+    const int unit = (x - seq0) / len;
+    const int u0 = seq0 + unit * len, u1 = u0 + len;  // the unit's items on the line
     const int rb = unit / H, h = unit - rb * H;
     const int x1 = min(run1, u1);
+    const int real = pieces ? u0 : u0 + kUnitCost;  // the first item that is work
+    if (x1 <= real) {
+      x = x1;
+      continue;
+    }
+    // its tiles here
+    const int tile0 = pieces ? (x - u0) * s.tiles / len : max(x - real, 0);
+    const int tile1 = pieces ? (x1 - u0) * s.tiles / len : x1 - real;
     const int first_token = p.one_each ? b : seq_start(p, b);
     const int rows = min(R, s.q_len * G - rb * R);
     const bool causal = !(p.flags & BSG_KV_NONCAUSAL);
@@ -131,7 +171,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
     const int i_first = rb * R / G, i_last = (rb * R + rows - 1) / G;
     const int lo = p.window > 0 ? max(0, pos0 + i_first - p.window + 1) : 0;
     const int hi = causal ? max(0, pos0 + i_last + 1) : s.len;
-    const int s0 = max(s.lo + (x - u0) * kTile, lo & ~15), s1 = min(s.lo + (x1 - u0) * kTile, hi);
+    const int s0 = max(s.lo + tile0 * kTile, lo & ~15), s1 = min(s.lo + tile1 * kTile, hi);
 
     // ---- queries
     v8h q[RT][NJ];
@@ -142,6 +182,11 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
       const int r = 16 * t + c, row = rb * R + (r < rows ? r : 0);
       load_query<O, D>(p, first_token, h, row, g, q[t], mul[t]);
       pos[t] = causal ? pos0 + row / G : s.len - 1;
+      // a scaled score is mul * s with mul > 0: the maximum is taken over the products themselves
+      if (p.score_mul < 0.0f)
+#pragma unroll
+        for (int k = 0; k < NJ; ++k) q[t][k] = -q[t][k];
+      mul[t] = __builtin_fmaxf(__builtin_fabsf(mul[t]), 1.17549435e-38f);
     }
 
     v4f o[RT][E];
@@ -155,94 +200,77 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
     }
 
     // ---- this wave's positions
-    const int steps = s1 > s0 ? (s1 - s0 + kTile - 1) / kTile : 0;
+    const int steps = s1 > s0 ? (s1 - s0 + kStep - 1) / kStep : 0;
     const int per_wave = (steps + 3) / 4;
-    const int w0 = s0 + wave * per_wave * kTile, w1 = min(s1, w0 + per_wave * kTile);
+    const int w0 = s0 + wave * per_wave * kStep, w1 = min(s1, w0 + per_wave * kStep);
     if (w0 < w1) {
       const int* table = p.pages + (int64_t)b * p.pages_stride;
       const int last_pos = hi - 1;
       int page_base = w0 >> p.page_shift;
       int page_ids = clamp_page(p, table[min(page_base + lane, last_pos >> p.page_shift)]);
       const int chunk = L::chunk(P);
-      // chunk of the 16 positions at t (clamped into the context), and their first slot
-      auto group_at = [&](int t, int& slot) -> const uint8_t* {
-        t = min(t, last_pos & ~15);
-        const int page = t >> p.page_shift;
-        if (page - page_base >= 64) {
-          page_base = page;
-          page_ids = clamp_page(p, table[min(page_base + lane, last_pos >> p.page_shift)]);
+      // a step's codes: NG groups of 16 positions, DEPTH steps in flight
+      uint32_t kq[DEPTH][NG][NJ], ks[DEPTH][NG], vq[DEPTH][NG][4], vs[DEPTH][NG];
+      auto load = [&](int d, int t0) {
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) {
+          const int t = min(t0 + 16 * gr, last_pos & ~15);  // (clamped into the context)
+          const int page = t >> p.page_shift;
+          if (page - page_base >= 64) {
+            page_base = page;
+            page_ids = clamp_page(p, table[min(page_base + lane, last_pos >> p.page_shift)]);
+          }
+          const int slot = t & (P - 1);
+          const uint8_t* at = p.cache + (int64_t)__builtin_amdgcn_readlane(page_ids, page - page_base) * p.page_stride +
+                              (int64_t)h * chunk;
+          const uint8_t* kp = at + (slot + c) * L::kRow + g * (4 * NJ);
+          if constexpr (D == 128) {
+            const v4i w = *(const v4i*)kp;
+#pragma unroll
+            for (int k = 0; k < NJ; ++k) kq[d][gr][k] = (uint32_t)w[k];
+            ks[d][gr] = *(const uint16_t*)(at + L::k_scales(P) + (slot + c) * L::kBlocks + 2 * g);
+          } else {
+            const uint2 w = *(const uint2*)kp;
+            kq[d][gr][0] = w.x;
+            kq[d][gr][1] = w.y;
+            ks[d][gr] = at[L::k_scales(P) + (slot + c) * L::kBlocks + g];
+          }
+          const uint8_t* vp = at + L::v_codes(P) + (slot + 4 * g) * L::kRow + c * (E / 2);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            vq[d][gr][k] = E == 8 ? *(const uint32_t*)(vp + k * L::kRow) : *(const uint16_t*)(vp + k * L::kRow);
+          vs[d][gr] = *(const uint32_t*)(at + L::v_scales(P) + (c * E / 16) * P + slot + 4 * g);
         }
-        slot = t & (P - 1);
-        return p.cache + (int64_t)__builtin_amdgcn_readlane(page_ids, page - page_base) * p.page_stride +
-               (int64_t)h * chunk;
       };
-      uint32_t kq[4][NJ], ks[4], vq[4][4], vs[4];
-      auto load_k = [&](int gr, const uint8_t* base, int slot) {
-        const uint8_t* kp = base + (slot + c) * L::kRow + g * (4 * NJ);
-        if constexpr (D == 128) {
-          const v4i w = *(const v4i*)kp;
-#pragma unroll
-          for (int j = 0; j < NJ; ++j) kq[gr][j] = (uint32_t)w[j];
-          ks[gr] = *(const uint16_t*)(base + L::k_scales(P) + (slot + c) * L::kBlocks + 2 * g);
-        } else {
-          const uint2 w = *(const uint2*)kp;
-          kq[gr][0] = w.x;
-          kq[gr][1] = w.y;
-          ks[gr] = base[L::k_scales(P) + (slot + c) * L::kBlocks + g];
-        }
-      };
-      auto load_v = [&](int gr, const uint8_t* base, int slot) {
-        const uint8_t* vp = base + L::v_codes(P) + (slot + 4 * g) * L::kRow + c * (E / 2);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          vq[gr][j] = E == 8 ? *(const uint32_t*)(vp + j * L::kRow) : *(const uint16_t*)(vp + j * L::kRow);
-        vs[gr] = *(const uint32_t*)(base + L::v_scales(P) + (c * E / 16) * P + slot + 4 * g);
-      };
-      const uint8_t* base[4];
-      int slot[4];
-#pragma unroll
-      for (int gr = 0; gr < 4; ++gr) {
-        base[gr] = group_at(w0 + 16 * gr, slot[gr]);
-        load_k(gr, base[gr], slot[gr]);
-        load_v(gr, base[gr], slot[gr]);
-      }
-      for (int t0 = w0; t0 < w1; t0 += kTile) {
-        const bool more = t0 + kTile < w1;
+      const int first_pos = causal ? pos0 + i_first : s.len - 1, last_row_pos = causal ? pos0 + i_last : s.len - 1;
+      auto step = [&](int d, int t0) {
         // -- scores
-        v4f sc[RT][4];
+        v4f sc[RT][NG];
 #pragma unroll
-        for (int gr = 0; gr < 4; ++gr) {
-          const uint32_t sp = scale_pair<kLow>(ks[gr]);
+        for (int gr = 0; gr < NG; ++gr) {
+          const uint32_t sp = scale_pair<kLow>(ks[d][gr]);
           const uint32_t sp0 = f16x2_splat_lo(sp), sp1 = f16x2_splat_hi(sp);
 #pragma unroll
           for (int t = 0; t < RT; ++t) sc[t][gr] = v4f{0, 0, 0, 0};
 #pragma unroll
-          for (int j = 0; j < NJ; ++j) {
-            const v8h a = __builtin_bit_cast(v8h, e2m1x8_scaled_f16x8(kq[gr][j], j < 2 ? sp0 : sp1));
+          for (int k = 0; k < NJ; ++k) {
+            const v8h a = __builtin_bit_cast(v8h, e2m1x8_scaled_f16x8(kq[d][gr][k], k < 2 ? sp0 : sp1));
 #pragma unroll
             for (int t = 0; t < RT; ++t)
-              sc[t][gr] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, q[t][j], sc[t][gr], 0, 0, 0);
+              sc[t][gr] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, q[t][k], sc[t][gr], 0, 0, 0);
           }
         }
-        if (more) {
-#pragma unroll
-          for (int gr = 0; gr < 4; ++gr) {
-            base[gr] = group_at(t0 + kTile + 16 * gr, slot[gr]);
-            load_k(gr, base[gr], slot[gr]);
-          }
-        }
-        // -- masks: only where a row does not see the whole tile
-        const int first_pos = causal ? pos0 + i_first : s.len - 1;
-        const int last_row_pos = causal ? pos0 + i_last : s.len - 1;
-        const bool edge = t0 + kTile - 1 > min(first_pos, w1 - 1) || (p.window > 0 && t0 <= last_row_pos - p.window);
+        // -- masks: only where a row does not see the whole step
+        const bool edge = t0 + kStep - 1 > min(first_pos, w1 - 1) || (p.window > 0 && t0 <= last_row_pos - p.window);
+        float scale[RT];
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-#pragma unroll
-          for (int gr = 0; gr < 4; ++gr) sc[t][gr] = sc[t][gr] * mul[t];
+          scale[t] = mul[t];
           if (p.softcap > 0.0f) {
-            const float cap = p.softcap * 1.44269504088896341f, inv = 2.0f / p.softcap;  // tanh(y) = 1 - 2 / (e^2y + 1)
+            const float cap = p.softcap * kLog2e, inv = 2.0f / p.softcap * mul[t];  // tanh(y) = 1 - 2 / (e^2y + 1)
+            scale[t] = 1.0f;
 #pragma unroll
-            for (int gr = 0; gr < 4; ++gr)
+            for (int gr = 0; gr < NG; ++gr)
 #pragma unroll
               for (int i = 0; i < 4; ++i)
                 sc[t][gr][i] = cap - 2.0f * cap * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(sc[t][gr][i] * inv) + 1.0f);
@@ -250,7 +278,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
           if (edge) {
             const int top = min(pos[t], w1 - 1), bottom = p.window > 0 ? pos[t] - p.window : -1;
 #pragma unroll
-            for (int gr = 0; gr < 4; ++gr)
+            for (int gr = 0; gr < NG; ++gr)
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const int at = t0 + 16 * gr + 4 * g + i;
@@ -264,45 +292,45 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
           // some rows only are taken out here and given to those rows below
           const int from = max(lo, w0), to = w1;
 #pragma unroll
-          for (int gr = 0; gr < 4; ++gr) {
+          for (int gr = 0; gr < NG; ++gr) {
             uint32_t keep = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int at = t0 + 16 * gr + 4 * g + i;
               if (at >= from && at < to) keep |= 0xFFu << (8 * i);
             }
-            vs[gr] &= keep;
-            const uint32_t bad = ((vs[gr] + 0x01010101u) & 0x80808080u) >> 7;  // 1 in each byte that is 0x7F
+            vs[d][gr] &= keep;
+            const uint32_t bad = ((vs[d][gr] + 0x01010101u) & 0x80808080u) >> 7;  // 1 in each byte that is 0x7F
             nan_codes |= bad;
-            vs[gr] &= ~(bad * 0x7Fu);
+            vs[d][gr] &= ~(bad * 0x7Fu);
           }
         }
         // -- softmax
-        v8h pt[RT][2];
+        v8h pt[RT][NG / 2];
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
           float top = sc[t][0][0];
 #pragma unroll
-          for (int gr = 0; gr < 4; ++gr)
+          for (int gr = 0; gr < NG; ++gr)
 #pragma unroll
             for (int i = 0; i < 4; ++i) top = __builtin_fmaxf(top, sc[t][gr][i]);
-          if (__any(top > m[t])) {
+          if (__any(top > m[t])) {  // m: maximum of the products, in units of 1 / scale
             const float grown = __builtin_fmaxf(m[t], max_over_g(top));
-            const float f = grown == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m[t] - grown);
+            const float f = grown == kNegInf ? 1.0f : __builtin_amdgcn_exp2f((m[t] - grown) * scale[t]);
             m[t] = grown;
             l[t] *= f;
 #pragma unroll
             for (int e = 0; e < E; ++e) o[t][e] *= f;
           }
-          const float off = m[t] == kNegInf ? 0.0f : m[t] - kPBias;
+          const float off = m[t] == kNegInf ? 0.0f : kPBias - m[t] * scale[t];
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
+          for (int k = 0; k < NG / 2; ++k)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
               float e4[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                e4[i] = __builtin_amdgcn_exp2f(sc[t][2 * k + half][i] - off);
+                e4[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][2 * k + half][i], scale[t], off));
                 l[t] += e4[i];
               }
               const v2h a = __builtin_convertvector((v2f{e4[0], e4[1]}), v2h), bb = __builtin_convertvector((v2f{e4[2], e4[3]}), v2h);
@@ -314,13 +342,13 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
         }
         // -- O^T += V^T P^T
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < NG / 2; ++k) {
           v4i frag[E];
 #pragma unroll
           for (int jj = 0; jj < 4; ++jj) {  // pairs of positions: two of each 16
-            const int gr = 2 * k + jj / 2, j = (jj & 1) * 2;
-            const v2h s2 = __builtin_bit_cast(v2h, (jj & 1) ? scale_pair<kHigh>(vs[gr]) : scale_pair<kLow>(vs[gr]));
-            const uint32_t a = vq[gr][j], bb = vq[gr][j + 1], mask = 0x0F0F0F0Fu;
+            const int gr = 2 * k + jj / 2, x2 = (jj & 1) * 2;
+            const v2h s2 = __builtin_bit_cast(v2h, (jj & 1) ? scale_pair<kHigh>(vs[d][gr]) : scale_pair<kLow>(vs[d][gr]));
+            const uint32_t a = vq[d][gr][x2], bb = vq[d][gr][x2 + 1], mask = 0x0F0F0F0Fu;
             const uint32_t even = (a & mask) | ((bb << 4) & ~mask), odd = ((a >> 4) & mask) | (bb & ~mask);
 #pragma unroll
             for (int e = 0; e < E; e += 2) {
@@ -337,7 +365,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
         if (__any(nan_codes)) {
           // rare: a NaN block among positions that not every row sees.  Output element i of tile e is
           // dim E (4g + i) + e, so element i lies in block E (4g + i) / 16.
-          for (int at = max(t0, max(lo, w0)); at < min(t0 + kTile, w1); ++at) {
+          for (int at = max(t0, max(lo, w0)); at < min(t0 + kStep, w1); ++at) {
             const int page = clamp_page(p, table[at >> p.page_shift]), sl = at & (P - 1);
             const uint8_t* codes = p.cache + (int64_t)page * p.page_stride + (int64_t)h * chunk + L::v_scales(P) + sl;
 #pragma unroll
@@ -351,12 +379,26 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
             }
           }
         }
-        if (more) {
+      };
 #pragma unroll
-          for (int gr = 0; gr < 4; ++gr) load_v(gr, base[gr], slot[gr]);
+      for (int d = 0; d < DEPTH; ++d) load(d, w0 + d * kStep);
+      int t0 = w0;
+      for (; t0 + (DEPTH - 1) * kStep < w1; t0 += DEPTH * kStep) {
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) {
+          step(d, t0 + d * kStep);
+          load(d, t0 + (d + DEPTH) * kStep);
         }
       }
+#pragma unroll
+      for (int d = 0; d < DEPTH - 1; ++d)
+        if (t0 + d * kStep < w1) step(d, t0 + d * kStep);
     }
+
+    // a scaled maximum from here on
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+      if (m[t] != kNegInf && p.softcap <= 0.0f) m[t] *= mul[t];
 
     // ---- join the waves
 #pragma unroll
@@ -376,11 +418,11 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
       }
     }
     __syncthreads();
-    const bool whole = x <= u0 && x1 >= u1;
-    const int wg0 = u0 / per, wgs = (u1 - 1) / per - wg0 + 1;  // the workgroups that share the unit
+    const bool whole = x <= real && x1 >= u1;
+    const int wg0 = real / per, wgs = (u1 - 1) / per - wg0 + 1;  // the workgroups that share the unit
     // Slot of the part that workgroup wg0 + k left: 2 (wg0 + k), or one more where the unit starts inside
     // that workgroup's run.
-    auto slot_of = [&](int k) { return 2 * (wg0 + k) + (u0 >= (wg0 + k) * per ? 1 : 0); };
+    auto slot_of = [&](int k) { return 2 * (wg0 + k) + (real >= (wg0 + k) * per ? 1 : 0); };
     const __amdgpu_buffer_rsrc_t parts = handoff_buffer(p.part, 2u * gridDim.x * SLOT * 4u);
     // element (row r, dims d .. d+3)
     auto store_out = [&](int r, int d, v4f y, float top, float sum) {
@@ -479,7 +521,7 @@ hipError_t launch(const KvArgs& a, int cus, hipStream_t stream) {
   const int64_t tiles = ((context < a.max_kv ? context : a.max_kv) + kTile - 1) / kTile + 1;
   // units: sum over sequences of ceil(tokens * group / R), at most one partial block each
   const int64_t units = ((int64_t)a.num_tokens * a.group / R + a.num_seqs) * a.kv_heads;
-  const int64_t want = (units * tiles + kMinTiles - 1) / kMinTiles, most = (int64_t)cus * kWgPerCu;
+  const int64_t want = units * ((tiles + kMinTiles - 1) / kMinTiles), most = (int64_t)cus * kWgPerCu;
   const dim3 grid((unsigned)(want < most ? want : most));
   const void* fn = R == 16 ? (const void*)&few_kernel<O, D, 1> : (const void*)&few_kernel<O, D, 2>;
   return hipLaunchKernel(fn, grid, dim3(kThreads), argv, 0, stream);
