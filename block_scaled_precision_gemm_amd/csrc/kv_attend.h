@@ -67,19 +67,24 @@ __device__ __forceinline__ uint16_t out_bits(float y) {
 }
 
 // Query row `row` (token first_token + row / group, head h * group + row % group) in the lanes of its
-// column (lane / 16 = g holds dims g D/4 .. (g+1) D/4 - 1) as fp16, and the base-2 score of one unit of
-// q . k as the products give it: keys decode times 2^-8, and bf16 rows are scaled so that their largest
-// magnitude lies in [2^14, 2^15), exact in fp16 down to 2^-39 of it.
-template <Out O, int D>
-__device__ __forceinline__ void load_query(const KvArgs& p, int first_token, int h, int row, int g, v8h q[D / 32], float& mul) {
-  constexpr int NJ = D / 32;
+// column: lane / 16 = g holds dims g D/4 .. (g+1) D/4 - 1.
+template <int D>
+__device__ __forceinline__ void load_query(const KvArgs& p, int first_token, int h, int row, int g, v4i w[D / 32]) {
   const int i = row / p.group, hq = row - i * p.group;
   const uint16_t* src = (const uint16_t*)p.q.ptr + (int64_t)(first_token + i) * p.q.token_stride +
                         (int64_t)(h * p.group + hq) * p.q.head_stride + g * (D / 4);
-  mul = p.score_mul * (kLog2e * 256.0f);
-  v4i w[NJ];
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) w[j] = *(const v4i*)(src + 8 * j);
+  for (int j = 0; j < D / 32; ++j) w[j] = *(const v4i*)(src + 8 * j);
+}
+
+// The row as fp16, and the base-2 score of one unit of q . k as the products give it, made positive (q
+// takes the sign), so that maxima can be taken over the products themselves.  Keys decode times 2^-8;
+// bf16 rows are scaled so that their largest magnitude lies in [2^14, 2^15), exact in fp16 down to 2^-39
+// of it.
+template <Out O, int D>
+__device__ __forceinline__ void convert_query(const KvArgs& p, const v4i w[D / 32], v8h q[D / 32], float& mul) {
+  constexpr int NJ = D / 32;
+  mul = p.score_mul * (kLog2e * 256.0f);
   if constexpr (O == Out::F16) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j) q[j] = __builtin_bit_cast(v8h, w[j]);
@@ -102,6 +107,10 @@ __device__ __forceinline__ void load_query(const KvArgs& p, int first_token, int
       for (int k = 0; k < 8; ++k) q[j][k] = (_Float16)__builtin_amdgcn_ldexpf(f[j][k], up);
     mul = __builtin_amdgcn_ldexpf(mul, -up);
   }
+  if (p.score_mul < 0.0f)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) q[j] = -q[j];
+  mul = __builtin_fmaxf(__builtin_fabsf(mul), 1.17549435e-38f);
 }
 
 hipError_t kv_attend_rows_launch(const KvArgs& a, int dtype, int head_dim, int cus, hipStream_t stream);

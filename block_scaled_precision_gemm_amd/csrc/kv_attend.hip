@@ -39,6 +39,20 @@ constexpr int kMinTiles = 2;    // a piece is at least a step of each wave
 constexpr int kUnitCost = 12;
 constexpr int kWgPerCu = 2;
 
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_add(int x) {
+  return x + __builtin_amdgcn_update_dpp(0, x, CTRL, ROWS, 0xF, false);
+}
+// Inclusive sums over the wave's lanes.
+__device__ __forceinline__ int wave_scan(int x) {
+  x = dpp_add<0x111, 0xF>(x);  // shift right within rows of 16 lanes by 1, 2, 4, 8
+  x = dpp_add<0x112, 0xF>(x);
+  x = dpp_add<0x114, 0xF>(x);
+  x = dpp_add<0x118, 0xF>(x);
+  x = dpp_add<0x142, 0xA>(x);  // lane 15 of rows 0 and 2 to rows 1 and 3
+  return dpp_add<0x143, 0xC>(x);  // lane 31 to rows 2 and 3
+}
+
 // What a unit covers.
 struct Span {
   int q_len, len;  // new tokens and context of the sequence
@@ -76,13 +90,8 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
   // ---- how the work is divided: all threads look at the sequences together
   const int per_thread = (p.num_seqs + kThreads - 1) / kThreads;
   auto block_sums = [&](int a, int b2, int& sum_a, int& sum_b, int& before) {  // and a's sum over earlier threads
-    int incl = a;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int y = __shfl_up(incl, o), z = __shfl_xor(b2, o);
-      if (lane >= o) incl += y;
-      b2 += z;
-    }
+    int incl = wave_scan(a);
+    b2 = wave_scan(b2);
     if (lane == 63) sh_sum[0][wave] = incl, sh_sum[1][wave] = b2;
     __syncthreads();
     sum_a = sum_b = 0;
@@ -173,20 +182,63 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
     const int hi = causal ? max(0, pos0 + i_last + 1) : s.len;
     const int s0 = max(s.lo + tile0 * kTile, lo & ~15), s1 = min(s.lo + tile1 * kTile, hi);
 
-    // ---- queries
+    // ---- this wave's positions
+    const int steps = s1 > s0 ? (s1 - s0 + kStep - 1) / kStep : 0;
+    const int per_wave = (steps + 3) / 4;
+    const int w0 = s0 + wave * per_wave * kStep, w1 = min(s1, w0 + per_wave * kStep);
+    const int* table = p.pages + (int64_t)b * p.pages_stride;
+    const int last_pos = max(hi - 1, 0), chunk = L::chunk(P);
+    // page numbers of the next 64 pages, one per lane
+    int page_base = min(w0, last_pos) >> p.page_shift;
+    int page_ids = clamp_page(p, table[min(page_base + lane, last_pos >> p.page_shift)]);
+    // the queries' loads are issued before the codes', and used after them
+    v4i raw[RT][NJ];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      const int r = 16 * t + c;
+      load_query<D>(p, first_token, h, rb * R + (r < rows ? r : 0), g, raw[t]);
+    }
+    // a step's codes: NG groups of 16 positions, DEPTH steps in flight
+    uint32_t kq[DEPTH][NG][NJ], ks[DEPTH][NG], vq[DEPTH][NG][4], vs[DEPTH][NG];
+    auto load = [&](int d, int t0) {
+#pragma unroll
+      for (int gr = 0; gr < NG; ++gr) {
+        const int t = min(t0 + 16 * gr, last_pos & ~15);  // (clamped into the context)
+        const int page = t >> p.page_shift;
+        if (page - page_base >= 64) {
+          page_base = page;
+          page_ids = clamp_page(p, table[min(page_base + lane, last_pos >> p.page_shift)]);
+        }
+        const int slot = t & (P - 1);
+        const uint8_t* at = p.cache + (int64_t)__builtin_amdgcn_readlane(page_ids, page - page_base) * p.page_stride +
+                            (int64_t)h * chunk;
+        const uint8_t* kp = at + (slot + c) * L::kRow + g * (4 * NJ);
+        if constexpr (D == 128) {
+          const v4i w = *(const v4i*)kp;
+#pragma unroll
+          for (int k = 0; k < NJ; ++k) kq[d][gr][k] = (uint32_t)w[k];
+          ks[d][gr] = *(const uint16_t*)(at + L::k_scales(P) + (slot + c) * L::kBlocks + 2 * g);
+        } else {
+          const uint2 w = *(const uint2*)kp;
+          kq[d][gr][0] = w.x;
+          kq[d][gr][1] = w.y;
+          ks[d][gr] = at[L::k_scales(P) + (slot + c) * L::kBlocks + g];
+        }
+        const uint8_t* vp = at + L::v_codes(P) + (slot + 4 * g) * L::kRow + c * (E / 2);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          vq[d][gr][k] = E == 8 ? *(const uint32_t*)(vp + k * L::kRow) : *(const uint16_t*)(vp + k * L::kRow);
+        vs[d][gr] = *(const uint32_t*)(at + L::v_scales(P) + (c * E / 16) * P + slot + 4 * g);
+      }
+    };
     v8h q[RT][NJ];
     float mul[RT];   // base-2 score of one accumulator unit
     int pos[RT];     // the row's position: it sees (pos - window, pos]
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
       const int r = 16 * t + c, row = rb * R + (r < rows ? r : 0);
-      load_query<O, D>(p, first_token, h, row, g, q[t], mul[t]);
+      convert_query<O, D>(p, raw[t], q[t], mul[t]);
       pos[t] = causal ? pos0 + row / G : s.len - 1;
-      // a scaled score is mul * s with mul > 0: the maximum is taken over the products themselves
-      if (p.score_mul < 0.0f)
-#pragma unroll
-        for (int k = 0; k < NJ; ++k) q[t][k] = -q[t][k];
-      mul[t] = __builtin_fmaxf(__builtin_fabsf(mul[t]), 1.17549435e-38f);
     }
 
     v4f o[RT][E];
@@ -199,49 +251,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
       for (int e = 0; e < E; ++e) o[t][e] = v4f{0, 0, 0, 0};
     }
 
-    // ---- this wave's positions
-    const int steps = s1 > s0 ? (s1 - s0 + kStep - 1) / kStep : 0;
-    const int per_wave = (steps + 3) / 4;
-    const int w0 = s0 + wave * per_wave * kStep, w1 = min(s1, w0 + per_wave * kStep);
     if (w0 < w1) {
-      const int* table = p.pages + (int64_t)b * p.pages_stride;
-      const int last_pos = hi - 1;
-      int page_base = w0 >> p.page_shift;
-      int page_ids = clamp_page(p, table[min(page_base + lane, last_pos >> p.page_shift)]);
-      const int chunk = L::chunk(P);
-      // a step's codes: NG groups of 16 positions, DEPTH steps in flight
-      uint32_t kq[DEPTH][NG][NJ], ks[DEPTH][NG], vq[DEPTH][NG][4], vs[DEPTH][NG];
-      auto load = [&](int d, int t0) {
-#pragma unroll
-        for (int gr = 0; gr < NG; ++gr) {
-          const int t = min(t0 + 16 * gr, last_pos & ~15);  // (clamped into the context)
-          const int page = t >> p.page_shift;
-          if (page - page_base >= 64) {
-            page_base = page;
-            page_ids = clamp_page(p, table[min(page_base + lane, last_pos >> p.page_shift)]);
-          }
-          const int slot = t & (P - 1);
-          const uint8_t* at = p.cache + (int64_t)__builtin_amdgcn_readlane(page_ids, page - page_base) * p.page_stride +
-                              (int64_t)h * chunk;
-          const uint8_t* kp = at + (slot + c) * L::kRow + g * (4 * NJ);
-          if constexpr (D == 128) {
-            const v4i w = *(const v4i*)kp;
-#pragma unroll
-            for (int k = 0; k < NJ; ++k) kq[d][gr][k] = (uint32_t)w[k];
-            ks[d][gr] = *(const uint16_t*)(at + L::k_scales(P) + (slot + c) * L::kBlocks + 2 * g);
-          } else {
-            const uint2 w = *(const uint2*)kp;
-            kq[d][gr][0] = w.x;
-            kq[d][gr][1] = w.y;
-            ks[d][gr] = at[L::k_scales(P) + (slot + c) * L::kBlocks + g];
-          }
-          const uint8_t* vp = at + L::v_codes(P) + (slot + 4 * g) * L::kRow + c * (E / 2);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            vq[d][gr][k] = E == 8 ? *(const uint32_t*)(vp + k * L::kRow) : *(const uint16_t*)(vp + k * L::kRow);
-          vs[d][gr] = *(const uint32_t*)(at + L::v_scales(P) + (c * E / 16) * P + slot + 4 * g);
-        }
-      };
       const int first_pos = causal ? pos0 + i_first : s.len - 1, last_row_pos = causal ? pos0 + i_last : s.len - 1;
       auto step = [&](int d, int t0) {
         // -- scores

@@ -65,22 +65,14 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
     const int r = w_row + 16 * t + c, row = rb * R + (r < rows ? r : 0);
-    load_query<O, D>(p, first_token, h, row, g, q[t], mul[t]);
+    v4i raw[NJ];
+    load_query<D>(p, first_token, h, row, g, raw);
+    convert_query<O, D>(p, raw, q[t], mul[t]);
     pos[t] = causal ? pos0 + row / G : len - 1;
   }
   // positions that all, and any, of the wave's rows see up to
   const int w_first = causal ? pos0 + (rb * R + min(w_row, rows - 1)) / G : len - 1;
   const int w_last = causal ? pos0 + (rb * R + min(w_row + 31, rows - 1)) / G : len - 1;
-  // a scaled score is mul * s with mul > 0: the maximum is taken over the products themselves
-  const bool negative = p.score_mul < 0.0f;
-#pragma unroll
-  for (int t = 0; t < RT; ++t) {
-    if (negative)
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) q[t][j] = -q[t][j];
-    mul[t] = __builtin_fmaxf(__builtin_fabsf(mul[t]), 1.17549435e-38f);
-  }
-
   v4f o[RT][E];
   float m[RT], l[RT];
 #pragma unroll
