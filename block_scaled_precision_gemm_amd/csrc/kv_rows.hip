@@ -10,9 +10,8 @@
 // The lane layouts, the softmax and the decoding are those of the few-row kernel (kv_attend.hip).  Each
 // wave keeps 32 rows, so a fragment read from LDS feeds two products.
 //
-// Workgroups that share a sequence and head follow each other at a distance of (sequences x heads), a
-// multiple of 8 for 8 heads, so that they run on one XCD and share its L2; the longest run first.  Where
-// the rows alone give too few workgroups, positions are split and the last workgroup of a row block
+// Workgroups that share a sequence and head run on one XCD where that can be arranged, and share its L2.
+// Where the rows alone give too few workgroups, positions are split and the last workgroup of a row block
 // joins the parts.
 //
 // Bound: matrix products and the softmax's and decoding's vector operations, at similar rates.
@@ -40,8 +39,19 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
   const int H = p.kv_heads, G = p.group, P = 1 << p.page_shift;
   const bool causal = !(p.flags & BSG_KV_NONCAUSAL);
 
-  // ---- unit and split: x = ((block from the last) * splits + split) * sequences * heads + (sequence, head)
-  const int bh = blockIdx.x % (p.num_seqs * H), rest = blockIdx.x / (p.num_seqs * H);
+  // ---- unit and split.  Groups (sequence, head) are a multiple of 8: workgroup x is on XCD x % 8 and so is
+  // all of a group, whose blocks follow each other there from the last (the longest) to the first.
+  // Otherwise groups alternate.
+  const int groups = p.num_seqs * H, per_group = gridDim.x / groups;
+  int bh, rest;
+  if (groups % 8 == 0) {
+    const int at = blockIdx.x >> 3;
+    bh = at / per_group * 8 + (blockIdx.x & 7);
+    rest = at % per_group;
+  } else {
+    bh = blockIdx.x % groups;
+    rest = blockIdx.x / groups;
+  }
   const int b = bh / H, h = bh - b * H, split = rest % p.splits;
   const int first_token = p.one_each ? b : seq_start(p, b);
   const int len = seq_len(p, b);
@@ -302,7 +312,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
     for (int i = 0; i < 4; ++i) bits[i] = out_bits<O>(none ? 0.0f : y[i] * f);
     return make_uint2(bits[0] | bits[1] << 16, bits[2] | bits[3] << 16);
   };
-  const uint32_t slot0 = (uint32_t)(blockIdx.x) * SLOT;  // of this split; the next one's is sequences * heads slots on
+  const uint32_t first_slot = (uint32_t)(bh * per_group + rest - split), slot0 = (first_slot + split) * SLOT;
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
     const int r = w_row + 16 * t + c;
@@ -330,13 +340,12 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
   if (p.splits == 1) return;
   int* counter = p.arrived + ((int64_t)first_token * G + (int64_t)rb * R) * H + h;
   if (!last_arrival(counter, p.splits, &sh_last)) return;
-  const uint32_t first_slot = (uint32_t)(blockIdx.x - split * p.num_seqs * H);
   for (int k = tid; k < rows * (D / 4); k += 64 * WAVES) {
     const int r = k / (D / 4), d = k % (D / 4) * 4;
     v4f ms[kJoin], ys[kJoin];
 #pragma unroll
     for (int i = 0; i < kJoin; ++i) {  // all in flight; splits past the last repeat it and count nothing
-      const uint32_t at = (first_slot + (uint32_t)(min(i, p.splits - 1) * p.num_seqs * H)) * SLOT;
+      const uint32_t at = (first_slot + (uint32_t)min(i, p.splits - 1)) * SLOT;
       ms[i] = handoff_load4(parts, at + R * D + 4 * r);
       ys[i] = handoff_load4(parts, at + r * D + d);
     }
