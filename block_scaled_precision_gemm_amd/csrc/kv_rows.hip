@@ -102,11 +102,19 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
     const bool do_v = kBoth || wave < 4, do_k = kBoth || wave >= 4;
     const int vt = wave & 3, kt = wave & 3;
     uint32_t kq[NJ], ks = 0, vq[2][4], vs[2];
+    // page numbers of the next 64 pages, one per lane
+    int page_base = t_begin >> p.page_shift;
+    int page_ids = clamp_page(p, table[min(page_base + lane, last_pos >> p.page_shift)]);
+    const uint8_t* head = p.cache + (int64_t)h * chunk;
     auto group_at = [&](int t, int& slot) -> const uint8_t* {
       t = min(t, last_pos & ~15);
       slot = t & (P - 1);
-      const int page = __builtin_amdgcn_readfirstlane(clamp_page(p, table[t >> p.page_shift]));
-      return p.cache + (int64_t)page * p.page_stride + (int64_t)h * chunk;
+      const int page = t >> p.page_shift;
+      if (page - page_base >= 64) {
+        page_base = page;
+        page_ids = clamp_page(p, table[min(page_base + lane, last_pos >> p.page_shift)]);
+      }
+      return head + (int64_t)__builtin_amdgcn_readlane(page_ids, page - page_base) * p.page_stride;
     };
     auto load = [&](int t0) {
       if (do_v) {
@@ -196,9 +204,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
       v4f sc[RT][4];
       if (mine) {
 #pragma unroll
-        for (int gr = 0; gr < 4; ++gr)
+        for (int j = 0; j < NJ; ++j)
 #pragma unroll
-          for (int j = 0; j < NJ; ++j) {
+          for (int gr = 0; gr < 4; ++gr) {
             const v8h a = __builtin_bit_cast(v8h, sh[buf].k[gr][j][lane]);
 #pragma unroll
             for (int t = 0; t < RT; ++t)
@@ -273,7 +281,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
 #pragma unroll
             for (int t = 0; t < RT; ++t) o[t][e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pt[t][k], o[t][e], 0, 0, 0);
           }
-        if (__builtin_amdgcn_readfirstlane(sh_nan[buf]) == t0) {
+        if (partly_hidden(t0) && __builtin_amdgcn_readfirstlane(sh_nan[buf]) == t0) {
           // rare: a NaN block among positions that not every row sees.  Output element i of tile e is
           // dim E (4g + i) + e, so element i lies in block E (4g + i) / 16.
           for (int at = max(t0, lo); at < min(t0 + kTile, t_end); ++at) {
