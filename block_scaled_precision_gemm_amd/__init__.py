@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 __all__ = ["Plan", "BsgError", "LibraryNotBuilt", "load_library", "bench_loop", "null_loop", "run_noalloc", "NOALLOC_SCRATCH_BYTES", "decode_nvfp4_f16",
            "FORMATS", "OUT_DTYPES", "SCALE_LAYOUTS", "abi_version", "packed_strides", "Problem", "PROBLEM_V1_SIZE", "PROBLEM_V2_SIZE",
@@ -74,8 +75,7 @@ def packed_strides(fmt: str, M: int, N: int, K: int, scale_layout: str = "linear
     return dict(a=int(M * lda * elem), b=int(N * ldb * elem), sa=sa, sb=sb, bias=0, d=2 * M * ldd)
 
 
-class Heads(ctypes.Structure):  # bsg_heads
-    _fields_ = [("ptr", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+_HEADS = struct.Struct("@Pqq").pack  # bsg_heads: pointer, token stride, head stride
 
 
 class KVProblem(ctypes.Structure):  # bsg_kv_problem
@@ -188,21 +188,30 @@ def _ptr(x) -> int | None:
     return x.data_ptr()
 
 
-_torch_cuda = None  # torch.cuda once a GPU was seen through it
+_current_stream = None  # returns torch's current stream as a handle, once a GPU was seen through torch
+
+
+def _find_current_stream():
+    """How to ask torch for its current stream; None without torch or a GPU."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    if not torch.cuda.is_available():
+        return None
+    raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+    if raw and device:
+        torch.cuda.current_stream()  # torch's own start-up
+        return lambda: raw(device())
+    return lambda: torch.cuda.current_stream().cuda_stream
 
 
 def _stream(s) -> int | None:
-    global _torch_cuda
+    global _current_stream
     if s is None:
-        if _torch_cuda is None:
-            try:
-                import torch
-            except ImportError:
-                return None
-            if not torch.cuda.is_available():
-                return None
-            _torch_cuda = torch.cuda
-        return _torch_cuda.current_stream().cuda_stream
+        if _current_stream is None:
+            _current_stream = _find_current_stream()
+        return _current_stream() if _current_stream else None
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -385,11 +394,12 @@ class KVPlan:
         self._h = h
         self.page_bytes = self.info()["page_stride"]
 
-    def _heads(self, t, tokens: int, heads: int):
-        if t.shape != (tokens, heads, self.head_dim) or t.element_size() != 2 or t.stride(2) != 1:
+    def _heads(self, t, tokens: int, heads: int) -> bytes:
+        token_stride, head_stride, one = t.stride() if t.dim() == 3 else (0, 0, 0)
+        if one != 1 or t.shape != (tokens, heads, self.head_dim) or t.element_size() != 2:
             raise ValueError(f"expected a 16-bit tensor [{tokens}][{heads}][{self.head_dim}] with contiguous rows, got "
                              f"{tuple(t.shape)} with strides {t.stride()}")
-        return ctypes.byref(Heads(t.data_ptr(), t.stride(0), t.stride(1)))
+        return _HEADS(t.data_ptr(), token_stride, head_stride)
 
     def append(self, batch: KVBatch, k, v, cache, q=None, q_out=None, rope=None, stream=None) -> None:
         """Store the batch's keys (rotated) and values; with q, write rotated queries to q_out (q: in place).
@@ -462,9 +472,10 @@ class MoEPlan:
         h = _VP()
         _check(lib.bsg_moe_plan_create(ctypes.byref(prob), ctypes.byref(h)))
         self._h = h
-        per = 2 if fmt == "nvfp4" else 1
-        self._sizes = {"w13": 2 * inter * hidden // per, "s13": 2 * inter * hidden // SCALE_BLOCK[fmt],
-                       "w2": inter * hidden // per, "s2": inter * hidden // SCALE_BLOCK[fmt]}
+        per, rows = 2 if fmt == "nvfp4" else 1, experts * inter * hidden
+        self._nr = experts * hidden
+        self._n13, self._ns13 = 2 * rows // per, 2 * rows // SCALE_BLOCK[fmt]
+        self._n2, self._ns2 = rows // per, rows // SCALE_BLOCK[fmt]
 
     def run(self, x, router, w13, s13, w2, s2, out, alpha13=None, alpha2=None, ids=None, weights=None, stream=None) -> None:
         """out = the layer applied to x [tokens][hidden] (row-strided views are fine).  w13, s13, w2, s2: uint8 codes
@@ -474,12 +485,15 @@ class MoEPlan:
         for t in (x, out):
             if t.shape != (tokens, self.hidden) or t.element_size() != 2 or t.stride(1) != 1:
                 raise ValueError(f"expected 16-bit rows [{tokens}][{self.hidden}], got {tuple(t.shape)} with strides {t.stride()}")
-        if router.shape != (self.experts, self.hidden) or router.element_size() != 2 or not router.is_contiguous():
-            raise ValueError(f"router must be a contiguous 16-bit tensor [{self.experts}][{self.hidden}]")
-        for name, t in (("w13", w13), ("s13", s13), ("w2", w2), ("s2", s2)):
-            if t.numel() != self.experts * self._sizes[name] or t.element_size() != 1 or not t.is_contiguous():
-                raise ValueError(f"{name} must hold {self.experts} x {self._sizes[name]} contiguous bytes")
-        for t, n in ((alpha13, self.experts), (alpha2, self.experts), (ids, tokens * self.top_k), (weights, tokens * self.top_k)):
+        choices = tokens * self.top_k
+        if not (router.numel() == self._nr and router.element_size() == 2 and router.is_contiguous()
+                and w13.numel() == self._n13 and w13.element_size() == 1 and w13.is_contiguous()
+                and s13.numel() == self._ns13 and s13.element_size() == 1 and s13.is_contiguous()
+                and w2.numel() == self._n2 and w2.element_size() == 1 and w2.is_contiguous()
+                and s2.numel() == self._ns2 and s2.element_size() == 1 and s2.is_contiguous()):
+            raise ValueError(f"router, w13, s13, w2 and s2 must be contiguous, of {self._nr} 16-bit values and {self._n13}, "
+                             f"{self._ns13}, {self._n2}, {self._ns2} bytes")
+        for t, n in ((alpha13, self.experts), (alpha2, self.experts), (ids, choices), (weights, choices)):
             if t is not None and (t.numel() != n or t.element_size() != 4 or not t.is_contiguous()):
                 raise ValueError("alpha13 and alpha2 have one 32-bit value per expert, ids and weights [tokens][top_k]")
         w = MoEWeights(ctypes.sizeof(MoEWeights), 0, router.data_ptr(), w13.data_ptr(), s13.data_ptr(), w2.data_ptr(),
