@@ -102,74 +102,37 @@ __device__ __forceinline__ Place place_of(const KvArgs& p, int t, int lane_in_ro
   return r;
 }
 
-template <Out O, int D>
-__global__ __launch_bounds__(kThreads) void append_kernel(KvArgs p) {
-  constexpr int W = D / 8, ROWS = kThreads / W;
-  const int tid = threadIdx.x, c = tid % W, row_shift = (tid & 63) / W * W;
-  const int t = blockIdx.x * ROWS + tid / W;
-  const int h = blockIdx.y;  // 0 .. kv_heads-1: keys, then values, then queries
-  const bool live = t < p.num_tokens;
-  const int tt = live ? t : p.num_tokens - 1;  // idle rows follow the last token, and store nothing
-  const int kind = h < p.kv_heads ? 0 : h < 2 * p.kv_heads ? 1 : 2;
-  const int hh = kind == 0 ? h : kind == 1 ? h - p.kv_heads : h - 2 * p.kv_heads;
-  const HeadsArg& src = kind == 0 ? p.k : kind == 1 ? p.v : p.q;
-  const uint16_t* row = (const uint16_t*)src.ptr + (int64_t)tt * src.token_stride + (int64_t)hh * src.head_stride;
-  const v4i w = *(const v4i*)(row + 8 * c);
-  const int R = 2 * p.rope_half, d0 = 8 * c;
-  const bool turned = kind != 1 && d0 < R;
-  const bool inter = p.flags & BSG_KV_ROPE_INTERLEAVED;
-  const bool upper = d0 >= p.rope_half;  // halves: this lane holds the second of each pair
-  v4i w2 = w;
-  if (turned && !inter) w2 = *(const v4i*)(row + (upper ? d0 - p.rope_half : d0 + p.rope_half));
-
-  const Place at = place_of<W>(p, tt, c, row_shift);
-  float x[8];
-  unpack8<O>(w, x);
-  if (turned) {
-    const int last = p.max_kv - 1;
-    const float* tab = p.rope + (int64_t)min(max(at.pos, 0), last) * R;
-    if (inter) {
-      const v4f cs = *(const v4f*)(tab + d0 / 2), sn = *(const v4f*)(tab + p.rope_half + d0 / 2);
+// Rotate the 8 dims of a lane: x, with y the partner dims (halves) or unused (neighbours).
+__device__ __forceinline__ void rotate8(float x[8], const float y[8], const float cs[8], const float sn[8], bool inter, bool upper) {
+  if (inter) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a = x[2 * i], b = x[2 * i + 1];
-        x[2 * i] = a * cs[i] - b * sn[i];
-        x[2 * i + 1] = b * cs[i] + a * sn[i];
-      }
-    } else {
-      const int i0 = upper ? d0 - p.rope_half : d0;
-      float y[8];
-      unpack8<O>(w2, y);
-      const v4f c0 = *(const v4f*)(tab + i0), c1 = *(const v4f*)(tab + i0 + 4);
-      const v4f s0 = *(const v4f*)(tab + p.rope_half + i0), s1 = *(const v4f*)(tab + p.rope_half + i0 + 4);
+    for (int i = 0; i < 4; ++i) {
+      const float a = x[2 * i], b = x[2 * i + 1];
+      x[2 * i] = a * cs[i] - b * sn[i];
+      x[2 * i + 1] = b * cs[i] + a * sn[i];
+    }
+  } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float cc = i < 4 ? c0[i & 3] : c1[i & 3], ss = i < 4 ? s0[i & 3] : s1[i & 3];
-        const float mine = x[i] * cc, other = y[i] * ss;
-        x[i] = upper ? mine + other : mine - other;
-      }
+    for (int i = 0; i < 8; ++i) {
+      const float mine = x[i] * cs[i], other = y[i] * sn[i];
+      x[i] = upper ? mine + other : mine - other;
     }
   }
+}
 
-  if (kind == 2) {
-    if (live)
-      *(v4i*)((uint16_t*)p.out.ptr + (int64_t)t * p.out.token_stride + (int64_t)hh * p.out.head_stride + d0) =
-          pack8<O>(x);
-    return;
-  }
-
-  const float inv = kind == 0 ? p.k_inv : p.v_inv;
+// A block's eight elements of this lane (the neighbour lane has the other eight): packed codes, and the
+// scale's code.
+__device__ __forceinline__ uint32_t quantize8(float x[8], float inv, int& code) {
   float amax = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     x[i] = x[i] * inv;
     amax = __builtin_elementwise_maximum(amax, __builtin_fabsf(x[i]));  // keeps a NaN
   }
-  const float other = __shfl_xor(amax, 1);
-  amax = __builtin_elementwise_maximum(amax, other);
+  amax = __builtin_elementwise_maximum(amax, __shfl_xor(amax, 1));
   const bool nan = amax != amax;
   const float s_raw = fminf(amax * (1.0f / 6.0f), 448.0f);
-  const int code = nan ? 0x7F : __builtin_amdgcn_cvt_pk_fp8_f32(s_raw, 0.0f, 0, false) & 0x7F;
+  code = nan ? 0x7F : __builtin_amdgcn_cvt_pk_fp8_f32(s_raw, 0.0f, 0, false) & 0x7F;
   const float s = nan ? 0.0f : __builtin_amdgcn_cvt_f32_fp8(code, 0);
   const float r = s > 0.0f ? 1.0f / s : 0.0f;
   uint32_t q = 0;
@@ -189,14 +152,76 @@ __global__ __launch_bounds__(kThreads) void append_kernel(KvArgs p) {
     if (i == 2) q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, z[0], z[1], 1.0f, 2);
     if (i == 3) q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, z[0], z[1], 1.0f, 3);
   }
-  if (!live || at.page < 0) return;
-  using L = PageLayout<D>;
-  const int P = 1 << p.page_shift;
-  uint8_t* chunk = p.cache + at.page + (int64_t)hh * L::chunk(P);
-  *(uint32_t*)(chunk + (kind ? L::v_codes(P) : 0) + at.slot * L::kRow + 4 * c) = q;
-  if (!(c & 1)) {
-    if (kind) chunk[L::v_scales(P) + (c >> 1) * P + at.slot] = (uint8_t)code;
-    else chunk[L::k_scales(P) + at.slot * L::kBlocks + (c >> 1)] = (uint8_t)code;
+  return q;
+}
+
+// Workgroup (x, y): ROWS tokens, and heads NB y .. NB y + NB - 1 of (keys, values, queries).  A lane's
+// rotation factors and place serve all of them, and their loads are in flight together.
+template <Out O, int D, int NB>
+__global__ __launch_bounds__(kThreads) void append_kernel(KvArgs p, int heads) {
+  constexpr int W = D / 8, ROWS = kThreads / W;
+  const int tid = threadIdx.x, c = tid % W, row_shift = (tid & 63) / W * W;
+  const int t = blockIdx.x * ROWS + tid / W;
+  const bool live = t < p.num_tokens;
+  const int tt = live ? t : p.num_tokens - 1;  // idle rows follow the last token, and store nothing
+  const int R = 2 * p.rope_half, d0 = 8 * c;
+  const bool inter = p.flags & BSG_KV_ROPE_INTERLEAVED, turns = d0 < R;
+  const bool upper = d0 >= p.rope_half;  // halves: this lane holds the second of each pair
+  const int d1 = !turns || inter ? d0 : upper ? d0 - p.rope_half : d0 + p.rope_half;  // the partners' dims
+  v4i w[NB], w2[NB];
+#pragma unroll
+  for (int k = 0; k < NB; ++k) {
+    const int h = min((int)blockIdx.y * NB + k, heads - 1);
+    const int kind = h < p.kv_heads ? 0 : h < 2 * p.kv_heads ? 1 : 2;
+    const int hh = kind == 0 ? h : kind == 1 ? h - p.kv_heads : h - 2 * p.kv_heads;
+    const HeadsArg& src = kind == 0 ? p.k : kind == 1 ? p.v : p.q;
+    const uint16_t* row = (const uint16_t*)src.ptr + (int64_t)tt * src.token_stride + (int64_t)hh * src.head_stride;
+    w[k] = *(const v4i*)(row + d0);
+    w2[k] = kind == 1 || inter ? w[k] : *(const v4i*)(row + d1);
+  }
+  const Place at = place_of<W>(p, tt, c, row_shift);
+  float cs[8], sn[8];
+  if (turns) {
+    const float* tab = p.rope + (int64_t)min(max(at.pos, 0), p.max_kv - 1) * R;
+    const int i0 = inter ? d0 / 2 : upper ? d0 - p.rope_half : d0;
+    const v4f c0 = *(const v4f*)(tab + i0), s0 = *(const v4f*)(tab + p.rope_half + i0);
+    const int i1 = inter ? i0 : i0 + 4;
+    const v4f c1 = *(const v4f*)(tab + i1), s1 = *(const v4f*)(tab + p.rope_half + i1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) cs[i] = c0[i], cs[4 + i] = c1[i], sn[i] = s0[i], sn[4 + i] = s1[i];
+  }
+#pragma unroll
+  for (int k = 0; k < NB; ++k) {
+    const int h = blockIdx.y * NB + k;
+    if (h >= heads) break;
+    const int kind = h < p.kv_heads ? 0 : h < 2 * p.kv_heads ? 1 : 2;
+    const int hh = kind == 0 ? h : kind == 1 ? h - p.kv_heads : h - 2 * p.kv_heads;
+    float x[8];
+    unpack8<O>(w[k], x);
+    if (turns && kind != 1) {
+      float y[8];
+      unpack8<O>(w2[k], y);
+      rotate8(x, y, cs, sn, inter, upper);
+    }
+    if (kind == 2) {
+      v4i* dst = (v4i*)((uint16_t*)p.out.ptr + (int64_t)t * p.out.token_stride + (int64_t)hh * p.out.head_stride + d0);
+      if (live) {
+        if constexpr (NB > 1) __builtin_nontemporal_store(pack8<O>(x), dst);  // (more than the L2s hold; 24.1 -> 22.8 us)
+        else *dst = pack8<O>(x);
+      }
+      continue;
+    }
+    int code;
+    const uint32_t q = quantize8(x, kind == 0 ? p.k_inv : p.v_inv, code);
+    if (!live || at.page < 0) continue;
+    using L = PageLayout<D>;
+    const int P = 1 << p.page_shift;
+    uint8_t* chunk = p.cache + at.page + (int64_t)hh * L::chunk(P);
+    *(uint32_t*)(chunk + (kind ? L::v_codes(P) : 0) + at.slot * L::kRow + 4 * c) = q;
+    if (!(c & 1)) {
+      if (kind) chunk[L::v_scales(P) + (c >> 1) * P + at.slot] = (uint8_t)code;
+      else chunk[L::k_scales(P) + at.slot * L::kBlocks + (c >> 1)] = (uint8_t)code;
+    }
   }
 }
 
@@ -235,11 +260,16 @@ __global__ __launch_bounds__(kThreads) void read_kernel(KvArgs p) {
 
 template <Out O, int D>
 hipError_t launch_append(const KvArgs& a, bool with_q, hipStream_t stream) {
-  constexpr int ROWS = kThreads / (D / 8);
+  constexpr int ROWS = kThreads / (D / 8), NB = 4;
   KvArgs args = a;
-  void* argv[] = {&args};
-  const dim3 grid((a.num_tokens + ROWS - 1) / ROWS, 2 * a.kv_heads + (with_q ? a.q_heads : 0));
-  return hipLaunchKernel((const void*)&append_kernel<O, D>, grid, dim3(kThreads), argv, 0, stream);
+  int heads = 2 * a.kv_heads + (with_q ? a.q_heads : 0);
+  void* argv[] = {&args, &heads};
+  const unsigned x = (a.num_tokens + ROWS - 1) / ROWS;
+  // Four heads to a workgroup share the rotation factors (4096 tokens, 48 heads of 128: 27.8 us with one
+  // head, 24.1 us with four); few tokens are spread over more workgroups, all being latency.
+  if ((int64_t)x * heads <= 2048)
+    return hipLaunchKernel((const void*)&append_kernel<O, D, 1>, dim3(x, heads), dim3(kThreads), argv, 0, stream);
+  return hipLaunchKernel((const void*)&append_kernel<O, D, NB>, dim3(x, (heads + NB - 1) / NB), dim3(kThreads), argv, 0, stream);
 }
 
 template <Out O, int D>
