@@ -316,7 +316,6 @@ struct Codes {
   static constexpr int kSlabBytes = NV ? kSlab / 2 : kSlab;     // code bytes of a slab of a row
   static constexpr int kSlabScales = kSlab / kBlock;
   static constexpr int kRegs = NV ? 4 : 8;
-  static constexpr int kDepth = 2;                              // slabs of weights in flight
 };
 
 // A lane's 32 codes of one row.
@@ -401,9 +400,8 @@ __device__ __forceinline__ void stage_scales(Scales<DEC, TILES>& sh, const uint8
 // read lie in different banks.  Read straight from memory in fragment order each lane would touch a
 // line of its own four times over (64 lines in each of four loads, against 64 of all the weights').
 constexpr int kXPitch = 2 * kSlab + 16;
-template <int PARTS>
 struct Slab {
-  uint8_t at[4][PARTS][16 * kXPitch];  // [wave][part]
+  uint8_t at[4][16 * kXPitch];  // [wave]; parts of the activations follow each other in it
 };
 
 // acc[tile] += rows x columns: tile m's 16 rows start at w[m] (codes) and sc[m] (scales); the columns are
@@ -411,19 +409,18 @@ struct Slab {
 // kNoColumn: none, zeros), part q `part` bytes further.  Slabs of 128 k go to the four waves in turn.
 constexpr uint32_t kNoColumn = 0x80000000u;
 template <Dec DEC, int TILES, int PARTS>
-__device__ __forceinline__ void products(Scales<DEC, TILES>& sh, Slab<PARTS>& slab, const uint8_t* const w[TILES],
+__device__ __forceinline__ void products(Scales<DEC, TILES>& sh, Slab& slab, const uint8_t* const w[TILES],
                                          const uint8_t* const sc[TILES], int K, int tid, int wave, const void* x,
                                          uint32_t x_bytes, const uint32_t column[4], uint32_t part, v4f acc[TILES]) {
   using C = Codes<DEC>;
-  constexpr int DEPTH = C::kDepth;
   const int lane = tid & 63, c = lane & 15, g = lane >> 4;
   const uint32_t at0 = c * (C::NV ? K / 2 : K) + g * (C::kSlabBytes / 4);
   const __amdgpu_buffer_rsrc_t xbuf = handoff_buffer(x, x_bytes);
-  Row<DEC> buf[DEPTH][TILES];
+  Row<DEC> rows[TILES];  // the next slab's weights
   v4u_t raw[PARTS][4];
-  auto fetch = [&](Row<DEC>* r, int s) {
+  auto fetch = [&](int s) {
 #pragma unroll
-    for (int m = 0; m < TILES; ++m) r[m].load(w[m] + (at0 + (uint32_t)s * C::kSlabBytes));
+    for (int m = 0; m < TILES; ++m) rows[m].load(w[m] + (at0 + (uint32_t)s * C::kSlabBytes));
   };
   auto fetch_x = [&](int s) {
     const uint32_t k = s * kSlab + 8 * c;  // the lane's 8 k of each of its columns
@@ -433,20 +430,19 @@ __device__ __forceinline__ void products(Scales<DEC, TILES>& sh, Slab<PARTS>& sl
       for (int i = 0; i < 4; ++i)  // beyond the buffer: zeros, and no memory access
         raw[q][i] = __builtin_amdgcn_raw_buffer_load_b128(xbuf, (int)(k < (uint32_t)K ? column[i] + 2 * k + q * part : kNoColumn), 0, 0);
   };
-  auto multiply = [&](const Row<DEC>* r, int chunk_slab, int next) {
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-#pragma unroll
-    for (int q = 0; q < PARTS; ++q)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) *(v4u_t*)&slab.at[wave][q][(4 * i + g) * kXPitch + 16 * c] = raw[q][i];
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();  // (one wave's LDS accesses are in order)
-    fetch_x(next);
+  auto multiply = [&](int chunk_slab, int next) {
     v4i v[PARTS][4];
 #pragma unroll
-    for (int q = 0; q < PARTS; ++q)
+    for (int q = 0; q < PARTS; ++q) {  // (one wave's LDS accesses are in order: the fences only keep them so)
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[q][j] = *(const v4i*)&slab.at[wave][q][c * kXPitch + 64 * g + 16 * j];
+      for (int i = 0; i < 4; ++i) *(v4u_t*)&slab.at[wave][(4 * i + g) * kXPitch + 16 * c] = raw[q][i];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[q][j] = *(const v4i*)&slab.at[wave][c * kXPitch + 64 * g + 16 * j];
+    }
+    fetch_x(next);
     uint32_t s[TILES];
 #pragma unroll
     for (int m = 0; m < TILES; ++m) {
@@ -457,7 +453,7 @@ __device__ __forceinline__ void products(Scales<DEC, TILES>& sh, Slab<PARTS>& sl
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int m = 0; m < TILES; ++m) {
-        const v4i a = r[m].fragment(j, s[m]);
+        const v4i a = rows[m].fragment(j, s[m]);
 #pragma unroll
         for (int q = 0; q < PARTS; ++q) acc[m] = mfma<C::F16>(a, v[q][j], acc[m]);
       }
@@ -468,47 +464,41 @@ __device__ __forceinline__ void products(Scales<DEC, TILES>& sh, Slab<PARTS>& sl
     // slabs past the last are read again as the last and not used
     const int mine = s1 < full ? (full - s1 + 3) / 4 : 0, last = s1 + 4 * (mine - 1);
     if (mine) {
-#pragma unroll
-      for (int d = 0; d < DEPTH; ++d) fetch(buf[d], min(s1 + 4 * d, last));
+      fetch(s1);
       fetch_x(s1);
     }
     if (k0) __syncthreads();
     stage_scales<DEC, TILES>(sh, sc, K, k0, n, tid);
     __syncthreads();
-    int i = 0;
-    for (; i + DEPTH <= mine; i += DEPTH) {
-#pragma unroll
-      for (int d = 0; d < DEPTH; ++d) {
-        const int s = s1 + 4 * (i + d);
-        multiply(buf[d], s - first, min(s + 4, last));
-        fetch(buf[d], min(s + 4 * DEPTH, last));
-      }
+    // One slab of weights ahead and four waves per SIMD: two slabs and three waves were slower (33 tokens,
+    // 64 experts of 4096 x 2048 in NVFP4: 134 and 94 us for the two products, 126 and 89 us so).
+    for (int i = 0; i < mine; ++i) {
+      const int s = s1 + 4 * i, next = min(s + 4, last);
+      multiply(s - first, next);
+      fetch(next);
     }
-#pragma unroll
-    for (int d = 0; d < DEPTH - 1; ++d)
-      if (i + d < mine) multiply(buf[d], s1 + 4 * (i + d) - first, min(s1 + 4 * (i + d + 1), last));
     if (n % kSlab && wave == full % 4) {  // the rest: lanes past the end count as zero
       fetch_x(full);
       if (full * kSlab + 32 * g < K) {
-        fetch(buf[0], full);
+        fetch(full);
       } else {
         // their scales are whatever LDS holds: zero them too, so that no NaN comes of it
 #pragma unroll
         for (int m = 0; m < TILES; ++m) {
-          buf[0][m].clear();
+          rows[m].clear();
 #pragma unroll
           for (int b = 0; b < C::kSlabScales / 4; ++b)
             sh.rows[16 * m + c][(full - first) * C::kSlabScales + g * (C::kSlabScales / 4) + b] = 0;
         }
       }
-      multiply(buf[0], full - first, full);
+      multiply(full - first, full);
     }
   }
 }
 
 // Workgroup (x, slot): SiLU(gate) up of dims 32x .. 32x+31 for the tokens of the slot's expert.
 template <bool NV, bool F16, bool ONE>
-__global__ __launch_bounds__(kThreads, NV ? 3 : 2) void gate_up_kernel(MoeArgs p) {
+__global__ __launch_bounds__(kThreads, NV ? 4 : 3) void gate_up_kernel(MoeArgs p) {
   constexpr int TILES = 4;  // gate rows 0..15, 16..31, up rows 0..15, 16..31
   constexpr Dec DEC = NV ? Dec::kNvF16 : Dec::kMxBf16;
   constexpr Prep PREP = kPrep<NV, F16>;
@@ -516,7 +506,7 @@ __global__ __launch_bounds__(kThreads, NV ? 3 : 2) void gate_up_kernel(MoeArgs p
   __shared__ union {
     struct {
       Scales<DEC, TILES> scales;
-      Slab<PARTS> slab;
+      Slab slab;
     };
     v4f acc[4][TILES][64];
   } sh;
@@ -595,13 +585,13 @@ __global__ __launch_bounds__(kThreads, NV ? 3 : 2) void gate_up_kernel(MoeArgs p
 // Workgroup (x, slot): output dims 64x .. 64x+63 of the slot's tokens, times their weights; the last
 // slot of a row of workgroups to finish adds each token's choices in the order of their rank.
 template <bool NV, bool F16>
-__global__ __launch_bounds__(kThreads, NV ? 3 : 2) void down_kernel(MoeArgs p) {
+__global__ __launch_bounds__(kThreads, 3) void down_kernel(MoeArgs p) {
   constexpr int TILES = 4;
   constexpr Dec DEC = NV ? Dec::kNvBf16 : Dec::kMxBf16;
   __shared__ union {
     struct {
       Scales<DEC, TILES> scales;
-      Slab<2> slab;
+      Slab slab;
     };
     v4f acc[4][TILES][64];
   } sh;
