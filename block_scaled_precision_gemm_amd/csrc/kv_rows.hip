@@ -11,28 +11,48 @@
 // wave keeps 32 rows, so a fragment read from LDS feeds two products.
 //
 // Workgroups that share a sequence and head run on one XCD where that can be arranged, and share its L2.
-// Where the rows alone give too few workgroups, positions are split and the last workgroup of a row block
-// joins the parts.
+// Where the rows alone give too few workgroups, positions are split and a second kernel joins the parts.
 //
 // Bound: matrix products and the softmax's and decoding's vector operations, at similar rates.
-#include "handoff.h"
 #include "kv_attend.h"
 
 namespace bsg {
 namespace {
 
+// Where the results of row block rb of a sequence and head go.
+template <Out O, int D, int R>
+struct Results {
+  const KvArgs& p;
+  int first_token, h, rb;
+  __device__ void store_lse(int row, float top, float sum) const {
+    const int i = (rb * R + row) / p.group, hq = rb * R + row - i * p.group;
+    p.lse[(int64_t)(first_token + i) * p.q_heads + h * p.group + hq] =
+        sum == 0.0f ? kNegInf : (top - kPBias + __builtin_amdgcn_logf(sum)) * kLn2;
+  }
+  __device__ uint16_t* out_at(int row, int d) const {
+    const int i = (rb * R + row) / p.group, hq = rb * R + row - i * p.group;
+    return (uint16_t*)p.out.ptr + (int64_t)(first_token + i) * p.out.token_stride + (int64_t)(h * p.group + hq) * p.out.head_stride + d;
+  }
+  __device__ static uint2 pack4(v4f y, float f, bool none) {
+    uint32_t bits[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bits[i] = out_bits<O>(none ? 0.0f : y[i] * f);
+    return make_uint2(bits[0] | bits[1] << 16, bits[2] | bits[3] << 16);
+  }
+};
+
 template <Out O, int D, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
   constexpr int RT = 2, R = 32 * WAVES;
   constexpr int NJ = D / 32, E = D / 16;
-  constexpr int SLOT = R * (D + 4);
+  constexpr int SLOT = R * (D + 2);  // a part: its rows' outputs, then their maxima and sums
   using L = PageLayout<D>;
   struct Buffer {
     v4i k[4][NJ][64];  // [16 positions][32 dims][lane]
     v4i v[2][E][64];   // [32 positions][dims E m + e][lane]
   };
   __shared__ Buffer sh[2];
-  __shared__ int sh_nan[2], sh_last;  // sh_nan: the buffer's tile, if it has such a NaN block (below)
+  __shared__ int sh_nan[2];  // sh_nan: the buffer's tile, if it has such a NaN block (below)
 
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int c = lane & 15, g = lane >> 4;
@@ -304,23 +324,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
   }
 
   // ---- results
-  const __amdgpu_buffer_rsrc_t parts = handoff_buffer(p.part, (uint32_t)gridDim.x * SLOT * 4u);
-  auto store_lse = [&](int row, float top, float sum) {
-    const int i = (rb * R + row) / G, hq = rb * R + row - i * G;
-    p.lse[(int64_t)(first_token + i) * p.q_heads + h * G + hq] =
-        sum == 0.0f ? kNegInf : (top - kPBias + __builtin_amdgcn_logf(sum)) * kLn2;
-  };
-  auto out_at = [&](int row, int d) {
-    const int i = (rb * R + row) / G, hq = rb * R + row - i * G;
-    return (uint16_t*)p.out.ptr + (int64_t)(first_token + i) * p.out.token_stride + (int64_t)(h * G + hq) * p.out.head_stride + d;
-  };
-  auto pack4 = [&](v4f y, float f, bool none) {
-    uint32_t bits[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) bits[i] = out_bits<O>(none ? 0.0f : y[i] * f);
-    return make_uint2(bits[0] | bits[1] << 16, bits[2] | bits[3] << 16);
-  };
-  const uint32_t first_slot = (uint32_t)(bh * per_group + rest - split), slot0 = (first_slot + split) * SLOT;
+  const Results<O, D, R> results{p, first_token, h, rb};
+  float* part = p.part + (int64_t)(bh * per_group + rest) * SLOT;
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
     const int r = w_row + 16 * t + c;
@@ -330,71 +335,105 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
       const float f = p.v_scale * 256.0f / sum;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        uint16_t* dst = out_at(r, E * (4 * g + i));
+        uint16_t* dst = results.out_at(r, E * (4 * g + i));
 #pragma unroll
         for (int e = 0; e < E; e += 4)
-          *(uint2*)(dst + e) = pack4(v4f{o[t][e][i], o[t][e + 1][i], o[t][e + 2][i], o[t][e + 3][i]}, f, sum == 0.0f);
+          *(uint2*)(dst + e) = results.pack4(v4f{o[t][e][i], o[t][e + 1][i], o[t][e + 2][i], o[t][e + 3][i]}, f, sum == 0.0f);
       }
-      if (p.lse && g == 0) store_lse(r, top, sum);
+      if (p.lse && g == 0) results.store_lse(r, top, sum);
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int e = 0; e < E; e += 4)
-          handoff_store4(parts, slot0 + r * D + E * (4 * g + i) + e, v4f{o[t][e][i], o[t][e + 1][i], o[t][e + 2][i], o[t][e + 3][i]});
-      if (g == 0) handoff_store4(parts, slot0 + R * D + 4 * r, v4f{top, sum, 0.0f, 0.0f});
+          *(v4f*)(part + r * D + E * (4 * g + i) + e) = v4f{o[t][e][i], o[t][e + 1][i], o[t][e + 2][i], o[t][e + 3][i]};
+      if (g == 0) *(v2f*)(part + R * D + 2 * r) = v2f{top, sum};
     }
-  }
-  if (p.splits == 1) return;
-  int* counter = p.arrived + ((int64_t)first_token * G + (int64_t)rb * R) * H + h;
-  if (!last_arrival(counter, p.splits, &sh_last)) return;
-  for (int k = tid; k < rows * (D / 4); k += 64 * WAVES) {
-    const int r = k / (D / 4), d = k % (D / 4) * 4;
-    v4f ms[kJoin], ys[kJoin];
-#pragma unroll
-    for (int i = 0; i < kJoin; ++i) {  // all in flight; splits past the last repeat it and count nothing
-      const uint32_t at = (first_slot + (uint32_t)min(i, p.splits - 1)) * SLOT;
-      ms[i] = handoff_load4(parts, at + R * D + 4 * r);
-      ys[i] = handoff_load4(parts, at + r * D + d);
-    }
-    float top = kNegInf, sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kJoin; ++i) top = __builtin_fmaxf(top, ms[i][0]);
-    v4f y = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < kJoin; ++i)
-      if (i < p.splits) {
-        const float f = ms[i][0] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(ms[i][0] - top);
-        sum += f * ms[i][1];
-        y += f * ys[i];
-      }
-    *(uint2*)out_at(r, d) = pack4(y, p.v_scale * 256.0f / sum, sum == 0.0f);
-    if (p.lse && d == 0) store_lse(r, top, sum);
   }
 }
 
-// Rows of a workgroup: 8 waves halve the decoding per row; 4 where no sequence fills more.
-int rows_waves(int64_t max_rows) { return max_rows > 128 ? 8 : 4; }
+// Joins the parts of split row blocks, with one thread for four dims of a row.  A kernel of its own, so that
+// the whole chip reads the parts: joined by the last workgroup of each block, 2 x 482 tokens, 8 heads on
+// 4 of 128 dims and a window of 781 took 67 us against 34.
+template <Out O, int D, int R>
+__global__ __launch_bounds__(256) void join_kernel(KvArgs p) {
+  constexpr int ROWS = 256 / (D / 4), SLOT = R * (D + 2), AT_ONCE = 8;
+  const int blocks_max = gridDim.x / (p.num_seqs * p.kv_heads * (R / ROWS));
+  const int unit = blockIdx.x / (R / ROWS), bh = unit / blocks_max;
+  const int b = bh / p.kv_heads, h = bh - b * p.kv_heads;
+  const int first_token = p.one_each ? b : seq_start(p, b);
+  const int q_len = p.one_each ? 1 : min(max(seq_start(p, b + 1) - first_token, 0), p.max_q);
+  const int blocks = (q_len * p.group + R - 1) / R, rb = blocks - 1 - (unit - bh * blocks_max);
+  if (rb < 0) return;
+  const int r = blockIdx.x % (R / ROWS) * ROWS + threadIdx.x / (D / 4), d = threadIdx.x % (D / 4) * 4;
+  if (r >= min(R, q_len * p.group - rb * R)) return;
+  const float* part = p.part + (int64_t)unit * p.splits * SLOT;
+  const int last = p.splits - 1;
+  float top = kNegInf, sum = 0.0f;
+  v4f y = {0, 0, 0, 0};
+  for (int s0 = 0; s0 <= last; s0 += AT_ONCE) {
+    v2f ms[AT_ONCE];
+    v4f ys[AT_ONCE];
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i) {  // all in flight; parts past the last repeat it and count nothing
+      const float* at = part + (int64_t)min(s0 + i, last) * SLOT;
+      ms[i] = *(const v2f*)(at + R * D + 2 * r);
+      ys[i] = *(const v4f*)(at + r * D + d);
+    }
+    float grown = top;
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i) grown = __builtin_fmaxf(grown, ms[i][0]);
+    const float f0 = top == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(top - grown);
+    sum *= f0;
+    y *= f0;
+    top = grown;
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i) {
+      if (s0 + i > last) continue;
+      const float f = ms[i][0] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(ms[i][0] - top);
+      sum += f * ms[i][1];
+      y += f * ys[i];
+    }
+  }
+  const Results<O, D, R> results{p, first_token, h, rb};
+  *(uint2*)results.out_at(r, d) = results.pack4(y, p.v_scale * 256.0f / sum, sum == 0.0f);
+  if (p.lse && d == 0) results.store_lse(r, top, sum);
+}
 
-template <Out O, int D>
+// Rows of a workgroup: 8 waves halve the decoding per row; 4 where no sequence fills more.
+template <Out O, int D, int WAVES>
 hipError_t launch(const KvArgs& a, int cus, hipStream_t stream) {
+  constexpr int R = 32 * WAVES;
   KvArgs args = a;
-  const int waves = rows_waves((int64_t)a.max_q * a.group), R = 32 * waves;
   const int64_t blocks = ((int64_t)a.max_q * a.group + R - 1) / R, groups = (int64_t)a.num_seqs * a.kv_heads;
   // units that exist, at most: ragged sequences leave some of the grid's without rows
   int64_t units = ((int64_t)a.num_tokens * a.group / R + a.num_seqs) * a.kv_heads;
   if (units > blocks * groups) units = blocks * groups;
-  const int64_t fill = (int64_t)cus * (8 / waves);  // workgroups that run at once
+  const int64_t fill = (int64_t)cus * (8 / WAVES);  // workgroups that run at once
   const int64_t tiles = ((int64_t)(a.window > 0 && a.window + a.max_q < a.max_kv ? a.window + a.max_q : a.max_kv) + kTile - 1) / kTile;
-  int64_t splits = (fill + units - 1) / units;
-  if (splits > tiles / 4) splits = tiles / 4;  // at least four tiles each
-  if (splits > kJoin) splits = kJoin;
-  if (splits < 1) splits = 1;
-  while (splits > 1 && blocks * groups * splits > 2 * fill) --splits;  // (the workspace's slots)
+  // The number of parts that takes the fewest tiles' time.  A workgroup's beginning and end cost about three
+  // tiles, the join two and one more for 8 parts.  At least two tiles per part; the workspace holds twice
+  // the workgroups that run at once.  (2 x 134 rows, 4 heads of 128, 2133 positions: 1 part 66 us, 7 parts 26.)
+  int64_t splits = 1, best = 0;
+  for (int64_t s = 1; s == 1 || (s <= tiles / 2 && blocks * groups * s <= 2 * fill); ++s) {
+    const int64_t cost = (units * s + fill - 1) / fill * ((tiles + s - 1) / s + 3) + (s > 1 ? 2 + s / 8 : 0);
+    if (s == 1 || cost < best) {
+      best = cost;
+      splits = s;
+    }
+  }
   args.splits = (int)splits;
   void* argv[] = {&args};
-  const void* fn = waves == 8 ? (const void*)&rows_kernel<O, D, 8> : (const void*)&rows_kernel<O, D, 4>;
-  return hipLaunchKernel(fn, dim3((unsigned)(blocks * groups * splits)), dim3(64 * waves), argv, 0, stream);
+  hipError_t err = hipLaunchKernel((const void*)&rows_kernel<O, D, WAVES>, dim3((unsigned)(blocks * groups * splits)),
+                                   dim3(64 * WAVES), argv, 0, stream);
+  if (err != hipSuccess || splits == 1) return err;
+  return hipLaunchKernel((const void*)&join_kernel<O, D, R>, dim3((unsigned)(blocks * groups * (R * (D / 4) / 256))), dim3(256),
+                         argv, 0, stream);
+}
+
+template <Out O, int D>
+hipError_t launch(const KvArgs& a, int cus, hipStream_t stream) {
+  return (int64_t)a.max_q * a.group > 128 ? launch<O, D, 8>(a, cus, stream) : launch<O, D, 4>(a, cus, stream);
 }
 
 }  // namespace
@@ -406,7 +445,7 @@ hipError_t kv_attend_rows_launch(const KvArgs& a, int dtype, int head_dim, int c
 
 size_t kv_rows_part_floats(const bsg_kv_problem& p, int cus) {
   if (p.max_tokens * (p.q_heads / p.kv_heads) <= 32) return 0;
-  return (size_t)2 * cus * 256 * (p.head_dim + 4);  // 2 x 8 waves per CU, 32 rows each
+  return (size_t)2 * cus * 256 * (p.head_dim + 2);  // 2 x 8 waves per CU, 32 rows each
 }
 
 }  // namespace bsg

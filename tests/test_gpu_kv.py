@@ -253,6 +253,51 @@ def test_attend_in_a_graph():
             assert torch.equal(out, eager), n
 
 
+@pytest.mark.parametrize("D,dtype", [(64, "bf16"), (128, "f16")])
+@pytest.mark.parametrize("kw", [{}, {"window": 300}, {"causal": False}], ids=str)
+@pytest.mark.parametrize("new,lens,G", [([9], [1500], 4), ([40, 3, 0, 21], [700, 64, 900, 129], 8), ([65, 10], [1100, 12], 2)])
+def test_many_rows_in_parts(new, lens, G, D, dtype, kw):
+    # few row blocks over long contexts: positions are split, some parts are empty for the shorter sequences
+    run_case(new, lens, H=1, G=G, D=D, dtype=dtype, P=32, seed=len(lens) + G, **kw)
+
+
+def test_nan_blocks_in_one_part():
+    def poison(c, pages):
+        c.part(pages[0][1000 // 16], 0, 3)[1, 1000 % 16] = 0x7F
+        c.part(pages[0][1195 // 16], 1, 3)[3, 1195 % 16] = 0x7F
+    got, _ = run_case([20, 1], [1200, 20], seed=17, edit=poison)
+    assert np.isnan(got[:20, :4, 16:32]).all() and not np.isnan(got[0, 4:]).any() and np.isnan(got[15, 4:, 48:64]).all()
+    got, _ = run_case([20, 1], [1200, 20], seed=18, edit=poison, window=190)
+    assert np.isnan(got[9, :4, 16:32]).all() and not np.isnan(got[10, :4]).any()
+
+
+def test_many_rows_in_parts_in_a_graph():
+    q_start, pages, n_pages = layout([30, 20], [900, 500], 16, 0)
+    c = filled([900, 500], 2, 64, 16, pages, n_pages, 1)
+    cache, pg, qs = dev(c.bytes), dev(pages), dev(q_start)
+    lens = dev(np.array([900, 500], np.int32))
+    q = torch.randn(50, 8, 64, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    out = torch.zeros_like(q)
+    with bsg.KVPlan(8, 2, 64, 16, n_pages, 64) as plan:
+        batch = bsg.KVBatch(qs, lens, pg, 50, 30, 900)
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            plan.attend(batch, q, cache, out)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            plan.attend(batch, q, cache, out)
+        for n in (900, 333, 30, 64):
+            lens.copy_(torch.tensor([n, n // 2]))
+            eager = torch.zeros_like(q)
+            plan.attend(batch, q, cache, eager)
+            torch.cuda.synchronize()
+            out.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, eager), n
+
+
 # ------------------------------------------------------------------------------------------------ append
 def append_case(new, lens, H, G, D, P, dtype, rope, interleaved, seed, k_scale=1.0, v_scale=1.0, special=None, scaling=None):
     q_start, pages, n_pages = layout(new, lens, P, seed)
