@@ -2,9 +2,10 @@
 //
 // Few tokens read many weights, so the layer is bound by the bytes of the chosen experts' weights,
 // and every kernel streams weight rows through registers into v_mfma_f32_16x16x32: rows of weights are
-// the product's first operand (16 rows), tokens the second (16 columns, unused ones zero).  A lane loads the codes of 32 consecutive k of one row (16 bytes of E2M1, 32 of E4M3) and
-// uses them in four products; the k order of a product is free, and the tokens' operand follows it.  A workgroup's waves take alternate slabs of 128 k and are
-// summed through LDS.
+// the product's first operand (16 rows), tokens the second (16 columns, unused ones zero).  A lane loads
+// the codes of 32 consecutive k of one row (16 bytes of E2M1, 32 of E4M3) and uses them in four products;
+// the k order of a product is free, and the tokens' operand follows it.  A workgroup's waves take alternate
+// slabs of 128 k and are summed through LDS.
 //
 // Decoded weights are exact: E2M1 * E4M3 has at most 6 significant bits, E4M3 * 2^e has 4.  MXFP8
 // weights decode to bf16, whose exponents hold any E8M0 scale.  NVFP4 weights decode to fp16 for the
@@ -16,6 +17,8 @@
 //
 // Three launches: the router must know every token's choice before weights can be read, and the second
 // product needs all of an expert's SiLU(gate) up.
+#include <type_traits>
+
 #include "codec.h"
 #include "handoff.h"
 #include "moe.h"
@@ -87,20 +90,18 @@ static_assert(BSG_MOE_MAX_TOKENS <= 64, "a bit for each token");
 static_assert(kMaxChoices <= kRouterThreads && BSG_MOE_MAX_EXPERTS <= kRouterThreads, "one thread for each");
 static_assert(BSG_MOE_MAX_TOP_K <= 64, "a lane for each of a token's choices");
 
-// The top k of one token, by a wave: lane i holds the logits of experts R i .. R i + R - 1, and k times
-// the largest is found and taken out (of equal ones the lowest lane's, and its lowest).  Lane i ends with
-// the expert of rank i and its weight (i < K); the last rank looked for is `last`.
-template <int R, class Load>
-__device__ __forceinline__ void top_k(int E, int last, bool keep, int lane, Load load, int& expert, float& weight) {
+// The top k of one token, by a wave: lane i holds the logits x of experts R i .. R i + R - 1 (the last
+// expert's again beyond it), and k times the largest is found and taken out (of equal ones the lowest
+// lane's, and its lowest).  Lane i ends with the expert of rank i and its weight (i < K); the last rank
+// looked for is `last`.
+template <int R>
+__device__ __forceinline__ void top_k(const float x[R], int E, int last, bool keep, int lane, int& expert, float& weight) {
   uint32_t key[R];
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int e = lane * R + r;
-    const float x = load(min(e, E - 1));
-    key[r] = e < E ? order_key(x) : 0u;
-  }
-  float all = 0.0f, mine = 0.0f;
+  for (int r = 0; r < R; ++r) key[r] = lane * R + r < E ? order_key(x[r]) : 0u;
+  float all = 0.0f;
   uint32_t top = 0;
+  uint32_t mine = 0;
   expert = 0;
   for (int k = 0; k <= last; ++k) {
     uint32_t best = key[0];
@@ -119,21 +120,24 @@ __device__ __forceinline__ void top_k(int E, int last, bool keep, int lane, Load
       }
     }
     int place = 0;
-    bool taken = lane != owner;
+    if constexpr (R == 1) {
+      key[0] = lane == owner ? 0u : key[0];
+    } else {
+      bool taken = lane != owner;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const bool hit = !taken && key[r] == most;
-      place = hit ? r : place;
-      key[r] = hit ? 0u : key[r];
-      taken |= hit;
+      for (int r = 0; r < R; ++r) {
+        const bool hit = !taken && key[r] == most;
+        place = hit ? r : place;
+        key[r] = hit ? 0u : key[r];
+        taken |= hit;
+      }
+      place = __builtin_amdgcn_readlane(place, owner);
     }
-    const int e = owner * R + __builtin_amdgcn_readlane(place, owner);
-    if (lane == k) {
-      expert = e;
-      mine = __builtin_amdgcn_exp2f((key_value(most) - key_value(top)) * kLog2e);
-    }
+    expert = lane == k ? owner * R + place : expert;
+    mine = lane == k ? most : mine;
   }
-  weight = mine / (keep ? all : wave_sum(mine));
+  weight = lane <= last ? __builtin_amdgcn_exp2f((key_value(mine) - key_value(top)) * kLog2e) : 0.0f;
+  weight /= keep ? all : wave_sum(weight);
 }
 
 // Top k of every token and the tokens of every expert; one workgroup, a wave for each token.  A choice's
@@ -142,12 +146,24 @@ template <int R>
 __device__ void choose(const MoeArgs& p, Choice& sh) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int E = p.experts, K = p.top_k, T = p.tokens, choices = T * K;
+  constexpr int N = BSG_MOE_MAX_TOKENS / kRouterWaves;
+  float x[N][R];  // the logits of all of the wave's tokens, in flight together
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (wave + i * kRouterWaves < T) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        x[i][r] = handoff_load(p.logits + (size_t)(wave + i * kRouterWaves) * E + min(lane * R + r, E - 1));
+    }
   if (tid < E) sh.tokens_of[tid] = 0;
   __syncthreads();
-  for (int t = wave; t < T; t += kRouterWaves) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int t = wave + i * kRouterWaves;
+    if (t >= T) break;
     int expert;
     float weight;
-    top_k<R>(E, K - 1, p.keep, lane, [&](int e) { return handoff_load(p.logits + (size_t)t * E + e); }, expert, weight);
+    top_k<R>(x[i], E, K - 1, p.keep, lane, expert, weight);
     if (lane < K) {
       const int c = t * K + lane;
       sh.chosen[c] = expert;
@@ -517,9 +533,15 @@ __global__ __launch_bounds__(kThreads, NV ? 4 : 3) void gate_up_kernel(MoeArgs p
     const int lane = threadIdx.x & 63, y = blockIdx.y, last = blockIdx.x ? y : p.top_k - 1;
     int expert;
     float weight;
-    auto load = [&](int e) { return p.logits[e]; };
-    if (p.experts <= 64) top_k<1>(p.experts, last, p.keep, lane, load, expert, weight);
-    else top_k<BSG_MOE_MAX_EXPERTS / 64>(p.experts, last, p.keep, lane, load, expert, weight);
+    auto choose_one = [&](auto each) {
+      constexpr int R = decltype(each)::value;
+      float x[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) x[r] = p.logits[min(lane * R + r, p.experts - 1)];
+      top_k<R>(x, p.experts, last, p.keep, lane, expert, weight);
+    };
+    if (p.experts <= 64) choose_one(std::integral_constant<int, 1>{});
+    else choose_one(std::integral_constant<int, BSG_MOE_MAX_EXPERTS / 64>{});
     slot = int4{__builtin_amdgcn_readlane(expert, y), y, 1, 0};
     if (blockIdx.x == 0 && (int)threadIdx.x == y) {
       p.slots[y] = slot;
@@ -659,9 +681,8 @@ hipError_t launch(const MoeArgs& a, hipStream_t stream) {
   MoeArgs args = a;
   void* argv[] = {&args};
   const unsigned tiles = (a.experts + 15) / 16 * ((a.tokens + 15) / 16);
-  hipError_t e = hipLaunchKernel((const void*)&router_kernel<NV, F16>,
-                                 dim3(tiles + a.tokens), dim3(kRouterThreads), argv, 0,
-                                 stream);
+  hipError_t e = hipLaunchKernel((const void*)&router_kernel<NV, F16>, dim3(tiles + a.tokens),
+                                 dim3(kRouterThreads), argv, 0, stream);
   if (e != hipSuccess) return e;
   // at most one slot per choice, and one per expert and kSlotRows choices
   const int choices = a.tokens * a.top_k, bound = a.experts + choices / kSlotRows;
