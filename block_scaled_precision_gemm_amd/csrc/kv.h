@@ -24,6 +24,7 @@ struct KvArgs {
   float k_inv, v_inv, v_scale, k_scale;
   // batch
   int num_seqs, num_tokens, max_q, max_kv;
+  int mixed;         // attention: 1: sequences of up to kFewRows rows are the few-row kernel's, others the many-row kernel's
   int one_each;      // 1: every sequence has exactly one new token (token t is sequence t)
   const int* q_start;
   const int* kv_len;
@@ -60,8 +61,6 @@ __device__ __forceinline__ int seq_start(const KvArgs& p, int b) {
 __device__ __forceinline__ int seq_len(const KvArgs& p, int b) { return min(max(p.kv_len[b], 0), p.max_kv); }
 
 __device__ __forceinline__ int clamp_page(const KvArgs& p, int page) { return min(max(page, 0), p.num_pages - 1); }
-
-typedef hipError_t (*KvLaunchFn)(const KvArgs& args, hipStream_t stream);
 
 // dtype: 0 bf16, 1 f16.  Each returns the launch status; D is 64 or 128.
 hipError_t kv_append_launch(const KvArgs& a, int dtype, int head_dim, bool with_q, hipStream_t stream);

@@ -10,6 +10,7 @@ typedef float v2f __attribute__((ext_vector_type(2)));
 constexpr int kTile = 64;       // positions of a tile
 constexpr float kPBias = 14.0f; // P is held as 2^14 P
 constexpr int kJoin = 16;       // parts joined at a time
+constexpr int kFewRows = 32;    // most query rows per sequence and key/value head of the few-row kernel
 constexpr float kNegInf = -__builtin_inff();
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 

@@ -57,14 +57,17 @@ __device__ __forceinline__ int wave_scan(int x) {
 struct Span {
   int q_len, len;  // new tokens and context of the sequence
   int lo, tiles;   // first position read (a multiple of 16), and tiles of each of its units
+  int blocks;      // its blocks of R rows
 };
 
+template <int R>
 __device__ __forceinline__ Span span_of(const KvArgs& p, int b) {
   Span s;
   s.len = seq_len(p, b);
   s.q_len = p.one_each ? 1 : min(max(seq_start(p, b + 1) - seq_start(p, b), 0), p.max_q);
   s.lo = p.window > 0 ? max(0, s.len - s.q_len - p.window + 1) & ~15 : 0;
   s.tiles = max(1, (s.len - s.lo + kTile - 1) / kTile);
+  s.blocks = p.mixed && s.q_len * p.group > kFewRows ? 0 : (s.q_len * p.group + R - 1) / R;
   return s;
 }
 
@@ -108,8 +111,8 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
   for (int i = 0; i < per_thread; ++i) {
     const int b = tid * per_thread + i;
     if (b < p.num_seqs) {
-      const Span s = span_of(p, b);
-      const int n = (s.q_len * G + R - 1) / R * H;
+      const Span s = span_of<R>(p, b);
+      const int n = s.blocks * H;
       tiles += n * s.tiles;
       units += n;
     }
@@ -125,8 +128,8 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
   for (int i = 0; i < per_thread; ++i) {
     const int b = tid * per_thread + i;
     if (b < p.num_seqs) {
-      const Span s = span_of(p, b);
-      mine += (s.q_len * G + R - 1) / R * H * items(s);
+      const Span s = span_of<R>(p, b);
+      mine += s.blocks * H * items(s);
     }
   }
   int total, unused;
@@ -138,8 +141,8 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
   if (before <= run0 && run0 < before + mine) {  // the one thread whose sequences hold the run's start
     int at = before, b = tid * per_thread;
     for (;; ++b) {
-      const Span s = span_of(p, b);
-      const int n = (s.q_len * G + R - 1) / R * H * items(s);
+      const Span s = span_of<R>(p, b);
+      const int n = s.blocks * H * items(s);
       if (run0 < at + n) break;
       at += n;
     }
@@ -151,13 +154,12 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
   int seq0 = __builtin_amdgcn_readfirstlane(sh_at[1]);  // line position of sequence b's first item
 
   for (int x = run0; x < run1;) {
-    Span s = span_of(p, b);
-    int blocks = (s.q_len * G + R - 1) / R, len = items(s);
-    while (x >= seq0 + blocks * H * len) {
-      seq0 += blocks * H * len;
+    Span s = span_of<R>(p, b);
+    int len = items(s);
+    while (x >= seq0 + s.blocks * H * len) {
+      seq0 += s.blocks * H * len;
       ++b;
-      s = span_of(p, b);
-      blocks = (s.q_len * G + R - 1) / R;
+      s = span_of<R>(p, b);
       len = items(s);
     }
     const int unit = (x - seq0) / len;
@@ -525,7 +527,8 @@ template <Out O, int D>
 hipError_t launch(const KvArgs& a, int cus, hipStream_t stream) {
   KvArgs args = a;
   void* argv[] = {&args};
-  const int64_t rows = (int64_t)a.max_q * a.group;
+  // Of a mixed batch most short sequences have one new token: 16 rows, and two blocks for the others.
+  const int64_t rows = (int64_t)(a.mixed ? 1 : a.max_q) * a.group;
   const int R = rows <= 16 ? 16 : 32;
   const int64_t context = a.window > 0 ? (int64_t)a.window + a.max_q + 16 : a.max_kv;
   const int64_t tiles = ((context < a.max_kv ? context : a.max_kv) + kTile - 1) / kTile + 1;
@@ -539,8 +542,22 @@ hipError_t launch(const KvArgs& a, int cus, hipStream_t stream) {
 
 }  // namespace
 
-hipError_t kv_attend_launch(const KvArgs& a, int dtype, int head_dim, int cus, hipStream_t stream) {
-  if ((int64_t)a.max_q * a.group > 32) return kv_attend_rows_launch(a, dtype, head_dim, cus, stream);
+// One token and whole prompts may share a batch.  Sequences of up to kFewRows rows are then left to the
+// few-row kernel and the others to the many-row kernel, which would walk a long context for a few rows with
+// one workgroup (a prompt of 512 tokens beside 63 single tokens at 1000 to 16000 positions, 32 heads on 8 of
+// 128 dims: 2073 us by that kernel alone, 228 by both).  The host does not know the sequences' tokens: it
+// looks for uneven batches in which the sequences besides a longest one must be short on average, or of eight
+// and more, where a launch that finds nothing to do (4 us) is small against the rest.
+hipError_t kv_attend_launch(const KvArgs& args, int dtype, int head_dim, int cus, hipStream_t stream) {
+  KvArgs a = args;
+  a.mixed = 0;
+  if ((int64_t)a.max_q * a.group > kFewRows) {
+    const int64_t others = (int64_t)(a.num_tokens - a.max_q) * a.group;
+    a.mixed = a.group <= kFewRows && a.num_tokens < (int64_t)a.num_seqs * a.max_q &&
+              (a.num_seqs >= 8 || others <= (int64_t)kFewRows * (a.num_seqs - 1));
+    const hipError_t e = kv_attend_rows_launch(a, dtype, head_dim, cus, stream);
+    if (e != hipSuccess || !a.mixed) return e;
+  }
   if (head_dim == 64) return dtype ? launch<Out::F16, 64>(a, cus, stream) : launch<Out::BF16, 64>(a, cus, stream);
   return dtype ? launch<Out::F16, 128>(a, cus, stream) : launch<Out::BF16, 128>(a, cus, stream);
 }

@@ -77,7 +77,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
   const int len = seq_len(p, b);
   const int q_len = p.one_each ? 1 : min(max(seq_start(p, b + 1) - first_token, 0), p.max_q);
   const int blocks = (q_len * G + R - 1) / R, rb = blocks - 1 - rest / p.splits;
-  if (rb < 0) return;
+  if (rb < 0 || (p.mixed && q_len * G <= kFewRows)) return;
   const int rows = min(R, q_len * G - rb * R), pos0 = len - q_len;
   const int i_first = rb * R / G, i_last = (rb * R + rows - 1) / G;
   const int lo = p.window > 0 ? max(0, pos0 + i_first - p.window + 1) : 0;
@@ -364,7 +364,7 @@ __global__ __launch_bounds__(256) void join_kernel(KvArgs p) {
   const int first_token = p.one_each ? b : seq_start(p, b);
   const int q_len = p.one_each ? 1 : min(max(seq_start(p, b + 1) - first_token, 0), p.max_q);
   const int blocks = (q_len * p.group + R - 1) / R, rb = blocks - 1 - (unit - bh * blocks_max);
-  if (rb < 0) return;
+  if (rb < 0 || (p.mixed && q_len * p.group <= kFewRows)) return;
   const int r = blockIdx.x % (R / ROWS) * ROWS + threadIdx.x / (D / 4), d = threadIdx.x % (D / 4) * 4;
   if (r >= min(R, q_len * p.group - rb * R)) return;
   const float* part = p.part + (int64_t)unit * p.splits * SLOT;
@@ -407,13 +407,15 @@ hipError_t launch(const KvArgs& a, int cus, hipStream_t stream) {
   KvArgs args = a;
   const int64_t blocks = ((int64_t)a.max_q * a.group + R - 1) / R, groups = (int64_t)a.num_seqs * a.kv_heads;
   // units that exist, at most: ragged sequences leave some of the grid's without rows
-  int64_t units = ((int64_t)a.num_tokens * a.group / R + a.num_seqs) * a.kv_heads;
+  const int64_t rows = (int64_t)a.num_tokens * a.group, most = a.mixed ? rows / kFewRows : a.num_seqs;
+  int64_t units = (rows / R + (most < a.num_seqs ? most : a.num_seqs)) * a.kv_heads;
   if (units > blocks * groups) units = blocks * groups;
   const int64_t fill = (int64_t)cus * (8 / WAVES);  // workgroups that run at once
   const int64_t tiles = ((int64_t)(a.window > 0 && a.window + a.max_q < a.max_kv ? a.window + a.max_q : a.max_kv) + kTile - 1) / kTile;
   // The number of parts that takes the fewest tiles' time.  A workgroup's beginning and end cost about three
   // tiles, the join two and one more for 8 parts.  At least two tiles per part; the workspace holds twice
-  // the workgroups that run at once.  (2 x 134 rows, 4 heads of 128, 2133 positions: 1 part 66 us, 7 parts 26.)
+  // the workgroups that run at once.  (2 x 134 tokens, 8 heads on 4 of 128 dims, 2133 positions: one part
+  // 86 us, so 26 us; one sequence of 1575 tokens, 4 heads on 1, 3756 positions: 141 and 40 us.)
   int64_t splits = 1, best = 0;
   for (int64_t s = 1; s == 1 || (s <= tiles / 2 && blocks * groups * s <= 2 * fill); ++s) {
     const int64_t cost = (units * s + fill - 1) / fill * ((tiles + s - 1) / s + 3) + (s > 1 ? 2 + s / 8 : 0);
@@ -444,7 +446,7 @@ hipError_t kv_attend_rows_launch(const KvArgs& a, int dtype, int head_dim, int c
 }
 
 size_t kv_rows_part_floats(const bsg_kv_problem& p, int cus) {
-  if (p.max_tokens * (p.q_heads / p.kv_heads) <= 32) return 0;
+  if (p.max_tokens * (p.q_heads / p.kv_heads) <= kFewRows) return 0;
   return (size_t)2 * cus * 256 * (p.head_dim + 2);  // 2 x 8 waves per CU, 32 rows each
 }
 

@@ -261,6 +261,17 @@ def test_many_rows_in_parts(new, lens, G, D, dtype, kw):
     run_case(new, lens, H=1, G=G, D=D, dtype=dtype, P=32, seed=len(lens) + G, **kw)
 
 
+@pytest.mark.parametrize("D,dtype,G", [(128, "bf16", 4), (64, "f16", 20)])
+@pytest.mark.parametrize("kw", [{}, {"window": 40}, {"causal": False}], ids=str)
+@pytest.mark.parametrize("new,lens", [
+    ([60, 1, 1], [150, 300, 17]),                                         # one prompt, single tokens
+    ([1, 3, 0, 45, 8, 9, 1, 33, 2], [700, 3, 40, 45, 8, 200, 0, 90, 65]),  # either side of the kernels' limit, empty ones
+    ([1] * 30 + [34] + [1] * 30, [5 + 7 * i for i in range(61)]),
+])
+def test_mixed_batches(new, lens, D, dtype, G, kw):
+    run_case(new, lens, H=1, G=G, D=D, dtype=dtype, seed=len(lens) + G, **kw)
+
+
 def test_nan_blocks_in_one_part():
     def poison(c, pages):
         c.part(pages[0][1000 // 16], 0, 3)[1, 1000 % 16] = 0x7F
