@@ -14,6 +14,8 @@
 // Where the rows alone give too few workgroups, positions are split and a second kernel joins the parts.
 //
 // Bound: matrix products and the softmax's and decoding's vector operations, at similar rates.
+#include <type_traits>
+
 #include "kv_attend.h"
 
 namespace bsg {
@@ -52,7 +54,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
     v4i v[2][E][64];   // [32 positions][dims E m + e][lane]
   };
   __shared__ Buffer sh[2];
-  __shared__ int sh_nan[2];  // sh_nan: the buffer's tile, if it has such a NaN block (below)
+  __shared__ int sh_nan[4];  // tile n's first position at n % 4, if it has such a NaN block (below)
 
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int c = lane & 15, g = lane >> 4;
@@ -88,7 +90,6 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
 
   // ---- queries
   const int w_row = 32 * wave;  // the wave's first row
-  const bool busy = w_row < rows;
   v8h q[RT][NJ];
   float mul[RT];
   int pos[RT];
@@ -116,54 +117,62 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
   if (t_begin < t_end) {
     const int* table = p.pages + (int64_t)b * p.pages_stride;
     const int last_pos = hi - 1, chunk = L::chunk(P);
-    // The tile's work is cut in 8 tasks: 0 .. 3 decode the values of positions 32 (task / 2) .. + 31 for
-    // even or odd dims, 4 .. 7 the keys of 16 positions each.  Wave w takes tasks w, w + WAVES, ...
-    constexpr bool kBoth = WAVES == 4;
-    const bool do_v = kBoth || wave < 4, do_k = kBoth || wave >= 4;
-    const int vt = wave & 3, kt = wave & 3;
+    // Decoding a tile is cut in tasks for four waves: the values of positions 32 (task / 2) .. + 31 for even
+    // or odd dims, and the keys of 16 positions.  Of eight waves the first four decode values, the others keys.
+    const int task = wave & 3;
     uint32_t kq[NJ], ks = 0, vq[2][4], vs[2];
-    // page numbers of the next 64 pages, one per lane
+    // Page numbers of 64 pages from page_base on, one per lane
     int page_base = t_begin >> p.page_shift;
     int page_ids = clamp_page(p, table[min(page_base + lane, last_pos >> p.page_shift)]);
-    const uint8_t* head = p.cache + (int64_t)h * chunk;
-    auto group_at = [&](int t, int& slot) -> const uint8_t* {
-      t = min(t, last_pos & ~15);
-      slot = t & (P - 1);
-      const int page = t >> p.page_shift;
-      if (page - page_base >= 64) {
-        page_base = page;
+    auto keep_pages = [&](int t0) {  // those of two tiles from t0 on (at most 9) are among them
+      const int first = min(t0, last_pos) >> p.page_shift;
+      if (first - page_base >= 48) {
+        page_base = first;
         page_ids = clamp_page(p, table[min(page_base + lane, last_pos >> p.page_shift)]);
       }
-      return head + (int64_t)__builtin_amdgcn_readlane(page_ids, page - page_base) * p.page_stride;
     };
-    auto load = [&](int t0) {
-      if (do_v) {
+    const uint8_t* head = p.cache + (int64_t)h * chunk;
+    auto group_at = [&](int t, int& slot) -> const uint8_t* {  // (clamped into the context)
+      t = min(t, last_pos & ~15);
+      slot = t & (P - 1);
+      return head + (int64_t)__builtin_amdgcn_readlane(page_ids, (t >> p.page_shift) - page_base) * p.page_stride;
+    };
+    // a lane's offsets from a group's codes and scales
+    const uint32_t v_lane = 4 * g * L::kRow + c * (E / 2), vs_lane = (c * E / 16) * P + 4 * g;
+    const uint32_t k_lane = c * L::kRow + g * (4 * NJ), ks_lane = c * L::kBlocks + g * (D / 64);
+    // g for paths that few tiles take: not known to be the same in every tile, so that nothing formed from it
+    // is kept in registers throughout
+    auto rare_g = [&] {
+      int x = g;
+      asm volatile("" : "+v"(x));
+      return x;
+    };
+    auto load_v = [&](int t0) __attribute__((always_inline)) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          int slot;
-          const uint8_t* at = group_at(t0 + 32 * (vt >> 1) + 16 * u, slot);
-          const uint8_t* vp = at + L::v_codes(P) + (slot + 4 * g) * L::kRow + c * (E / 2);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            vq[u][j] = E == 8 ? *(const uint32_t*)(vp + j * L::kRow) : *(const uint16_t*)(vp + j * L::kRow);
-          vs[u] = *(const uint32_t*)(at + L::v_scales(P) + (c * E / 16) * P + slot + 4 * g);
-        }
-      }
-      if (do_k) {
+      for (int u = 0; u < 2; ++u) {
         int slot;
-        const uint8_t* at = group_at(t0 + 16 * kt, slot);
-        const uint8_t* kp = at + (slot + c) * L::kRow + g * (4 * NJ);
-        if constexpr (D == 128) {
-          const v4i w = *(const v4i*)kp;
+        const uint8_t* at = group_at(t0 + 32 * (task >> 1) + 16 * u, slot);
+        const uint8_t *codes = at + L::v_codes(P) + slot * L::kRow, *scales = at + L::v_scales(P) + slot;
 #pragma unroll
-          for (int j = 0; j < NJ; ++j) kq[j] = (uint32_t)w[j];
-          ks = *(const uint16_t*)(at + L::k_scales(P) + (slot + c) * L::kBlocks + 2 * g);
-        } else {
-          const uint2 w = *(const uint2*)kp;
-          kq[0] = w.x;
-          kq[1] = w.y;
-          ks = at[L::k_scales(P) + (slot + c) * L::kBlocks + g];
-        }
+        for (int j = 0; j < 4; ++j)
+          vq[u][j] = E == 8 ? *(const uint32_t*)(codes + v_lane + j * L::kRow) : *(const uint16_t*)(codes + v_lane + j * L::kRow);
+        vs[u] = *(const uint32_t*)(scales + vs_lane);
+      }
+    };
+    auto load_k = [&](int t0) __attribute__((always_inline)) {
+      int slot;
+      const uint8_t* at = group_at(t0 + 16 * task, slot);
+      const uint8_t *codes = at + slot * L::kRow, *scales = at + L::k_scales(P) + slot * L::kBlocks;
+      if constexpr (D == 128) {
+        const v4i w = *(const v4i*)(codes + k_lane);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) kq[j] = (uint32_t)w[j];
+        ks = *(const uint16_t*)(scales + ks_lane);
+      } else {
+        const uint2 w = *(const uint2*)(codes + k_lane);
+        kq[0] = w.x;
+        kq[1] = w.y;
+        ks = scales[ks_lane];
       }
     };
     // some row of the workgroup does not see all of the tile at t0
@@ -171,156 +180,216 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
     auto partly_hidden = [&](int t0) {
       return t0 + kTile - 1 > min(all_first, t_end - 1) || (p.window > 0 && t0 <= any_last - p.window);
     };
-    auto decode = [&](int t0, int buf) {
-      if (do_v) {
-        if (partly_hidden(t0)) {
-          // positions outside the workgroup's count as zero, whatever their slots hold; NaN blocks that
-          // only some rows see are taken out and given to those rows by the waves
-          uint32_t bad = 0;
+    // Of a tile that is partly hidden, positions outside the workgroup's count as zero, whatever their slots hold,
+    // and NaN blocks that only some rows see are taken out and given to those rows by the waves (take_nans).
+    auto mask_v = [&](int t0) __attribute__((always_inline)) {
+      if (!partly_hidden(t0)) return;
+      const int g4 = 4 * rare_g();
+      uint32_t bad = 0;
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            uint32_t keep = 0;
+      for (int u = 0; u < 2; ++u) {
+        uint32_t keep = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int at = t0 + 32 * (vt >> 1) + 16 * u + 4 * g + i;
-              if (at >= lo && at < t_end) keep |= 0xFFu << (8 * i);
-            }
-            vs[u] &= keep;
-            const uint32_t hit = ((vs[u] + 0x01010101u) & 0x80808080u) >> 7;
-            bad |= hit;
-            vs[u] &= ~(hit * 0x7Fu);
-          }
-          if (__any(bad) && lane == 0) sh_nan[buf] = t0;
+        for (int i = 0; i < 4; ++i) {
+          const int at = t0 + 32 * (task >> 1) + 16 * u + g4 + i;
+          if (at >= lo && at < t_end) keep |= 0xFFu << (8 * i);
         }
-        const int odd = vt & 1;
-        v4i frag[E / 2];
+        vs[u] &= keep;
+        const uint32_t hit = ((vs[u] + 0x01010101u) & 0x80808080u) >> 7;
+        bad |= hit;
+        vs[u] &= ~(hit * 0x7Fu);
+      }
+      if (__any(bad) && lane == 0) sh_nan[(t0 - t_begin) / kTile & 3] = t0;
+    };
+    // Fragment e of the wave's decoded values (positions pairs[2u], pairs[2u + 1]: u = 0, 1), and j of its keys
+    uint32_t pairs[4];
+    v2h v_s[4];
+    const int odd = task & 1, down = 4 * odd;
+    auto decode_v = [&](int e, int buf) __attribute__((always_inline)) {
+      if (e == 0) {
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj) {
           const int u = jj / 2, j = (jj & 1) * 2;
-          const v2h s2 = __builtin_bit_cast(v2h, (jj & 1) ? scale_pair<kHigh>(vs[u]) : scale_pair<kLow>(vs[u]));
-          const uint32_t a = vq[u][j], bb = vq[u][j + 1], mask = 0x0F0F0F0Fu;
-          const uint32_t pairs = odd ? ((a >> 4) & mask) | (bb & ~mask) : (a & mask) | ((bb << 4) & ~mask);
+          v_s[jj] = __builtin_bit_cast(v2h, (jj & 1) ? scale_pair<kHigh>(vs[u]) : scale_pair<kLow>(vs[u]));
+          const uint32_t mask = 0x0F0F0F0Fu;
+          pairs[jj] = ((vq[u][j] >> down) & mask) | ((vq[u][j + 1] << (4 - down)) & ~mask);
+        }
+      }
+      v4i frag;
 #pragma unroll
-          for (int e = 0; e < E / 2; ++e) frag[e][jj] = __builtin_bit_cast(int, fp4_pair(pairs, e) * s2);
+      for (int jj = 0; jj < 4; ++jj) frag[jj] = __builtin_bit_cast(int, fp4_pair(pairs[jj], e) * v_s[jj]);
+      sh[buf].v[task >> 1][2 * e + odd][lane] = frag;
+    };
+    auto decode_k = [&](int j, int buf) __attribute__((always_inline)) {
+      const uint32_t sp = scale_pair<kLow>(ks);
+      sh[buf].k[task][j][lane] = e2m1x8_scaled_f16x8(kq[j], j < 2 ? f16x2_splat_lo(sp) : f16x2_splat_hi(sp));
+    };
+    v4f sc[RT][4];
+    v8h pt[RT][2];
+    if (tid < 4) sh_nan[tid] = -1;
+    // before the first tile there are no weights and values: zeros
+#pragma unroll
+    for (int t = 0; t < RT; ++t) pt[t][0] = pt[t][1] = v8h{};
+    for (int i = tid; i < 2 * E * 64; i += 64 * WAVES) (&sh[1].v[0][0][0])[i] = v4i{0, 0, 0, 0};
+    __syncthreads();
+    // A slot's products: the last tile's outputs, then (SCORES) this tile's scores, each fragment read from LDS
+    // kFly fragments before its two products.  Between them the wave decodes its part of this tile's values into
+    // buffer buf and of the next tile's keys into the other, and loads the following ones: its vector operations
+    // run beside its products.
+    auto products = [&](auto scores, auto do_v, auto do_k, int t0, int buf) __attribute__((always_inline)) {
+      constexpr int NO = 2 * E, N = NO + (scores.value ? 4 * NJ : 0);
+      constexpr int NV = do_v.value ? E / 2 : 0, NU = NV + (do_k.value ? NJ : 0);
+      constexpr int kFly = 6;
+      v8h frag[kFly];
+      auto read = [&](int i) {
+        return __builtin_bit_cast(v8h, i < NO ? sh[buf ^ 1].v[i / E][i % E][lane] : sh[buf].k[(i - NO) % 4][(i - NO) / 4][lane]);
+      };
+#pragma unroll
+      for (int i = 0; i < kFly; ++i) frag[i] = read(i);
+      __builtin_amdgcn_sched_group_barrier(0x100, kFly, 0);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const v8h a = frag[i % kFly];
+        if (i + kFly < N) frag[i % kFly] = read(i + kFly);
+        if (i < NO) {
+#pragma unroll
+          for (int t = 0; t < RT; ++t) o[t][i % E] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pt[t][i / E], o[t][i % E], 0, 0, 0);
+        } else {
+          const int j = (i - NO) / 4, gr = (i - NO) % 4;
+#pragma unroll
+          for (int t = 0; t < RT; ++t)
+            sc[t][gr] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, q[t][j], j ? sc[t][gr] : v4f{0, 0, 0, 0}, 0, 0, 0);
         }
 #pragma unroll
-        for (int e = 0; e < E / 2; ++e) sh[buf].v[vt >> 1][2 * e + odd][lane] = frag[e];
-      }
-      if (do_k) {
-        const uint32_t sp = scale_pair<kLow>(ks), sp0 = f16x2_splat_lo(sp), sp1 = f16x2_splat_hi(sp);
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) sh[buf].k[kt][j][lane] = e2m1x8_scaled_f16x8(kq[j], j < 2 ? sp0 : sp1);
+        for (int u = 0; u < NU; ++u)
+          if (i == (u + 1) * N / (NU + 2)) {
+            if (u < NV) decode_v(u, buf);
+            else decode_k(u - NV, buf ^ 1);
+          }
+        if (NU && i == (NU + 1) * N / (NU + 2)) {
+          if (do_v.value) load_v(t0 + kTile);
+          if (do_k.value) load_k(t0 + 2 * kTile);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, RT, 0);
+        if (i + kFly < N) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
       }
     };
-    if (tid < 2) sh_nan[tid] = -1;
-    load(t_begin);
-    __syncthreads();
-    decode(t_begin, 0);
-    load(t_begin + kTile);  // (clamped into the context)
-    __syncthreads();
-    int buf = 0;
-    for (int t0 = t_begin; t0 < t_end; t0 += kTile, buf ^= 1) {
-      const bool mine = busy && t0 <= w_last && !(p.window > 0 && t0 + kTile - 1 <= w_first - p.window);
-      v4f sc[RT][4];
-      if (mine) {
+    auto softmax = [&](int t0) __attribute__((always_inline)) {
+      const bool edge = t0 + kTile - 1 > min(w_first, t_end - 1) || (p.window > 0 && t0 <= w_last - p.window);
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
-#pragma unroll
-          for (int gr = 0; gr < 4; ++gr) {
-            const v8h a = __builtin_bit_cast(v8h, sh[buf].k[gr][j][lane]);
-#pragma unroll
-            for (int t = 0; t < RT; ++t)
-              sc[t][gr] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, q[t][j], j ? sc[t][gr] : v4f{0, 0, 0, 0}, 0, 0, 0);
-          }
-      }
-      if (t0 + kTile < t_end) {
-        decode(t0 + kTile, buf ^ 1);
-        if (t0 + 2 * kTile < t_end) load(t0 + 2 * kTile);
-      }
-      if (mine) {
-        const bool edge = t0 + kTile - 1 > min(w_first, t_end - 1) || (p.window > 0 && t0 <= w_last - p.window);
-        v8h pt[RT][2];
-#pragma unroll
-        for (int t = 0; t < RT; ++t) {
-          float scale = mul[t];
-          if (p.softcap > 0.0f) {
-            const float cap = p.softcap * kLog2e, inv = 2.0f / p.softcap * mul[t];  // tanh(y) = 1 - 2 / (e^2y + 1)
-            scale = 1.0f;
-#pragma unroll
-            for (int gr = 0; gr < 4; ++gr)
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                sc[t][gr][i] = cap - 2.0f * cap * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(sc[t][gr][i] * inv) + 1.0f);
-          }
-          if (edge) {
-            const int top = min(pos[t], t_end - 1), bottom = p.window > 0 ? pos[t] - p.window : -1;
-#pragma unroll
-            for (int gr = 0; gr < 4; ++gr)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int at = t0 + 16 * gr + 4 * g + i;
-                sc[t][gr][i] = at <= top && at > bottom ? sc[t][gr][i] : kNegInf;
-              }
-          }
-          float top = sc[t][0][0];
+      for (int t = 0; t < RT; ++t) {
+        float scale = mul[t];
+        if (p.softcap > 0.0f) {
+          const float cap = p.softcap * kLog2e, inv = 2.0f / p.softcap * mul[t];  // tanh(y) = 1 - 2 / (e^2y + 1)
+          scale = 1.0f;
 #pragma unroll
           for (int gr = 0; gr < 4; ++gr)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) top = __builtin_fmaxf(top, sc[t][gr][i]);
-          if (__any(top > m[t])) {  // m: maximum of the products
-            const float grown = __builtin_fmaxf(m[t], max_over_g(top));
-            const float f = grown == kNegInf ? 1.0f : __builtin_amdgcn_exp2f((m[t] - grown) * scale);
-            m[t] = grown;
-            l[t] *= f;
+            for (int i = 0; i < 4; ++i)
+              sc[t][gr][i] = cap - 2.0f * cap * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(sc[t][gr][i] * inv) + 1.0f);
+        }
+        if (edge) {
+          const int first = t0 + 4 * rare_g(), top = min(pos[t], t_end - 1), bottom = p.window > 0 ? pos[t] - p.window : -1;
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[t][e] *= f;
-          }
-          const float off = m[t] == kNegInf ? 0.0f : kPBias - m[t] * scale;
+          for (int gr = 0; gr < 4; ++gr)
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              float e4[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                e4[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][2 * k + half][i], scale, off));
-                l[t] += e4[i];
-              }
-              const v2h x = __builtin_convertvector((v2f{e4[0], e4[1]}), v2h), y = __builtin_convertvector((v2f{e4[2], e4[3]}), v2h);
-              pt[t][k][4 * half] = x[0];
-              pt[t][k][4 * half + 1] = x[1];
-              pt[t][k][4 * half + 2] = y[0];
-              pt[t][k][4 * half + 3] = y[1];
+            for (int i = 0; i < 4; ++i) {
+              const int at = first + 16 * gr + i;
+              sc[t][gr][i] = at <= top && at > bottom ? sc[t][gr][i] : kNegInf;
             }
         }
+        float top = sc[t][0][0];
+#pragma unroll
+        for (int gr = 0; gr < 4; ++gr)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top = __builtin_fmaxf(top, sc[t][gr][i]);
+        if (__any(top > m[t])) {  // m: maximum of the products
+          const float grown = __builtin_fmaxf(m[t], max_over_g(top));
+          const float f = grown == kNegInf ? 1.0f : __builtin_amdgcn_exp2f((m[t] - grown) * scale);
+          m[t] = grown;
+          l[t] *= f;
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[t][e] *= f;
+        }
+        const float off = m[t] == kNegInf ? 0.0f : kPBias - m[t] * scale;
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const v8h a = __builtin_bit_cast(v8h, sh[buf].v[k][e][lane]);
-#pragma unroll
-            for (int t = 0; t < RT; ++t) o[t][e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pt[t][k], o[t][e], 0, 0, 0);
-          }
-        if (partly_hidden(t0) && __builtin_amdgcn_readfirstlane(sh_nan[buf]) == t0) {
-          // rare: a NaN block among positions that not every row sees.  Output element i of tile e is
-          // dim E (4g + i) + e, so element i lies in block E (4g + i) / 16.
-          for (int at = max(t0, lo); at < min(t0 + kTile, t_end); ++at) {
-            const int page = clamp_page(p, table[at >> p.page_shift]), sl = at & (P - 1);
-            const uint8_t* codes = p.cache + (int64_t)page * p.page_stride + (int64_t)h * chunk + L::v_scales(P) + sl;
+          for (int half = 0; half < 2; ++half) {
+            float e4[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const bool bad = codes[E * (4 * g + i) / 16 * P] == 0x7F;
-#pragma unroll
-              for (int t = 0; t < RT; ++t)
-                if (bad && at <= pos[t] && (p.window <= 0 || at > pos[t] - p.window))
-#pragma unroll
-                  for (int e = 0; e < E; ++e) o[t][e][i] = __builtin_nanf("");
+              e4[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][2 * k + half][i], scale, off));
+              l[t] += e4[i];
             }
+            const v2h x = __builtin_convertvector((v2f{e4[0], e4[1]}), v2h), y = __builtin_convertvector((v2f{e4[2], e4[3]}), v2h);
+            pt[t][k][4 * half] = x[0];
+            pt[t][k][4 * half + 1] = x[1];
+            pt[t][k][4 * half + 2] = y[0];
+            pt[t][k][4 * half + 3] = y[1];
+          }
+      }
+    };
+    auto take_nans = [&](int t0) __attribute__((always_inline)) {
+      if (partly_hidden(t0) && __builtin_amdgcn_readfirstlane(sh_nan[(t0 - t_begin) / kTile & 3]) == t0) {
+        // rare: a NaN block among positions that not every row sees.  Output element i of tile e is
+        // dim E (4g + i) + e, so element i lies in block E (4g + i) / 16.
+        for (int at = max(t0, lo); at < min(t0 + kTile, t_end); ++at) {
+          const int page = clamp_page(p, table[at >> p.page_shift]), sl = at & (P - 1);
+          const uint8_t* codes = p.cache + (int64_t)page * p.page_stride + (int64_t)h * chunk + L::v_scales(P) + sl;
+          const int g4 = 4 * rare_g();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bool bad = codes[E * (g4 + i) / 16 * P] == 0x7F;
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+              if (bad && at <= pos[t] && (p.window <= 0 || at > pos[t] - p.window))
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[t][e][i] = __builtin_nanf("");
           }
         }
       }
+    };
+    // One barrier per tile.  Between two of them the first waves do tile t's products (and the outputs of tile
+    // t - 1) and then its softmax; of eight waves the last four do the softmax of tile t - 1 first, so that
+    // each SIMD has one wave in matrix products and one in vector operations.  Values of tile t and keys of
+    // tile t + 1 are decoded meanwhile, into the buffers that were read before the last barrier.
+    auto tile_end = [] {
+      __builtin_amdgcn_sched_barrier(0);
       __syncthreads();
-    }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto run = [&](auto do_v, auto do_k) __attribute__((always_inline)) {
+      constexpr bool late = !do_v.value;
+      if (do_v.value) {
+        load_v(t_begin);
+        mask_v(t_begin);
+      }
+      if (do_k.value) {
+        load_k(t_begin);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) decode_k(j, 0);
+        load_k(t_begin + kTile);
+      }
+      tile_end();
+      int buf = 0;
+      for (int t0 = t_begin; t0 < t_end; t0 += kTile, buf ^= 1) {
+        if (late && t0 > t_begin) softmax(t0 - kTile);
+        products(std::true_type{}, do_v, do_k, t0, buf);
+        if (t0 > t_begin) take_nans(t0 - kTile);
+        if (!late) softmax(t0);
+        keep_pages(t0 + 2 * kTile);
+        if (do_v.value) mask_v(t0 + kTile);
+        tile_end();
+      }
+      const int t_last = t_begin + (t_end - 1 - t_begin) / kTile * kTile;
+      if (late) softmax(t_last);
+      products(std::false_type{}, std::false_type{}, std::false_type{}, t_end, buf);
+      take_nans(t_last);
+    };
+    if constexpr (WAVES == 4) run(std::true_type{}, std::true_type{});
+    else if (wave < 4) run(std::true_type{}, std::false_type{});
+    else run(std::false_type{}, std::true_type{});
   }
 
   // ---- results
