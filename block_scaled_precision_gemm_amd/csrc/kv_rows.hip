@@ -21,6 +21,11 @@
 namespace bsg {
 namespace {
 
+// P is held as 2^kBias P, relative to a row's reference m: a maximum of its products that is only replaced (and
+// the row's sums rescaled) once some product lies more than kSlack above it.  P then stays below 2^15, and
+// weights down to 2^-34 of the largest are kept (fp16 steps are 2^-24).
+constexpr float kBias = 10.0f, kSlack = 5.0f;
+
 // Where the results of row block rb of a sequence and head go.
 template <Out O, int D, int R>
 struct Results {
@@ -29,7 +34,7 @@ struct Results {
   __device__ void store_lse(int row, float top, float sum) const {
     const int i = (rb * R + row) / p.group, hq = rb * R + row - i * p.group;
     p.lse[(int64_t)(first_token + i) * p.q_heads + h * p.group + hq] =
-        sum == 0.0f ? kNegInf : (top - kPBias + __builtin_amdgcn_logf(sum)) * kLn2;
+        sum == 0.0f ? kNegInf : (top - kBias + __builtin_amdgcn_logf(sum)) * kLn2;
   }
   __device__ uint16_t* out_at(int row, int d) const {
     const int i = (rb * R + row) / p.group, hq = rb * R + row - i * p.group;
@@ -239,7 +244,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
     auto products = [&](auto scores, auto do_v, auto do_k, int t0, int buf) __attribute__((always_inline)) {
       constexpr int NO = 2 * E, N = NO + (scores.value ? 4 * NJ : 0);
       constexpr int NV = do_v.value ? E / 2 : 0, NU = NV + (do_k.value ? NJ : 0);
-      constexpr int kFly = 6;
+      constexpr int kFly = 5;
       v8h frag[kFly];
       auto read = [&](int i) {
         return __builtin_bit_cast(v8h, i < NO ? sh[buf ^ 1].v[i / E][i % E][lane] : sh[buf].k[(i - NO) % 4][(i - NO) / 4][lane]);
@@ -303,7 +308,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
         for (int gr = 0; gr < 4; ++gr)
 #pragma unroll
           for (int i = 0; i < 4; ++i) top = __builtin_fmaxf(top, sc[t][gr][i]);
-        if (__any(top > m[t])) {  // m: maximum of the products
+        if (__any((top - m[t]) * scale > kSlack)) {
           const float grown = __builtin_fmaxf(m[t], max_over_g(top));
           const float f = grown == kNegInf ? 1.0f : __builtin_amdgcn_exp2f((m[t] - grown) * scale);
           m[t] = grown;
@@ -311,7 +316,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
 #pragma unroll
           for (int e = 0; e < E; ++e) o[t][e] *= f;
         }
-        const float off = m[t] == kNegInf ? 0.0f : kPBias - m[t] * scale;
+        const float off = m[t] == kNegInf ? 0.0f : kBias - m[t] * scale;
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -375,7 +380,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
       int buf = 0;
       for (int t0 = t_begin; t0 < t_end; t0 += kTile, buf ^= 1) {
         if (late && t0 > t_begin) softmax(t0 - kTile);
+        __builtin_amdgcn_s_setprio(1);  // products first: the other wave's operations fit between them
         products(std::true_type{}, do_v, do_k, t0, buf);
+        __builtin_amdgcn_s_setprio(0);
         if (t0 > t_begin) take_nans(t0 - kTile);
         if (!late) softmax(t0);
         keep_pages(t0 + 2 * kTile);
