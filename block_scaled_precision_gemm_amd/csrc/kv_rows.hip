@@ -2,18 +2,24 @@
 //
 // A workgroup holds R = 32 WAVES query rows (new tokens x the heads that share a key/value head) of one
 // sequence and walks the positions that they see in tiles of 64.  Each tile is decoded once by the
-// workgroup, from packed codes in registers to fp16 fragments in LDS, while the previous tile is
-// multiplied (two buffers, one barrier per tile).  Fragments are stored in the order in which the lanes
-// of a product read them, so every LDS access is 1 KB in a row:
+// workgroup, from packed codes in registers to fp16 fragments in LDS (two buffers, one barrier per tile).
+// Fragments are stored in the order in which the lanes of a product read them, so every LDS access is 1 KB
+// in a row:
 // * keys: 16 positions x 32 dims per fragment, S^T = K Q^T;
 // * values: 16 dims x 32 positions, O^T += V^T P^T, with P^T straight from S^T's registers.
-// The lane layouts, the softmax and the decoding are those of the few-row kernel (kv_attend.hip).  Each
-// wave keeps 32 rows, so a fragment read from LDS feeds two products.
+// The lane layouts and the decoding are those of the few-row kernel (kv_attend.hip).  Each wave keeps 32
+// rows, so a fragment read from LDS feeds two products.
 //
-// Workgroups that share a sequence and head run on one XCD where that can be arranged, and share its L2.
-// Where the rows alone give too few workgroups, positions are split and a second kernel joins the parts.
+// Bound: per tile and wave 64 products (about 1040 cycles of the SIMD's matrix unit) and 230 vector
+// operations (about 1150 cycles).  A SIMD holds two waves, and they only overlap if one multiplies while
+// the other does its softmax: half of the waves go through a tile in the other order (run, below), products
+// have priority, and fragments are read six ahead.  2 x 2048 tokens against 8192 and 3351 positions, 32
+// heads on 8 of 128: 361 us with all waves in step, 338 us half a tile apart, 306 us with priority, 289 us
+// with fewer rescalings (1100 TFLOP/s); 203 us for the products alone, without decoding, loads and softmax.
 //
-// Bound: matrix products and the softmax's and decoding's vector operations, at similar rates.
+// Workgroups that share a sequence and head run on one XCD where that can be arranged, and share its L2
+// (the same case: 618 us with sequences in turn, 458 us so).  Where the rows alone give too few workgroups,
+// positions are split and a second kernel joins the parts.
 #include <type_traits>
 
 #include "kv_attend.h"
@@ -237,14 +243,14 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
     for (int t = 0; t < RT; ++t) pt[t][0] = pt[t][1] = v8h{};
     for (int i = tid; i < 2 * E * 64; i += 64 * WAVES) (&sh[1].v[0][0][0])[i] = v4i{0, 0, 0, 0};
     __syncthreads();
-    // A slot's products: the last tile's outputs, then (SCORES) this tile's scores, each fragment read from LDS
+    // A tile's products: the last tile's outputs, then this tile's scores, each fragment read from LDS
     // kFly fragments before its two products.  Between them the wave decodes its part of this tile's values into
     // buffer buf and of the next tile's keys into the other, and loads the following ones: its vector operations
     // run beside its products.
     auto products = [&](auto scores, auto do_v, auto do_k, int t0, int buf) __attribute__((always_inline)) {
       constexpr int NO = 2 * E, N = NO + (scores.value ? 4 * NJ : 0);
       constexpr int NV = do_v.value ? E / 2 : 0, NU = NV + (do_k.value ? NJ : 0);
-      constexpr int kFly = 5;
+      constexpr int kFly = 6;
       v8h frag[kFly];
       auto read = [&](int i) {
         return __builtin_bit_cast(v8h, i < NO ? sh[buf ^ 1].v[i / E][i % E][lane] : sh[buf].k[(i - NO) % 4][(i - NO) / 4][lane]);
