@@ -20,7 +20,8 @@ struct MoeArgs {
   float* weights;
   int64_t x_stride, out_stride;
   // workspace
-  float* logits;     // [tokens][experts]
+  int router_parts;  // of the logits' sums over hidden
+  float* logits;     // [router_parts][tokens][experts]
   uint16_t* xs;      // x as the first product takes it: [tokens][hidden], or [2][tokens][hidden] bf16 parts of it
   int* x_exp;        // [tokens] powers of two of scaled rows
   uint16_t* h;       // [2][tokens * top_k][inter] bf16 parts of SiLU(gate) up, rows grouped by expert

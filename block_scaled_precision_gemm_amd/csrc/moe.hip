@@ -48,6 +48,7 @@ __device__ __forceinline__ float bf16_value(uint16_t b) { return __builtin_bit_c
 constexpr int kRouterThreads = 1024, kRouterWaves = kRouterThreads / 64;
 constexpr int kMaxChoices = BSG_MOE_MAX_TOKENS * BSG_MOE_MAX_TOP_K;
 constexpr float kLog2e = 1.44269504088896341f;
+constexpr int kRouterParts = 4;  // most parts that the logits' sums are cut into
 
 // Order of floats as unsigned: larger float, larger key; NaN above all; -0 as 0.  No logit's key is 0.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -155,6 +156,14 @@ __device__ void choose(const MoeArgs& p, Choice& sh) {
       for (int r = 0; r < R; ++r)
         x[i][r] = handoff_load(p.logits + (size_t)(wave + i * kRouterWaves) * E + min(lane * R + r, E - 1));
     }
+  for (int part = 1; part < p.router_parts; ++part)
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (wave + i * kRouterWaves < T) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          x[i][r] += handoff_load(p.logits + (size_t)(part * T + wave + i * kRouterWaves) * E + min(lane * R + r, E - 1));
+      }
   if (tid < E) sh.tokens_of[tid] = 0;
   __syncthreads();
 #pragma unroll
@@ -263,7 +272,7 @@ __device__ __forceinline__ void prepare_row(const MoeArgs& p, int t, uint32_t* s
   }
 }
 
-// Workgroups 0 .. tiles - 1: the logits of one tile of 16 experts and 16 tokens, the waves taking
+// The first workgroups: a part of the sums of one tile of 16 experts and 16 tokens' logits, the waves taking
 // alternate steps of 32 k, up to eight of them in flight; the last of these workgroups to finish chooses.  The
 // others prepare one token's row each.
 template <bool NV, bool F16>
@@ -274,18 +283,20 @@ __global__ __launch_bounds__(kRouterThreads) void router_kernel(MoeArgs p) {
     uint32_t most[kRouterWaves];
   } sh;
   __shared__ int last;
-  const int tiles_e = (p.experts + 15) / 16, tiles = tiles_e * ((p.tokens + 15) / 16);
-  if ((int)blockIdx.x >= tiles) {
-    prepare_row<kPrep<NV, F16>>(p, blockIdx.x - tiles, sh.most);
+  const int tiles_e = (p.experts + 15) / 16, tiles = tiles_e * ((p.tokens + 15) / 16), logits = tiles * p.router_parts;
+  if ((int)blockIdx.x >= logits) {
+    prepare_row<kPrep<NV, F16>>(p, blockIdx.x - logits, sh.most);
     return;
   }
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, c = lane & 15, g = lane >> 4;
-  const int e0 = blockIdx.x % tiles_e * 16, t0 = blockIdx.x / tiles_e * 16;
+  const int tile = blockIdx.x % tiles, part = blockIdx.x / tiles;
+  const int e0 = tile % tiles_e * 16, t0 = tile / tiles_e * 16;
   const uint16_t* a = p.router + (size_t)min(e0 + c, p.experts - 1) * p.hidden + 8 * g;
   const uint16_t* b = p.x + (int64_t)min(t0 + c, p.tokens - 1) * p.x_stride + 8 * g;
   v4f acc = {0, 0, 0, 0};
-  const int steps = p.hidden / 32;
-  int s0 = wave;
+  const int all = p.hidden / 32, each = (all + p.router_parts - 1) / p.router_parts;
+  const int steps = min(all, (part + 1) * each);
+  int s0 = part * each + wave;
   auto batch = [&](auto size) __attribute__((always_inline)) {
     constexpr int B = decltype(size)::value;
     v4i aw[B], bw[B];
@@ -304,7 +315,7 @@ __global__ __launch_bounds__(kRouterThreads) void router_kernel(MoeArgs p) {
     }
     s0 += B * kRouterWaves;
   };
-  // (eight steps at once for hidden 1024 repeated six of them: 6.9 us for one token and 32 experts, ROUT so)
+  // (always eight at once repeated steps of short rows: 6.9 us for one token, 32 experts, hidden 1024, 3.5 us so)
   while (s0 + 4 * kRouterWaves < steps) batch(std::integral_constant<int, 8>{});
   if (s0 + 2 * kRouterWaves < steps) batch(std::integral_constant<int, 4>{});
   if (s0 < steps) batch(std::integral_constant<int, 2>{});
@@ -317,9 +328,9 @@ __global__ __launch_bounds__(kRouterThreads) void router_kernel(MoeArgs p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (t0 + c < p.tokens && e0 + 4 * g + i < p.experts)
-        handoff_store(p.logits + (size_t)(t0 + c) * p.experts + e0 + 4 * g + i, s[i]);
+        handoff_store(p.logits + (size_t)(part * p.tokens + t0 + c) * p.experts + e0 + 4 * g + i, s[i]);
   }
-  if (p.tokens == 1 || !last_arrival(p.arrived, tiles, &last)) return;  // (one token: gate_up_kernel chooses)
+  if (p.tokens == 1 || !last_arrival(p.arrived, logits, &last)) return;  // (one token: gate_up_kernel chooses)
   if (p.experts <= 64) choose<1>(p, sh.choice);
   else if (p.experts <= 128) choose<2>(p, sh.choice);
   else choose<BSG_MOE_MAX_EXPERTS / 64>(p, sh.choice);
@@ -544,6 +555,9 @@ __global__ __launch_bounds__(kThreads, NV ? 4 : 3) void gate_up_kernel(MoeArgs p
       float x[R];
 #pragma unroll
       for (int r = 0; r < R; ++r) x[r] = p.logits[min(lane * R + r, p.experts - 1)];
+      for (int part = 1; part < p.router_parts; ++part)
+#pragma unroll
+        for (int r = 0; r < R; ++r) x[r] += p.logits[part * p.experts + min(lane * R + r, p.experts - 1)];
       top_k<R>(x, p.experts, last, p.keep, lane, expert, weight);
     };
     if (p.experts <= 64) choose_one(std::integral_constant<int, 1>{});
@@ -687,7 +701,12 @@ hipError_t launch(const MoeArgs& a, hipStream_t stream) {
   MoeArgs args = a;
   void* argv[] = {&args};
   const unsigned tiles = (a.experts + 15) / 16 * ((a.tokens + 15) / 16);
-  hipError_t e = hipLaunchKernel((const void*)&router_kernel<NV, F16>, dim3(tiles + a.tokens),
+  // Parts of 1024 k where there are few tiles: a compute unit reads a tile's 256 KB (hidden 4096) in 3.5 us (1 token, 64
+  // experts: 7.1 us whole, 4.5 in 4 parts; 33 tokens: 16.8 and 14.4).  Many tiles fill more compute units, and
+  // their parts would all pass through the one that chooses.
+  const int parts = (a.hidden + 1023) / 1024;
+  args.router_parts = tiles > 32 ? 1 : parts < kRouterParts ? parts : kRouterParts;
+  hipError_t e = hipLaunchKernel((const void*)&router_kernel<NV, F16>, dim3(tiles * args.router_parts + a.tokens),
                                  dim3(kRouterThreads), argv, 0, stream);
   if (e != hipSuccess) return e;
   // at most one slot per choice, and one per expert and kSlotRows choices
@@ -714,7 +733,7 @@ size_t moe_workspace(const bsg_moe_problem& p, uint8_t* base, MoeArgs* a, size_t
     at += (bytes + 255) & ~(size_t)255;
     return base ? base + here : nullptr;
   };
-  a->logits = (float*)take(T * p.experts * 4);
+  a->logits = (float*)take(kRouterParts * T * p.experts * 4);
   a->xs = (uint16_t*)take(2 * T * p.hidden * 2);
   a->x_exp = (int*)take(T * 4);
   a->h = (uint16_t*)take(2 * rows * p.inter * 2);
