@@ -21,9 +21,8 @@
 //   of 8 positions, interleaves the nibbles of two positions (4 operations for 16 values), and decodes
 //   each byte to the pair (position j, position j + 1), which one packed multiply scales by the pair of
 //   scales, stored with the position fastest for this purpose.
-// Softmax: running maximum m and sum l per row, in fp32 and base 2; accumulators are rescaled only when
-// some row's maximum grew.  P is rounded to fp16 for its product, offset by 2^14 so that weights down to
-// 2^-38 of the largest are kept (fp16 steps are 2^-24); l sums the unrounded values.
+// Softmax: reference m (kv_attend.h; here always the maximum) and sum l per row, in fp32 and base 2.  P is
+// rounded to fp16 for its product; l sums the unrounded values.
 //
 // Bound: bytes of the cache (D 9/8 bytes per position and head) where contexts are long; for short ones the
 // chain of dependent trips to memory (lengths, page numbers, codes, the join), about 10 us.  Measured, heads
@@ -205,6 +204,9 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
     }
     // a step's codes: NG groups of 16 positions, DEPTH steps in flight
     uint32_t kq[DEPTH][NG][NJ], ks[DEPTH][NG], vq[DEPTH][NG][4], vs[DEPTH][NG];
+    // a lane's offsets from a group's codes and scales
+    const uint32_t k_lane = c * L::kRow + g * (4 * NJ), ks_lane = c * L::kBlocks + g * (D / 64);
+    const uint32_t v_lane = 4 * g * L::kRow + c * (E / 2), vs_lane = (c * E / 16) * P + 4 * g;
     auto load = [&](int d, int t0) {
 #pragma unroll
       for (int gr = 0; gr < NG; ++gr) {
@@ -217,23 +219,23 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
         const int slot = t & (P - 1);
         const uint8_t* at = p.cache + (int64_t)__builtin_amdgcn_readlane(page_ids, page - page_base) * p.page_stride +
                             (int64_t)h * chunk;
-        const uint8_t* kp = at + (slot + c) * L::kRow + g * (4 * NJ);
+        const uint8_t *k_codes = at + slot * L::kRow, *k_scales = at + L::k_scales(P) + slot * L::kBlocks;
+        const uint8_t *v_codes = at + L::v_codes(P) + slot * L::kRow, *v_scales = at + L::v_scales(P) + slot;
         if constexpr (D == 128) {
-          const v4i w = *(const v4i*)kp;
+          const v4i w = *(const v4i*)(k_codes + k_lane);
 #pragma unroll
           for (int k = 0; k < NJ; ++k) kq[d][gr][k] = (uint32_t)w[k];
-          ks[d][gr] = *(const uint16_t*)(at + L::k_scales(P) + (slot + c) * L::kBlocks + 2 * g);
+          ks[d][gr] = *(const uint16_t*)(k_scales + ks_lane);
         } else {
-          const uint2 w = *(const uint2*)kp;
+          const uint2 w = *(const uint2*)(k_codes + k_lane);
           kq[d][gr][0] = w.x;
           kq[d][gr][1] = w.y;
-          ks[d][gr] = at[L::k_scales(P) + (slot + c) * L::kBlocks + g];
+          ks[d][gr] = k_scales[ks_lane];
         }
-        const uint8_t* vp = at + L::v_codes(P) + (slot + 4 * g) * L::kRow + c * (E / 2);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          vq[d][gr][k] = E == 8 ? *(const uint32_t*)(vp + k * L::kRow) : *(const uint16_t*)(vp + k * L::kRow);
-        vs[d][gr] = *(const uint32_t*)(at + L::v_scales(P) + (c * E / 16) * P + slot + 4 * g);
+          vq[d][gr][k] = E == 8 ? *(const uint32_t*)(v_codes + v_lane + k * L::kRow) : *(const uint16_t*)(v_codes + v_lane + k * L::kRow);
+        vs[d][gr] = *(const uint32_t*)(v_scales + vs_lane);
       }
     };
     v8h q[RT][NJ];
@@ -291,12 +293,12 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
                 sc[t][gr][i] = cap - 2.0f * cap * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(sc[t][gr][i] * inv) + 1.0f);
           }
           if (edge) {
-            const int top = min(pos[t], w1 - 1), bottom = p.window > 0 ? pos[t] - p.window : -1;
+            const int first = t0 + 4 * rare(g), top = min(pos[t], w1 - 1), bottom = p.window > 0 ? pos[t] - p.window : -1;
 #pragma unroll
             for (int gr = 0; gr < NG; ++gr)
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const int at = t0 + 16 * gr + 4 * g + i;
+                const int at = first + 16 * gr + i;
                 sc[t][gr][i] = at <= top && at > bottom ? sc[t][gr][i] : kNegInf;
               }
           }
@@ -305,13 +307,13 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
         if (edge) {
           // positions that no row sees count as zero, whatever their slots hold; NaN blocks seen by
           // some rows only are taken out here and given to those rows below
-          const int from = max(lo, w0), to = w1;
+          const int first = t0 + 4 * rare(g), from = max(lo, w0), to = w1;
 #pragma unroll
           for (int gr = 0; gr < NG; ++gr) {
             uint32_t keep = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int at = t0 + 16 * gr + 4 * g + i;
+              const int at = first + 16 * gr + i;
               if (at >= from && at < to) keep |= 0xFFu << (8 * i);
             }
             vs[d][gr] &= keep;
@@ -329,7 +331,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
           for (int gr = 0; gr < NG; ++gr)
 #pragma unroll
             for (int i = 0; i < 4; ++i) top = __builtin_fmaxf(top, sc[t][gr][i]);
-          if (__any(top > m[t])) {  // m: maximum of the products, in units of 1 / scale
+          if (__any(top > m[t])) {  // (kSlack would save nothing here: 79.9 and 79.6 us for the 64 tokens above)
             const float grown = __builtin_fmaxf(m[t], max_over_g(top));
             const float f = grown == kNegInf ? 1.0f : __builtin_amdgcn_exp2f((m[t] - grown) * scale[t]);
             m[t] = grown;
@@ -385,7 +387,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
             const uint8_t* codes = p.cache + (int64_t)page * p.page_stride + (int64_t)h * chunk + L::v_scales(P) + sl;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const bool bad = codes[E * (4 * g + i) / 16 * P] == 0x7F;
+              const bool bad = codes[E * (4 * rare(g) + i) / 16 * P] == 0x7F;
 #pragma unroll
               for (int t = 0; t < RT; ++t)
                 if (bad && at <= pos[t] && (p.window <= 0 || at > pos[t] - p.window))

@@ -27,11 +27,6 @@
 namespace bsg {
 namespace {
 
-// P is held as 2^kBias P, relative to a row's reference m: a maximum of its products that is only replaced (and
-// the row's sums rescaled) once some product lies more than kSlack above it.  P then stays below 2^15, and
-// weights down to 2^-34 of the largest are kept (fp16 steps are 2^-24).
-constexpr float kBias = 10.0f, kSlack = 5.0f;
-
 // Where the results of row block rb of a sequence and head go.
 template <Out O, int D, int R>
 struct Results {
@@ -40,7 +35,7 @@ struct Results {
   __device__ void store_lse(int row, float top, float sum) const {
     const int i = (rb * R + row) / p.group, hq = rb * R + row - i * p.group;
     p.lse[(int64_t)(first_token + i) * p.q_heads + h * p.group + hq] =
-        sum == 0.0f ? kNegInf : (top - kBias + __builtin_amdgcn_logf(sum)) * kLn2;
+        sum == 0.0f ? kNegInf : (top - kPBias + __builtin_amdgcn_logf(sum)) * kLn2;
   }
   __device__ uint16_t* out_at(int row, int d) const {
     const int i = (rb * R + row) / p.group, hq = rb * R + row - i * p.group;
@@ -151,13 +146,6 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
     // a lane's offsets from a group's codes and scales
     const uint32_t v_lane = 4 * g * L::kRow + c * (E / 2), vs_lane = (c * E / 16) * P + 4 * g;
     const uint32_t k_lane = c * L::kRow + g * (4 * NJ), ks_lane = c * L::kBlocks + g * (D / 64);
-    // g for paths that few tiles take: not known to be the same in every tile, so that nothing formed from it
-    // is kept in registers throughout
-    auto rare_g = [&] {
-      int x = g;
-      asm volatile("" : "+v"(x));
-      return x;
-    };
     auto load_v = [&](int t0) __attribute__((always_inline)) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
@@ -195,7 +183,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
     // and NaN blocks that only some rows see are taken out and given to those rows by the waves (take_nans).
     auto mask_v = [&](int t0) __attribute__((always_inline)) {
       if (!partly_hidden(t0)) return;
-      const int g4 = 4 * rare_g();
+      const int g4 = 4 * rare(g);
       uint32_t bad = 0;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
@@ -300,7 +288,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
               sc[t][gr][i] = cap - 2.0f * cap * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(sc[t][gr][i] * inv) + 1.0f);
         }
         if (edge) {
-          const int first = t0 + 4 * rare_g(), top = min(pos[t], t_end - 1), bottom = p.window > 0 ? pos[t] - p.window : -1;
+          const int first = t0 + 4 * rare(g), top = min(pos[t], t_end - 1), bottom = p.window > 0 ? pos[t] - p.window : -1;
 #pragma unroll
           for (int gr = 0; gr < 4; ++gr)
 #pragma unroll
@@ -322,7 +310,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
 #pragma unroll
           for (int e = 0; e < E; ++e) o[t][e] *= f;
         }
-        const float off = m[t] == kNegInf ? 0.0f : kBias - m[t] * scale;
+        const float off = m[t] == kNegInf ? 0.0f : kPBias - m[t] * scale;
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -348,7 +336,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
         for (int at = max(t0, lo); at < min(t0 + kTile, t_end); ++at) {
           const int page = clamp_page(p, table[at >> p.page_shift]), sl = at & (P - 1);
           const uint8_t* codes = p.cache + (int64_t)page * p.page_stride + (int64_t)h * chunk + L::v_scales(P) + sl;
-          const int g4 = 4 * rare_g();
+          const int g4 = 4 * rare(g);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const bool bad = codes[E * (g4 + i) / 16 * P] == 0x7F;
