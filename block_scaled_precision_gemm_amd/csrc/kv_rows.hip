@@ -14,8 +14,8 @@
 // operations (about 1150 cycles).  A SIMD holds two waves, and they only overlap if one multiplies while
 // the other does its softmax: half of the waves go through a tile in the other order (run, below), products
 // have priority, and fragments are read six ahead.  2 x 2048 tokens against 8192 and 3351 positions, 32
-// heads on 8 of 128: 361 us with all waves in step, 338 us half a tile apart, 306 us with priority, 275 us
-// with fewer rescalings (1160 TFLOP/s); the products alone, without decoding, loads and softmax, 203 us.
+// heads on 8 of 128: 361 us with all waves in step, 338 us half a tile apart, 306 us with priority, 270 us
+// with fewer rescalings (1180 TFLOP/s); the products alone, without decoding, loads and softmax, 203 us.
 //
 // Workgroups that share a sequence and head run on one XCD where that can be arranged, and share its L2
 // (the same case: 618 us with sequences in turn, 458 us so).  Where the rows alone give too few workgroups,

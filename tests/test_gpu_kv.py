@@ -282,6 +282,35 @@ def test_nan_blocks_in_one_part():
     assert np.isnan(got[9, :4, 16:32]).all() and not np.isnan(got[10, :4]).any()
 
 
+@pytest.mark.parametrize("new,H,D,dtype", [(40, 512, 64, "f16"), (150, 256, 128, "bf16")])
+@pytest.mark.parametrize("P,window", [(16, 0), (16, 1100), (128, 0)])
+def test_many_rows_over_many_pages_in_one_part(new, H, D, dtype, P, window):
+    # heads enough for every compute unit: one workgroup walks a whole context, past the pages it looks up at first.
+    # The cache is filled by append and its values are taken from read (both checked above byte by byte).
+    n = 1301
+    g = torch.Generator().manual_seed(new)
+    q_start, pages, n_pages = layout([n], [n], P, 7)
+    lens, pg = dev(np.array([n], np.int32)), dev(pages)
+    print(f"[kv] many pages {new} {H} {D} {dtype} {P} {window}", flush=True)
+    with bsg.KVPlan(H, H, D, P, n_pages, n, dtype=dtype, window=window) as plan:
+        kv = [torch.randn(n, H, D, generator=g).to(DT[dtype]).cuda() for _ in range(2)]
+        cache = torch.full((n_pages * plan.page_bytes,), 0x7F, dtype=torch.uint8, device="cuda")
+        whole = bsg.KVBatch(dev(q_start), lens, pg, n, n, n)
+        plan.append(whole, *kv, cache)
+        plan.read(whole, cache, *kv)
+        q = torch.randn(new, H, D, generator=g).to(DT[dtype]).cuda()
+        out, lse = torch.zeros_like(q), torch.zeros(new, H, device="cuda")
+        plan.attend(bsg.KVBatch(dev(np.array([0, new], np.int32)), lens, pg, new, new, n), q, cache, out, lse=lse)
+        torch.cuda.synchronize()
+    qd, k, v = (x.double().transpose(0, 1).contiguous() for x in (q, *kv))
+    s = torch.matmul(qd, k.transpose(1, 2).contiguous()) * D ** -0.5
+    i, j = torch.arange(n - new, n, device="cuda")[:, None], torch.arange(n, device="cuda")[None]
+    s = s.masked_fill((j > i) | (j <= i - window if window else j < 0), float("-inf"))
+    want = torch.matmul(s.softmax(-1), v).transpose(0, 1)
+    check(out.double().cpu().numpy(), lse.double().cpu().numpy(), want.cpu().numpy(), s.logsumexp(-1).T.cpu().numpy(), dtype,
+          float(v.abs().max()), f"many pages {new} {H} {D} {P} {window}")
+
+
 def test_many_rows_in_parts_in_a_graph():
     q_start, pages, n_pages = layout([30, 20], [900, 500], 16, 0)
     c = filled([900, 500], 2, 64, 16, pages, n_pages, 1)
