@@ -30,6 +30,7 @@
 // positions, 32 heads on 4: 28 us (2.7 TB/s); one over 1001 positions, 32 heads on 8: 10 us.
 #include "handoff.h"
 #include "kv_attend.h"
+#include "kv_split.h"
 
 namespace bsg {
 namespace {
@@ -174,8 +175,8 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
       continue;
     }
     // its tiles here
-    const int tile0 = pieces ? (x - u0) * s.tiles / len : max(x - real, 0);
-    const int tile1 = pieces ? (x1 - u0) * s.tiles / len : x1 - real;
+    const int tile0 = pieces ? piece_begin(x - u0, len, s.tiles) : max(x - real, 0);
+    const int tile1 = pieces ? piece_begin(x1 - u0, len, s.tiles) : x1 - real;
     const int first_token = p.one_each ? b : seq_start(p, b);
     const int rows = min(R, s.q_len * G - rb * R);
     const bool causal = !(p.flags & BSG_KV_NONCAUSAL);

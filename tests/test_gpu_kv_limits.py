@@ -1,0 +1,48 @@
+"""Paged attention at the ends of its arguments' ranges: very long contexts, weights far below the largest, soft caps far
+above the scores, unbounded windows, the largest magnitudes, uneven batches.  References are 64-bit (kv_ref), or closed
+forms where a cache's pages repeat."""
+import numpy as np
+import pytest
+import torch
+
+import block_scaled_precision_gemm_amd as bsg
+import kv_ref
+from test_gpu_kv import DT, UNIT, attend, check, dev, filled, layout, run_case
+
+pytestmark = pytest.mark.gpu
+
+
+def repeated(c, table, q, scale, dtype, **kw):
+    """One query over positions whose pages are table's: (out, lse) of the library and of the closed form.  H = 1."""
+    P, D, n = c.p, c.dim, len(table) * c.p
+    with bsg.KVPlan(q.shape[0], 1, D, P, len(c.bytes), 1, dtype=dtype, scale=scale, **kw) as plan:
+        b = bsg.KVBatch(dev(np.array([0, 1], np.int32)), dev(np.array([n], np.int32)), dev(table[None].astype(np.int32)), 1, 1, n)
+        qd = torch.from_numpy(q[None]).to(DT[dtype]).cuda()
+        out, lse = torch.full_like(qd, 7.0), torch.full((1, q.shape[0]), 7.0, device="cuda")
+        plan.attend(b, qd, dev(c.bytes), out, lse=lse)
+        torch.cuda.synchronize()
+    times = np.bincount(table, minlength=len(c.bytes))
+    k, v = (np.array([[c.load(p, s, 0, is_v) for s in range(P)] for p in range(len(times))]) for is_v in (False, True))
+    s = np.einsum("psd,hd->hps", k, qd.double().cpu().numpy()[0]) * scale
+    top = s.max((1, 2))
+    w = np.exp(s - top[:, None, None]) * times[:, None]
+    total = w.sum((1, 2))
+    return (out.double().cpu().numpy()[0], lse.double().cpu().numpy()[0], np.einsum("hps,psd->hd", w, v) / total[:, None],
+            top + np.log(total))
+
+
+def test_half_a_billion_positions():
+    # one sequence and one head cut into as many pieces as the card takes: their bounds pass 2^31 on the way.  A piece that
+    # is left out changes the log-sum-exp by 1/511 or more; sums of 2^16 terms a lane in 32 bits are off by about 2^-24 2^8.
+    rng = np.random.default_rng(0)
+    c = kv_ref.Cache(2, 1, 64, 256)
+    for page in range(2):
+        for is_v in (False, True):
+            code, s = kv_ref.quantize(rng.standard_normal((256, 64)))
+            for p in range(256):
+                c.store(page, p, 0, is_v, code[p], s[p])
+    table = (np.arange(1 << 21) % 3 == 2).astype(np.int32)
+    print("[kv] 2^29 positions", flush=True)
+    got, lse, want, want_lse = repeated(c, table, rng.standard_normal((1, 64)), 0.125, "f16")
+    assert np.abs(lse - want_lse).max() < 2.0 ** -10
+    assert np.abs(got - want).max() < 2.0 ** -10
