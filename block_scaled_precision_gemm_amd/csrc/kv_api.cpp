@@ -8,6 +8,7 @@
 #include <new>
 
 #include "kv.h"
+#include "kv_split.h"
 #include "plan.h"
 
 struct bsg_kv_plan_s {
@@ -350,10 +351,9 @@ bsg_status bsg_kv_attend(bsg_kv_plan plan, const bsg_kv_batch* batch, const bsg_
     return BSG_ERR_ALIGN;
   }
   a.lse = lse;
-  // the kernels count tiles of 64 positions over all units in 32 bits
-  const double units = ((double)a.num_tokens * a.group / 16 + a.num_seqs) * a.kv_heads;
   const double grid = ((double)a.max_q * a.group / 128 + 1) * a.num_seqs * a.kv_heads * 16;
-  if (units * ((double)a.max_kv / 64 + 2) >= 2147483648.0 || grid >= 2147483648.0) {
+  if (!bsg::line_fits(a.num_tokens, a.group, a.num_seqs, a.kv_heads, bsg::context_positions(a.window, a.max_q, a.max_kv)) ||
+      grid >= 2147483648.0) {
     set_error("%d tokens of %d sequences over contexts of up to %d positions are too many for one call", a.num_tokens,
               a.num_seqs, a.max_kv);
     return BSG_ERR_UNSUPPORTED;

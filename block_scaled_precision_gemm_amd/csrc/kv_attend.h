@@ -2,12 +2,12 @@
 #pragma once
 
 #include "kv.h"
+#include "kv_split.h"
 
 namespace bsg {
 
 typedef float v2f __attribute__((ext_vector_type(2)));
 
-constexpr int kTile = 64;       // positions of a tile
 // P is held as 2^kPBias P, relative to a row's reference m: a maximum of its products, which the many-row kernel
 // only replaces (and rescales the row's sums) once some product lies more than kSlack above it.  P then stays
 // below 2^15, and weights down to 2^-34 of the largest are kept (fp16 steps are 2^-24).

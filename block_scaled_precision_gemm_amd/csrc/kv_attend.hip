@@ -30,16 +30,12 @@
 // positions, 32 heads on 4: 28 us (2.7 TB/s); one over 1001 positions, 32 heads on 8: 10 us.
 #include "handoff.h"
 #include "kv_attend.h"
-#include "kv_split.h"
 
 namespace bsg {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMinTiles = 2;    // a piece is at least a step of each wave
-// What a unit costs a workgroup besides its tiles, in tiles: queries, the pipeline's filling, joining the
-// waves (measured with 64 contexts up to 16384: 10 us for each further unit of a run, 0.7 us per tile).
-constexpr int kUnitCost = 12;
 constexpr int kWgPerCu = 2;
 
 template <int CTRL, int ROWS>
@@ -536,8 +532,7 @@ hipError_t launch(const KvArgs& a, int cus, hipStream_t stream) {
   // Of a mixed batch most short sequences have one new token: 16 rows, and two blocks for the others.
   const int64_t rows = (int64_t)(a.mixed ? 1 : a.max_q) * a.group;
   const int R = rows <= 16 ? 16 : 32;
-  const int64_t context = a.window > 0 ? (int64_t)a.window + a.max_q + 16 : a.max_kv;
-  const int64_t tiles = ((context < a.max_kv ? context : a.max_kv) + kTile - 1) / kTile + 1;
+  const int64_t tiles = (context_positions(a.window, a.max_q, a.max_kv) + kTile - 1) / kTile + 1;
   // units: sum over sequences of ceil(tokens * group / R), at most one partial block each
   const int64_t units = ((int64_t)a.num_tokens * a.group / R + a.num_seqs) * a.kv_heads;
   const int64_t want = units * ((tiles + kMinTiles - 1) / kMinTiles), most = (int64_t)cus * kWgPerCu;

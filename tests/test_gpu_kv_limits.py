@@ -46,3 +46,15 @@ def test_half_a_billion_positions():
     got, lse, want, want_lse = repeated(c, table, rng.standard_normal((1, 64)), 0.125, "f16")
     assert np.abs(lse - want_lse).max() < 2.0 ** -10
     assert np.abs(got - want).max() < 2.0 ** -10
+
+
+def test_more_units_than_a_call_can_count_are_refused():
+    n = 1 << 24
+    lens, pages = torch.ones(n, dtype=torch.int32, device="cuda"), torch.zeros(n, 1, dtype=torch.int32, device="cuda")
+    x = torch.zeros(1, 16, 64, dtype=torch.bfloat16, device="cuda").expand(n, 16, 64)
+    with bsg.KVPlan(16, 16, 64, 16, 1, n) as plan:
+        batch = bsg.KVBatch(torch.arange(n + 1, dtype=torch.int32, device="cuda"), lens, pages, n, 1, 1)
+        with pytest.raises(bsg.BsgError) as e:
+            plan.attend(batch, x, torch.zeros(plan.page_bytes, dtype=torch.uint8, device="cuda"), x)
+        assert e.value.status_name == "BSG_ERR_UNSUPPORTED"
+        torch.cuda.synchronize()
