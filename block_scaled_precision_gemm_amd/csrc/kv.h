@@ -40,6 +40,7 @@ struct KvArgs {
   int* group_arrived;  // arrival counters of groups of parts, and of units; zero between calls
   int* arrived;
   int splits;        // position splits of the many-row kernel
+  int row_groups, row_width, row_listed;  // its workgroups (kv_split.h)
 };
 
 // Byte offsets inside the chunk of one head of a page (P = page tokens, D = head dim).

@@ -351,9 +351,8 @@ bsg_status bsg_kv_attend(bsg_kv_plan plan, const bsg_kv_batch* batch, const bsg_
     return BSG_ERR_ALIGN;
   }
   a.lse = lse;
-  const double grid = ((double)a.max_q * a.group / 128 + 1) * a.num_seqs * a.kv_heads * 16;
-  if (!bsg::line_fits(a.num_tokens, a.group, a.num_seqs, a.kv_heads, bsg::context_positions(a.window, a.max_q, a.max_kv)) ||
-      grid >= 2147483648.0) {
+  if (!bsg::attend_fits(a.num_tokens, a.num_seqs, a.max_q, a.group, a.kv_heads,
+                        bsg::context_positions(a.window, a.max_q, a.max_kv))) {
     set_error("%d tokens of %d sequences over contexts of up to %d positions are too many for one call", a.num_tokens,
               a.num_seqs, a.max_kv);
     return BSG_ERR_UNSUPPORTED;

@@ -21,7 +21,6 @@ __device__ __forceinline__ int rare(int x) {
 }
 
 constexpr int kJoin = 16;       // parts joined at a time
-constexpr int kFewRows = 32;    // most query rows per sequence and key/value head of the few-row kernel
 constexpr float kNegInf = -__builtin_inff();
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 

@@ -551,11 +551,8 @@ hipError_t launch(const KvArgs& a, int cus, hipStream_t stream) {
 // and more, where a launch that finds nothing to do (4 us) is small against the rest.
 hipError_t kv_attend_launch(const KvArgs& args, int dtype, int head_dim, int cus, hipStream_t stream) {
   KvArgs a = args;
-  a.mixed = 0;
+  a.mixed = mixed_batch(a.num_tokens, a.num_seqs, a.max_q, a.group);
   if ((int64_t)a.max_q * a.group > kFewRows) {
-    const int64_t others = (int64_t)(a.num_tokens - a.max_q) * a.group;
-    a.mixed = a.group <= kFewRows && a.num_tokens < (int64_t)a.num_seqs * a.max_q &&
-              (a.num_seqs >= 8 || others <= (int64_t)kFewRows * (a.num_seqs - 1));
     const hipError_t e = kv_attend_rows_launch(a, dtype, head_dim, cus, stream);
     if (e != hipSuccess || !a.mixed) return e;
   }

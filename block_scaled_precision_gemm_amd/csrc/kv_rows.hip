@@ -49,6 +49,39 @@ struct Results {
   }
 };
 
+// Row block `at` of a group: its sequence, head, and which of the sequence's blocks of R rows, the last one first.
+struct RowBlock {
+  int b, h, first_token, q_len;
+  int rb;  // < 0: none
+};
+
+template <int R>
+__device__ __forceinline__ RowBlock row_block(const KvArgs& p, int group, int at, int lane) {
+  RowBlock s;
+  if (p.row_listed) {
+    int lo = 0;
+    for (int n = p.num_seqs; n > 1;) {  // the last sequence that starts at or before the slot: 64 pivots a step
+      const int step = (n + 63) / 64, i = lane * step;
+      const bool le = i < n && row_slot(seq_start(p, lo + i), lo + i, p.group, R) <= at;
+      const int parts = max(__popcll(__ballot(le)), 1) - 1;
+      lo += parts * step;
+      n = min(step, n - parts * step);
+    }
+    s.b = __builtin_amdgcn_readfirstlane(lo);
+    s.h = group;
+    at -= row_slot(seq_start(p, s.b), s.b, p.group, R);
+  } else {
+    s.b = group / p.kv_heads;
+    s.h = group - s.b * p.kv_heads;
+  }
+  s.first_token = p.one_each ? s.b : seq_start(p, s.b);
+  s.q_len = p.one_each ? 1 : min(max(seq_start(p, s.b + 1) - s.first_token, 0), p.max_q);
+  const int blocks = (s.q_len * p.group + R - 1) / R;
+  const bool other = p.mixed && s.q_len * p.group <= kFewRows;  // the few-row kernel's
+  s.rb = other || at < 0 ? -1 : blocks - 1 - at;
+  return s;
+}
+
 template <Out O, int D, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
   constexpr int RT = 2, R = 32 * WAVES;
@@ -67,25 +100,24 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
   const int H = p.kv_heads, G = p.group, P = 1 << p.page_shift;
   const bool causal = !(p.flags & BSG_KV_NONCAUSAL);
 
-  // ---- unit and split.  Groups (sequence, head) are a multiple of 8: workgroup x is on XCD x % 8 and so is
-  // all of a group, whose blocks follow each other there from the last (the longest) to the first.
+  // ---- block and split.  Groups (kv_split.h) are a multiple of 8: workgroup x is on XCD x % 8 and so is all of a
+  // group, whose blocks follow each other there, each sequence's from the last (the longest) to the first.
   // Otherwise groups alternate.
-  const int groups = p.num_seqs * H, per_group = gridDim.x / groups;
-  int bh, rest;
-  if (groups % 8 == 0) {
+  const int per_group = p.row_width * p.splits;
+  int group, rest;
+  if (p.row_groups % 8 == 0) {
     const int at = blockIdx.x >> 3;
-    bh = at / per_group * 8 + (blockIdx.x & 7);
+    group = at / per_group * 8 + (blockIdx.x & 7);
     rest = at % per_group;
   } else {
-    bh = blockIdx.x % groups;
-    rest = blockIdx.x / groups;
+    group = blockIdx.x % p.row_groups;
+    rest = blockIdx.x / p.row_groups;
   }
-  const int b = bh / H, h = bh - b * H, split = rest % p.splits;
-  const int first_token = p.one_each ? b : seq_start(p, b);
+  const int split = rest % p.splits;
+  const RowBlock block = row_block<R>(p, group, rest / p.splits, lane);
+  if (block.rb < 0) return;
+  const int b = block.b, h = block.h, rb = block.rb, first_token = block.first_token, q_len = block.q_len;
   const int len = seq_len(p, b);
-  const int q_len = p.one_each ? 1 : min(max(seq_start(p, b + 1) - first_token, 0), p.max_q);
-  const int blocks = (q_len * G + R - 1) / R, rb = blocks - 1 - rest / p.splits;
-  if (rb < 0 || (p.mixed && q_len * G <= kFewRows)) return;
   const int rows = min(R, q_len * G - rb * R), pos0 = len - q_len;
   const int i_first = rb * R / G, i_last = (rb * R + rows - 1) / G;
   const int lo = p.window > 0 ? max(0, pos0 + i_first - p.window + 1) : 0;
@@ -395,7 +427,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
 
   // ---- results
   const Results<O, D, R> results{p, first_token, h, rb};
-  float* part = p.part + (int64_t)(bh * per_group + rest) * SLOT;
+  float* part = p.part + (int64_t)(group * per_group + rest) * SLOT;
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
     const int r = w_row + 16 * t + c;
@@ -428,13 +460,10 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
 template <Out O, int D, int R>
 __global__ __launch_bounds__(256) void join_kernel(KvArgs p) {
   constexpr int ROWS = 256 / (D / 4), SLOT = R * (D + 2), AT_ONCE = 8;
-  const int blocks_max = gridDim.x / (p.num_seqs * p.kv_heads * (R / ROWS));
-  const int unit = blockIdx.x / (R / ROWS), bh = unit / blocks_max;
-  const int b = bh / p.kv_heads, h = bh - b * p.kv_heads;
-  const int first_token = p.one_each ? b : seq_start(p, b);
-  const int q_len = p.one_each ? 1 : min(max(seq_start(p, b + 1) - first_token, 0), p.max_q);
-  const int blocks = (q_len * p.group + R - 1) / R, rb = blocks - 1 - (unit - bh * blocks_max);
-  if (rb < 0 || (p.mixed && q_len * p.group <= kFewRows)) return;
+  const int unit = blockIdx.x / (R / ROWS), group = unit / p.row_width;
+  const RowBlock block = row_block<R>(p, group, unit - group * p.row_width, threadIdx.x & 63);
+  if (block.rb < 0) return;
+  const int h = block.h, rb = block.rb, first_token = block.first_token, q_len = block.q_len;
   const int r = blockIdx.x % (R / ROWS) * ROWS + threadIdx.x / (D / 4), d = threadIdx.x % (D / 4) * 4;
   if (r >= min(R, q_len * p.group - rb * R)) return;
   const float* part = p.part + (int64_t)unit * p.splits * SLOT;
@@ -470,16 +499,19 @@ __global__ __launch_bounds__(256) void join_kernel(KvArgs p) {
   if (p.lse && d == 0) results.store_lse(r, top, sum);
 }
 
-// Rows of a workgroup: 8 waves halve the decoding per row; 4 where no sequence fills more.
 template <Out O, int D, int WAVES>
 hipError_t launch(const KvArgs& a, int cus, hipStream_t stream) {
   constexpr int R = 32 * WAVES;
   KvArgs args = a;
-  const int64_t blocks = ((int64_t)a.max_q * a.group + R - 1) / R, groups = (int64_t)a.num_seqs * a.kv_heads;
-  // units that exist, at most: ragged sequences leave some of the grid's without rows
+  const RowsGrid grid = rows_grid(R, a.num_tokens, a.num_seqs, a.max_q, a.group, a.kv_heads);
+  const int64_t places = grid.groups * grid.width;
+  args.row_groups = (int)grid.groups;
+  args.row_width = (int)grid.width;
+  args.row_listed = grid.listed;
+  // units that exist, at most: ragged sequences leave some of the places without rows
   const int64_t rows = (int64_t)a.num_tokens * a.group, most = a.mixed ? rows / kFewRows : a.num_seqs;
   int64_t units = (rows / R + (most < a.num_seqs ? most : a.num_seqs)) * a.kv_heads;
-  if (units > blocks * groups) units = blocks * groups;
+  if (units > places) units = places;
   const int64_t fill = (int64_t)cus * (8 / WAVES);  // workgroups that run at once
   const int64_t tiles = ((int64_t)(a.window > 0 && a.window + a.max_q < a.max_kv ? a.window + a.max_q : a.max_kv) + kTile - 1) / kTile;
   // The number of parts that takes the fewest tiles' time.  A workgroup's beginning and end cost about three
@@ -487,7 +519,7 @@ hipError_t launch(const KvArgs& a, int cus, hipStream_t stream) {
   // the workgroups that run at once.  (2 x 134 tokens, 8 heads on 4 of 128 dims, 2133 positions: one part
   // 86 us, so 26 us; one sequence of 1575 tokens, 4 heads on 1, 3756 positions: 141 and 40 us.)
   int64_t splits = 1, best = 0;
-  for (int64_t s = 1; s == 1 || (s <= tiles / 2 && blocks * groups * s <= 2 * fill); ++s) {
+  for (int64_t s = 1; s == 1 || (s <= tiles / 2 && places * s <= 2 * fill); ++s) {
     const int64_t cost = (units * s + fill - 1) / fill * ((tiles + s - 1) / s + 3) + (s > 1 ? 2 + s / 8 : 0);
     if (s == 1 || cost < best) {
       best = cost;
@@ -496,16 +528,16 @@ hipError_t launch(const KvArgs& a, int cus, hipStream_t stream) {
   }
   args.splits = (int)splits;
   void* argv[] = {&args};
-  hipError_t err = hipLaunchKernel((const void*)&rows_kernel<O, D, WAVES>, dim3((unsigned)(blocks * groups * splits)),
+  hipError_t err = hipLaunchKernel((const void*)&rows_kernel<O, D, WAVES>, dim3((unsigned)(places * splits)),
                                    dim3(64 * WAVES), argv, 0, stream);
   if (err != hipSuccess || splits == 1) return err;
-  return hipLaunchKernel((const void*)&join_kernel<O, D, R>, dim3((unsigned)(blocks * groups * (R * (D / 4) / 256))), dim3(256),
+  return hipLaunchKernel((const void*)&join_kernel<O, D, R>, dim3((unsigned)(places * (R * (D / 4) / 256))), dim3(256),
                          argv, 0, stream);
 }
 
 template <Out O, int D>
 hipError_t launch(const KvArgs& a, int cus, hipStream_t stream) {
-  return (int64_t)a.max_q * a.group > 128 ? launch<O, D, 8>(a, cus, stream) : launch<O, D, 4>(a, cus, stream);
+  return rows_waves(a.max_q, a.group) == 8 ? launch<O, D, 8>(a, cus, stream) : launch<O, D, 4>(a, cus, stream);
 }
 
 }  // namespace

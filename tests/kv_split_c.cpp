@@ -7,5 +7,15 @@ int64_t context_positions(int window, int max_q, int max_kv) { return bsg::conte
 int line_fits(int64_t tokens, int group, int64_t seqs, int kv_heads, int64_t context) {
   return bsg::line_fits(tokens, group, seqs, kv_heads, context);
 }
+void rows_grid(int rows, int64_t tokens, int64_t seqs, int max_q, int group, int kv_heads, int64_t out[3]) {
+  const bsg::RowsGrid g = bsg::rows_grid(rows, tokens, seqs, max_q, group, kv_heads);
+  out[0] = g.listed;
+  out[1] = g.groups;
+  out[2] = g.width;
+}
+int row_slot(int start, int b, int group, int rows) { return bsg::row_slot(start, b, group, rows); }
+int attend_fits(int64_t tokens, int64_t seqs, int max_q, int group, int kv_heads, int64_t context) {
+  return bsg::attend_fits(tokens, seqs, max_q, group, kv_heads, context);
+}
 int unit_cost(void) { return bsg::kUnitCost; }
 }

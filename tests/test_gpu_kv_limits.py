@@ -58,3 +58,40 @@ def test_more_units_than_a_call_can_count_are_refused():
             plan.attend(batch, x, torch.zeros(plan.page_bytes, dtype=torch.uint8, device="cuda"), x)
         assert e.value.status_name == "BSG_ERR_UNSUPPORTED"
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("new,lens,G", [
+    ([300] + [1] * 20, [400] + [5 + 9 * i for i in range(20)], 4),               # one prompt, single tokens
+    ([0, 2, 330, 0, 9, 1, 1, 8, 7, 30, 1, 0], [9, 2, 330, 0, 40, 700, 1, 8, 3, 30, 64, 5], 4),
+    ([1] * 70 + [280] + [3] * 70, [9 + i for i in range(70)] + [500] + [40 + i for i in range(70)], 4),  # past 64 sequences
+    ([40] + [1] * 9 + [5, 0], [900] + [30 + i for i in range(9)] + [5, 3], 40),   # groups that are too wide for the other kernel
+])
+@pytest.mark.parametrize("H,D,dtype,kw", [(1, 64, "f16", {}), (8, 64, "bf16", {"window": 50}), (3, 128, "bf16", {"causal": False})], ids=str)
+def test_uneven_batches_list_their_row_blocks(new, lens, G, H, D, dtype, kw):
+    run_case(new, lens, H=H, G=G, D=D, dtype=dtype, seed=len(new) + H, **kw)
+
+
+def test_a_long_prompt_beside_many_single_tokens():
+    # 64 heads on 8: 32768 new tokens of one sequence and one of 1023 others, in one call and apart
+    n, others, hq, hk, D, P = 32768, 1023, 64, 8, 64, 64
+    g = torch.Generator(device="cuda").manual_seed(0)
+    q = torch.randn(n + others, hq, D, generator=g, device="cuda").bfloat16()
+    lens = torch.randint(1, 200, (others,), generator=g, device="cuda", dtype=torch.int32)
+    pages = torch.randint(0, 600, (others + 1, n // P), generator=g, device="cuda", dtype=torch.int32)
+    with bsg.KVPlan(hq, hk, D, P, 600, n + others) as plan:
+        cache = torch.randint(0, 56, (600 * plan.page_bytes,), generator=g, device="cuda", dtype=torch.uint8)
+        print("[kv] 32768 tokens beside 1023 single ones", flush=True)
+
+        def attend(a, z, starts, lens, pages, max_q, max_kv):
+            out, lse = torch.zeros_like(q[a:z]), torch.zeros(z - a, hq, device="cuda")
+            plan.attend(bsg.KVBatch(dev(np.array(starts, np.int32)), lens, pages, z - a, max_q, max_kv), q[a:z], cache, out, lse=lse)
+            torch.cuda.synchronize()
+            return out, lse
+        one = torch.tensor([n], dtype=torch.int32, device="cuda")
+        whole = attend(0, n + others, np.r_[0, n:n + others + 1], torch.cat((one, lens)), pages, n, n)
+        apart = [attend(0, n, [0, n], one, pages[:1], n, n), attend(n, n + others, np.arange(others + 1), lens, pages[1:], 1, n)]
+    for got, want in zip(whole, zip(*apart)):
+        want = torch.cat(want)
+        assert torch.isfinite(got).all()
+        # values reach 6 x 0.94 (E4M3 code 55): the two calls differ by their roundings only
+        assert ((got.float() - want.float()).abs() <= 2.0 ** -7 * want.abs() + 2.0 ** -10 * 5.7).all()

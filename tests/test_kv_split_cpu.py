@@ -5,6 +5,7 @@ import os
 import shutil
 import subprocess
 
+import numpy as np
 import pytest
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -21,7 +22,15 @@ def split(tmp_path_factory):
     lib, i64 = ctypes.CDLL(lib), ctypes.c_int64
     lib.context_positions.restype = i64
     lib.line_fits.argtypes = [i64, ctypes.c_int, i64, ctypes.c_int, i64]
+    lib.rows_grid.argtypes = [ctypes.c_int, i64, i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, i64 * 3]
+    lib.attend_fits.argtypes = [i64, i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, i64]
     return lib
+
+
+def rows_grid(split, rows, new, group, heads):
+    out = (ctypes.c_int64 * 3)()
+    split.rows_grid(rows, sum(new), len(new), max(new), group, heads, out)
+    return bool(out[0]), out[1], out[2]
 
 
 @pytest.mark.parametrize("tiles", [1, 2, 9, 512, 4_202_521, 1 << 23, (1 << 24) - 1, 1 << 24])
@@ -55,3 +64,37 @@ def test_positions_that_are_seen(split, window):
         for max_kv in (1, 900, 1 << 30):
             want = min(max_kv, window + max_q + 16) if window else max_kv
             assert split.context_positions(window, max_q, max_kv) == want
+
+
+def test_a_long_prompt_beside_many_single_tokens_fits_a_launch(split):
+    # 1024 row blocks for each of 1024 sequences and 8 heads would be 2^23 workgroups of 512 threads, one more than a
+    # launch may have; 33791 tokens of 64 heads fill about 1056 blocks of 256 rows per head
+    new = [32768] + [1] * 1023
+    listed, groups, width = rows_grid(split, 256, new, 8, 8)
+    assert listed and groups == 8 and 1056 <= width <= 1056 + 1024
+    assert split.attend_fits(sum(new), len(new), max(new), 8, 8, 1 << 17)
+    assert split.attend_fits(32768, 1, 32768, 8, 8, 1 << 20)         # that prompt alone over a million positions
+    assert not split.attend_fits(1 << 22, 1 << 22, 1, 512, 2, 4096)  # 2^23 blocks: refused, not launched
+
+
+@pytest.mark.parametrize("rows", [128, 256])
+@pytest.mark.parametrize("group", [1, 3, 8, 40, 256])
+def test_listed_blocks_have_slots_of_their_own(split, rows, group):
+    rng = np.random.default_rng(rows + group)
+    for new in ([1], [0, 0, 5], [600] + [1] * 70, list(rng.integers(0, 90, 200)), [0] * 65 + [900] + [33] * 64):
+        new = [int(n) for n in new]
+        starts = np.concatenate([[0], np.cumsum(new)])
+        slots = [split.row_slot(int(s), b, group, rows) for b, s in enumerate(starts)]
+        assert slots[0] == 0
+        for b, n in enumerate(new):
+            assert slots[b + 1] > slots[b] and slots[b + 1] - slots[b] >= -(-n * group // rows)
+        listed, groups, width = rows_grid(split, rows, new, group, 3)
+        blocks = -(-max(new) * group // rows)
+        assert (groups, width) == ((3, slots[-1]) if listed else (3 * len(new), blocks))
+        assert groups * width <= 3 * 2 * slots[-1]  # never more than twice the blocks that can exist
+    assert split.row_slot(1 << 24, 1 << 24, 64, 128) == (1 << 23) + (1 << 24)
+
+
+def test_even_batches_keep_a_group_for_each_sequence_and_head(split):
+    assert rows_grid(split, 256, [2048, 2048], 4, 8) == (False, 16, 32)
+    assert rows_grid(split, 128, [20], 4, 1) == (False, 1, 1)
