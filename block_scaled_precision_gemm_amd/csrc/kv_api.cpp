@@ -236,7 +236,7 @@ bsg_status bsg_kv_plan_create(const bsg_kv_problem* problem, bsg_kv_plan* out_pl
   a.page_shift = __builtin_ctz((unsigned)p.page_tokens);
   a.num_pages = (int)p.num_pages;
   a.rope_half = p.rope_dim / 2;
-  a.window = p.window;
+  a.window = bsg::kept_window(p.window);
   a.flags = (int)p.flags;
   a.page_stride = p.page_stride;
   a.score_mul = p.scale * p.k_scale;

@@ -513,7 +513,8 @@ hipError_t launch(const KvArgs& a, int cus, hipStream_t stream) {
   int64_t units = (rows / R + (most < a.num_seqs ? most : a.num_seqs)) * a.kv_heads;
   if (units > places) units = places;
   const int64_t fill = (int64_t)cus * (8 / WAVES);  // workgroups that run at once
-  const int64_t tiles = ((int64_t)(a.window > 0 && a.window + a.max_q < a.max_kv ? a.window + a.max_q : a.max_kv) + kTile - 1) / kTile;
+  const int64_t seen = a.window > 0 ? (int64_t)a.window + a.max_q : a.max_kv;
+  const int64_t tiles = ((seen < a.max_kv ? seen : a.max_kv) + kTile - 1) / kTile;
   // The number of parts that takes the fewest tiles' time.  A workgroup's beginning and end cost about three
   // tiles, the join two and one more for 8 parts.  At least two tiles per part; the workspace holds twice
   // the workgroups that run at once.  (2 x 134 tokens, 8 heads on 4 of 128 dims, 2133 positions: one part

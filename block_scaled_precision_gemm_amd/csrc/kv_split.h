@@ -13,6 +13,9 @@ constexpr int kFewRows = 32;  // most query rows per sequence and key/value head
 // for each further unit of a run, 0.7 us per tile).
 constexpr int kUnitCost = 12;
 
+// A window that no context reaches (max_kv is at most 2^30) is none: differences of positions and window stay in 32 bits.
+constexpr int kept_window(int window) { return window >= 1 << 30 ? 0 : window; }
+
 // Positions that some row of a sequence sees, at most: 16 more than window and new tokens, spans starting at multiples of 16.
 constexpr int64_t context_positions(int window, int max_q, int max_kv) {
   const int64_t seen = window > 0 ? (int64_t)window + max_q + 16 : max_kv;

@@ -3,6 +3,7 @@
 
 extern "C" {
 int piece_begin(int at, int pieces, int tiles) { return bsg::piece_begin(at, pieces, tiles); }
+int kept_window(int window) { return bsg::kept_window(window); }
 int64_t context_positions(int window, int max_q, int max_kv) { return bsg::context_positions(window, max_q, max_kv); }
 int line_fits(int64_t tokens, int group, int64_t seqs, int kv_heads, int64_t context) {
   return bsg::line_fits(tokens, group, seqs, kv_heads, context);

@@ -95,3 +95,13 @@ def test_a_long_prompt_beside_many_single_tokens():
         assert torch.isfinite(got).all()
         # values reach 6 x 0.94 (E4M3 code 55): the two calls differ by their roundings only
         assert ((got.float() - want.float()).abs() <= 2.0 ** -7 * want.abs() + 2.0 ** -10 * 5.7).all()
+
+
+@pytest.mark.parametrize("window", [(1 << 30) - 1, 1 << 30, (1 << 31) - 1])
+def test_windows_without_an_end(window):
+    # more new tokens than positions: the first queries see nothing, the others all up to their own
+    run_case([7, 2, 1], [3, 1, 90], seed=23, window=window)
+    run_case([70, 40], [20, 500], seed=24, window=window)
+    args = dict(new=[40], lens=[900], H=1, G=4, D=64, P=32, dtype="f16", seed=25)
+    for a, b in zip(run_case(**args, window=window), run_case(**args)):
+        assert np.array_equal(a, b)  # cut into the same parts as without a window

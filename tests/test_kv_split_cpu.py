@@ -98,3 +98,12 @@ def test_listed_blocks_have_slots_of_their_own(split, rows, group):
 def test_even_batches_keep_a_group_for_each_sequence_and_head(split):
     assert rows_grid(split, 256, [2048, 2048], 4, 8) == (False, 16, 32)
     assert rows_grid(split, 128, [20], 4, 1) == (False, 1, 1)
+
+
+def test_windows_that_no_context_reaches_are_none(split):
+    for window in (0, 1, 900, (1 << 30) - 1):
+        assert split.kept_window(window) == window
+    for window in (1 << 30, (1 << 31) - 1):
+        assert split.kept_window(window) == 0
+    # what kernels form from a window that is kept: position, new tokens and window at their largest
+    assert -(1 << 31) < -(1 << 24) - ((1 << 30) - 1) and (1 << 30) - 1 + (1 << 30) < 1 << 31
