@@ -90,8 +90,9 @@ __device__ __forceinline__ void load_query(const KvArgs& p, int first_token, int
 
 // The row as fp16, and the base-2 score of one unit of q . k as the products give it, made positive (q
 // takes the sign), so that maxima can be taken over the products themselves.  Keys decode times 2^-8;
-// bf16 rows are scaled so that their largest magnitude lies in [2^14, 2^15), exact in fp16 down to 2^-39
-// of it.
+// bf16 rows are scaled so that their largest magnitude lies in [2^14, 2^15): fp16's steps are then 2^-39 of it and
+// less, so that all 8 bits of an element are kept down to 2^-31 of it.  (A row with an infinity or a NaN is scaled as
+// if its largest were 2^127, so that its finite elements stay finite.)
 template <Out O, int D>
 __device__ __forceinline__ void convert_query(const KvArgs& p, const v4i w[D / 32], v8h q[D / 32], float& mul) {
   constexpr int NJ = D / 32;
@@ -111,7 +112,7 @@ __device__ __forceinline__ void convert_query(const KvArgs& p, const v4i w[D / 3
       }
     most = max_over_g(most);
     const int e = (int)(__builtin_bit_cast(uint32_t, most) >> 23) - 127;  // -127 for zero and subnormals
-    const int up = e > 127 ? 0 : max(14 - e, -110);                       // inf or NaN: as it is
+    const int up = 14 - min(e, 127);
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
 #pragma unroll
@@ -121,7 +122,7 @@ __device__ __forceinline__ void convert_query(const KvArgs& p, const v4i w[D / 3
   if (p.score_mul < 0.0f)
 #pragma unroll
     for (int j = 0; j < NJ; ++j) q[j] = -q[j];
-  mul = __builtin_fmaxf(__builtin_fabsf(mul), 1.17549435e-38f);
+  mul = __builtin_amdgcn_fmed3f(__builtin_fabsf(mul), 1.17549435e-38f, 3.402823466e38f);
 }
 
 hipError_t kv_attend_rows_launch(const KvArgs& a, int dtype, int head_dim, int cus, hipStream_t stream);

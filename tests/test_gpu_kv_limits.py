@@ -105,3 +105,19 @@ def test_windows_without_an_end(window):
     args = dict(new=[40], lens=[900], H=1, G=4, D=64, P=32, dtype="f16", seed=25)
     for a, b in zip(run_case(**args, window=window), run_case(**args)):
         assert np.array_equal(a, b)  # cut into the same parts as without a window
+
+
+def test_queries_up_to_the_largest_bf16():
+    def case(new, lens, seed):
+        q_start, pages, n_pages = layout(new, lens, 16, seed)
+        c = filled(lens, 2, 64, 16, pages, n_pages, seed + 1)
+        q = torch.randn(sum(new), 8, 64, generator=torch.Generator().manual_seed(seed)) * 1e38
+        q = q.clamp(-3.38e38, 3.38e38).bfloat16()
+        q[0, 0, 5] = torch.finfo(torch.bfloat16).max
+        scale = 3e-38
+        want, wl = kv_ref.attend(q.double().numpy(), c, q_start, lens, pages, 2, scale=float(np.float32(scale)))
+        got, lse = attend(c, q.cuda(), q_start, lens, pages, 2, 16, 64, "bf16", scale=scale)
+        assert np.isfinite(want).all()
+        check(got, lse, want, wl, "bf16", 4.5, f"largest {new}")
+    case([3, 1], [90, 40], 26)
+    case([50], [120], 27)
