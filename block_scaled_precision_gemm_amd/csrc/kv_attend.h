@@ -90,7 +90,7 @@ __device__ __forceinline__ void load_query(const KvArgs& p, int first_token, int
 
 // The row as fp16, and the base-2 score of one unit of q . k as the products give it, made positive (q
 // takes the sign), so that maxima can be taken over the products themselves.  Keys decode times 2^-8;
-// bf16 rows are scaled so that their largest magnitude lies in [2^14, 2^15): fp16's steps are then 2^-39 of it and
+// bf16 rows are scaled so that their largest magnitude lies in [2^14, 2^15): fp16's steps are then 2^-38 of it and
 // less, so that all 8 bits of an element are kept down to 2^-31 of it.  (A row with an infinity or a NaN is scaled as
 // if its largest were 2^127, so that its finite elements stay finite.)
 template <Out O, int D>

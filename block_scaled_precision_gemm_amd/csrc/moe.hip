@@ -244,12 +244,12 @@ __device__ __forceinline__ void prepare_row(const MoeArgs& p, int t, uint32_t* s
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < kRouterWaves; ++k) most = max(most, shared[k]);
-    // largest magnitude to [2^7, 2^8): exact in fp16 down to 2^-32 of it, and products with decoded
-    // weights (below 2^4) stay far inside fp32; rows with an infinity or a NaN are left as they are
-    const int e = (int)(most >> 7) - 127, up = e > 127 ? 0 : max(7 - e, -110);
+    // Largest magnitude to [2^7, 2^8): fp16's steps are then 2^-31 of it and less, all 8 bits of an element are kept
+    // down to 2^-24 of it, and products with decoded weights (below 2^4) stay far inside fp32.  (Rows of bf16 subnormals:
+    // short of it, still exact.  Rows with an infinity or a NaN: as if their largest were 2^127.)
+    const int up = min(7 - min((int)(most >> 7) - 127, 127), 127);
     if (tid == 0) p.x_exp[t] = up;
-    scale = __builtin_amdgcn_ldexpf(1.0f, min(up, 127));  // (rows of bf16 subnormals: short of it, still exact)
-    if (up > 127 && tid == 0) p.x_exp[t] = 127;
+    scale = __builtin_amdgcn_ldexpf(1.0f, up);
   }
   for (int i = 8 * tid; i < p.hidden; i += 8 * kRouterThreads) {
     if (PREP != Prep::kScaled || p.hidden > 8 * kRouterThreads) w = *(const v4i*)(x + i);  // else still held

@@ -10,8 +10,9 @@
  *     out = sum over the chosen experts of w y, in the order of their rank
  * with expert weights in the library's block-scaled operand formats (bsg.h; the B operand, row-major
  * scales): w13 [experts][2 inter][hidden], w2 [experts][hidden][inter], each expert's codes and scales
- * following the previous one's.  Sums are fp32; activations enter the products at full precision (16
- * significant bits for SiLU(gate) up); out is rounded once.
+ * following the previous one's.  Sums are fp32; out is rounded once.  x enters its products as it is, except that
+ * beside NVFP4 weights elements of a bf16 token below 2^-24 of its largest magnitude keep fewer than their 8 bits
+ * (steps of 2^-31 of that magnitude).  SiLU(gate) up is held in two bf16 parts, 16 significant bits.
  *
  * Conventions are those of bsg.h: a plan made once, O(1) host work per call, no allocation or
  * synchronisation in a call (it can be captured into a HIP graph), bsg_status and bsg_last_error().

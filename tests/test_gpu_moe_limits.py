@@ -1,0 +1,34 @@
+"""The expert layer at the ends of its arguments' ranges, against the 64-bit reference of moe_ref."""
+import numpy as np
+import pytest
+import torch
+
+import block_scaled_precision_gemm_amd as bsg
+import moe_ref
+from test_gpu_moe import DT, UNIT, dev
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("T", [1, 5])
+def test_tokens_up_to_the_largest_bf16(T):
+    # weights of 2^-9 times E2M1 and alphas near 2^-120 keep every result of the definition inside fp32
+    E, K, H, I = 4, 2, 128, 64
+    rng = np.random.default_rng(T)
+    w13, w2 = rng.integers(0, 256, (E, 2 * I, H // 2), np.uint8), rng.integers(0, 256, (E, H, I // 2), np.uint8)
+    s13, s2 = np.full((E, 2 * I, H // 16), 1, np.uint8), np.full((E, H, I // 16), 40, np.uint8)
+    x = torch.from_numpy(rng.standard_normal((T, H)) * 1e38).clamp(-3.38e38, 3.38e38).bfloat16()
+    x[0, 7] = torch.finfo(torch.bfloat16).max
+    router = torch.from_numpy(rng.integers(1, 4, (E, H)) * rng.choice([-1.0, 1.0], (E, H)) * 2.0 ** -126).bfloat16()
+    a13 = (rng.uniform(0.5, 2.0, E) * 2.0 ** -122).astype(np.float32)
+    want, ids, _ = moe_ref.moe("nvfp4", x.double().numpy(), router.double().numpy(), w13, s13, w2, s2, K, a13)
+    assert np.isfinite(want).all()
+    out, got_ids = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda"), torch.zeros(T, K, dtype=torch.int32, device="cuda")
+    print(f"[moe] largest bf16 T={T}", flush=True)
+    with bsg.MoEPlan("nvfp4", E, K, H, I, T) as plan:
+        plan.run(x.cuda(), router.cuda(), dev(w13), dev(s13), dev(w2), dev(s2), out, alpha13=dev(a13), ids=got_ids)
+        torch.cuda.synchronize()
+    assert np.array_equal(got_ids.cpu().numpy(), ids)
+    got = out.double().cpu().numpy()
+    lim = UNIT["bf16"] * np.abs(want) + 2.0 ** -13 * np.sqrt((want ** 2).mean(1, keepdims=True))
+    assert (np.abs(got - want) <= lim).all()
