@@ -20,7 +20,7 @@ struct KvArgs {
   int num_pages, rope_half, window, flags;
   int64_t page_stride;
   float score_mul;   // scale * k_scale: score = score_mul * q . (stored k)
-  float softcap;     // 0: none
+  float cap, cap_inv;  // the soft cap in base 2, and its reciprocal; 0: none
   float k_inv, v_inv, v_scale, k_scale;
   // batch
   int num_seqs, num_tokens, max_q, max_kv;

@@ -240,7 +240,8 @@ bsg_status bsg_kv_plan_create(const bsg_kv_problem* problem, bsg_kv_plan* out_pl
   a.flags = (int)p.flags;
   a.page_stride = p.page_stride;
   a.score_mul = p.scale * p.k_scale;
-  a.softcap = p.softcap;
+  a.cap = p.softcap * 1.44269504088896341f;
+  a.cap_inv = p.softcap > 0.0f ? 1.0f / a.cap : 0.0f;
   a.k_scale = p.k_scale;
   a.v_scale = p.v_scale;
   a.k_inv = 1.0f / p.k_scale;

@@ -125,6 +125,57 @@ __device__ __forceinline__ void convert_query(const KvArgs& p, const v4i w[D / 3
   mul = __builtin_amdgcn_fmed3f(__builtin_fabsf(mul), 1.17549435e-38f, 3.402823466e38f);
 }
 
+// The soft cap c of a row's scores, c tanh(score / c), on the products s whose score is s mul (all in base 2; the results are
+// products too).  With y = s mul / c:
+// * up to y = 1/4: y - y^3/3 + 2 y^5/15 - 17 y^7/315, the next term being 2^-21 of y there;
+// * beyond: 1 - 2 / (e^2y + 1), within 2^-20 from there on.  For small y it would lose the digits that y shares with 1, an
+//   error of 2^-22 c: a score of 4 under a cap of 1e5 would be off by 0.02, but by no more than 2^-16 under one of 64.
+// Caps are mostly far above the scores, so a wave looks first whether any of its scores is beyond.  If so, all of them take
+// the second form under caps up to 64, and each its own under others.  64 tokens over up to 16384 positions, 64 heads on 8,
+// and 2 x 2048 tokens against 8192 and 3351 positions, 32 heads on 8: 141 and 404 us with no score beyond, 143 and 441 us
+// with some and the second form for all, 153 and 554 us with some and both forms.
+constexpr float kLowCap = 64.0f * kLog2e;
+template <int N>
+__device__ __forceinline__ void soft_cap(const KvArgs& p, float mul, v4f s[N]) {
+  const float to_y = __builtin_fminf(mul * p.cap_inv, 3e38f);
+  float most = 0.0f;
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) most = __builtin_fmaxf(most, __builtin_fabsf(s[k][i]));
+  auto small = [&](float x, float z) {
+    return x * __builtin_fmaf(z, __builtin_fmaf(z, __builtin_fmaf(z, -17.0f / 315, 2.0f / 15), -1.0f / 3), 1.0f);
+  };
+  if (!__any(most * to_y >= 0.25f)) {
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float y = s[k][i] * to_y;
+        s[k][i] = small(s[k][i], y * y);
+      }
+  } else {
+    const float to_exp = to_y * (2.0f * kLog2e), cap = p.cap * __builtin_amdgcn_rcpf(mul);
+    auto large = [&](float x) {
+      return cap * __builtin_fmaf(-2.0f, __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(x * to_exp) + 1.0f), 1.0f);
+    };
+    if (p.cap <= kLowCap) {
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[k][i] = large(s[k][i]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float x = s[k][i], y = x * to_y, z = y * y;
+          s[k][i] = z >= 0.0625f ? large(x) : small(x, z);
+        }
+    }
+  }
+}
+
 hipError_t kv_attend_rows_launch(const KvArgs& a, int dtype, int head_dim, int cus, hipStream_t stream);
 // Floats of parts that kv_attend_rows_launch may use.
 size_t kv_rows_part_floats(const bsg_kv_problem& p, int cus);

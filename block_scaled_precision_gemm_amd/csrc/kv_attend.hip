@@ -276,19 +276,9 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
         }
         // -- masks: only where a row does not see the whole step
         const bool edge = t0 + kStep - 1 > min(first_pos, w1 - 1) || (p.window > 0 && t0 <= last_row_pos - p.window);
-        float scale[RT];
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-          scale[t] = mul[t];
-          if (p.softcap > 0.0f) {
-            const float cap = p.softcap * kLog2e, inv = 2.0f / p.softcap * mul[t];  // tanh(y) = 1 - 2 / (e^2y + 1)
-            scale[t] = 1.0f;
-#pragma unroll
-            for (int gr = 0; gr < NG; ++gr)
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                sc[t][gr][i] = cap - 2.0f * cap * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(sc[t][gr][i] * inv) + 1.0f);
-          }
+          if (p.cap > 0.0f) soft_cap<NG>(p, mul[t], sc[t]);
           if (edge) {
             const int first = t0 + 4 * rare(g), top = min(pos[t], w1 - 1), bottom = p.window > 0 ? pos[t] - p.window : -1;
 #pragma unroll
@@ -330,13 +320,13 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
             for (int i = 0; i < 4; ++i) top = __builtin_fmaxf(top, sc[t][gr][i]);
           if (__any(top > m[t])) {  // (kSlack would save nothing here: 79.9 and 79.6 us for the 64 tokens above)
             const float grown = __builtin_fmaxf(m[t], max_over_g(top));
-            const float f = grown == kNegInf ? 1.0f : __builtin_amdgcn_exp2f((m[t] - grown) * scale[t]);
+            const float f = grown == kNegInf ? 1.0f : __builtin_amdgcn_exp2f((m[t] - grown) * mul[t]);
             m[t] = grown;
             l[t] *= f;
 #pragma unroll
             for (int e = 0; e < E; ++e) o[t][e] *= f;
           }
-          const float off = m[t] == kNegInf ? 0.0f : kPBias - m[t] * scale[t];
+          const float off = m[t] == kNegInf ? 0.0f : kPBias - m[t] * mul[t];
 #pragma unroll
           for (int k = 0; k < NG / 2; ++k)
 #pragma unroll
@@ -344,7 +334,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
               float e4[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                e4[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][2 * k + half][i], scale[t], off));
+                e4[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][2 * k + half][i], mul[t], off));
                 l[t] += e4[i];
               }
               const v2h a = __builtin_convertvector((v2f{e4[0], e4[1]}), v2h), bb = __builtin_convertvector((v2f{e4[2], e4[3]}), v2h);
@@ -412,7 +402,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
     // a scaled maximum from here on
 #pragma unroll
     for (int t = 0; t < RT; ++t)
-      if (m[t] != kNegInf && p.softcap <= 0.0f) m[t] *= mul[t];
+      if (m[t] != kNegInf) m[t] *= mul[t];
 
     // ---- join the waves
 #pragma unroll

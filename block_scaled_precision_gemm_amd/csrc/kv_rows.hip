@@ -309,16 +309,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
       const bool edge = t0 + kTile - 1 > min(w_first, t_end - 1) || (p.window > 0 && t0 <= w_last - p.window);
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
-        float scale = mul[t];
-        if (p.softcap > 0.0f) {
-          const float cap = p.softcap * kLog2e, inv = 2.0f / p.softcap * mul[t];  // tanh(y) = 1 - 2 / (e^2y + 1)
-          scale = 1.0f;
-#pragma unroll
-          for (int gr = 0; gr < 4; ++gr)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              sc[t][gr][i] = cap - 2.0f * cap * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(sc[t][gr][i] * inv) + 1.0f);
-        }
+        const float scale = mul[t];
+        if (p.cap > 0.0f) soft_cap<4>(p, scale, sc[t]);
         if (edge) {
           const int first = t0 + 4 * rare(g), top = min(pos[t], t_end - 1), bottom = p.window > 0 ? pos[t] - p.window : -1;
 #pragma unroll
@@ -431,7 +423,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
     const int r = w_row + 16 * t + c;
-    const float sum = sum_over_g(l[t]), top = m[t] == kNegInf ? kNegInf : p.softcap > 0.0f ? m[t] : m[t] * mul[t];
+    const float sum = sum_over_g(l[t]), top = m[t] == kNegInf ? kNegInf : m[t] * mul[t];
     if (r >= rows) continue;
     if (p.splits == 1) {
       const float f = p.v_scale * 256.0f / sum;

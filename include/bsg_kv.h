@@ -61,7 +61,7 @@ typedef struct bsg_kv_problem {
   int32_t rope_dim;     /* rotated dims, 0 or a multiple of 16 up to head_dim */
   int32_t window;       /* > 0: a query at position p sees positions (p - window, p]; 0 = all */
   float scale;          /* of the scores; 0 = 1 / sqrt(head_dim) */
-  float softcap;        /* > 0: scores become softcap * tanh(score / softcap); 0 = none */
+  float softcap;        /* > 0: scores become softcap * tanh(score / softcap), within 2^-16 or 2^-19 of that; 0 = none */
   float k_scale, v_scale; /* global scales of stored keys and values; 0 = 1 */
   int32_t device;       /* HIP device ordinal; -1 = the current device at create time */
 } bsg_kv_problem;

@@ -121,3 +121,11 @@ def test_queries_up_to_the_largest_bf16():
         check(got, lse, want, wl, "bf16", 4.5, f"largest {new}")
     case([3, 1], [90, 40], 26)
     case([50], [120], 27)
+
+
+@pytest.mark.parametrize("softcap", [0.5, 8.0, 50.0, 65.0, 2500.0, 1e5, 1e30, 3e38])
+@pytest.mark.parametrize("new,lens", [([3, 1], [90, 300]), ([40, 70], [300, 200])], ids=["few", "many"])
+def test_soft_caps(softcap, new, lens):
+    # a capped score is within 2^-19 of itself, or 2^-16, so a cap far above the scores changes nothing
+    run_case(new, lens, D=64, dtype="f16", seed=21, softcap=softcap, q_gain=2.0)
+    run_case(new, lens, D=128, dtype="bf16", seed=22, softcap=softcap)
