@@ -8,11 +8,6 @@ namespace bsg {
 
 typedef float v2f __attribute__((ext_vector_type(2)));
 
-// P is held as 2^kPBias P, relative to a row's reference m: a maximum of its products, which the many-row kernel
-// only replaces (and rescales the row's sums) once some product lies more than kSlack above it.  P then stays
-// below 2^15, and weights down to 2^-34 of the largest are kept (fp16 steps are 2^-24).
-constexpr float kPBias = 10.0f, kSlack = 5.0f;
-
 // x, but not known to be the same in every iteration: for paths that few of them take, so that nothing formed
 // from it is kept in registers throughout a loop.
 __device__ __forceinline__ int rare(int x) {

@@ -21,8 +21,8 @@
 //   of 8 positions, interleaves the nibbles of two positions (4 operations for 16 values), and decodes
 //   each byte to the pair (position j, position j + 1), which one packed multiply scales by the pair of
 //   scales, stored with the position fastest for this purpose.
-// Softmax: reference m (kv_attend.h; here always the maximum) and sum l per row, in fp32 and base 2.  P is
-// rounded to fp16 for its product; l sums the unrounded values.
+// Softmax: maximum m and sum l per row, in fp32 and base 2.  P is rounded to fp16 for its product, 2^-11 of itself at most (a
+// second product for what is left would double the work beside the loads); l sums the unrounded values.
 //
 // Bound: bytes of the cache (D 9/8 bytes per position and head) where contexts are long; for short ones the
 // chain of dependent trips to memory (lengths, page numbers, codes, the join), about 10 us.  Measured, heads
@@ -37,6 +37,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMinTiles = 2;    // a piece is at least a step of each wave
 constexpr int kWgPerCu = 2;
+// P is held as 2^kPBias P, relative to the row's maximum in the wave's run so far: at most 2^14, and weights down to 2^-38 of
+// the largest are kept (fp16 steps are 2^-24).
+constexpr float kPBias = 14.0f;
 
 template <int CTRL, int ROWS>
 __device__ __forceinline__ int dpp_add(int x) {
@@ -318,7 +321,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
           for (int gr = 0; gr < NG; ++gr)
 #pragma unroll
             for (int i = 0; i < 4; ++i) top = __builtin_fmaxf(top, sc[t][gr][i]);
-          if (__any(top > m[t])) {  // (kSlack would save nothing here: 79.9 and 79.6 us for the 64 tokens above)
+          if (__any(top > m[t])) {  // (replacing m less often saves nothing here: 79.9 and 79.6 us for the 64 tokens above)
             const float grown = __builtin_fmaxf(m[t], max_over_g(top));
             const float f = grown == kNegInf ? 1.0f : __builtin_amdgcn_exp2f((m[t] - grown) * mul[t]);
             m[t] = grown;

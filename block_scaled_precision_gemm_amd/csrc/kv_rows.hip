@@ -27,6 +27,11 @@
 namespace bsg {
 namespace {
 
+// P is held as 2^kPBias P, relative to a row's reference m: a maximum of its products, which is only replaced (and the
+// row's sums rescaled) once some product lies more than kSlack above it.  P then stays below 2^15, and weights down to
+// 2^-34 of the largest are kept (fp16 steps are 2^-24).
+constexpr float kPBias = 10.0f, kSlack = 5.0f;
+
 // Where the results of row block rb of a sequence and head go.
 template <Out O, int D, int R>
 struct Results {

@@ -129,3 +129,22 @@ def test_soft_caps(softcap, new, lens):
     # a capped score is within 2^-19 of itself, or 2^-16, so a cap far above the scores changes nothing
     run_case(new, lens, D=64, dtype="f16", seed=21, softcap=softcap, q_gain=2.0)
     run_case(new, lens, D=128, dtype="bf16", seed=22, softcap=softcap)
+
+
+def test_weights_far_below_the_largest_are_kept():
+    # in each run of 32 positions (a wave's) one of weight 1 and value 0 beside 31 of weight 2^-36 and value 6: beside 2^14
+    # those are 2^-22 in fp16, exactly, and what is left is the output's rounding
+    c = kv_ref.Cache(1, 1, 64, 128)
+    code, s = kv_ref.quantize(np.full(64, 6.0))
+    one, s1 = kv_ref.quantize(np.r_[6.0, np.zeros(63)])
+    for p in range(128):
+        c.store(0, p, 0, True, code, s)
+    for p in (5, 37, 69, 101):
+        c.store(0, p, 0, False, one, s1)
+        c.store(0, p, 0, True, np.zeros(64, np.uint8), np.zeros(4, np.uint8))
+    q = np.zeros((1, 64))
+    q[0, 0] = 1.0
+    got, lse, want, want_lse = repeated(c, np.zeros(1, np.int32), q, float(np.float32(36 * np.log(2.0) / 6)), "bf16")
+    assert 2.6e-9 < want.min() and want.max() < 2.8e-9
+    assert (np.abs(got - want) <= 2.0 ** -8 * want).all(), (got, want)
+    assert np.abs(lse - want_lse).max() < 1e-4
