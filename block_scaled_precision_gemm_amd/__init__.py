@@ -4,8 +4,8 @@ key/value cache with its attention (include/bsg_kv.h) and the mixture-of-experts
 
 Argument marshalling only: every step runs in the HIP library.  Tensors are passed as
 device pointers (anything with .data_ptr(), or a plain int); streams as hipStream_t handles (an
-object with .cuda_stream, an int, or None for torch's current stream).  PyTorch is only used, when
-present, to find the current stream.
+object with .cuda_stream, an int, or None for torch's current stream).  PyTorch is used to find the
+current stream, when present, and to know the types of the tensors that KVPlan and MoEPlan are given.
 
 The library is loaded on first use and a missing build raises LibraryNotBuilt: there is no fallback.
 """
@@ -339,6 +339,12 @@ def pack_scales(src, dst, rows: int, codes_per_row: int, stream=None) -> None:
     _check(load_library().bsg_pack_scales(_ptr(src), _ptr(dst), rows, codes_per_row, _stream(stream)))
 
 
+def _dtypes(name: str) -> tuple:
+    """Types of tensors that hold 16-bit numbers of the named type: its own, or integers with their bits."""
+    import torch
+    return ({"bf16": torch.bfloat16, "f16": torch.float16}[name], torch.int16, torch.uint16)
+
+
 KV_ROPE_INTERLEAVED, KV_NONCAUSAL = 1, 2
 ROPE_LAYOUTS = ("half", "interleaved")
 
@@ -362,7 +368,7 @@ class KVBatch:
         for t in (q_start, kv_len, pages):
             if t.element_size() != 4 or t.is_floating_point() or (t.numel() and t.stride(-1) != 1):
                 raise ValueError("q_start, kv_len and pages must be int32 with contiguous rows")
-        self.num_tokens, self._held = num_tokens, (q_start, kv_len, pages)
+        self.num_tokens, self.max_kv, self.columns, self._held = num_tokens, max_kv, pages.shape[1], (q_start, kv_len, pages)
         stride = pages.stride(0) if seqs > 1 else pages.shape[1]
         self._args = KVBatchArgs(ctypes.sizeof(KVBatchArgs), seqs, num_tokens, max_q, max_kv, q_start.data_ptr(),
                                  kv_len.data_ptr(), pages.data_ptr(), stride)
@@ -372,9 +378,11 @@ class KVBatch:
 class KVPlan:
     """A plan of the paged NVFP4 cache and its attention for one geometry (bsg_kv.h): append, attend, read.
 
-    The cache is a uint8 device tensor of num_pages * page_bytes bytes (or with page_stride between pages).
-    q, k, v and outputs: 16-bit tensors [tokens][heads][head_dim] of `dtype`, any token and head strides that
-    are multiples of 8 elements.  window > 0: causal attention to the last `window` positions only.
+    The cache is a contiguous device tensor of num_pages * page_stride bytes (the last page's padding may be missing);
+    page_bytes is what a page holds, page_stride the bytes from one to the next, the same unless page_stride is given.
+    q, k, v and outputs: tensors [tokens][heads][head_dim] of `dtype` (or 16-bit integers that hold its bits), any
+    token and head strides that are multiples of 8 elements.  window > 0: causal attention to the last `window`
+    positions only.
     """
 
     def __init__(self, q_heads: int, kv_heads: int, head_dim: int, page_tokens: int, num_pages: int, max_tokens: int,
@@ -392,14 +400,29 @@ class KVPlan:
         h = _VP()
         _check(lib.bsg_kv_plan_create(ctypes.byref(prob), ctypes.byref(h)))
         self._h = h
-        self.page_bytes = self.info()["page_stride"]
+        info = self.info()
+        self.page_tokens, self.page_bytes, self.page_stride = page_tokens, info["page_bytes"], info["page_stride"]
+        self._cache_bytes = (num_pages - 1) * self.page_stride + self.page_bytes
+        self._dtypes = _dtypes(dtype)
 
     def _heads(self, t, tokens: int, heads: int) -> bytes:
         token_stride, head_stride, one = t.stride() if t.dim() == 3 else (0, 0, 0)
-        if one != 1 or t.shape != (tokens, heads, self.head_dim) or t.element_size() != 2:
-            raise ValueError(f"expected a 16-bit tensor [{tokens}][{heads}][{self.head_dim}] with contiguous rows, got "
-                             f"{tuple(t.shape)} with strides {t.stride()}")
+        if one != 1 or t.shape != (tokens, heads, self.head_dim) or t.dtype not in self._dtypes:
+            raise ValueError(f"expected a 16-bit tensor [{tokens}][{heads}][{self.head_dim}] of the plan's dtype with "
+                             f"contiguous rows, got {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
         return _HEADS(t.data_ptr(), token_stride, head_stride)
+
+    def _cache(self, t) -> int | None:
+        if t is None or isinstance(t, int):
+            return t
+        if t.nbytes < self._cache_bytes or not t.is_contiguous():
+            raise ValueError(f"the cache must be contiguous and of {self._cache_bytes} bytes or more")
+        return t.data_ptr()
+
+    def _batch(self, batch: KVBatch):
+        if batch.columns * self.page_tokens < batch.max_kv and batch.num_tokens:  # (the library sees only the rows' stride)
+            raise BsgError(2, f"{batch.columns} pages of {self.page_tokens} positions must cover max_kv = {batch.max_kv}")
+        return batch._ref
 
     def append(self, batch: KVBatch, k, v, cache, q=None, q_out=None, rope=None, stream=None) -> None:
         """Store the batch's keys (rotated) and values; with q, write rotated queries to q_out (q: in place).
@@ -409,23 +432,23 @@ class KVPlan:
                                  or not rope.is_contiguous()):
             raise ValueError(f"rope must be a contiguous float32 tensor [rows][2][{self.rope_dim // 2}]")
         _check(self._lib.bsg_kv_append(
-            self._h, batch._ref, None if q is None else self._heads(q, n, self.q_heads),
+            self._h, self._batch(batch), None if q is None else self._heads(q, n, self.q_heads),
             self._heads(k, n, self.kv_heads), self._heads(v, n, self.kv_heads),
             None if q_out is None else self._heads(q_out, n, self.q_heads), _ptr(rope),
-            0 if rope is None else rope.shape[0], _ptr(cache), _stream(stream)))
+            0 if rope is None else rope.shape[0], self._cache(cache), _stream(stream)))
 
     def attend(self, batch: KVBatch, q, cache, out, lse=None, stream=None) -> None:
         """out = attention of the batch's queries over the cache; lse: float32 [tokens][q_heads] or None."""
         n = batch.num_tokens
         if lse is not None and (lse.shape != (n, self.q_heads) or lse.element_size() != 4 or not lse.is_contiguous()):
             raise ValueError(f"lse must be a contiguous float32 tensor [{n}][{self.q_heads}]")
-        _check(self._lib.bsg_kv_attend(self._h, batch._ref, self._heads(q, n, self.q_heads), _ptr(cache),
+        _check(self._lib.bsg_kv_attend(self._h, self._batch(batch), self._heads(q, n, self.q_heads), self._cache(cache),
                                        self._heads(out, n, self.q_heads), _ptr(lse), _stream(stream)))
 
     def read(self, batch: KVBatch, cache, k, v, stream=None) -> None:
         """k, v = the values that the cache holds at the positions of the batch's new tokens."""
         n = batch.num_tokens
-        _check(self._lib.bsg_kv_read(self._h, batch._ref, _ptr(cache), self._heads(k, n, self.kv_heads),
+        _check(self._lib.bsg_kv_read(self._h, self._batch(batch), self._cache(cache), self._heads(k, n, self.kv_heads),
                                      self._heads(v, n, self.kv_heads), _stream(stream)))
 
     def info(self) -> dict:
@@ -472,6 +495,7 @@ class MoEPlan:
         h = _VP()
         _check(lib.bsg_moe_plan_create(ctypes.byref(prob), ctypes.byref(h)))
         self._h = h
+        self._dtypes = _dtypes(dtype)
         per, rows = 2 if fmt == "nvfp4" else 1, experts * inter * hidden
         self._nr = experts * hidden
         self._n13, self._ns13 = 2 * rows // per, 2 * rows // SCALE_BLOCK[fmt]
@@ -483,15 +507,16 @@ class MoEPlan:
         (float32) [tokens][top_k]: the routing, or None."""
         tokens = x.shape[0]
         for t in (x, out):
-            if t.shape != (tokens, self.hidden) or t.element_size() != 2 or t.stride(1) != 1:
-                raise ValueError(f"expected 16-bit rows [{tokens}][{self.hidden}], got {tuple(t.shape)} with strides {t.stride()}")
+            if t.shape != (tokens, self.hidden) or t.dtype not in self._dtypes or t.stride(1) != 1:
+                raise ValueError(f"expected 16-bit rows [{tokens}][{self.hidden}] of the plan's dtype, got {t.dtype} "
+                                 f"{tuple(t.shape)} with strides {t.stride()}")
         choices = tokens * self.top_k
-        if not (router.numel() == self._nr and router.element_size() == 2 and router.is_contiguous()
+        if not (router.numel() == self._nr and router.dtype in self._dtypes and router.is_contiguous()
                 and w13.numel() == self._n13 and w13.element_size() == 1 and w13.is_contiguous()
                 and s13.numel() == self._ns13 and s13.element_size() == 1 and s13.is_contiguous()
                 and w2.numel() == self._n2 and w2.element_size() == 1 and w2.is_contiguous()
                 and s2.numel() == self._ns2 and s2.element_size() == 1 and s2.is_contiguous()):
-            raise ValueError(f"router, w13, s13, w2 and s2 must be contiguous, of {self._nr} 16-bit values and {self._n13}, "
+            raise ValueError(f"router, w13, s13, w2 and s2 must be contiguous, of {self._nr} values of the plan's dtype and {self._n13}, "
                              f"{self._ns13}, {self._n2}, {self._ns2} bytes")
         for t, n in ((alpha13, self.experts), (alpha2, self.experts), (ids, choices), (weights, choices)):
             if t is not None and (t.numel() != n or t.element_size() != 4 or not t.is_contiguous()):
