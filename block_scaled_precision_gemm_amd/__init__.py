@@ -345,6 +345,11 @@ def _dtypes(name: str) -> tuple:
     return ({"bf16": torch.bfloat16, "f16": torch.float16}[name], torch.int16, torch.uint16)
 
 
+def _f32_i32() -> tuple:
+    import torch
+    return torch.float32, torch.int32
+
+
 KV_ROPE_INTERLEAVED, KV_NONCAUSAL = 1, 2
 ROPE_LAYOUTS = ("half", "interleaved")
 
@@ -403,7 +408,7 @@ class KVPlan:
         info = self.info()
         self.page_tokens, self.page_bytes, self.page_stride = page_tokens, info["page_bytes"], info["page_stride"]
         self._cache_bytes = (num_pages - 1) * self.page_stride + self.page_bytes
-        self._dtypes = _dtypes(dtype)
+        self._dtypes, (self._f32, _) = _dtypes(dtype), _f32_i32()
 
     def _heads(self, t, tokens: int, heads: int) -> bytes:
         token_stride, head_stride, one = t.stride() if t.dim() == 3 else (0, 0, 0)
@@ -428,7 +433,7 @@ class KVPlan:
         """Store the batch's keys (rotated) and values; with q, write rotated queries to q_out (q: in place).
         rope: float32 table [rows][2][rope_dim / 2] (rope_table makes one)."""
         n = batch.num_tokens
-        if rope is not None and (rope.shape[1:] != (2, self.rope_dim // 2) or rope.element_size() != 4
+        if rope is not None and (rope.shape[1:] != (2, self.rope_dim // 2) or rope.dtype != self._f32
                                  or not rope.is_contiguous()):
             raise ValueError(f"rope must be a contiguous float32 tensor [rows][2][{self.rope_dim // 2}]")
         _check(self._lib.bsg_kv_append(
@@ -440,7 +445,7 @@ class KVPlan:
     def attend(self, batch: KVBatch, q, cache, out, lse=None, stream=None) -> None:
         """out = attention of the batch's queries over the cache; lse: float32 [tokens][q_heads] or None."""
         n = batch.num_tokens
-        if lse is not None and (lse.shape != (n, self.q_heads) or lse.element_size() != 4 or not lse.is_contiguous()):
+        if lse is not None and (lse.shape != (n, self.q_heads) or lse.dtype != self._f32 or not lse.is_contiguous()):
             raise ValueError(f"lse must be a contiguous float32 tensor [{n}][{self.q_heads}]")
         _check(self._lib.bsg_kv_attend(self._h, self._batch(batch), self._heads(q, n, self.q_heads), self._cache(cache),
                                        self._heads(out, n, self.q_heads), _ptr(lse), _stream(stream)))
@@ -495,7 +500,7 @@ class MoEPlan:
         h = _VP()
         _check(lib.bsg_moe_plan_create(ctypes.byref(prob), ctypes.byref(h)))
         self._h = h
-        self._dtypes = _dtypes(dtype)
+        self._dtypes, (self._f32, self._i32) = _dtypes(dtype), _f32_i32()
         per, rows = 2 if fmt == "nvfp4" else 1, experts * inter * hidden
         self._nr = experts * hidden
         self._n13, self._ns13 = 2 * rows // per, 2 * rows // SCALE_BLOCK[fmt]
@@ -518,9 +523,10 @@ class MoEPlan:
                 and s2.numel() == self._ns2 and s2.element_size() == 1 and s2.is_contiguous()):
             raise ValueError(f"router, w13, s13, w2 and s2 must be contiguous, of {self._nr} values of the plan's dtype and {self._n13}, "
                              f"{self._ns13}, {self._n2}, {self._ns2} bytes")
-        for t, n in ((alpha13, self.experts), (alpha2, self.experts), (ids, choices), (weights, choices)):
-            if t is not None and (t.numel() != n or t.element_size() != 4 or not t.is_contiguous()):
-                raise ValueError("alpha13 and alpha2 have one 32-bit value per expert, ids and weights [tokens][top_k]")
+        f32, i32 = self._f32, self._i32
+        for t, n, d in ((alpha13, self.experts, f32), (alpha2, self.experts, f32), (ids, choices, i32), (weights, choices, f32)):
+            if t is not None and (t.numel() != n or t.dtype != d or not t.is_contiguous()):
+                raise ValueError("alpha13 and alpha2 are float32 [experts], ids int32 and weights float32 [tokens][top_k]")
         w = MoEWeights(ctypes.sizeof(MoEWeights), 0, router.data_ptr(), w13.data_ptr(), s13.data_ptr(), w2.data_ptr(),
                        s2.data_ptr(), _ptr(alpha13), _ptr(alpha2))
         _check(self._lib.bsg_moe_run(self._h, tokens, x.data_ptr(), x.stride(0) if tokens > 1 else self.hidden,

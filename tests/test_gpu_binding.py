@@ -73,3 +73,21 @@ def test_tensors_of_another_type(dtype, other):
         plan.run(x, router, *a, x.clone())
         plan.run(x.view(torch.int16), router, *a, x.clone())
         torch.cuda.synchronize()
+
+
+def test_other_32_bit_numbers():
+    x, k = (torch.zeros(2, h, 64, dtype=torch.bfloat16, device="cuda") for h in (4, 2))
+    batch = bsg.KVBatch(dev(np.array([0, 1, 2], np.int32)), dev(np.array([3, 4], np.int32)), dev(np.zeros((2, 1), np.int32)), 2, 1, 16)
+    ints, floats = torch.int32, torch.float32
+    with bsg.KVPlan(4, 2, 64, 16, 4, 8, rope_dim=64) as plan:
+        cache = torch.zeros(4 * plan.page_bytes, dtype=torch.uint8, device="cuda")
+        for f in (lambda: plan.append(batch, k, k, cache, rope=torch.zeros(16, 2, 32, dtype=ints, device="cuda")),
+                  lambda: plan.attend(batch, x, cache, x.clone(), lse=torch.zeros(2, 4, dtype=ints, device="cuda"))):
+            with pytest.raises(ValueError):
+                f()
+    w = {k: dev(v) for k, v in weights_of("nvfp4", 2, 64, 32, 0).items()}
+    x, router = torch.zeros(2, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(2, 64, dtype=torch.bfloat16, device="cuda")
+    with bsg.MoEPlan("nvfp4", 2, 1, 64, 32, 2) as plan:
+        for name, n, t in (("alpha13", 2, ints), ("alpha2", 2, ints), ("ids", 2, floats), ("weights", 2, ints)):
+            with pytest.raises(ValueError):
+                plan.run(x, router, w["w13"], w["s13"], w["w2"], w["s2"], x.clone(), **{name: torch.zeros(n, dtype=t, device="cuda")})
