@@ -145,7 +145,7 @@ __device__ __forceinline__ uint32_t quantize8(float x[8], float inv, int& code) 
       // beyond 3 * 448 * 6 every element saturates: the clamp keeps infinities out of the correction
       const float y = __builtin_amdgcn_fmed3f(x[2 * i + j], -8192.0f, 8192.0f);
       const float z0 = y * r;
-      z[j] = __builtin_fmaf(__builtin_fmaf(-z0, s, y), r, z0);
+      z[j] = __builtin_copysignf(__builtin_fmaf(__builtin_fmaf(-z0, s, y), r, z0), y);  // (of y = -0 the correction is +0)
     }
     // the byte to replace is an immediate
     if (i == 0) q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, z[0], z[1], 1.0f, 0);

@@ -7,7 +7,7 @@ import torch
 
 import block_scaled_precision_gemm_amd as bsg
 import kv_ref
-from test_gpu_kv import DT, UNIT, attend, check, dev, filled, layout, run_case
+from test_gpu_kv import DT, append_case, attend, check, dev, filled, layout, run_case
 
 pytestmark = pytest.mark.gpu
 
@@ -148,3 +148,28 @@ def test_weights_far_below_the_largest_are_kept():
     assert 2.6e-9 < want.min() and want.max() < 2.8e-9
     assert (np.abs(got - want) <= 2.0 ** -8 * want).all(), (got, want)
     assert np.abs(lse - want_lse).max() < 1e-4
+
+
+@pytest.mark.parametrize("D,new", [(64, [4000, 0, 99, 1]), (128, [1, 2050, 49])])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("rope,interleaved", [(0, False), (64, False), (64, True), (32, True)])
+def test_append_of_many_tokens(D, new, dtype, rope, interleaved):
+    # enough rows for workgroups of four heads each; 18 heads leave two of them in the last
+    append_case(new, [n + 7 * i for i, n in enumerate(new)], 3, 4, D, 64, dtype, rope, interleaved, seed=len(new) + rope)
+
+
+def test_append_keeps_the_sign_of_zeros():
+    # -0 rounds to E2M1's -0 (code 8), beside other elements and in a block of zeros
+    x = torch.zeros(1, 1, 64, dtype=torch.bfloat16, device="cuda")
+    x[0, 0, 1:32:2] = -0.0
+    x[0, 0, 0] = 3.0
+    with bsg.KVPlan(1, 1, 64, 16, 1, 1) as plan:
+        cache = torch.full((plan.page_bytes,), 0x55, dtype=torch.uint8, device="cuda")
+        batch = bsg.KVBatch(dev(np.array([0, 1], np.int32)), dev(np.array([1], np.int32)), dev(np.zeros((1, 1), np.int32)), 1, 1, 1)
+        plan.append(batch, x, x, cache)
+        k, v = torch.ones_like(x), torch.ones_like(x)
+        plan.read(batch, cache, k, v)
+        torch.cuda.synchronize()
+    for part in (cache[:32], cache[16 * 32:16 * 32 + 32]):
+        assert part.tolist() == [0x87] + [0x80] * 15 + [0] * 16
+    assert torch.equal(k.view(torch.int16), x.view(torch.int16)) and torch.equal(v.view(torch.int16), x.view(torch.int16))
