@@ -173,3 +173,64 @@ def test_append_keeps_the_sign_of_zeros():
     for part in (cache[:32], cache[16 * 32:16 * 32 + 32]):
         assert part.tolist() == [0x87] + [0x80] * 15 + [0] * 16
     assert torch.equal(k.view(torch.int16), x.view(torch.int16)) and torch.equal(v.view(torch.int16), x.view(torch.int16))
+
+
+@pytest.mark.parametrize("new,lens", [([9, 1], [130, 300]), ([40, 33], [90, 700])], ids=["4 waves", "8 waves"])
+def test_scales_and_large_scores_of_many_rows(new, lens):
+    run_case(new, lens, seed=31, scale=0.3, k_scale=0.25, v_scale=3.0)
+    run_case(new, lens, D=64, dtype="f16", seed=32, scale=-0.2, k_scale=4.0, v_scale=0.125)
+    run_case(new, lens, seed=33, q_gain=300.0)
+    run_case(new, lens, seed=34, q_gain=1e-30)
+    run_case(new, lens, D=64, seed=35, q_gain=1e30, scale=1e-30)
+
+
+def ramp(n, D, rise):
+    """Keys along one direction whose scores against it (at scale 1 / sqrt(D)) rise by `rise` (base 2) each 64 positions."""
+    d = np.where(np.arange(D) % 3 == 1, -1.0, 1.0)
+    return np.arange(n)[:, None] * d * (rise * np.log(2.0) / 64 / np.sqrt(D)), d
+
+
+@pytest.mark.parametrize("rise", [0.3, 1.0, 2.4, 4.9, 7.0, -3.0])
+@pytest.mark.parametrize("new,D,dtype", [(9, 64, "f16"), (9, 128, "bf16"), (40, 128, "f16"), (40, 64, "bf16")])
+def test_scores_that_rise_slowly(rise, new, D, dtype):
+    # the reference of a row's weights is only replaced when a score lies 5 above it: between, weights reach 2^15.  Rows'
+    # own slopes differ, some fall.  Split positions (kv_ref), and one workgroup per row block (512 heads).
+    n, G = 1200, 4
+    q_start, pages, n_pages = layout([new], [n], 32, 40)
+    c = filled([n], 1, D, 32, pages, n_pages, 41)
+    k, d = ramp(n, D, rise)
+    code, s = kv_ref.quantize(k)
+    for p in range(n):
+        c.store(pages[0][p // 32], p % 32, 0, False, code[p], s[p])
+    rng = np.random.default_rng(42)
+    slopes = rng.uniform(-1, 1, (new, G, 1))
+    slopes[0, 0] = slopes[-1, -1] = 1.0
+    q = torch.from_numpy(slopes * d + 0.05 * rng.standard_normal((new, G, D))).to(DT[dtype])
+    want, wl = kv_ref.attend(q.double().numpy(), c, q_start, [n], pages, 1)
+    print(f"[kv] rise {rise} {new} {D} {dtype}", flush=True)
+    got, lse = attend(c, q.cuda(), q_start, [n], pages, 1, 32, D, dtype)
+    check(got, lse, want, wl, dtype, 5.0, f"rise {rise} {new} {D} {dtype}")
+    H, n = 512, 450
+    q_start, pages, n_pages = layout([n], [n], 32, 43)
+    lens, pg = dev(np.array([n], np.int32)), dev(pages)
+    g = torch.Generator().manual_seed(44)
+    rows = 40 if new == 9 else 150
+    with bsg.KVPlan(H, H, D, 32, n_pages, n, dtype=dtype) as plan:
+        kv = [torch.from_numpy(ramp(n, D, rise)[0])[:, None].expand(n, H, D).to(DT[dtype]).contiguous().cuda(),
+              torch.randn(n, H, D, generator=g).to(DT[dtype]).cuda()]
+        cache = torch.full((n_pages * plan.page_bytes,), 0x7F, dtype=torch.uint8, device="cuda")
+        whole = bsg.KVBatch(dev(q_start), lens, pg, n, n, n)
+        plan.append(whole, *kv, cache)
+        plan.read(whole, cache, *kv)
+        q = (torch.rand(rows, H, 1, generator=g) * 2 - 1) * torch.from_numpy(d) + 0.05 * torch.randn(rows, H, D, generator=g)
+        q = q.to(DT[dtype]).cuda()
+        out, lse = torch.zeros_like(q), torch.zeros(rows, H, device="cuda")
+        plan.attend(bsg.KVBatch(dev(np.array([0, rows], np.int32)), lens, pg, rows, rows, n), q, cache, out, lse=lse)
+        torch.cuda.synchronize()
+    qd, k, v = (x.double().transpose(0, 1).contiguous() for x in (q, *kv))
+    s = torch.matmul(qd, k.transpose(1, 2).contiguous()) * D ** -0.5
+    hidden = torch.arange(n, device="cuda")[None] > torch.arange(n - rows, n, device="cuda")[:, None]
+    s = s.masked_fill(hidden, float("-inf"))
+    want = torch.matmul(s.softmax(-1), v).transpose(0, 1)
+    check(out.double().cpu().numpy(), lse.double().cpu().numpy(), want.cpu().numpy(), s.logsumexp(-1).T.cpu().numpy(), dtype,
+          float(v.abs().max()), f"rise {rise} {rows} rows of {H} heads")

@@ -5,7 +5,7 @@ import torch
 
 import block_scaled_precision_gemm_amd as bsg
 import moe_ref
-from test_gpu_moe import DT, UNIT, dev
+from test_gpu_moe import UNIT, dev, run_case
 
 pytestmark = pytest.mark.gpu
 
@@ -32,3 +32,17 @@ def test_tokens_up_to_the_largest_bf16(T):
     got = out.double().cpu().numpy()
     lim = UNIT["bf16"] * np.abs(want) + 2.0 ** -13 * np.sqrt((want ** 2).mean(1, keepdims=True))
     assert (np.abs(got - want) <= lim).all()
+
+
+@pytest.mark.parametrize("fmt,dtype", [("nvfp4", "bf16"), ("nvfp4", "f16"), ("mxfp8", "bf16"), ("mxfp8", "f16")])
+@pytest.mark.parametrize("H,I", [(4128, 64), (64, 4128), (8224, 32), (96, 8224), (4096, 4224)])
+@pytest.mark.parametrize("T", [1, 17])
+def test_rows_longer_than_a_chunk(fmt, dtype, H, I, T):
+    # scales are staged 4096 at a time, tokens prepared 8192 at a time; the rest of the last chunk is no whole slab
+    run_case(fmt, T, 3, 2, H, I, dtype, seed=H + I)
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp8"])
+def test_a_row_of_65536(fmt):
+    run_case(fmt, 3, 2, 1, 65536, 32, "bf16", seed=5)
+    run_case(fmt, 3, 2, 1, 32, 65536, "bf16", seed=6)
