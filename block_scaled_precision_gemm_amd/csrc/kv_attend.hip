@@ -434,12 +434,12 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
     // element (row r, dims d .. d+3)
     auto store_out = [&](int r, int d, v4f y, float top, float sum) {
       const int i = (rb * R + r) / G, hq = rb * R + r - i * G;
-      const float f = p.v_scale * 256.0f / sum;
-      const bool none = sum == 0.0f;  // an empty row gives zeros
+      const float f = 256.0f / sum, gain = p.v_scale;  // (one after the other: v_scale may be near fp32's ends)
+      const bool none = sum == 0.0f;                   // an empty row gives zeros
       uint16_t* dst = (uint16_t*)p.out.ptr + (int64_t)(first_token + i) * p.out.token_stride +
                       (int64_t)(h * G + hq) * p.out.head_stride + d;
-      const uint32_t a = out_bits<O>(none ? 0.0f : y[0] * f), bq = out_bits<O>(none ? 0.0f : y[1] * f);
-      const uint32_t cc = out_bits<O>(none ? 0.0f : y[2] * f), dd = out_bits<O>(none ? 0.0f : y[3] * f);
+      const uint32_t a = out_bits<O>(none ? 0.0f : y[0] * f * gain), bq = out_bits<O>(none ? 0.0f : y[1] * f * gain);
+      const uint32_t cc = out_bits<O>(none ? 0.0f : y[2] * f * gain), dd = out_bits<O>(none ? 0.0f : y[3] * f * gain);
       *(uint2*)dst = make_uint2(a | bq << 16, cc | dd << 16);
       if (p.lse && d == 0)
         p.lse[(int64_t)(first_token + i) * p.q_heads + h * G + hq] =

@@ -46,10 +46,11 @@ struct Results {
     const int i = (rb * R + row) / p.group, hq = rb * R + row - i * p.group;
     return (uint16_t*)p.out.ptr + (int64_t)(first_token + i) * p.out.token_stride + (int64_t)(h * p.group + hq) * p.out.head_stride + d;
   }
-  __device__ static uint2 pack4(v4f y, float f, bool none) {
+  // Four outputs from sums of weighted values, 256 over the weights' sum, and whether that is zero.
+  __device__ uint2 pack4(v4f y, float f, bool none) const {
     uint32_t bits[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) bits[i] = out_bits<O>(none ? 0.0f : y[i] * f);
+    for (int i = 0; i < 4; ++i) bits[i] = out_bits<O>(none ? 0.0f : y[i] * f * p.v_scale);  // (v_scale may be near fp32's ends)
     return make_uint2(bits[0] | bits[1] << 16, bits[2] | bits[3] << 16);
   }
 };
@@ -431,7 +432,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
     const float sum = sum_over_g(l[t]), top = m[t] == kNegInf ? kNegInf : m[t] * mul[t];
     if (r >= rows) continue;
     if (p.splits == 1) {
-      const float f = p.v_scale * 256.0f / sum;
+      const float f = 256.0f / sum;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         uint16_t* dst = results.out_at(r, E * (4 * g + i));
@@ -492,7 +493,7 @@ __global__ __launch_bounds__(256) void join_kernel(KvArgs p) {
     }
   }
   const Results<O, D, R> results{p, first_token, h, rb};
-  *(uint2*)results.out_at(r, d) = results.pack4(y, p.v_scale * 256.0f / sum, sum == 0.0f);
+  *(uint2*)results.out_at(r, d) = results.pack4(y, 256.0f / sum, sum == 0.0f);
   if (p.lse && d == 0) results.store_lse(r, top, sum);
 }
 

@@ -234,3 +234,10 @@ def test_scores_that_rise_slowly(rise, new, D, dtype):
     want = torch.matmul(s.softmax(-1), v).transpose(0, 1)
     check(out.double().cpu().numpy(), lse.double().cpu().numpy(), want.cpu().numpy(), s.logsumexp(-1).T.cpu().numpy(), dtype,
           float(v.abs().max()), f"rise {rise} {rows} rows of {H} heads")
+
+
+@pytest.mark.parametrize("v_scale", [3e36, 2e-38])
+def test_value_scales_at_the_ends_of_their_range(v_scale):
+    # the results are v_scale times ordinary numbers and fit bf16; the largest stored value is below 6 x 448 of them
+    for new, lens in (([1, 3], [90, 300]), ([40], [200]), ([12], [900])):
+        run_case(new, lens, D=64, seed=50, v_scale=v_scale)
