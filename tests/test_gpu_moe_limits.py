@@ -5,7 +5,7 @@ import torch
 
 import block_scaled_precision_gemm_amd as bsg
 import moe_ref
-from test_gpu_moe import UNIT, dev, run_case
+from test_gpu_moe import UNIT, dev, run_case, weights_of
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +46,34 @@ def test_rows_longer_than_a_chunk(fmt, dtype, H, I, T):
 def test_a_row_of_65536(fmt):
     run_case(fmt, 3, 2, 1, 65536, 32, "bf16", seed=5)
     run_case(fmt, 3, 2, 1, 32, 65536, "bf16", seed=6)
+
+
+@pytest.mark.parametrize("T", [1, 4])
+def test_nan_and_extreme_scale_codes_of_weights(T):
+    # E8M0 0 is 2^-127 and 255 NaN; E4M3 0x7F is NaN, as a weight and as an NVFP4 scale
+    for fmt, top, least in (("mxfp8", 255, 0), ("nvfp4", 0x7F, 1)):
+        E, H, I = 2, 64, 64
+        w = {k: v.copy() for k, v in weights_of(fmt, E, H, I, 60).items()}
+        w["s2"][1, 5, 1] = top             # output dim 5 of expert 1
+        w["s13"][0, 3, 0] = least          # one gate row of expert 0: zero beside the others, or nearly
+        if fmt == "mxfp8":
+            w["w2"][1, 9, 40] = 0x7F
+        x = torch.randn(T, H, generator=torch.Generator().manual_seed(61)).bfloat16()
+        router = torch.zeros(E, H, dtype=torch.bfloat16)
+        for e in range(E):  # each expert alone, by the sign of its logits
+            r = router.clone()
+            ones = x.clone()
+            ones[:, 0] = 1.0
+            r[e, 0] = 8.0
+            want, ids, _ = moe_ref.moe(fmt, ones.double().numpy(), r.double().numpy(), w["w13"], w["s13"], w["w2"], w["s2"], 1)
+            assert (ids == e).all()
+            out = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+            with bsg.MoEPlan(fmt, E, 1, H, I, T) as plan:
+                plan.run(ones.cuda(), r.cuda(), dev(w["w13"]), dev(w["s13"]), dev(w["w2"]), dev(w["s2"]), out)
+                torch.cuda.synchronize()
+            got = out.double().cpu().numpy()
+            bad = np.isnan(want)
+            assert np.array_equal(np.isnan(got), bad), (fmt, e)
+            assert bad[:, 5].all() == (e == 1) and bad.any() == (e == 1)
+            scale = np.sqrt(np.nanmean(want ** 2, 1, keepdims=True))
+            assert (np.abs(got - want)[~bad] <= (UNIT["bf16"] * np.abs(want) + 2.0 ** -13 * scale)[~bad]).all(), (fmt, e)
