@@ -66,7 +66,8 @@ constexpr bool attend_fits(int64_t tokens, int64_t seqs, int max_q, int group, i
   const int waves = rows_waves(max_q, group);
   const RowsGrid grid = rows_grid(32 * waves, tokens, seqs, max_q, group, kv_heads);
   if (grid.groups * grid.width * (64 * waves) >= (int64_t)1 << 32) return false;
-  const int64_t few = tokens < seqs * kFewRows / group ? tokens : seqs * kFewRows / group;  // tokens of short sequences
+  // whatever the starts say, a sequence is given to the few-row kernel with kFewRows rows at most
+  const int64_t few = seqs * kFewRows / group;
   return !mixed_batch(tokens, seqs, max_q, group) || line_fits(few, group, seqs, kv_heads, context);
 }
 

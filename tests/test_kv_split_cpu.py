@@ -107,3 +107,16 @@ def test_windows_that_no_context_reaches_are_none(split):
         assert split.kept_window(window) == 0
     # what kernels form from a window that is kept: position, new tokens and window at their largest
     assert -(1 << 31) < -(1 << 24) - ((1 << 30) - 1) and (1 << 30) - 1 + (1 << 30) < 1 << 31
+
+
+def test_short_sequences_of_mixed_batches_are_counted_whatever_the_starts_say(split):
+    # two blocks of 16 rows for every sequence, also where the batch has fewer tokens than that
+    cost, limit, seen = split.unit_cost(), 1 << 31, set()
+    for seqs in (2, 8, 1 << 10, 1 << 17, 1 << 20, 1 << 23):
+        for group in (1, 4, 16):
+            for kv in (64, 4096, 1 << 20):
+                for heads in (1, 8, 12):
+                    fits = bool(split.attend_fits(33 + seqs, seqs, 33, group, heads, kv))
+                    assert not fits or 2 * seqs * heads * (-(-kv // 64) + cost) + 512 < limit
+                    seen.add(fits)
+    assert seen == {True, False}
