@@ -114,7 +114,7 @@ def test_short_sequences_of_mixed_batches_are_counted_whatever_the_starts_say(sp
     cost, limit, seen = split.unit_cost(), 1 << 31, set()
     for seqs in (2, 8, 1 << 10, 1 << 17, 1 << 20, 1 << 23):
         for group in (1, 4, 16):
-            for kv in (64, 4096, 1 << 20):
+            for kv in (64, 4096, 10240, 1 << 20):
                 for heads in (1, 8, 12):
                     fits = bool(split.attend_fits(33 + seqs, seqs, 33, group, heads, kv))
                     assert not fits or 2 * seqs * heads * (-(-kv // 64) + cost) + 512 < limit
