@@ -558,8 +558,10 @@ def rope_table(rows: int, rope_dim: int, base: float = 10000.0, scaling: tuple |
       ("linear", f)        positions divided by f;
       ("base", f)          base multiplied by f^(R / (R - 2)): the slowest pair slows down by f, the fastest not at all;
       ("parts", f, n)      pairs that turn more than 32 times in the trained n positions stay, pairs that turn less than
-                           once slow down by f, those between go linearly from one to the other; cosines and sines are
-                           multiplied by 1 + 0.1 ln f.
+                           once slow down by f, those between go from one to the other linearly in the pair's index;
+                           cosines and sines are multiplied by 1 + 0.1 ln f.  The ends of that line are where a pair would
+                           turn 32 times and once, not rounded to whole pairs: programs that round them give the pairs in
+                           between slightly other speeds, and tables for models trained so are made elsewhere.
     Angles are formed in 64 bits (in 32, position 100000 would be off by 0.004 rad)."""
     import numpy as np
 

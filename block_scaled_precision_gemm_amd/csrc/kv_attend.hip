@@ -540,8 +540,11 @@ hipError_t launch(const KvArgs& a, int cus, hipStream_t stream) {
 // few-row kernel and the others to the many-row kernel, which would walk a long context for a few rows with
 // one workgroup (a prompt of 512 tokens beside 63 single tokens at 1000 to 16000 positions, 32 heads on 8 of
 // 128 dims: 2073 us by that kernel alone, 208 by both).  The host does not know the sequences' tokens: it
-// looks for uneven batches in which the sequences besides a longest one must be short on average, or of eight
-// and more, where a launch that finds nothing to do (4 us) is small against the rest.
+// looks for uneven batches in which the sequences besides a longest one must be short on average, or of eight and
+// more.  Eight is a compromise: a launch that finds nothing to do costs 2 to 3 us at any number (8 prompts of 100 to 500
+// tokens 84 us by one kernel, 87 by both), and what short sequences gain depends on their contexts, which the host does not
+// know (4 prompts of 300 tokens and 4 single ones, 32 heads on 8 of 128 dims: single ones over 4000 positions 105 and 54
+// us, over 1000 38 and 48 us; with 2 of each 70 and 56, 42 and 51 us).
 hipError_t kv_attend_launch(const KvArgs& args, int dtype, int head_dim, int cus, hipStream_t stream) {
   KvArgs a = args;
   a.mixed = mixed_batch(a.num_tokens, a.num_seqs, a.max_q, a.group);

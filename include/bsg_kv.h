@@ -59,7 +59,7 @@ typedef struct bsg_kv_problem {
   int64_t max_tokens;   /* the most new tokens, and the most sequences, of a call */
   uint32_t flags;       /* BSG_KV_* */
   int32_t rope_dim;     /* rotated dims, 0 or a multiple of 16 up to head_dim */
-  int32_t window;       /* > 0: a query at position p sees positions (p - window, p]; 0 = all */
+  int32_t window;       /* > 0: a query at position p sees positions (p - window, p]; 0 (or 2^30 and more) = all */
   float scale;          /* of the scores; 0 = 1 / sqrt(head_dim) */
   float softcap;        /* > 0: scores become softcap * tanh(score / softcap), within 2^-16 or 2^-19 of that; 0 = none */
   float k_scale, v_scale; /* global scales of stored keys and values; 0 = 1 */
@@ -70,8 +70,9 @@ typedef struct bsg_kv_batch {
   uint32_t struct_size; /* = sizeof(bsg_kv_batch) */
   int32_t num_seqs;     /* 0 .. max_tokens */
   int64_t num_tokens;   /* new tokens of all sequences = q_start[num_seqs], 0 .. max_tokens */
-  int32_t max_q;        /* no sequence has more new tokens than this */
-  int32_t max_kv;       /* no kv_len is larger than this (larger ones are read as this) */
+  int32_t max_q;        /* no sequence has more new tokens than this; in [num_tokens / num_seqs, num_tokens] */
+  int32_t max_kv;       /* no kv_len is larger than this (bsg_kv_attend reads larger ones as this; bsg_kv_append and
+                         * bsg_kv_read take positions from kv_len as it is and leave out those from max_kv on) */
   const int32_t* q_start; /* device [num_seqs + 1], ascending from 0 */
   const int32_t* kv_len;  /* device [num_seqs] */
   const int32_t* pages;   /* device [num_seqs][pages_stride] */
@@ -119,8 +120,11 @@ bsg_status bsg_kv_append(bsg_kv_plan plan, const bsg_kv_batch* batch, const bsg_
 /* out = softmax(scale * k_scale * q . K) V * v_scale over each query's visible positions; a query that
  * sees none gives zeros.  lse (or NULL): float [num_tokens][q_heads], the natural logarithm of the sum
  * of the exponentials of the scores (-inf where none is visible).  Cache slots that no query sees are
- * never used as numbers.  Page numbers outside [0, num_pages) are read as the nearest valid page.
- * Errors: as bsg_kv_append. */
+ * never used as numbers.  Page numbers outside [0, num_pages) are read as the nearest valid page.  Scores,
+ * their statistics and all sums are fp32; the weights are rounded to fp16 for their products with V (2^-11 of
+ * themselves; those below 2^-34 of a row's largest may count as zero), and the output is rounded once.
+ * Errors: as bsg_kv_append, and BSG_ERR_UNSUPPORTED for more work than one call can count: about 2^31 tiles of 64
+ * positions over all sequences, heads and blocks of 16 rows, or 2^32 threads of the many-row kernel. */
 bsg_status bsg_kv_attend(bsg_kv_plan plan, const bsg_kv_batch* batch, const bsg_heads* q, const void* cache,
                          const bsg_heads* out, float* lse, void* stream);
 
