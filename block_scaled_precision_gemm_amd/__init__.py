@@ -1,11 +1,12 @@
 """Python binding of the C ABI of libbsg.so: the block-scaled GEMM (include/bsg.h), the paged NVFP4
-key/value cache with its attention (include/bsg_kv.h) and the mixture-of-experts layer for few tokens
-(include/bsg_moe.h).
+key/value cache with its attention (include/bsg_kv.h), the mixture-of-experts layer for few tokens
+(include/bsg_moe.h), and E4M3 products with a scale for each block of 128 with the gated feed-forward block over them
+(include/bsg_f8.h).
 
 Argument marshalling only: every step runs in the HIP library.  Tensors are passed as
 device pointers (anything with .data_ptr(), or a plain int); streams as hipStream_t handles (an
 object with .cuda_stream, an int, or None for torch's current stream).  PyTorch is used to find the
-current stream, when present, and to know the types of the tensors that KVPlan and MoEPlan are given.
+current stream, when present, and to know the types of the tensors that plans are given.
 
 The library is loaded on first use and a missing build raises LibraryNotBuilt: there is no fallback.
 """
@@ -18,7 +19,8 @@ import struct
 __all__ = ["Plan", "BsgError", "LibraryNotBuilt", "load_library", "bench_loop", "null_loop", "run_noalloc", "NOALLOC_SCRATCH_BYTES", "decode_nvfp4_f16",
            "FORMATS", "OUT_DTYPES", "SCALE_LAYOUTS", "abi_version", "packed_strides", "Problem", "PROBLEM_V1_SIZE", "PROBLEM_V2_SIZE",
            "pack_scales", "scales_ktile_bytes",
-           "KVPlan", "KVBatch", "kv_page_bytes", "rope_table", "MoEPlan"]
+           "KVPlan", "KVBatch", "kv_page_bytes", "rope_table", "MoEPlan",
+           "F8Plan", "F8FFNPlan", "f8_quantize", "f8_scales_shape"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libbsg.so")
@@ -111,6 +113,25 @@ class MoEWeights(ctypes.Structure):  # bsg_moe_weights
                 ("alpha13", ctypes.c_void_p), ("alpha2", ctypes.c_void_p)]
 
 
+class F8Problem(ctypes.Structure):  # bsg_f8_problem
+    _fields_ = [("struct_size", ctypes.c_uint32), ("dtype", ctypes.c_int32), ("flags", ctypes.c_uint32), ("device", ctypes.c_int32),
+                ("n", ctypes.c_int64), ("k", ctypes.c_int64), ("max_tokens", ctypes.c_int64)]
+
+
+class F8Rows(ctypes.Structure):  # bsg_f8_rows
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("stride", ctypes.c_int64), ("scale_stride", ctypes.c_int64)]
+
+
+class F8FFNProblem(ctypes.Structure):  # bsg_f8_ffn_problem
+    _fields_ = [("struct_size", ctypes.c_uint32), ("dtype", ctypes.c_int32), ("flags", ctypes.c_uint32), ("device", ctypes.c_int32),
+                ("hidden", ctypes.c_int64), ("inter", ctypes.c_int64), ("max_tokens", ctypes.c_int64)]
+
+
+class F8FFNWeights(ctypes.Structure):  # bsg_f8_ffn_weights
+    _fields_ = [("struct_size", ctypes.c_uint32), ("reserved", ctypes.c_uint32), ("w13", ctypes.c_void_p), ("s13", ctypes.c_void_p),
+                ("w2", ctypes.c_void_p), ("s2", ctypes.c_void_p)]
+
+
 class PlanInfo(ctypes.Structure):
     _fields_ = [("struct_size", ctypes.c_uint32), ("variant", ctypes.c_char * 64), ("tile_m", ctypes.c_int32),
                 ("tile_n", ctypes.c_int32), ("tile_k", ctypes.c_int32), ("grid_x", ctypes.c_uint32),
@@ -149,6 +170,16 @@ _SIGNATURES = {
     "bsg_moe_plan_create": (ctypes.c_int, [ctypes.POINTER(MoEProblem), ctypes.POINTER(_VP)]),
     "bsg_moe_plan_destroy": (ctypes.c_int, [_VP]),
     "bsg_moe_run": (ctypes.c_int, [_VP, ctypes.c_int64, _VP, ctypes.c_int64, _VP, _VP, ctypes.c_int64, _VP, _VP, _VP]),
+    "bsg_f8_quantize": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, _VP, ctypes.c_int64, _VP, ctypes.c_int64,
+                                       _VP, ctypes.c_int64, _VP]),
+    "bsg_f8_plan_create": (ctypes.c_int, [ctypes.POINTER(F8Problem), ctypes.POINTER(_VP)]),
+    "bsg_f8_plan_destroy": (ctypes.c_int, [_VP]),
+    "bsg_f8_plan_workspace": (ctypes.c_int, [_VP, ctypes.POINTER(ctypes.c_uint64)]),
+    "bsg_f8_run": (ctypes.c_int, [_VP, ctypes.c_int64, _VP, _VP, _VP, _VP, _VP, ctypes.c_int64, _VP]),
+    "bsg_f8_ffn_plan_create": (ctypes.c_int, [ctypes.POINTER(F8FFNProblem), ctypes.POINTER(_VP)]),
+    "bsg_f8_ffn_plan_destroy": (ctypes.c_int, [_VP]),
+    "bsg_f8_ffn_plan_workspace": (ctypes.c_int, [_VP, ctypes.POINTER(ctypes.c_uint64)]),
+    "bsg_f8_ffn_run": (ctypes.c_int, [_VP, ctypes.c_int64, _VP, ctypes.c_int64, _VP, _VP, ctypes.c_int64, _VP]),
     "bsg_bench_null_loop": (ctypes.c_int, [ctypes.c_int, _VP, ctypes.POINTER(ctypes.c_double),
                                            ctypes.POINTER(ctypes.c_double)]),
 }
@@ -536,6 +567,168 @@ class MoEPlan:
     def close(self) -> None:
         if self._h is not None and self._h.value:
             _check(self._lib.bsg_moe_plan_destroy(self._h))
+        self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+
+F8_BIAS = 1
+F8_BLOCK = 128
+
+
+def _f8_blocks(n: int) -> int:
+    return (n + F8_BLOCK - 1) // F8_BLOCK
+
+
+def f8_scales_shape(rows: int, cols: int) -> tuple[int, int]:
+    """Shape of the float32 scales of rows [rows][cols]: [blocks of 128 columns][rows rounded up to a multiple of 4]."""
+    return _f8_blocks(cols), (rows + 3) // 4 * 4
+
+
+def _f8_rows(t, rows: int, cols: int, what: str) -> int:
+    """Bytes from row to row of a tensor of codes."""
+    if t.dim() != 2 or t.shape != (rows, cols) or t.element_size() != 1 or t.stride(1) != 1:
+        raise ValueError(f"{what} must be codes of one byte [{rows}][{cols}] with contiguous rows, got {t.dtype} {tuple(t.shape)} "
+                         f"with strides {t.stride()}")
+    return t.stride(0) if rows > 1 else _f8_round16(cols)
+
+
+def _f8_round16(n: int) -> int:
+    return (n + 15) // 16 * 16
+
+
+def _f8_scales(t, rows: int, cols: int, f32) -> int:
+    """Floats from block to block of a tensor of rows' scales."""
+    if t.dim() != 2 or t.dtype != f32 or t.shape[0] != _f8_blocks(cols) or t.shape[1] < rows or t.stride(1) != 1:
+        raise ValueError(f"scales must be float32 [{_f8_blocks(cols)}][{rows} or more] with contiguous rows, got {t.dtype} "
+                         f"{tuple(t.shape)} with strides {t.stride()}")
+    if t.shape[1] % 4:
+        raise BsgError(4, f"scales have {t.shape[1]} columns, not a multiple of 4 (f8_scales_shape)")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _f8_matrix(t, rows: int, cols: int, dtypes, what: str) -> int:
+    """Elements from row to row of a 16-bit tensor."""
+    if t.dim() != 2 or t.shape != (rows, cols) or t.dtype not in dtypes or t.stride(1) != 1:
+        raise ValueError(f"{what} must be a 16-bit tensor [{rows}][{cols}] of the dtype asked for with contiguous rows, got "
+                         f"{t.dtype} {tuple(t.shape)} with strides {t.stride()}")
+    return t.stride(0) if rows > 1 else cols
+
+
+def _f8_weights(checks, f32) -> None:
+    for name, w, s, nw, ns in checks:
+        if w.element_size() != 1 or w.numel() != nw or not w.is_contiguous() or s.dtype != f32 or s.numel() != ns or not s.is_contiguous():
+            raise ValueError(f"{name} must be {nw} contiguous codes of one byte with {ns} contiguous float32 scales, got "
+                             f"{w.dtype} {tuple(w.shape)} and {s.dtype} {tuple(s.shape)}")
+
+
+def f8_quantize(x, codes, scales, stream=None) -> None:
+    """codes (one byte each: uint8 or float8_e4m3fn) [rows][cols] and scales (float32, f8_scales_shape) = x [rows][cols] of
+    bfloat16 or float16 as E4M3 with the least power of two that fits for each 128 columns (bsg_f8_quantize)."""
+    import torch
+    if x.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"x must be bfloat16 or float16, got {x.dtype}")
+    rows, cols = x.shape
+    _check(load_library().bsg_f8_quantize(
+        OUT_DTYPES["bf16" if x.dtype == torch.bfloat16 else "f16"], rows, cols, x.data_ptr(),
+        _f8_matrix(x, rows, cols, (x.dtype,), "x"), codes.data_ptr(), _f8_rows(codes, rows, cols, "codes"), scales.data_ptr(),
+        _f8_scales(scales, rows, cols, torch.float32), _stream(stream)))
+
+
+class F8Plan:
+    """A plan of products of E4M3 rows of k with a scale for each 128 of them and weights [n][k] with a scale for each
+    128 x 128 of them, outputs of `dtype` (bsg_f8.h)."""
+
+    def __init__(self, n: int, k: int, max_tokens: int, dtype: str = "bf16", bias: bool = False, device: int = -1):
+        self._h = None
+        self._lib = lib = load_library()
+        self.n, self.k, self.bias = n, k, bias
+        prob = F8Problem(ctypes.sizeof(F8Problem), OUT_DTYPES[dtype], F8_BIAS if bias else 0, device, n, k, max_tokens)
+        h = _VP()
+        _check(lib.bsg_f8_plan_create(ctypes.byref(prob), ctypes.byref(h)))
+        self._h = h
+        self._dtypes, (self._f32, _) = _dtypes(dtype), _f32_i32()
+        self._nw, self._ns = n * k, _f8_blocks(n) * _f8_blocks(k)
+
+    def run(self, x, x_scales, w, w_scales, out, bias=None, stream=None) -> None:
+        """out [tokens][n] = x w^T (+ bias).  x, x_scales: as f8_quantize writes them; w: codes [n][k], w_scales: float32
+        [blocks of n][blocks of k]; bias: float32 [n], where the plan has one.  x and out may be strided by rows."""
+        tokens = x.shape[0]
+        _f8_weights((("w", w, w_scales, self._nw, self._ns),), self._f32)
+        if self.bias and (bias is None or bias.dtype != self._f32 or bias.shape != (self.n,) or not bias.is_contiguous()):
+            raise ValueError(f"the plan needs a contiguous float32 bias [{self.n}]")
+        rows = F8Rows(x.data_ptr(), x_scales.data_ptr(), _f8_rows(x, tokens, self.k, "x"),
+                      _f8_scales(x_scales, tokens, self.k, self._f32))
+        _check(self._lib.bsg_f8_run(self._h, tokens, ctypes.byref(rows), w.data_ptr(), w_scales.data_ptr(),
+                                    bias.data_ptr() if self.bias else None, out.data_ptr(),
+                                    _f8_matrix(out, tokens, self.n, self._dtypes, "out"), _stream(stream)))
+
+    def workspace_bytes(self) -> int:
+        n = ctypes.c_uint64()
+        _check(self._lib.bsg_f8_plan_workspace(self._h, ctypes.byref(n)))
+        return n.value
+
+    def close(self) -> None:
+        if self._h is not None and self._h.value:
+            _check(self._lib.bsg_f8_plan_destroy(self._h))
+        self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+
+class F8FFNPlan:
+    """A plan of the gated feed-forward block over such weights: out = quantize(SiLU(x w1^T) * (x w3^T)) w2^T, x quantised
+    on the way in (bsg_f8.h)."""
+
+    def __init__(self, hidden: int, inter: int, max_tokens: int, dtype: str = "bf16", device: int = -1):
+        self._h = None
+        self._lib = lib = load_library()
+        self.hidden, self.inter = hidden, inter
+        prob = F8FFNProblem(ctypes.sizeof(F8FFNProblem), OUT_DTYPES[dtype], 0, device, hidden, inter, max_tokens)
+        h = _VP()
+        _check(lib.bsg_f8_ffn_plan_create(ctypes.byref(prob), ctypes.byref(h)))
+        self._h = h
+        self._dtypes, (self._f32, _) = _dtypes(dtype), _f32_i32()
+        self._n13, self._n2, self._ns = 2 * inter * hidden, inter * hidden, _f8_blocks(inter) * _f8_blocks(hidden)
+
+    def run(self, x, w13, s13, w2, s2, out, stream=None) -> None:
+        """x, out: [tokens][hidden] (row-strided views are fine); w13: codes [2 inter][hidden], gate's rows, then up's, s13:
+        float32 [2][blocks of inter][blocks of hidden]; w2: codes [hidden][inter], s2: [blocks of hidden][blocks of inter]."""
+        tokens = x.shape[0]
+        _f8_weights((("w13", w13, s13, self._n13, 2 * self._ns), ("w2", w2, s2, self._n2, self._ns)), self._f32)
+        w = F8FFNWeights(ctypes.sizeof(F8FFNWeights), 0, w13.data_ptr(), s13.data_ptr(), w2.data_ptr(), s2.data_ptr())
+        _check(self._lib.bsg_f8_ffn_run(self._h, tokens, x.data_ptr(), _f8_matrix(x, tokens, self.hidden, self._dtypes, "x"),
+                                        ctypes.byref(w), out.data_ptr(),
+                                        _f8_matrix(out, tokens, self.hidden, self._dtypes, "out"), _stream(stream)))
+
+    def workspace_bytes(self) -> int:
+        n = ctypes.c_uint64()
+        _check(self._lib.bsg_f8_ffn_plan_workspace(self._h, ctypes.byref(n)))
+        return n.value
+
+    def close(self) -> None:
+        if self._h is not None and self._h.value:
+            _check(self._lib.bsg_f8_ffn_plan_destroy(self._h))
         self._h = None
 
     def __del__(self):
