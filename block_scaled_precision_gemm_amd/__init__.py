@@ -166,6 +166,7 @@ _SIGNATURES = {
     "bsg_kv_page_bytes": (ctypes.c_int64, [ctypes.c_int32] * 3),
     "bsg_kv_append": (ctypes.c_int, [_VP] * 7 + [ctypes.c_int64, _VP, _VP]),
     "bsg_kv_attend": (ctypes.c_int, [_VP] * 7),
+    "bsg_kv_attend_shared": (ctypes.c_int, [_VP, _VP, ctypes.c_int64] + [_VP] * 5),
     "bsg_kv_read": (ctypes.c_int, [_VP] * 6),
     "bsg_moe_plan_create": (ctypes.c_int, [ctypes.POINTER(MoEProblem), ctypes.POINTER(_VP)]),
     "bsg_moe_plan_destroy": (ctypes.c_int, [_VP]),
@@ -473,13 +474,15 @@ class KVPlan:
             None if q_out is None else self._heads(q_out, n, self.q_heads), _ptr(rope),
             0 if rope is None else rope.shape[0], self._cache(cache), _stream(stream)))
 
-    def attend(self, batch: KVBatch, q, cache, out, lse=None, stream=None) -> None:
-        """out = attention of the batch's queries over the cache; lse: float32 [tokens][q_heads] or None."""
+    def attend(self, batch: KVBatch, q, cache, out, lse=None, stream=None, shared: int = 0) -> None:
+        """out = attention of the batch's queries over the cache; lse: float32 [tokens][q_heads] or None.  shared: that many
+        first positions (whole pages) lie in the same pages for all sequences, and are read once where that pays."""
         n = batch.num_tokens
         if lse is not None and (lse.shape != (n, self.q_heads) or lse.dtype != self._f32 or not lse.is_contiguous()):
             raise ValueError(f"lse must be a contiguous float32 tensor [{n}][{self.q_heads}]")
-        _check(self._lib.bsg_kv_attend(self._h, self._batch(batch), self._heads(q, n, self.q_heads), self._cache(cache),
-                                       self._heads(out, n, self.q_heads), _ptr(lse), _stream(stream)))
+        _check(self._lib.bsg_kv_attend_shared(self._h, self._batch(batch), shared, self._heads(q, n, self.q_heads),
+                                              self._cache(cache), self._heads(out, n, self.q_heads), _ptr(lse),
+                                              _stream(stream)))
 
     def read(self, batch: KVBatch, cache, k, v, stream=None) -> None:
         """k, v = the values that the cache holds at the positions of the batch's new tokens."""

@@ -41,6 +41,11 @@ struct KvArgs {
   int* arrived;
   int splits;        // position splits of the many-row kernel
   int row_groups, row_width, row_listed;  // its workgroups (kv_split.h)
+  // positions below `shared` lie in the same pages for all sequences; where they are read once for all, by the many-row
+  // kernel, it leaves parts for the few-row kernel, which reads what lies behind them
+  int shared;
+  float* shared_part;
+  int shared_rows, shared_width, shared_splits;  // rows of its blocks, blocks of a head, parts of a block; 0: none
 };
 
 // Byte offsets inside the chunk of one head of a page (P = page tokens, D = head dim).
@@ -66,6 +71,7 @@ __device__ __forceinline__ int clamp_page(const KvArgs& p, int page) { return mi
 // dtype: 0 bf16, 1 f16.  Each returns the launch status; D is 64 or 128.
 hipError_t kv_append_launch(const KvArgs& a, int dtype, int head_dim, bool with_q, hipStream_t stream);
 hipError_t kv_read_launch(const KvArgs& a, int dtype, int head_dim, hipStream_t stream);
+// (a.shared: what the caller says that all sequences share, whether or not that is made use of)
 hipError_t kv_attend_launch(const KvArgs& a, int dtype, int head_dim, int cus, hipStream_t stream);
 
 // Workspace of the attention kernels for calls of up to max_tokens tokens: floats of partials, then

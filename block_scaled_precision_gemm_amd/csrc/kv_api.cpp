@@ -339,12 +339,23 @@ bsg_status bsg_kv_append(bsg_kv_plan plan, const bsg_kv_batch* batch, const bsg_
 
 bsg_status bsg_kv_attend(bsg_kv_plan plan, const bsg_kv_batch* batch, const bsg_heads* q, const void* cache,
                          const bsg_heads* out, float* lse, void* stream) {
+  return bsg_kv_attend_shared(plan, batch, 0, q, cache, out, lse, stream);
+}
+
+bsg_status bsg_kv_attend_shared(bsg_kv_plan plan, const bsg_kv_batch* batch, int64_t shared, const bsg_heads* q,
+                                const void* cache, const bsg_heads* out, float* lse, void* stream) {
   bsg_status st = check_plan(plan);
   if (st != BSG_OK) return st;
   bsg::KvArgs a;
   bool empty = false;
   st = take_batch(plan, batch, &a, &empty);
   if (st != BSG_OK || empty) return st;
+  if (shared < 0 || shared > batch->max_kv || shared % plan->problem.page_tokens) {
+    set_error("shared must be whole pages of %d positions in [0, max_kv = %d] (got %lld)", plan->problem.page_tokens,
+              batch->max_kv, (long long)shared);
+    return BSG_ERR_SHAPE;
+  }
+  a.shared = (int)shared;
   if ((st = take_heads(q, "q", &a.q)) != BSG_OK || (st = take_heads(out, "out", &a.out)) != BSG_OK) return st;
   if ((st = take_cache(cache, &a)) != BSG_OK) return st;
   if ((uintptr_t)lse & 3u) {
@@ -359,8 +370,8 @@ bsg_status bsg_kv_attend(bsg_kv_plan plan, const bsg_kv_batch* batch, const bsg_
     return BSG_ERR_UNSUPPORTED;
   }
   if (plan->log_level >= 2)
-    fprintf(stderr, "bsg: kv attend %d tokens of %d sequences, contexts up to %d, stream=%p\n", a.num_tokens, a.num_seqs,
-            a.max_kv, stream);
+    fprintf(stderr, "bsg: kv attend %d tokens of %d sequences, contexts up to %d, %d shared, stream=%p\n", a.num_tokens,
+            a.num_seqs, a.max_kv, a.shared, stream);
   return launched(bsg::kv_attend_launch(a, plan->dtype, plan->problem.head_dim, plan->cus, (hipStream_t)stream),
                   "bsg_kv_attend");
 }

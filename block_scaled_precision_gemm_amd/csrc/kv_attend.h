@@ -172,6 +172,11 @@ __device__ __forceinline__ void soft_cap(const KvArgs& p, float mul, v4f s[N]) {
 }
 
 hipError_t kv_attend_rows_launch(const KvArgs& a, int dtype, int head_dim, int cus, hipStream_t stream);
+// All rows of the batch over the first a->shared positions; fills in where the parts are.  Whether they fit the workspace.
+bool kv_shared_fits(const KvArgs& a, int cus);
+hipError_t kv_attend_shared_launch(KvArgs* a, int dtype, int head_dim, int cus, hipStream_t stream);
+// 2^kRowsBias P is what the many-row kernels' parts hold, relative to their maxima.
+constexpr float kRowsBias = 10.0f;
 // Floats of parts that kv_attend_rows_launch may use.
 size_t kv_rows_part_floats(const bsg_kv_problem& p, int cus);
 

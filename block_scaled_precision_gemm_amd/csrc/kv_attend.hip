@@ -67,10 +67,43 @@ __device__ __forceinline__ Span span_of(const KvArgs& p, int b) {
   Span s;
   s.len = seq_len(p, b);
   s.q_len = p.one_each ? 1 : min(max(seq_start(p, b + 1) - seq_start(p, b), 0), p.max_q);
-  s.lo = p.window > 0 ? max(0, s.len - s.q_len - p.window + 1) & ~15 : 0;
+  s.lo = p.window > 0 ? max(0, s.len - s.q_len - p.window + 1) & ~15 : p.shared;
   s.tiles = max(1, (s.len - s.lo + kTile - 1) / kTile);
   s.blocks = p.mixed && s.q_len * p.group > kFewRows ? 0 : (s.q_len * p.group + R - 1) / R;
   return s;
+}
+
+// Join a row's parts of the shared positions to its sums (four dims of the output): row `row` of the batch.
+template <int D>
+__device__ __forceinline__ void join_shared(const KvArgs& p, int h, int row, int d, v4f& y, float& top, float& sum) {
+  constexpr int AT_ONCE = 8;
+  const int R = p.shared_rows, block = row / R, r = row - block * R, last = p.shared_splits - 1;
+  const int slot = R * (D + 2);
+  const float* part = p.shared_part + (int64_t)((h + 1) * p.shared_width - 1 - block) * p.shared_splits * slot;
+  for (int s0 = 0; s0 <= last; s0 += AT_ONCE) {
+    v2f ms[AT_ONCE];
+    v4f ys[AT_ONCE];
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i) {  // all in flight; parts past the last repeat it and count nothing
+      const float* at = part + (int64_t)min(s0 + i, last) * slot;
+      ms[i] = *(const v2f*)(at + R * D + 2 * r);
+      ys[i] = *(const v4f*)(at + r * D + d);
+    }
+    float grown = top;
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i) grown = __builtin_fmaxf(grown, ms[i][0] + (kPBias - kRowsBias));
+    const float f0 = top == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(top - grown);
+    sum *= f0;
+    y *= f0;
+    top = grown;
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i) {
+      if (s0 + i > last) continue;
+      const float f = ms[i][0] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(ms[i][0] + (kPBias - kRowsBias) - top);
+      sum += f * ms[i][1];
+      y += f * ys[i];
+    }
+  }
 }
 
 template <Out O, int D, int RT>
@@ -182,7 +215,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
     const int pos0 = s.len - s.q_len;  // position of the sequence's first new token
     // positions seen by some row of the block
     const int i_first = rb * R / G, i_last = (rb * R + rows - 1) / G;
-    const int lo = p.window > 0 ? max(0, pos0 + i_first - p.window + 1) : 0;
+    const int lo = p.window > 0 ? max(0, pos0 + i_first - p.window + 1) : p.shared;
     const int hi = causal ? max(0, pos0 + i_last + 1) : s.len;
     const int s0 = max(s.lo + tile0 * kTile, lo & ~15), s1 = min(s.lo + tile1 * kTile, hi);
 
@@ -433,6 +466,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
     const __amdgpu_buffer_rsrc_t parts = handoff_buffer(p.part, 2u * gridDim.x * SLOT * 4u);
     // element (row r, dims d .. d+3)
     auto store_out = [&](int r, int d, v4f y, float top, float sum) {
+      if (p.shared) join_shared<D>(p, h, first_token * G + rb * R + r, d, y, top, sum);
       const int i = (rb * R + r) / G, hq = rb * R + r - i * G;
       const float f = 256.0f / sum, gain = p.v_scale;  // (one after the other: v_scale may be near fp32's ends)
       const bool none = sum == 0.0f;                   // an empty row gives zeros
@@ -525,7 +559,7 @@ hipError_t launch(const KvArgs& a, int cus, hipStream_t stream) {
   // Of a mixed batch most short sequences have one new token: 16 rows, and two blocks for the others.
   const int64_t rows = (int64_t)(a.mixed ? 1 : a.max_q) * a.group;
   const int R = rows <= 16 ? 16 : 32;
-  const int64_t tiles = (context_positions(a.window, a.max_q, a.max_kv) + kTile - 1) / kTile + 1;
+  const int64_t tiles = (context_positions(a.window, a.max_q, a.max_kv) - a.shared + kTile - 1) / kTile + 1;
   // units: sum over sequences of ceil(tokens * group / R), at most one partial block each
   const int64_t units = ((int64_t)a.num_tokens * a.group / R + a.num_seqs) * a.kv_heads;
   const int64_t want = units * ((tiles + kMinTiles - 1) / kMinTiles), most = (int64_t)cus * kWgPerCu;
@@ -533,6 +567,16 @@ hipError_t launch(const KvArgs& a, int cus, hipStream_t stream) {
   const void* fn = R == 16 ? (const void*)&few_kernel<O, D, 1> : (const void*)&few_kernel<O, D, 2>;
   return hipLaunchKernel(fn, grid, dim3(kThreads), argv, 0, stream);
 }
+
+// Whether positions that all sequences share are read once for all of them, by the many-row kernel, and only what lies
+// behind them by the few-row kernel for each.
+bool shared_pays(const KvArgs& a, int cus) {
+  return a.shared > 0 && a.window == 0 && a.num_seqs > 1 && (int64_t)a.max_q * a.group <= kFewRows &&
+         (int64_t)a.num_tokens * a.group > kFewRows && kv_shared_fits(a, cus);
+}
+
+// Floats of the few-row kernel's parts: two for each workgroup, of up to 32 rows.
+size_t few_part_floats(int head_dim, int cus) { return (size_t)cus * kWgPerCu * 2 * 32 * (head_dim + 4); }
 
 }  // namespace
 
@@ -547,6 +591,13 @@ hipError_t launch(const KvArgs& a, int cus, hipStream_t stream) {
 // us, over 1000 38 and 48 us; with 2 of each 70 and 56, 42 and 51 us).
 hipError_t kv_attend_launch(const KvArgs& args, int dtype, int head_dim, int cus, hipStream_t stream) {
   KvArgs a = args;
+  if (shared_pays(a, cus)) {
+    a.shared_part = a.part + few_part_floats(head_dim, cus);
+    const hipError_t e = kv_attend_shared_launch(&a, dtype, head_dim, cus, stream);
+    if (e != hipSuccess) return e;
+  } else {
+    a.shared = 0;
+  }
   a.mixed = mixed_batch(a.num_tokens, a.num_seqs, a.max_q, a.group);
   if ((int64_t)a.max_q * a.group > kFewRows) {
     const hipError_t e = kv_attend_rows_launch(a, dtype, head_dim, cus, stream);
@@ -558,9 +609,8 @@ hipError_t kv_attend_launch(const KvArgs& args, int dtype, int head_dim, int cus
 
 void kv_workspace(const bsg_kv_problem& p, int cus, size_t* part_floats, size_t* counters, size_t* group_counters) {
   const size_t slots = (size_t)cus * kWgPerCu * 2;
-  const size_t rows = kv_rows_part_floats(p, cus);
-  *part_floats = slots * 32 * (p.head_dim + 4);
-  if (*part_floats < rows) *part_floats = rows;
+  // the few-row kernel's parts, then the many-row kernel's of shared positions (others begin where the former do)
+  *part_floats = few_part_floats(p.head_dim, cus) + kv_rows_part_floats(p, cus);
   *counters = slots + (size_t)p.max_tokens * p.q_heads;
   *group_counters = slots;
 }

@@ -34,7 +34,7 @@ namespace {
 // that is always the maximum (and 2^14, kept down to 2^-38): 2 x 2048 tokens 296 us, heads of 64 229 us, against 278 and 203;
 // root mean square error of fp16 outputs of order 0.1 3.34e-5 against 3.40e-5, and 2.83e-5 with weights in fp32, most of
 // it the output's own rounding; of bf16 ones the same.
-constexpr float kPBias = 10.0f, kSlack = 5.0f;
+constexpr float kPBias = kRowsBias, kSlack = 5.0f;
 
 // Where the results of row block rb of a sequence and head go.
 template <Out O, int D, int R>
@@ -65,9 +65,11 @@ struct RowBlock {
   int rb;  // < 0: none
 };
 
-template <int R>
+template <int R, bool SHARED = false>
 __device__ __forceinline__ RowBlock row_block(const KvArgs& p, int group, int at, int lane) {
   RowBlock s;
+  if constexpr (SHARED)  // all tokens of the batch, as if they were one sequence's; pages are those of the first
+    return {0, group, 0, p.num_tokens, (p.num_tokens * p.group + R - 1) / R - 1 - at};
   if (p.row_listed) {
     int lo = 0;
     for (int n = p.num_seqs; n > 1;) {  // the last sequence that starts at or before the slot: 64 pivots a step
@@ -92,7 +94,33 @@ __device__ __forceinline__ RowBlock row_block(const KvArgs& p, int group, int at
   return s;
 }
 
-template <Out O, int D, int WAVES>
+// The last position that token i of the batch sees: the wave looks for the sequence of its first token `i0` together, and
+// each lane for its own among the 64 from there on.
+__device__ __forceinline__ int last_seen(const KvArgs& p, int i0, int i, int lane, bool causal) {
+  int b = i;
+  if (!p.one_each) {
+    int lo = 0;
+    for (int n = p.num_seqs; n > 1;) {  // the last sequence that starts at or before the token: 64 pivots a step
+      const int step = (n + 63) / 64, at = lane * step;
+      const bool le = at < n && seq_start(p, lo + at) <= i0;
+      const int parts = max(__popcll(__ballot(le)), 1) - 1;
+      lo += parts * step;
+      n = min(step, n - parts * step);
+    }
+    const int start = seq_start(p, min(lo + lane, p.num_seqs));
+    int at = 0;
+#pragma unroll
+    for (int step = 32; step > 0; step /= 2) at += __shfl(start, at + step) <= i ? step : 0;
+    for (b = min(lo + at, p.num_seqs - 1); b + 1 < p.num_seqs && seq_start(p, b + 1) <= i;) ++b;  // (beyond many empty ones)
+  }
+  const int len = seq_len(p, b);
+  if (!causal || p.one_each) return len - 1;
+  const int start = seq_start(p, b);
+  return len - min(max(seq_start(p, b + 1) - start, 0), p.max_q) + i - start;
+}
+
+// SHARED: all rows of the batch over its first p.shared positions, which are the same for all sequences.
+template <Out O, int D, int WAVES, bool SHARED>
 __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
   constexpr int RT = 2, R = 32 * WAVES;
   constexpr int NJ = D / 32, E = D / 16;
@@ -104,6 +132,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
   };
   __shared__ Buffer sh[2];
   __shared__ int sh_nan[4];  // tile n's first position at n % 4, if it has such a NaN block (below)
+  __shared__ int sh_seen[SHARED ? WAVES : 1];
 
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int c = lane & 15, g = lane >> 4;
@@ -124,14 +153,14 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
     rest = blockIdx.x / p.row_groups;
   }
   const int split = rest % p.splits;
-  const RowBlock block = row_block<R>(p, group, rest / p.splits, lane);
+  const RowBlock block = row_block<R, SHARED>(p, group, rest / p.splits, lane);
   if (block.rb < 0) return;
   const int b = block.b, h = block.h, rb = block.rb, first_token = block.first_token, q_len = block.q_len;
-  const int len = seq_len(p, b);
+  const int len = SHARED ? p.shared : seq_len(p, b);
   const int rows = min(R, q_len * G - rb * R), pos0 = len - q_len;
   const int i_first = rb * R / G, i_last = (rb * R + rows - 1) / G;
   const int lo = p.window > 0 ? max(0, pos0 + i_first - p.window + 1) : 0;
-  const int hi = causal ? max(0, pos0 + i_last + 1) : len;
+  const int hi = causal && !SHARED ? max(0, pos0 + i_last + 1) : len;
   const int base = lo & ~15, all = hi > base ? (hi - base + kTile - 1) / kTile : 0;
   const int per = (all + p.splits - 1) / p.splits;
   const int t_begin = base + split * per * kTile, t_end = min(hi, t_begin + per * kTile);
@@ -148,9 +177,20 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
     load_query<D>(p, first_token, h, row, g, raw);
     convert_query<O, D>(p, raw, q[t], mul[t]);
     pos[t] = causal ? pos0 + row / G : len - 1;
+    if constexpr (SHARED) {
+      const int i0 = (rb * R + (w_row < rows ? w_row : 0)) / G;
+      pos[t] = min(last_seen(p, i0, r < rows ? row / G : i0, lane, causal), len - 1);
+    }
   }
   // positions that all, and any, of the wave's rows see up to
-  const int w_first = causal ? pos0 + (rb * R + min(w_row, rows - 1)) / G : len - 1;
+  int w_first = causal ? pos0 + (rb * R + min(w_row, rows - 1)) / G : len - 1;
+  if constexpr (SHARED) {
+    w_first = min(pos[0], pos[1]);
+#pragma unroll
+    for (int d = 1; d < 16; d *= 2) w_first = min(w_first, __shfl_xor(w_first, d));
+    w_first = __builtin_amdgcn_readfirstlane(w_first);
+    if (lane == 0) sh_seen[wave] = w_first;
+  }
   const int w_last = causal ? pos0 + (rb * R + min(w_row + 31, rows - 1)) / G : len - 1;
   v4f o[RT][E];
   float m[RT], l[RT];
@@ -217,7 +257,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
       }
     };
     // some row of the workgroup does not see all of the tile at t0
-    const int all_first = causal ? pos0 + i_first : len - 1, any_last = causal ? pos0 + i_last : len - 1;
+    int all_first = causal ? pos0 + i_first : len - 1;
+    const int any_last = causal ? pos0 + i_last : len - 1;
     auto partly_hidden = [&](int t0) {
       return t0 + kTile - 1 > min(all_first, t_end - 1) || (p.window > 0 && t0 <= any_last - p.window);
     };
@@ -273,6 +314,12 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
     for (int t = 0; t < RT; ++t) pt[t][0] = pt[t][1] = v8h{};
     for (int i = tid; i < 2 * E * 64; i += 64 * WAVES) (&sh[1].v[0][0][0])[i] = v4i{0, 0, 0, 0};
     __syncthreads();
+    if constexpr (SHARED) {
+      all_first = sh_seen[0];
+#pragma unroll
+      for (int w = 1; w < WAVES; ++w) all_first = min(all_first, sh_seen[w]);
+      all_first = __builtin_amdgcn_readfirstlane(all_first);
+    }
     // A tile's products: the last tile's outputs, then this tile's scores, each fragment read from LDS
     // kFly fragments before its two products.  Between them the wave decodes its part of this tile's values into
     // buffer buf and of the next tile's keys into the other, and loads the following ones: its vector operations
@@ -435,7 +482,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
     const int r = w_row + 16 * t + c;
     const float sum = sum_over_g(l[t]), top = m[t] == kNegInf ? kNegInf : m[t] * mul[t];
     if (r >= rows) continue;
-    if (p.splits == 1) {
+    if (!SHARED && p.splits == 1) {
       const float f = 256.0f / sum;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -501,6 +548,22 @@ __global__ __launch_bounds__(256) void join_kernel(KvArgs p) {
   if (p.lse && d == 0) results.store_lse(r, top, sum);
 }
 
+// The number of parts that takes the fewest tiles' time.  A workgroup's beginning and end cost about three
+// tiles, the join two and one more for 8 parts.  At least two tiles per part; the workspace holds twice
+// the workgroups that run at once.  (2 x 134 tokens, 8 heads on 4 of 128 dims, 2133 positions: one part
+// 86 us, so 26 us; one sequence of 1575 tokens, 4 heads on 1, 3756 positions: 141 and 40 us.)
+int64_t cheapest_splits(int64_t units, int64_t places, int64_t tiles, int64_t fill) {
+  int64_t splits = 1, best = 0;
+  for (int64_t s = 1; s == 1 || (s <= tiles / 2 && places * s <= 2 * fill); ++s) {
+    const int64_t cost = (units * s + fill - 1) / fill * ((tiles + s - 1) / s + 3) + (s > 1 ? 2 + s / 8 : 0);
+    if (s == 1 || cost < best) {
+      best = cost;
+      splits = s;
+    }
+  }
+  return splits;
+}
+
 template <Out O, int D, int WAVES>
 hipError_t launch(const KvArgs& a, int cus, hipStream_t stream) {
   constexpr int R = 32 * WAVES;
@@ -517,21 +580,10 @@ hipError_t launch(const KvArgs& a, int cus, hipStream_t stream) {
   const int64_t fill = (int64_t)cus * (8 / WAVES);  // workgroups that run at once
   const int64_t seen = a.window > 0 ? (int64_t)a.window + a.max_q : a.max_kv;
   const int64_t tiles = ((seen < a.max_kv ? seen : a.max_kv) + kTile - 1) / kTile;
-  // The number of parts that takes the fewest tiles' time.  A workgroup's beginning and end cost about three
-  // tiles, the join two and one more for 8 parts.  At least two tiles per part; the workspace holds twice
-  // the workgroups that run at once.  (2 x 134 tokens, 8 heads on 4 of 128 dims, 2133 positions: one part
-  // 86 us, so 26 us; one sequence of 1575 tokens, 4 heads on 1, 3756 positions: 141 and 40 us.)
-  int64_t splits = 1, best = 0;
-  for (int64_t s = 1; s == 1 || (s <= tiles / 2 && places * s <= 2 * fill); ++s) {
-    const int64_t cost = (units * s + fill - 1) / fill * ((tiles + s - 1) / s + 3) + (s > 1 ? 2 + s / 8 : 0);
-    if (s == 1 || cost < best) {
-      best = cost;
-      splits = s;
-    }
-  }
+  const int64_t splits = cheapest_splits(units, places, tiles, fill);
   args.splits = (int)splits;
   void* argv[] = {&args};
-  hipError_t err = hipLaunchKernel((const void*)&rows_kernel<O, D, WAVES>, dim3((unsigned)(places * splits)),
+  hipError_t err = hipLaunchKernel((const void*)&rows_kernel<O, D, WAVES, false>, dim3((unsigned)(places * splits)),
                                    dim3(64 * WAVES), argv, 0, stream);
   if (err != hipSuccess || splits == 1) return err;
   return hipLaunchKernel((const void*)&join_kernel<O, D, R>, dim3((unsigned)(places * (R * (D / 4) / 256))), dim3(256),
@@ -543,7 +595,42 @@ hipError_t launch(const KvArgs& a, int cus, hipStream_t stream) {
   return rows_waves(a.max_q, a.group) == 8 ? launch<O, D, 8>(a, cus, stream) : launch<O, D, 4>(a, cus, stream);
 }
 
+template <Out O, int D, int WAVES>
+hipError_t launch_shared(KvArgs* a, int cus, hipStream_t stream) {
+  constexpr int R = 32 * WAVES;
+  const int64_t width = ((int64_t)a->num_tokens * a->group + R - 1) / R, places = width * a->kv_heads;
+  const int64_t fill = (int64_t)cus * (8 / WAVES), tiles = (a->shared + kTile - 1) / kTile;
+  const int64_t splits = cheapest_splits(places, places, tiles, fill);
+  a->shared_rows = R;
+  a->shared_width = (int)width;
+  a->shared_splits = (int)splits;
+  KvArgs args = *a;
+  args.part = a->shared_part;
+  args.row_groups = a->kv_heads;
+  args.row_width = (int)width;
+  args.row_listed = 0;
+  args.splits = (int)splits;
+  void* argv[] = {&args};
+  return hipLaunchKernel((const void*)&rows_kernel<O, D, WAVES, true>, dim3((unsigned)(places * splits)), dim3(64 * WAVES),
+                         argv, 0, stream);
+}
+
+template <Out O, int D>
+hipError_t launch_shared(KvArgs* a, int cus, hipStream_t stream) {
+  return rows_waves(a->num_tokens, a->group) == 8 ? launch_shared<O, D, 8>(a, cus, stream) : launch_shared<O, D, 4>(a, cus, stream);
+}
+
 }  // namespace
+
+bool kv_shared_fits(const KvArgs& a, int cus) {
+  const int waves = rows_waves(a.num_tokens, a.group);
+  return ((int64_t)a.num_tokens * a.group + 32 * waves - 1) / (32 * waves) * a.kv_heads <= (int64_t)2 * cus * (8 / waves);
+}
+
+hipError_t kv_attend_shared_launch(KvArgs* a, int dtype, int head_dim, int cus, hipStream_t stream) {
+  if (head_dim == 64) return dtype ? launch_shared<Out::F16, 64>(a, cus, stream) : launch_shared<Out::BF16, 64>(a, cus, stream);
+  return dtype ? launch_shared<Out::F16, 128>(a, cus, stream) : launch_shared<Out::BF16, 128>(a, cus, stream);
+}
 
 hipError_t kv_attend_rows_launch(const KvArgs& a, int dtype, int head_dim, int cus, hipStream_t stream) {
   if (head_dim == 64) return dtype ? launch<Out::F16, 64>(a, cus, stream) : launch<Out::BF16, 64>(a, cus, stream);

@@ -128,6 +128,15 @@ bsg_status bsg_kv_append(bsg_kv_plan plan, const bsg_kv_batch* batch, const bsg_
 bsg_status bsg_kv_attend(bsg_kv_plan plan, const bsg_kv_batch* batch, const bsg_heads* q, const void* cache,
                          const bsg_heads* out, float* lse, void* stream);
 
+/* bsg_kv_attend for sequences that begin alike: the first `shared` positions (whole pages, at most max_kv) lie in the same
+ * pages for all of them.  That is the caller's promise: the first shared / page_tokens entries of every sequence's row of
+ * `pages` are the same, also where its context is shorter (only those of the first row are looked at for them).  The result
+ * is bsg_kv_attend's but for the order of sums; the shared positions are read and multiplied once for the whole batch where
+ * that pays: plans without a window, more than one sequence, at most 32 and together more than 32 query rows (new tokens x
+ * query heads per key/value head).  Elsewhere, and with shared 0, the call is bsg_kv_attend.  Errors: as bsg_kv_attend. */
+bsg_status bsg_kv_attend_shared(bsg_kv_plan plan, const bsg_kv_batch* batch, int64_t shared, const bsg_heads* q,
+                                const void* cache, const bsg_heads* out, float* lse, void* stream);
+
 /* The values that the cache holds at the positions of the batch's new tokens: k, v
  * [num_tokens][kv_heads][head_dim] (rounded to the plan's dtype; exact while k_scale and v_scale are
  * powers of two that keep them in its range).  Tokens that bsg_kv_append would not store read as zeros.
