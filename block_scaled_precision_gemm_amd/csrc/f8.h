@@ -44,4 +44,7 @@ hipError_t f8_few_launch(const F8Args& a, Src src, bool gated, int dtype, hipStr
 // Any number of tokens, as codes.  Gated results are codes with scales.  dtype: 0 bf16, 1 f16.
 hipError_t f8_tiled_launch(const F8Args& a, bool gated, int dtype, int cus, hipStream_t stream);
 
+// The same, in tiles of 256 x 256 (gated: 128 outputs).
+hipError_t f8_pp_launch(const F8Args& a, bool gated, int dtype, int cus, hipStream_t stream);
+
 }  // namespace bsg

@@ -230,7 +230,7 @@ hipError_t launch(F8Args a, hipStream_t stream) {
 template <Out O>
 hipError_t plain(const F8Args& a, int cus, hipStream_t stream) {
   const int64_t large = (int64_t)((a.tokens + 255) / 256) * ((a.n + 255) / 256);
-  return large >= cus ? launch<256, 256, 2, 4, 1, false, O>(a, stream) : launch<128, 128, 2, 2, 2, false, O>(a, stream);
+  return large >= cus ? f8_pp_launch(a, false, O == Out::F16, cus, stream) : launch<128, 128, 2, 2, 2, false, O>(a, stream);
 }
 
 }  // namespace
@@ -238,7 +238,7 @@ hipError_t plain(const F8Args& a, int cus, hipStream_t stream) {
 hipError_t f8_tiled_launch(const F8Args& a, bool gated, int dtype, int cus, hipStream_t stream) {
   if (!gated) return dtype ? plain<Out::F16>(a, cus, stream) : plain<Out::BF16>(a, cus, stream);
   const int64_t large = (int64_t)((a.tokens + 255) / 256) * ((a.n + 127) / 128);
-  return large >= cus ? launch<256, 256, 2, 4, 1, true, Out::BF16>(a, stream)
+  return large >= cus ? f8_pp_launch(a, true, dtype, cus, stream)
                       : launch<256, 64, 4, 2, 1, true, Out::BF16>(a, stream);
 }
 
