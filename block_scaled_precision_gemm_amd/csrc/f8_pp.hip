@@ -6,11 +6,11 @@
 // * Each product of a block of 128 is by itself (v_mfma_f32_16x16x128_f8f6f4 with a third operand of zero) and added by
 //   vector operations with the factor sx sw, of which a lane has one for its token of each 16: a product takes the matrix
 //   unit 32 cycles, its four additions take 16 of the vector unit.  A result is added two products after its own, when it
-//   has arrived.
+//   has arrived, a phase's last two in the wave's next memory phase (456 us with a wait for them, 441 without).
 // * The two waves of a SIMD alternate between a memory phase (fragments of the next half of the wave's rows from LDS,
 //   copies) and a compute phase (16 products, 512 cycles).  Group 1 starts one phase late, so one group computes while the
 //   other moves data; one barrier per phase keeps them in step.  The tiled kernel's loop, in which both waves of a SIMD
-//   read and multiply at the same times, took 577 us for 8192^3, this one 456 us (2410 TFLOP/s).
+//   read and multiply at the same times, took 577 us for 8192^3, this one 441 us (2490 TFLOP/s).
 // * Memory to LDS by buffer_load_dwordx4 ... lds, two stages of 128 bytes of K, a quarter of the next one in every memory
 //   phase.  A row is 8 chunks of 16 bytes; chunk q of row R is stored at q ^ ((R >> 1) & 7), so that the 16 lanes of a
 //   fragment's read hit distinct banks.  Rows are ordered as in the tiled kernel, so that a lane's results are neighbours.
@@ -47,11 +47,10 @@ __device__ __forceinline__ void copy4(__amdgpu_buffer_rsrc_t b, uint8_t* dst, in
 
 __device__ __forceinline__ void barrier_only() { asm volatile("s_barrier" ::: "memory"); }
 
-// LDS operations done, at most N loads in flight (N < 0: any number), then the barrier.
+// At most N loads in flight, then the barrier.
 template <int N>
-__device__ __forceinline__ void phase_end() {
-  if constexpr (N < 0) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  else asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+__device__ __forceinline__ void loads_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ int2 tile_of(int bid, int tiles_m, int tiles_n) {
@@ -170,7 +169,7 @@ __global__ __launch_bounds__(THREADS, 2) void pp_kernel(F8Args p) {
     copy_quarter(I0{}, I0{}, 0);
     copy_quarter(I0{}, I1{}, 0);
     copy_scales(I0{}, 0);
-    phase_end<0>();
+    loads_barrier<0>();
     if (grp == 1) barrier_only();
 
     // One memory and one compute phase: rows 64 half .. of the wave's rows, K tile kt.  With phases 4 h .. 4 h + 3 those of
@@ -181,49 +180,60 @@ __global__ __launch_bounds__(THREADS, 2) void pp_kernel(F8Args p) {
     // stage copied into was last read by group 0 at 4 h - 2 and by group 1 at 4 h - 1, before either copies into what the
     // other reads (group 0: tokens 128 .. 255 at 4 h + 2; group 1: tokens 0 .. 127 at 4 h + 1).
     float fct[TT];
+    v4f late[2];  // the last two products of a compute phase, added in the next memory phase
+#pragma unroll
+    for (int j = 0; j < TT; ++j) fct[j] = 0.0f;
+    late[0] = late[1] = v4f{0, 0, 0, 0};
+    auto add = [&](int i, int j, v4f y) __attribute__((always_inline)) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(fct[j], y[e], acc[i][j][e]);
+    };
     auto step = [&](auto sc, auto hc, int kt) __attribute__((always_inline)) {
       constexpr int stage = decltype(sc)::value, half = decltype(hc)::value;
       __builtin_amdgcn_sched_barrier(0);
       read_frags(sc, hc);
       copy_quarter(std::integral_constant<int, stage ^ 1>{}, hc, kt + 1);
       if constexpr (half == 1) copy_scales(std::integral_constant<int, stage ^ 1>{}, kt + 1);
+      add(4 * (half ^ 1) + 3, 2, late[0]);
+      add(4 * (half ^ 1) + 3, 3, late[1]);
+      asm volatile("" ::"v"(acc[4 * (half ^ 1) + 3][2]), "v"(acc[4 * (half ^ 1) + 3][3]));  // (not later)
       __builtin_amdgcn_sched_barrier(0);
-      if constexpr (half == 1) {
-        if (grp == 1) phase_end<CPW + 1>();
-        else phase_end<-1>();
-      } else {
-        phase_end<-1>();
-      }
-      __builtin_amdgcn_sched_barrier(0);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       if (half == 0 || GATED) {
         const float b = __builtin_bit_cast(
             float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sw_lane[GATED ? half : 0]), kt & 63));
 #pragma unroll
         for (int j = 0; j < TT; ++j) fct[j] = xsc[j] * b;
       }
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (half == 1) {
+        if (grp == 1) loads_barrier<CPW + 1>();
+        else barrier_only();
+      } else {
+        barrier_only();
+      }
+      __builtin_amdgcn_sched_barrier(0);
       __builtin_amdgcn_s_setprio(1);
       v4f y[4 * TT];
 #pragma unroll
-      for (int q = 0; q < 4 * TT + 2; ++q) {
-        if (q < 4 * TT) {
-          y[q] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[q / TT], xf[q % TT], v4f{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        }
+      for (int q = 0; q < 4 * TT; ++q) {
+        y[q] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[q / TT], xf[q % TT], v4f{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
         if (q >= 2) {
-          const int u = q - 2;
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            acc[4 * half + u / TT][u % TT][e] = __builtin_fmaf(fct[u % TT], y[u][e], acc[4 * half + u / TT][u % TT][e]);
+          add(4 * half + (q - 2) / TT, (q - 2) % TT, y[q - 2]);
           __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
         }
       }
-      // (this empty asm that reads the sums keeps them in this phase: they could sink past the barriers)
+      late[0] = y[4 * TT - 2];
+      late[1] = y[4 * TT - 1];
+      // (this empty asm that reads the results keeps them in this phase: they could sink past the barriers)
 #define BSG_ROW(i) "v"(acc[4 * half + i][0]), "v"(acc[4 * half + i][1]), "v"(acc[4 * half + i][2]), "v"(acc[4 * half + i][3])
-      asm volatile("" ::BSG_ROW(0), BSG_ROW(1), BSG_ROW(2), BSG_ROW(3));
+      asm volatile("" ::BSG_ROW(0), BSG_ROW(1), BSG_ROW(2), "v"(acc[4 * half + 3][0]), "v"(acc[4 * half + 3][1]), "v"(late[0]),
+                   "v"(late[1]));
 #undef BSG_ROW
       __builtin_amdgcn_s_setprio(0);
       __builtin_amdgcn_sched_barrier(0);
-      if constexpr (half == 1) phase_end<0>();
+      if constexpr (half == 1) loads_barrier<0>();
       else barrier_only();
     };
     int kt = 0;
@@ -245,6 +255,8 @@ __global__ __launch_bounds__(THREADS, 2) void pp_kernel(F8Args p) {
     }
     // Group 0 catches up with group 1's last compute phase; every wave has then drained its copies and reads.
     __builtin_amdgcn_sched_barrier(0);
+    add(NT - 1, 2, late[0]);
+    add(NT - 1, 3, late[1]);
     if (grp == 0) barrier_only();
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 
