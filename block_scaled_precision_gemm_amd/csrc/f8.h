@@ -20,6 +20,10 @@ struct F8Args {
   int64_t out_stride;    // elements
   float* so;             // scales of codes, [ceil(n / 128)][so_stride]
   int64_t so_stride;
+  // workspace, and parts of K (the tiled kernel's)
+  float* part;
+  int* arrived;          // one for each tile, zero between calls
+  int splits;
 };
 
 // How token rows come: codes with scales, or values of 16 or 32 bits.
@@ -37,12 +41,16 @@ __device__ __forceinline__ float f8_scale(uint32_t b) {
 hipError_t f8_quantize_launch(Src src, int64_t rows, int64_t cols, const void* x, int64_t x_stride, void* codes,
                               int64_t codes_stride, float* scales, int64_t scale_stride, hipStream_t stream);
 
-// Up to kF8FewTokens tokens.  Gated results are fp32 values [tokens][out_stride].
-constexpr int kF8FewTokens = 64;
+// dtype: 0 bf16, 1 f16.
+// Up to kF8OneTile tokens.  Gated results are fp32 values [tokens][out_stride].
+constexpr int kF8OneTile = 16;
 hipError_t f8_few_launch(const F8Args& a, Src src, bool gated, int dtype, hipStream_t stream);
 
-// Any number of tokens, as codes.  Gated results are codes with scales.  dtype: 0 bf16, 1 f16.
+// Any number of tokens, as codes; up to kF8FewTokens with products of widened codes.  Gated results are codes with scales.
+constexpr int kF8FewTokens = 64;
 hipError_t f8_tiled_launch(const F8Args& a, bool gated, int dtype, int cus, hipStream_t stream);
+// Its workspace for calls of up to max_tokens: parts, then counters.
+void f8_workspace(int64_t max_tokens, int cus, uint64_t* part_bytes, uint64_t* counter_bytes);
 
 // The same, in tiles of 256 x 256 (gated: 128 outputs).
 hipError_t f8_pp_launch(const F8Args& a, bool gated, int dtype, int cus, hipStream_t stream);

@@ -13,6 +13,10 @@ struct bsg_f8_plan_s {
   uint32_t magic;
   bsg_f8_problem problem;
   int device, cus, dtype, log_level;
+  void* workspace;  // parts of products whose K is split, and their counters, or null
+  uint64_t workspace_bytes;
+  float* part;
+  int* arrived;
 };
 
 struct bsg_f8_ffn_plan_s {
@@ -26,7 +30,9 @@ struct bsg_f8_ffn_plan_s {
   uint8_t* h_codes;   // [max_tokens][inter]
   float* x_scales;    // [B(hidden)][padded tokens]
   float* h_scales;    // [B(inter)][padded tokens]
-  float* h;           // [up to kF8FewTokens][inter]: SiLU(gate) up where it is not made codes at once
+  float* h;           // [up to kF8OneTile][inter]: SiLU(gate) up where it is not made codes at once
+  float* part;        // as in bsg_f8_plan_s
+  int* arrived;
 };
 
 namespace {
@@ -154,8 +160,25 @@ bsg_status bsg_f8_plan_create(const bsg_f8_problem* problem, bsg_f8_plan* out_pl
   plan->cus = cus;
   plan->dtype = problem->dtype == BSG_OUT_F16;
   plan->log_level = log_level();
+  uint64_t part = 0, counters = 0;
+  bsg::f8_workspace(problem->max_tokens, cus, &part, &counters);
+  plan->workspace_bytes = part + counters;
+  if (plan->workspace_bytes) {
+    st = bsg::device_alloc(dev, plan->workspace_bytes, &plan->workspace);
+    if (st == BSG_OK) {
+      plan->part = (float*)plan->workspace;
+      plan->arrived = (int*)((uint8_t*)plan->workspace + part);
+      st = bsg::device_clear(dev, plan->arrived, counters);
+      if (st != BSG_OK) bsg::device_free(dev, plan->workspace);
+    }
+    if (st != BSG_OK) {
+      delete plan;
+      return st;
+    }
+  }
   if (plan->log_level >= 1)
-    fprintf(stderr, "bsg: f8 plan n=%lld k=%lld on device %d\n", (long long)problem->n, (long long)problem->k, dev);
+    fprintf(stderr, "bsg: f8 plan n=%lld k=%lld workspace %llu B on device %d\n", (long long)problem->n, (long long)problem->k,
+            (unsigned long long)plan->workspace_bytes, dev);
   *out_plan = plan;
   return BSG_OK;
 }
@@ -167,6 +190,7 @@ bsg_status bsg_f8_plan_destroy(bsg_f8_plan plan) {
     return BSG_ERR_NULL;
   }
   plan->magic = 0;
+  bsg::device_free(plan->device, plan->workspace);  // hipFree waits for work still using it
   delete plan;
   return BSG_OK;
 }
@@ -176,7 +200,7 @@ bsg_status bsg_f8_plan_workspace(bsg_f8_plan plan, uint64_t* bytes) {
     set_error("invalid plan or null bytes");
     return BSG_ERR_NULL;
   }
-  *bytes = 0;
+  *bytes = plan->workspace_bytes;
   return BSG_OK;
 }
 
@@ -214,10 +238,12 @@ bsg_status bsg_f8_run(bsg_f8_plan plan, int64_t tokens, const bsg_f8_rows* x, co
   a.bias = with_bias ? bias : nullptr;
   a.out = (uint8_t*)out;
   a.out_stride = out_stride;
+  a.part = plan->part;
+  a.arrived = plan->arrived;
   if (plan->log_level >= 2) fprintf(stderr, "bsg: f8 run tokens=%lld stream=%p\n", (long long)tokens, stream);
   const hipStream_t s = (hipStream_t)stream;
-  return launched(tokens <= bsg::kF8FewTokens ? bsg::f8_few_launch(a, bsg::Src::CODES, false, plan->dtype, s)
-                                              : bsg::f8_tiled_launch(a, false, plan->dtype, plan->cus, s),
+  return launched(tokens <= bsg::kF8OneTile ? bsg::f8_few_launch(a, bsg::Src::CODES, false, plan->dtype, s)
+                                            : bsg::f8_tiled_launch(a, false, plan->dtype, plan->cus, s),
                   "bsg_f8_run");
 }
 
@@ -247,8 +273,9 @@ bsg_status bsg_f8_ffn_plan_create(const bsg_f8_ffn_problem* problem, bsg_f8_ffn_
   plan->cus = cus;
   plan->dtype = problem->dtype == BSG_OUT_F16;
   plan->log_level = log_level();
-  const int64_t t = problem->max_tokens, few = t < bsg::kF8FewTokens ? t : bsg::kF8FewTokens;
-  uint64_t at = 0;
+  const int64_t t = problem->max_tokens, few = t < bsg::kF8OneTile ? t : bsg::kF8OneTile;
+  uint64_t at = 0, part_bytes = 0, counter_bytes = 0;
+  bsg::f8_workspace(t, cus, &part_bytes, &counter_bytes);
   auto take = [&](uint64_t bytes) {
     const uint64_t here = at;
     at += (bytes + 255) / 256 * 256;
@@ -257,6 +284,7 @@ bsg_status bsg_f8_ffn_plan_create(const bsg_f8_ffn_problem* problem, bsg_f8_ffn_
   const uint64_t x_codes = take(t * problem->hidden), h_codes = take(t * problem->inter);
   const uint64_t x_scales = take(4 * padded(t) * bsg::f8_blocks(problem->hidden));
   const uint64_t h_scales = take(4 * padded(t) * bsg::f8_blocks(problem->inter)), h = take(4 * few * problem->inter);
+  const uint64_t part = take(part_bytes), arrived = take(counter_bytes);
   plan->workspace_bytes = at;
   if ((st = bsg::device_alloc(dev, at, &plan->workspace)) != BSG_OK) {
     delete plan;
@@ -268,6 +296,13 @@ bsg_status bsg_f8_ffn_plan_create(const bsg_f8_ffn_problem* problem, bsg_f8_ffn_
   plan->x_scales = (float*)(base + x_scales);
   plan->h_scales = (float*)(base + h_scales);
   plan->h = (float*)(base + h);
+  plan->part = (float*)(base + part);
+  plan->arrived = (int*)(base + arrived);
+  if (counter_bytes && (st = bsg::device_clear(dev, plan->arrived, counter_bytes)) != BSG_OK) {
+    bsg::device_free(dev, plan->workspace);
+    delete plan;
+    return st;
+  }
   if (plan->log_level >= 1)
     fprintf(stderr, "bsg: f8 ffn plan hidden=%lld inter=%lld workspace %llu B on device %d\n", (long long)problem->hidden,
             (long long)problem->inter, (unsigned long long)at, dev);
@@ -353,8 +388,10 @@ bsg_status bsg_f8_ffn_run(bsg_f8_ffn_plan plan, int64_t tokens, const void* x, i
   b.sw = w->s2;
   b.out = (uint8_t*)out;
   b.out_stride = out_stride;
+  a.part = b.part = plan->part;
+  a.arrived = b.arrived = plan->arrived;
   hipError_t e = hipSuccess;
-  if (tokens <= 16) {  // both products quantise what they read
+  if (tokens <= bsg::kF8OneTile) {  // both products quantise what they read
     a.x = (const uint8_t*)x;
     a.x_stride = 2 * x_stride;
     a.out = (uint8_t*)plan->h;
@@ -365,18 +402,10 @@ bsg_status bsg_f8_ffn_run(bsg_f8_ffn_plan plan, int64_t tokens, const void* x, i
     return launched(e, "bsg_f8_ffn_run");
   }
   e = bsg::f8_quantize_launch(src, tokens, p.hidden, x, x_stride, plan->x_codes, p.hidden, plan->x_scales, pad, s);
-  if (tokens <= bsg::kF8FewTokens) {
-    a.out = (uint8_t*)plan->h;
-    if (e == hipSuccess) e = bsg::f8_few_launch(a, bsg::Src::CODES, true, plan->dtype, s);
-    if (e == hipSuccess)
-      e = bsg::f8_quantize_launch(bsg::Src::F32, tokens, p.inter, plan->h, p.inter, plan->h_codes, p.inter, plan->h_scales, pad, s);
-    if (e == hipSuccess) e = bsg::f8_few_launch(b, bsg::Src::CODES, false, plan->dtype, s);
-  } else {
-    a.out = plan->h_codes;
-    a.so = plan->h_scales;
-    if (e == hipSuccess) e = bsg::f8_tiled_launch(a, true, plan->dtype, plan->cus, s);
-    if (e == hipSuccess) e = bsg::f8_tiled_launch(b, false, plan->dtype, plan->cus, s);
-  }
+  a.out = plan->h_codes;
+  a.so = plan->h_scales;
+  if (e == hipSuccess) e = bsg::f8_tiled_launch(a, true, plan->dtype, plan->cus, s);
+  if (e == hipSuccess) e = bsg::f8_tiled_launch(b, false, plan->dtype, plan->cus, s);
   return launched(e, "bsg_f8_ffn_run");
 }
 

@@ -73,6 +73,34 @@ struct Values16 {
   }
 };
 
+// 32 codes as fp16.
+__device__ __forceinline__ void f8_widen(v4i a, v4i b, v8h out[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v2h h[4];
+#pragma unroll
+    for (int d = 0; d < 2; ++d) {
+      const int w = j < 2 ? a[2 * j + d] : b[2 * (j - 2) + d];
+      h[2 * d] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false);
+      h[2 * d + 1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true);
+    }
+    out[j] = v8h{h[0][0], h[0][1], h[1][0], h[1][1], h[2][0], h[2][1], h[3][0], h[3][1]};
+  }
+}
+
+// Four values as codes.
+__device__ __forceinline__ int f8_codes4(v4f v, float scale) {
+  v2s w = {0, 0};
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, v[0], v[1], scale, false);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, v[2], v[3], scale, true);
+  return __builtin_bit_cast(int, w);
+}
+
+// SiLU(gate) up, with the hardware's exponential and reciprocal (1 ulp each).
+__device__ __forceinline__ float f8_gated(float gate, float up) {
+  return gate * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-gate * 1.44269504088896341f)) * up;
+}
+
 constexpr int kF8Nan = 0x7F7F7F7F;  // four codes of a block that holds an infinity or a NaN
 __device__ __forceinline__ bool f8_not_finite(uint32_t amax) { return amax >= 0x7F800000u; }
 

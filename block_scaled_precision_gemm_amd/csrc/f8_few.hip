@@ -1,4 +1,4 @@
-// Products in E4M3 with a scale for each block of 128, for up to 64 tokens: the weights stream through.
+// Products in E4M3 with a scale for each block of 128, for up to 16 tokens: the weights stream through.
 //
 // A workgroup takes 16 RT weight rows; its eight waves take every eighth block of 128 along k and are joined through
 // LDS, in the order of the waves.  Weights go from memory to registers in the layout of a matrix product's operand: lane l
@@ -12,7 +12,6 @@
 // would turn one in 400 of the block's inner values to a neighbouring code.
 #include "epilogue.h"
 #include "f8_codec.h"
-#include "kv_attend.h"
 
 namespace bsg {
 namespace {
@@ -23,21 +22,6 @@ constexpr int kRaw = 0x00020000;
 
 __device__ __forceinline__ v4i load16(__amdgpu_buffer_rsrc_t b, int voff, int soff) {
   return __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(b, voff, soff, 0));
-}
-
-// 32 codes as fp16.
-__device__ __forceinline__ void widen(v4i a, v4i b, v8h out[4]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    v2h h[4];
-#pragma unroll
-    for (int d = 0; d < 2; ++d) {
-      const int w = j < 2 ? a[2 * j + d] : b[2 * (j - 2) + d];
-      h[2 * d] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false);
-      h[2 * d + 1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true);
-    }
-    out[j] = v8h{h[0][0], h[0][1], h[1][0], h[1][1], h[2][0], h[2][1], h[3][0], h[3][1]};
-  }
 }
 
 // The largest of a value over the four lanes of a column.
@@ -117,12 +101,12 @@ __global__ __launch_bounds__(kThreads) void few_kernel(F8Args p) {
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
       if constexpr (S == Src::CODES) {
-        widen(q.x[t][0].v[0], q.x[t][1].v[0], x[t]);
+        f8_widen(q.x[t][0].v[0], q.x[t][1].v[0], x[t]);
         sx[t] = q.sx[t];
       } else {
         const uint32_t most = umax_over_g(max(q.x[t][0].amax(), q.x[t][1].amax()));
         sx[t] = f8_scale(most);
-        widen(q.x[t][0].codes(sx[t]), q.x[t][1].codes(sx[t]), x[t]);
+        f8_widen(q.x[t][0].codes(sx[t]), q.x[t][1].codes(sx[t]), x[t]);
         if (f8_not_finite(most)) sx[t] = __builtin_nanf("");
       }
     }
@@ -134,7 +118,7 @@ __global__ __launch_bounds__(kThreads) void few_kernel(F8Args p) {
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
       v8h w[4];
-      widen(q.w[r][0], q.w[r][1], w);
+      f8_widen(q.w[r][0], q.w[r][1], w);
       v4f y[TT];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -177,7 +161,7 @@ __global__ __launch_bounds__(kThreads) void few_kernel(F8Args p) {
       v4f h;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        h[j] = gate[j] * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-gate[j] * kLog2e)) * up[j];
+        h[j] = f8_gated(gate[j], up[j]);
       *(v4f*)((float*)p.out + token * p.out_stride + n) = h;
     } else {
       v4f y = sum_of(r * TT + t, l);
@@ -195,24 +179,11 @@ hipError_t launch(F8Args a, hipStream_t stream) {
                          dim3(kThreads), argv, 0, stream);
 }
 
-template <bool GATED, Out O>
-hipError_t codes(const F8Args& a, hipStream_t stream) {
-  constexpr int R = GATED ? 2 : 1;
-  switch ((a.tokens + 15) / 16) {
-    case 1: return launch<Src::CODES, 1, R, GATED, O, 4>(a, stream);
-    case 2: return launch<Src::CODES, 2, 2, GATED, O, 2>(a, stream);
-    case 3: return launch<Src::CODES, 3, 2, GATED, O, 2>(a, stream);
-    default: return launch<Src::CODES, 4, 2, GATED, O, 2>(a, stream);
-  }
-}
-
 }  // namespace
 
 hipError_t f8_few_launch(const F8Args& a, Src src, bool gated, int dtype, hipStream_t stream) {
-  if (src == Src::CODES) {
-    if (gated) return codes<true, Out::BF16>(a, stream);
-    return dtype ? codes<false, Out::F16>(a, stream) : codes<false, Out::BF16>(a, stream);
-  }
+  if (src == Src::CODES)
+    return dtype ? launch<Src::CODES, 1, 1, false, Out::F16, 4>(a, stream) : launch<Src::CODES, 1, 1, false, Out::BF16, 4>(a, stream);
   if (gated)
     return src == Src::F16 ? launch<Src::F16, 1, 2, true, Out::F16, 2>(a, stream)
                            : launch<Src::BF16, 1, 2, true, Out::BF16, 2>(a, stream);

@@ -24,7 +24,6 @@
 
 #include "epilogue.h"
 #include "f8_codec.h"
-#include "kv_attend.h"
 
 namespace bsg {
 namespace {
@@ -70,7 +69,8 @@ template <bool GATED, Out O>
 __global__ __launch_bounds__(THREADS, 2) void pp_kernel(F8Args p) {
   constexpr int NS = GATED ? 2 : 1, BH = BN / NS;  // BH: outputs of a tile
   __shared__ __attribute__((aligned(1024))) uint8_t lds[SCALES + 2 * SCALE_STAGE];
-  __shared__ uint32_t sh_most[GATED ? BT : 1];
+  // (one variable, reused for the results' largest magnitudes: beside a second one every read of LDS waits for all copies)
+  uint32_t* const sh_most = (uint32_t*)(lds + SCALES);
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int grp = wave >> 2, ws = wave & 3, c = lane & 15, g = lane >> 4;
   const int tiles_t = (p.tokens + BT - 1) / BT, tiles_n = (p.n + BH - 1) / BH, k = p.k, KT = p.kb;
@@ -271,8 +271,7 @@ __global__ __launch_bounds__(THREADS, 2) void pp_kernel(F8Args p) {
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float gate = acc[i][j][e];
-            const float h = gate * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-gate * kLog2e)) * acc[4 + i][j][e];
+            const float h = f8_gated(acc[i][j][e], acc[4 + i][j][e]);  // (a scalar: bits of a vector's element are its first's)
             acc[i][j][e] = h;
             most = max(most, __builtin_bit_cast(uint32_t, h) & 0x7FFFFFFFu);
           }
@@ -288,10 +287,7 @@ __global__ __launch_bounds__(THREADS, 2) void pp_kernel(F8Args p) {
         v4i q;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          v2s w = {0, 0};
-          w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, acc[i][j][0], acc[i][j][1], s, false);
-          w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, acc[i][j][2], acc[i][j][3], s, true);
-          q[i] = f8_not_finite(most) ? kF8Nan : __builtin_bit_cast(int, w);
+          q[i] = f8_not_finite(most) ? kF8Nan : f8_codes4(acc[i][j], s);
         }
         if (t < tokens) {
           if (n < p.n) *(v4i*)(p.out + (int64_t)(t0 + t) * p.out_stride + n) = q;

@@ -1,4 +1,4 @@
-// Rows of 16- or 32-bit values to E4M3 codes with a power-of-two scale for each block of 128 (include/bsg_f8.h).
+// Rows of 16-bit values to E4M3 codes with a power-of-two scale for each block of 128 (include/bsg_f8.h).
 //
 // A lane holds 16 consecutive values, so 8 lanes hold a block.  A workgroup takes 16 rows of 8 blocks, two blocks of all
 // rows at a time: a row's part is at least 512 bytes in a row, and the 16 scales of a block are neighbours in memory.
@@ -51,9 +51,7 @@ __global__ __launch_bounds__(kThreads) void quant_kernel(const uint8_t* x, int64
 
 hipError_t f8_quantize_launch(Src src, int64_t rows, int64_t cols, const void* x, int64_t x_stride, void* codes,
                               int64_t codes_stride, float* scales, int64_t scale_stride, hipStream_t stream) {
-  const void* fn = src == Src::BF16 ? (const void*)&quant_kernel<Src::BF16>
-                   : src == Src::F16 ? (const void*)&quant_kernel<Src::F16>
-                                     : (const void*)&quant_kernel<Src::F32>;
+  const void* fn = src == Src::BF16 ? (const void*)&quant_kernel<Src::BF16> : (const void*)&quant_kernel<Src::F16>;
   const int64_t bytes = x_stride * f8_src_bytes(src);
   int n = (int)cols;
   void* argv[] = {&x, (void*)&bytes, &codes, &codes_stride, &scales, &scale_stride, &rows, &n};

@@ -1,17 +1,24 @@
-// Products in E4M3 with a scale for each block of 128, for many tokens: tiles of BN weight rows and BT tokens.
+// Products in E4M3 with a scale for each block of 128, in tiles of BN weight rows and BT tokens, K split over workgroups
+// where there are few tiles.
 //
-// * K in steps of one block (128 bytes of a row).  Both operands go from memory to LDS with buffer_load_dwordx4 ... lds,
-//   two stages, one barrier per step.  A row is 128 bytes = 8 chunks of 16; chunk q of row R is stored at q ^ ((R >> 1) & 7),
-//   so that the fragments' reads hit distinct banks.
-// * v_mfma_f32_16x16x128_f8f6f4 with weights as rows and tokens as columns, each product of a block by itself (its
-//   third operand is zero), added by vector operations with the factor sx sw, of which a lane has one per 16 tokens: two
-//   instructions of a wave's matrix unit leave room for the eight that add their results.
+// * K in steps of one block (128 bytes of a row).  Both operands go from memory to LDS with buffer_load_dwordx4 ... lds, in
+//   STAGES stages, STAGES - 1 steps ahead, one barrier per step.  A row is 128 bytes = 8 chunks of 16; chunk q of row R is
+//   stored at q ^ ((R >> 1) & 7), so that the fragments' reads hit distinct banks.
+// * Weights are the rows and tokens the columns of the matrix products; each block's product is by itself and is added by
+//   vector operations with the factor sx sw, of which a lane has one per 16 tokens.  A wave's tokens' scales come with the
+//   copies, the weights' are kept 64 blocks at a time, one per lane.
 // * LDS rows are ordered so that a lane's results are neighbours in memory: tokens TT c + j (c = lane % 16, tile j), whose
-//   scales are one load, and 8 consecutive outputs (16 bytes of 16-bit values, 64 bytes of a row per 4 lanes) or, gated,
+//   scales are one read, and 8 consecutive outputs (16 bytes of 16-bit values, 64 bytes of a row per 4 lanes) or, gated,
 //   all of a lane's codes of a token.
+// * WIDE: codes are widened to fp16, which holds every E4M3 value, and multiplied by v_mfma_f32_16x16x32_f16: exact products,
+//   sums in fp32.  Otherwise v_mfma_f32_16x16x128_f8f6f4, which aligns the products of a group to the largest and keeps 14
+//   bits: 1.4e-5 of the result (measured), well below a rounding of bf16 or fp16, at four times the rate.  Few tokens are
+//   bound by the weights' bytes either way.
+// * Split K: the parts (fp32) go to the plan's workspace in the order in which the threads hold them, and the last workgroup
+//   of a tile adds them in the order of the parts, so that the order of every sum is fixed.
 #include "epilogue.h"
 #include "f8_codec.h"
-#include "kv_attend.h"
+#include "handoff.h"
 
 namespace bsg {
 namespace {
@@ -20,94 +27,100 @@ constexpr int kOut = (int)0x80000000u;  // an offset past any buffer: zeros, no 
 constexpr int kRaw = 0x00020000;
 typedef __attribute__((address_space(3))) void lds_void;
 
-// 16 bytes per lane from memory to 1 KiB of LDS at dst (uniform).
+// 16 or 4 bytes per lane from memory to LDS at dst (uniform), lane after lane.
 __device__ __forceinline__ void copy16(__amdgpu_buffer_rsrc_t b, uint8_t* dst, int voff, int soff) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_void*)dst, 16, voff, soff, 0, 0);
 }
-
-template <int BN_, int BT_, int WN_, int WT_, int WG_>
-struct Cfg {
-  static constexpr int BN = BN_, BT = BT_, WN = WN_, WT = WT_;
-  static constexpr int WAVES = WN * WT, THREADS = 64 * WAVES, PER_CU = WG_;
-  static constexpr int NT = BN / WN / 16, TT = BT / WT / 16;  // a wave's tiles of 16 rows and 16 tokens
-  static constexpr int STAGE = (BN + BT) * 128, COPIES = (BN + BT) / 8 / WAVES;
-  static_assert(COPIES * 8 * WAVES == BN + BT && BN % (8 * WAVES) == 0, "copies: whole instructions of one operand");
-  static_assert(NT % 2 == 0 && 128 % (16 * NT) == 0, "a wave's rows share a block of scales");
-};
-
-__device__ __forceinline__ int2 tile_of(int bid, int tiles_m, int tiles_n) {
-  const int T = tiles_m * tiles_n;
-  int id = bid;
-  if ((T & 7) == 0) id = (bid & 7) * (T >> 3) + (bid >> 3);  // contiguous range per XCD
-  constexpr int GM = 8;
-  const int per_group = GM * tiles_n;
-  const int group = id / per_group;
-  const int first_m = group * GM;
-  const int gsize = min(tiles_m - first_m, GM);
-  const int in_group = id - group * per_group;
-  return make_int2(first_m + in_group % gsize, in_group / gsize);
+__device__ __forceinline__ void copy4(__amdgpu_buffer_rsrc_t b, uint8_t* dst, int voff, int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_void*)dst, 4, voff, soff, 0, 0);
 }
 
-template <int BN, int BT, int WN, int WT, int WG, bool GATED, Out O>
-__global__ __launch_bounds__(64 * WN * WT, WN* WT* WG / 4) void tiled_kernel(F8Args p) {
-  using C = Cfg<BN, BT, WN, WT, WG>;
-  constexpr int NT = C::NT, TT = C::TT, NS = GATED ? 2 : 1, BH = C::BN / NS;  // BH: outputs of a tile
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * C::STAGE];
-  __shared__ uint32_t sh_most[GATED ? C::BT : 1];
+// Tile and part of a workgroup.  Workgroups go to the 8 XCDs in turn; each XCD gets a contiguous range of tiles, token
+// tiles first in groups of 8, so that those that share weights share an L2.
+__device__ __forceinline__ int3 tile_of(int bid, int tiles_t, int tiles_n) {
+  const int T = tiles_t * tiles_n, s = bid / T, b = bid - s * T;
+  const int x = b & 7, q = T >> 3, r = T & 7;
+  const int id = x * q + min(x, r) + (b >> 3);
+  constexpr int GM = 8;
+  const int per_group = GM * tiles_n, group = id / per_group, first = group * GM, size = min(tiles_t - first, GM);
+  const int in_group = id - group * per_group;
+  return make_int3(first + in_group % size, in_group / size, s);
+}
+
+template <int BN, int BT, int WN, int WT, int STAGES, int PER_CU, bool GATED, bool WIDE, Out O>
+__global__ __launch_bounds__(64 * WN * WT, WN* WT* PER_CU / 4) void tiled_kernel(F8Args p) {
+  constexpr int WAVES = WN * WT, THREADS = 64 * WAVES;
+  constexpr int NT = BN / WN / 16, TT = BT / WT / 16;  // a wave's tiles of 16 rows and 16 tokens
+  constexpr int STAGE = (BN + BT) * 128, COPIES = (BN + BT) / 8 / WAVES;
+  constexpr int NS = GATED ? 2 : 1, BH = BN / NS;  // BH: outputs of a tile
+  static_assert(COPIES * 8 * WAVES == BN + BT && BN % (8 * WAVES) == 0, "copies: whole instructions of one operand");
+  static_assert(NT % 2 == 0 && 128 % (16 * NT) == 0 && TT <= 4, "a wave's rows share a block of scales");
+  static_assert(STAGES * (STAGE + 256 * WAVES) * PER_CU <= 160 * 1024, "LDS");
+  // stages, tokens' scales of each stage and wave; after the loop reused for a flag and the results' largest magnitudes.
+  // (One variable: beside a second one every read of LDS waits for all copies.)
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[STAGES * (STAGE + 256 * WAVES)];
+  uint8_t* const sc_all = lds + STAGES * STAGE;
+  int* const sh_last = (int*)sc_all;
+  uint32_t* const sh_most = (uint32_t*)sc_all + 64;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int c = lane & 15, g = lane >> 4;
-  const int wn = wave / C::WT, wt = wave % C::WT;
-  const int2 at = tile_of(blockIdx.x, (p.tokens + C::BT - 1) / C::BT, (p.n + BH - 1) / BH);
-  const int t0 = at.x * C::BT, n0 = at.y * BH, k = p.k;
-  const int tokens = min(C::BT, p.tokens - t0), outs = min(BH, p.n - n0);
+  const int wn = wave / WT, wt = wave % WT;
+  const int tiles_t = (p.tokens + BT - 1) / BT, tiles_n = (p.n + BH - 1) / BH;
+  const int3 at = tile_of(blockIdx.x, tiles_t, tiles_n);
+  const int t0 = at.x * BT, n0 = at.y * BH, k = p.k;
+  const int tokens = min(BT, p.tokens - t0), outs = min(BH, p.n - n0);
+  const int b0 = (int)((int64_t)at.z * p.kb / p.splits), b1 = (int)((int64_t)(at.z + 1) * p.kb / p.splits);
 
   // ---- copies: instruction i of the tile fills LDS rows 8 i .. 8 i + 7, eight lanes a row
-  const __amdgpu_buffer_rsrc_t xb =
-      __builtin_amdgcn_make_buffer_rsrc((void*)(p.x + t0 * p.x_stride), (short)0, (tokens - 1) * (int)p.x_stride + k, kRaw);
+  const __amdgpu_buffer_rsrc_t xb = __builtin_amdgcn_make_buffer_rsrc((void*)(p.x + (int64_t)t0 * p.x_stride), (short)0,
+                                                                      (tokens - 1) * (int)p.x_stride + k, kRaw);
   __amdgpu_buffer_rsrc_t wb[NS];
 #pragma unroll
   for (int s = 0; s < NS; ++s)
     wb[s] = __builtin_amdgcn_make_buffer_rsrc((void*)(p.w + ((int64_t)s * p.n + n0) * k), (short)0, outs * k, kRaw);
-  int voff[C::COPIES], kpos[C::COPIES];
+  int voff[COPIES], kpos[COPIES];
 #pragma unroll
-  for (int i = 0; i < C::COPIES; ++i) {
-    const int ins = wave + C::WAVES * i, R = 8 * ins + (lane >> 3);
+  for (int i = 0; i < COPIES; ++i) {
+    const int ins = wave + WAVES * i, R = 8 * ins + (lane >> 3);
     kpos[i] = 16 * ((lane & 7) ^ ((R >> 1) & 7));
-    if (8 * ins < C::BN) {
+    if (8 * ins < BN) {
       const int r = R & 15, i16 = R / 16 % NT, w = R / (16 * NT);  // tile i16 of wave row w
       const int row = GATED ? 8 * NT * w + 2 * NT * (r >> 2) + 4 * (i16 % (NT / 2)) + (r & 3)
                             : 16 * NT * w + 32 * (i16 >> 1) + 8 * (r >> 2) + 4 * (i16 & 1) + (r & 3);
       voff[i] = row * k + kpos[i];
     } else {
-      const int Q = R - C::BN;
+      const int Q = R - BN;
       voff[i] = (Q / (16 * TT) * 16 * TT + TT * (Q & 15) + Q / 16 % TT) * (int)p.x_stride + kpos[i];
     }
   }
+  const int my_t = t0 + 16 * TT * wt;
+  const int my_scales = (int)max((int64_t)0, min((int64_t)16 * TT, p.sx_stride - my_t));
+  // Every step has the same number of copies: those past the last have an offset past the buffers.
   auto copy = [&](int b, int stage) __attribute__((always_inline)) {
-    const int left = k - 128 * b;
+    const bool real = b < b1;
+    const int left = real ? k - 128 * b : 0, col = real ? 128 * b : 0;
 #pragma unroll
-    for (int i = 0; i < C::COPIES; ++i) {
-      const int ins = wave + C::WAVES * i;
+    for (int i = 0; i < COPIES; ++i) {
+      const int ins = wave + WAVES * i;
       // (instructions of one i are all of one operand: BN is a multiple of 8 WAVES)
-      const bool weights = 8 * C::WAVES * i < C::BN;
+      const bool weights = 8 * WAVES * i < BN;
       const bool up = GATED && weights && 8 * ins / 16 % NT >= NT / 2;
-      copy16(weights ? (up ? wb[NS - 1] : wb[0]) : xb, lds + stage * C::STAGE + ins * 1024, kpos[i] < left ? voff[i] : kOut,
-             128 * b);
+      copy16(weights ? (up ? wb[NS - 1] : wb[0]) : xb, lds + stage * STAGE + ins * 1024, kpos[i] < left ? voff[i] : kOut, col);
     }
+    const __amdgpu_buffer_rsrc_t sb = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(p.sx + min(b, p.kb - 1) * p.sx_stride + my_t), (short)0, real ? 4 * my_scales : 0, kRaw);
+    copy4(sb, sc_all + (stage * WAVES + wave) * 256, 4 * lane, 0);
   };
-
-  // ---- scales
   const float* sw[NS];
+  float sw_lane[NS];
 #pragma unroll
-  for (int s = 0; s < NS; ++s) sw[s] = p.sw + ((int64_t)s * f8_blocks(p.n) + min(n0 + BH / C::WN * wn, p.n - 1) / 128) * p.kb;
-  const int first = t0 + 16 * TT * wt + TT * c;
-  const float* sx = p.sx + min((int64_t)first, p.sx_stride - TT);
-  float x_s[TT], w_s[NS];
-  auto scales = [&](int b) __attribute__((always_inline)) {
+  for (int s = 0; s < NS; ++s) sw[s] = p.sw + ((int64_t)s * f8_blocks(p.n) + min(n0 + BH / WN * wn, p.n - 1) / 128) * p.kb;
+  auto load_sw = [&](int b) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < TT; ++j) x_s[j] = sx[b * p.sx_stride + j];
-#pragma unroll
-    for (int s = 0; s < NS; ++s) w_s[s] = sw[s][b];
+    for (int s = 0; s < NS; ++s) {
+      sw_lane[s] = sw[s][min(b + lane, p.kb - 1)];
+      asm volatile("s_waitcnt vmcnt(0)" : "+v"(sw_lane[s])::"memory");  // (so that no wait is left in the loop)
+    }
   };
 
   v4f acc[NT][TT];
@@ -115,46 +128,110 @@ __global__ __launch_bounds__(64 * WN * WT, WN* WT* WG / 4) void tiled_kernel(F8A
   for (int i = 0; i < NT; ++i)
 #pragma unroll
     for (int j = 0; j < TT; ++j) acc[i][j] = v4f{0, 0, 0, 0};
-
-  copy(0, 0);
-  scales(0);
+  load_sw(b0);
+#pragma unroll
+  for (int d = 0; d < STAGES - 1; ++d) copy(b0 + d, d);
   const int f = (c >> 1) & 7, ch0 = 16 * (g ^ f), ch1 = 16 * ((g + 4) ^ f);
-  for (int b = 0; b < p.kb; ++b) {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    float s[NS][TT];
+  for (int b = b0, stage = 0; b < b1; ++b) {
+    // this step's copies have landed, those of the STAGES - 2 following ones may be in flight; everyone has read the stage
+    // that is copied into next
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((STAGES - 2) * (COPIES + 1)) : "memory");
+    copy(b + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1);
+    const uint8_t* tile = lds + stage * STAGE;
+    const float* sc = (const float*)(sc_all + (stage * WAVES + wave) * 256) + TT * c;
+    float fct[NS][TT];
 #pragma unroll
-    for (int a = 0; a < NS; ++a)
+    for (int s = 0; s < NS; ++s) {
+      const float one = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sw_lane[s]), (b - b0) & 63));
 #pragma unroll
-      for (int j = 0; j < TT; ++j) s[a][j] = x_s[j] * w_s[a];
-    if (b + 1 < p.kb) {
-      copy(b + 1, (b + 1) & 1);
-      scales(b + 1);
+      for (int j = 0; j < TT; ++j) fct[s][j] = sc[j] * one;
     }
-    const uint8_t* stage = lds + (b & 1) * C::STAGE;
-    auto frag = [&](int row) {
-      const v4i lo = *(const v4i*)(stage + row * 128 + ch0), hi = *(const v4i*)(stage + row * 128 + ch1);
-      return v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    auto half_frag = [&](int row, int ch) { return *(const v4i*)(tile + row * 128 + ch); };
+    auto x_row = [&](int j) { return BN + 16 * (TT * wt + j) + c; };
+    auto w_row = [&](int i) { return 16 * (NT * wn + i) + c; };
+    auto add = [&](int i, int j, v4f y) __attribute__((always_inline)) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(fct[GATED && i >= NT / 2][j], y[e], acc[i][j][e]);
     };
-    v8i x[TT];
+    if constexpr (WIDE) {
+      v8h x[TT][4];
 #pragma unroll
-    for (int j = 0; j < TT; ++j) x[j] = frag(C::BN + 16 * (TT * wt + j) + c);
+      for (int j = 0; j < TT; ++j) f8_widen(half_frag(x_row(j), ch0), half_frag(x_row(j), ch1), x[j]);
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const v8i w = frag(16 * (NT * wn + i) + c);
+      for (int i = 0; i < NT; ++i) {
+        v8h w[4];
+        f8_widen(half_frag(w_row(i), ch0), half_frag(w_row(i), ch1), w);
+        v4f y[TT];
 #pragma unroll
-      for (int j = 0; j < TT; ++j) {
-        const v4f y = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x[j], v4f{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+        for (int u = 0; u < 4; ++u)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(s[GATED && i >= NT / 2][j], y[e], acc[i][j][e]);
+          for (int j = 0; j < TT; ++j)
+            y[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[u], x[j][u], u ? y[j] : v4f{0, 0, 0, 0}, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < TT; ++j) add(i, j, y[j]);
+      }
+    } else {
+      auto frag = [&](int row) {
+        const v4i lo = half_frag(row, ch0), hi = half_frag(row, ch1);
+        return v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+      };
+      v8i x[TT], w[NT];
+#pragma unroll
+      for (int j = 0; j < TT; ++j) x[j] = frag(x_row(j));
+#pragma unroll
+      for (int i = 0; i < NT; ++i) w[i] = frag(w_row(i));
+      v4f y[NT * TT];
+#pragma unroll
+      for (int q = 0; q < NT * TT + 2; ++q) {
+        if (q < NT * TT) {
+          y[q] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[q / TT], x[q % TT], v4f{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        }
+        if (q >= 2) {
+          add((q - 2) / TT, (q - 2) % TT, y[q - 2]);
+          __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+        }
       }
     }
+    stage = stage == STAGES - 1 ? 0 : stage + 1;
+    if (((b + 1 - b0) & 63) == 0) load_sw(b + 1);
+  }
+
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+
+  // ---- parts
+  if (p.splits > 1) {
+    const int tile = at.y * tiles_t + at.x;
+    const __amdgpu_buffer_rsrc_t parts =
+        handoff_buffer(p.part, (uint32_t)(tiles_t * tiles_n * p.splits) * (BN * BT * 4u));
+    auto at_part = [&](int s, int r) { return (uint32_t)((tile * p.splits + s) * (BN * BT) + (r * THREADS + tid) * 4); };
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < TT; ++j) handoff_store4(parts, at_part(at.z, i * TT + j), acc[i][j]);
+    if (!last_arrival(p.arrived + tile, p.splits, sh_last)) return;
+    v4f sum[NT][TT];
+    for (int s = 0; s < p.splits; ++s) {
+      v4f y[NT][TT];
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < TT; ++j) y[i][j] = handoff_load4(parts, at_part(s, i * TT + j));
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < TT; ++j) sum[i][j] = s ? sum[i][j] + y[i][j] : y[i][j];
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < TT; ++j) acc[i][j] = sum[i][j];
   }
 
   // ---- results
   if constexpr (GATED) {
     constexpr int H = NT / 2;
-    for (int i = tid; i < C::BT; i += C::THREADS) sh_most[i] = 0;
+    for (int i = tid; i < BT; i += THREADS) sh_most[i] = 0;
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < TT; ++j) {
@@ -163,8 +240,7 @@ __global__ __launch_bounds__(64 * WN * WT, WN* WT* WG / 4) void tiled_kernel(F8A
       for (int i = 0; i < H; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float gate = acc[i][j][e];
-          const float h = gate * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-gate * kLog2e)) * acc[H + i][j][e];
+          const float h = f8_gated(acc[i][j][e], acc[H + i][j][e]);  // (a scalar: bits of a vector's element are its first's)
           acc[i][j][e] = h;
           most = max(most, __builtin_bit_cast(uint32_t, h) & 0x7FFFFFFFu);
         }
@@ -179,12 +255,7 @@ __global__ __launch_bounds__(64 * WN * WT, WN* WT* WG / 4) void tiled_kernel(F8A
       const float s = f8_scale(most);
       int q[H];
 #pragma unroll
-      for (int i = 0; i < H; ++i) {
-        v2s w = {0, 0};
-        w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, acc[i][j][0], acc[i][j][1], s, false);
-        w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, acc[i][j][2], acc[i][j][3], s, true);
-        q[i] = f8_not_finite(most) ? kF8Nan : __builtin_bit_cast(int, w);
-      }
+      for (int i = 0; i < H; ++i) q[i] = f8_not_finite(most) ? kF8Nan : f8_codes4(acc[i][j], s);
       if (t < tokens) {
         uint8_t* dst = p.out + (int64_t)(t0 + t) * p.out_stride + n;
         if (n < p.n) {
@@ -218,28 +289,66 @@ __global__ __launch_bounds__(64 * WN * WT, WN* WT* WG / 4) void tiled_kernel(F8A
   }
 }
 
-template <int BN, int BT, int WN, int WT, int WG, bool GATED, Out O>
-hipError_t launch(F8Args a, hipStream_t stream) {
+// A shape of tile for a call: how many workgroups, and how many parts of K.
+struct Cut {
+  int64_t tiles, splits;
+  double cost;
+};
+
+// The number of parts that takes the fewest steps' time.  A workgroup's beginning and end cost about BEGIN steps, parts
+// JOIN and one for every EACH of them.  At least four steps a part; all parts' workgroups run at once.
+template <int BN, int BT, int PER_CU, bool GATED>
+Cut cut_of(const F8Args& a, int cus, double step) {
   constexpr int BH = BN / (GATED ? 2 : 1);
+  Cut best = {(int64_t)((a.tokens + BT - 1) / BT) * ((a.n + BH - 1) / BH), 1, 0};
+  const int64_t fill = (int64_t)cus * PER_CU;
+  for (int64_t s = 1; s == 1 || (s <= a.kb / 4 && best.tiles * s <= fill); ++s) {
+    const double cost = (double)((best.tiles * s + fill - 1) / fill) * ((a.kb + s - 1) / s + 4) * step + (s > 1 ? 3 + 0.5 * s : 0);
+    if (s == 1 || cost < best.cost) {
+      best.cost = cost;
+      best.splits = s;
+    }
+  }
+  return best;
+}
+
+template <int BN, int BT, int WN, int WT, int STAGES, int PER_CU, bool GATED, bool WIDE, Out O>
+hipError_t launch(F8Args a, const Cut& cut, hipStream_t stream) {
+  a.splits = (int)cut.splits;
   void* argv[] = {&a};
-  const int64_t tiles = (int64_t)((a.tokens + BT - 1) / BT) * ((a.n + BH - 1) / BH);
-  return hipLaunchKernel((const void*)&tiled_kernel<BN, BT, WN, WT, WG, GATED, O>, dim3((unsigned)tiles), dim3(64 * WN * WT),
-                         argv, 0, stream);
+  return hipLaunchKernel((const void*)&tiled_kernel<BN, BT, WN, WT, STAGES, PER_CU, GATED, WIDE, O>,
+                         dim3((unsigned)(cut.tiles * cut.splits)), dim3(64 * WN * WT), argv, 0, stream);
 }
 
 template <Out O>
 hipError_t plain(const F8Args& a, int cus, hipStream_t stream) {
+  if (a.tokens <= 32) return launch<128, 32, 4, 1, 3, 2, false, true, O>(a, cut_of<128, 32, 2, false>(a, cus, 1.0), stream);
+  if (a.tokens <= kF8FewTokens)
+    return launch<128, 64, 4, 1, 3, 2, false, true, O>(a, cut_of<128, 64, 2, false>(a, cus, 1.0), stream);
   const int64_t large = (int64_t)((a.tokens + 255) / 256) * ((a.n + 255) / 256);
-  return large >= cus ? f8_pp_launch(a, false, O == Out::F16, cus, stream) : launch<128, 128, 2, 2, 2, false, O>(a, stream);
+  if (large >= cus) return f8_pp_launch(a, false, O == Out::F16, cus, stream);
+  const Cut small = cut_of<128, 64, 2, false>(a, cus, 1.0), middle = cut_of<128, 128, 1, false>(a, cus, 1.0);
+  return small.cost < middle.cost ? launch<128, 64, 4, 1, 3, 2, false, false, O>(a, small, stream)
+                                  : launch<128, 128, 2, 4, 4, 1, false, false, O>(a, middle, stream);
 }
 
 }  // namespace
 
 hipError_t f8_tiled_launch(const F8Args& a, bool gated, int dtype, int cus, hipStream_t stream) {
   if (!gated) return dtype ? plain<Out::F16>(a, cus, stream) : plain<Out::BF16>(a, cus, stream);
+  if (a.tokens <= kF8FewTokens)
+    return launch<256, 64, 4, 2, 3, 1, true, true, Out::BF16>(a, cut_of<256, 64, 1, true>(a, cus, 1.0), stream);
   const int64_t large = (int64_t)((a.tokens + 255) / 256) * ((a.n + 127) / 128);
-  return large >= cus ? f8_pp_launch(a, true, dtype, cus, stream)
-                      : launch<256, 64, 4, 2, 1, true, Out::BF16>(a, stream);
+  if (large >= cus) return f8_pp_launch(a, true, dtype, cus, stream);
+  const Cut small = cut_of<256, 64, 1, true>(a, cus, 1.0), middle = cut_of<256, 128, 1, true>(a, cus, 1.6);
+  return small.cost < middle.cost ? launch<256, 64, 4, 2, 3, 1, true, false, Out::BF16>(a, small, stream)
+                                  : launch<256, 128, 4, 2, 3, 1, true, false, Out::BF16>(a, middle, stream);
+}
+
+void f8_workspace(int64_t max_tokens, int cus, uint64_t* part_bytes, uint64_t* counter_bytes) {
+  // at most two workgroups of 128 x 64, or one of 256 x 128, per CU
+  *part_bytes = max_tokens > kF8OneTile ? (uint64_t)cus * (256 * 128 * 4) : 0;
+  *counter_bytes = max_tokens > kF8OneTile ? (uint64_t)cus * 2 * 4 : 0;
 }
 
 }  // namespace bsg
