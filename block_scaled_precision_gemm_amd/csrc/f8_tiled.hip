@@ -2,7 +2,7 @@
 // where there are few tiles.
 //
 // * K in steps of one block (128 bytes of a row).  Both operands go from memory to LDS with buffer_load_dwordx4 ... lds, in
-//   STAGES stages, STAGES - 1 steps ahead, one barrier per step.  A row is 128 bytes = 8 chunks of 16; chunk q of row R is
+//   STAGES stages, as many steps ahead, and fragments from LDS to registers one step ahead; one barrier per step.  A row is 128 bytes = 8 chunks of 16; chunk q of row R is
 //   stored at q ^ ((R >> 1) & 7), so that the fragments' reads hit distinct banks.
 // * Weights are the rows and tokens the columns of the matrix products; each block's product is by itself and is added by
 //   vector operations with the factor sx sw, of which a lane has one per 16 tokens.  A wave's tokens' scales come with the
@@ -12,10 +12,13 @@
 //   all of a lane's codes of a token.
 // * WIDE: codes are widened to fp16, which holds every E4M3 value, and multiplied by v_mfma_f32_16x16x32_f16: exact products,
 //   sums in fp32.  Otherwise v_mfma_f32_16x16x128_f8f6f4, which aligns the products of a group to the largest and keeps 14
-//   bits: 1.4e-5 of the result (measured), well below a rounding of bf16 or fp16, at four times the rate.  Few tokens are
-//   bound by the weights' bytes either way.
+//   bits: 1.4e-5 of the result (measured), well below a rounding of bf16 or fp16, at four times the rate.  But where the
+//   results become codes, one in 400 then gets a neighbouring code; over few tokens that can be 1% of an output, so the gated
+//   product of up to 64 is WIDE.
 // * Split K: the parts (fp32) go to the plan's workspace in the order in which the threads hold them, and the last workgroup
 //   of a tile adds them in the order of the parts, so that the order of every sum is fixed.
+#include <type_traits>
+
 #include "epilogue.h"
 #include "f8_codec.h"
 #include "handoff.h"
@@ -96,20 +99,24 @@ __global__ __launch_bounds__(64 * WN * WT, WN* WT* PER_CU / 4) void tiled_kernel
   const int my_t = t0 + 16 * TT * wt;
   const int my_scales = (int)max((int64_t)0, min((int64_t)16 * TT, p.sx_stride - my_t));
   // Every step has the same number of copies: those past the last have an offset past the buffers.
-  auto copy = [&](int b, int stage) __attribute__((always_inline)) {
+  auto copy_one = [&](int i, int b, int stage) __attribute__((always_inline)) {
     const bool real = b < b1;
     const int left = real ? k - 128 * b : 0, col = real ? 128 * b : 0;
-#pragma unroll
-    for (int i = 0; i < COPIES; ++i) {
-      const int ins = wave + WAVES * i;
-      // (instructions of one i are all of one operand: BN is a multiple of 8 WAVES)
-      const bool weights = 8 * WAVES * i < BN;
-      const bool up = GATED && weights && 8 * ins / 16 % NT >= NT / 2;
-      copy16(weights ? (up ? wb[NS - 1] : wb[0]) : xb, lds + stage * STAGE + ins * 1024, kpos[i] < left ? voff[i] : kOut, col);
+    if (i == COPIES) {
+      const __amdgpu_buffer_rsrc_t sb = __builtin_amdgcn_make_buffer_rsrc(
+          (void*)(p.sx + min(b, p.kb - 1) * p.sx_stride + my_t), (short)0, real ? 4 * my_scales : 0, kRaw);
+      copy4(sb, sc_all + (stage * WAVES + wave) * 256, 4 * lane, 0);
+      return;
     }
-    const __amdgpu_buffer_rsrc_t sb = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)(p.sx + min(b, p.kb - 1) * p.sx_stride + my_t), (short)0, real ? 4 * my_scales : 0, kRaw);
-    copy4(sb, sc_all + (stage * WAVES + wave) * 256, 4 * lane, 0);
+    const int ins = wave + WAVES * i;
+    // (instructions of one i are all of one operand: BN is a multiple of 8 WAVES)
+    const bool weights = 8 * WAVES * i < BN;
+    const bool up = GATED && weights && 8 * ins / 16 % NT >= NT / 2;
+    copy16(weights ? (up ? wb[NS - 1] : wb[0]) : xb, lds + stage * STAGE + ins * 1024, kpos[i] < left ? voff[i] : kOut, col);
+  };
+  auto copy = [&](int b, int stage) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i <= COPIES; ++i) copy_one(i, b, stage);
   };
   const float* sw[NS];
   float sw_lane[NS];
@@ -128,27 +135,38 @@ __global__ __launch_bounds__(64 * WN * WT, WN* WT* PER_CU / 4) void tiled_kernel
   for (int i = 0; i < NT; ++i)
 #pragma unroll
     for (int j = 0; j < TT; ++j) acc[i][j] = v4f{0, 0, 0, 0};
-  load_sw(b0);
-#pragma unroll
-  for (int d = 0; d < STAGES - 1; ++d) copy(b0 + d, d);
   const int f = (c >> 1) & 7, ch0 = 16 * (g ^ f), ch1 = 16 * ((g + 4) ^ f);
-  for (int b = b0, stage = 0; b < b1; ++b) {
-    // this step's copies have landed, those of the STAGES - 2 following ones may be in flight; everyone has read the stage
-    // that is copied into next
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((STAGES - 2) * (COPIES + 1)) : "memory");
-    copy(b + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1);
+  // A step's fragments are read a step ahead, into the other of two sets of registers.
+  struct Frags {
+    v4i x[TT][2], w[NT][2];
+    float sx[TT];
+  } set[2];
+  auto read = [&](Frags& q, int stage) __attribute__((always_inline)) {
     const uint8_t* tile = lds + stage * STAGE;
     const float* sc = (const float*)(sc_all + (stage * WAVES + wave) * 256) + TT * c;
+#pragma unroll
+    for (int j = 0; j < TT; ++j) {
+      const uint8_t* row = tile + (BN + 16 * (TT * wt + j) + c) * 128;
+      q.x[j][0] = *(const v4i*)(row + ch0);
+      q.x[j][1] = *(const v4i*)(row + ch1);
+      q.sx[j] = sc[j];
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const uint8_t* row = tile + (16 * (NT * wn + i) + c) * 128;
+      q.w[i][0] = *(const v4i*)(row + ch0);
+      q.w[i][1] = *(const v4i*)(row + ch1);
+    }
+  };
+  // `also(i)`, i = 0 .. COPIES, is called between the products
+  auto multiply = [&](const Frags& q, int b, auto also) __attribute__((always_inline)) {
     float fct[NS][TT];
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
       const float one = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sw_lane[s]), (b - b0) & 63));
 #pragma unroll
-      for (int j = 0; j < TT; ++j) fct[s][j] = sc[j] * one;
+      for (int j = 0; j < TT; ++j) fct[s][j] = q.sx[j] * one;
     }
-    auto half_frag = [&](int row, int ch) { return *(const v4i*)(tile + row * 128 + ch); };
-    auto x_row = [&](int j) { return BN + 16 * (TT * wt + j) + c; };
-    auto w_row = [&](int i) { return 16 * (NT * wn + i) + c; };
     auto add = [&](int i, int j, v4f y) __attribute__((always_inline)) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(fct[GATED && i >= NT / 2][j], y[e], acc[i][j][e]);
@@ -156,11 +174,13 @@ __global__ __launch_bounds__(64 * WN * WT, WN* WT* PER_CU / 4) void tiled_kernel
     if constexpr (WIDE) {
       v8h x[TT][4];
 #pragma unroll
-      for (int j = 0; j < TT; ++j) f8_widen(half_frag(x_row(j), ch0), half_frag(x_row(j), ch1), x[j]);
+      for (int j = 0; j < TT; ++j) f8_widen(q.x[j][0], q.x[j][1], x[j]);
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
+#pragma unroll
+        for (int u = i * (COPIES + 1) / NT; u < (i + 1) * (COPIES + 1) / NT; ++u) also(u);
         v8h w[4];
-        f8_widen(half_frag(w_row(i), ch0), half_frag(w_row(i), ch1), w);
+        f8_widen(q.w[i][0], q.w[i][1], w);
         v4f y[TT];
 #pragma unroll
         for (int u = 0; u < 4; ++u)
@@ -171,32 +191,60 @@ __global__ __launch_bounds__(64 * WN * WT, WN* WT* PER_CU / 4) void tiled_kernel
         for (int j = 0; j < TT; ++j) add(i, j, y[j]);
       }
     } else {
-      auto frag = [&](int row) {
-        const v4i lo = half_frag(row, ch0), hi = half_frag(row, ch1);
-        return v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-      };
-      v8i x[TT], w[NT];
-#pragma unroll
-      for (int j = 0; j < TT; ++j) x[j] = frag(x_row(j));
-#pragma unroll
-      for (int i = 0; i < NT; ++i) w[i] = frag(w_row(i));
+      auto join = [](const v4i v[2]) { return v8i{v[0][0], v[0][1], v[0][2], v[0][3], v[1][0], v[1][1], v[1][2], v[1][3]}; };
       v4f y[NT * TT];
 #pragma unroll
-      for (int q = 0; q < NT * TT + 2; ++q) {
-        if (q < NT * TT) {
-          y[q] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[q / TT], x[q % TT], v4f{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+      for (int q2 = 0; q2 < NT * TT + 2; ++q2) {
+        if (q2 < NT * TT) {
+          y[q2] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(q.w[q2 / TT]), join(q.x[q2 % TT]), v4f{0, 0, 0, 0}, 0, 0, 0,
+                                                                  0, 0, 0);
           __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+#pragma unroll
+          for (int u = q2 * (COPIES + 1) / (NT * TT); u < (q2 + 1) * (COPIES + 1) / (NT * TT); ++u) {
+            also(u);
+            __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+          }
         }
-        if (q >= 2) {
-          add((q - 2) / TT, (q - 2) % TT, y[q - 2]);
+        if (q2 >= 2) {
+          add((q2 - 2) / TT, (q2 - 2) % TT, y[q2 - 2]);
           __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
         }
       }
+      // (this empty asm that reads the sums keeps their additions here: put off, they need registers for every product)
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < TT; ++j) asm volatile("" ::"v"(acc[i][j]));
     }
+  };
+  // at most N copies in flight (those of later steps), LDS reads done, everyone here
+  auto arrive = [](auto n) __attribute__((always_inline)) {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(decltype(n)::value) : "memory");
+  };
+  constexpr int N = COPIES + 1;
+  load_sw(b0);
+#pragma unroll
+  for (int d = 0; d < STAGES; ++d) copy(b0 + d, d);
+  arrive(std::integral_constant<int, (STAGES - 1) * N>{});
+  read(set[0], 0);
+  int stage = 0;
+  // Step b: the next step's copies have landed and everyone has read this step's stage, which is copied into.
+  auto step = [&](const Frags& now, Frags& next, int b) __attribute__((always_inline)) {
+    __builtin_amdgcn_sched_barrier(0);
+    arrive(std::integral_constant<int, (STAGES - 2) * N>{});
+    const int old = stage;
     stage = stage == STAGES - 1 ? 0 : stage + 1;
+    read(next, stage);
+    __builtin_amdgcn_sched_barrier(0);  // (left alone, the reads come last, and the next step waits for them)
+    multiply(now, b, [&](int i) __attribute__((always_inline)) { copy_one(i, b + STAGES, old); });
     if (((b + 1 - b0) & 63) == 0) load_sw(b + 1);
+  };
+  int b = b0;
+  for (; b + 2 <= b1; b += 2) {
+    step(set[0], set[1], b);
+    step(set[1], set[0], b + 1);
   }
-
+  if (b < b1) multiply(set[0], b, [](int) {});
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 
   // ---- parts
@@ -289,27 +337,48 @@ __global__ __launch_bounds__(64 * WN * WT, WN* WT* PER_CU / 4) void tiled_kernel
   }
 }
 
-// A shape of tile for a call: how many workgroups, and how many parts of K.
+// A kernel's way to do a call, and what it costs, in microseconds.
 struct Cut {
   int64_t tiles, splits;
   double cost;
 };
 
-// The number of parts that takes the fewest steps' time.  A workgroup's beginning and end cost about BEGIN steps, parts
-// JOIN and one for every EACH of them.  At least four steps a part; all parts' workgroups run at once.
+// What a shape of tile takes: to begin and end, a step with one workgroup on a CU and with PER_CU, and joining parts
+// (JOIN + s JOIN_EACH).  Measured with 61 to 2048 tokens, n and k of 512 to 8192.
+struct Times {
+  double begin, step_alone, step_full, join, join_each;
+};
+constexpr Times kT64x32 = {3.4, 0.25, 0.42, 1.4, 0.5}, kT64x64 = {3.5, 0.33, 0.58, 1.6, 0.8}, kT128x64 = {4.1, 0.43, 0.73, 1.0, 1.15},
+                kT128x128 = {4.8, 0.62, 0.62, 1.8, 1.4};
+constexpr Times kG256x32 = {4.5, 0.6, 0.6, 1.2, 0.8}, kG256x64Wide = {5.0, 1.0, 1.0, 1.5, 1.2}, kG256x64 = {5.0, 0.78, 0.78, 1.5, 1.2},
+                kG256x128 = {6.0, 1.05, 1.05, 2.5, 2.5};
+constexpr double kBytesPerUs = 4.8e6;  // of weights that come from memory
+
+// The number of parts of K that takes the least time: at least four blocks a part, and all parts' workgroups run at once.
 template <int BN, int BT, int PER_CU, bool GATED>
-Cut cut_of(const F8Args& a, int cus, double step) {
+Cut cut_of(const F8Args& a, int cus, const Times& t) {
   constexpr int BH = BN / (GATED ? 2 : 1);
   Cut best = {(int64_t)((a.tokens + BT - 1) / BT) * ((a.n + BH - 1) / BH), 1, 0};
-  const int64_t fill = (int64_t)cus * PER_CU;
-  for (int64_t s = 1; s == 1 || (s <= a.kb / 4 && best.tiles * s <= fill); ++s) {
-    const double cost = (double)((best.tiles * s + fill - 1) / fill) * ((a.kb + s - 1) / s + 4) * step + (s > 1 ? 3 + 0.5 * s : 0);
+  const double memory = (GATED ? 2.0 : 1.0) * a.n * a.k / kBytesPerUs;
+  for (int64_t s = 1; s == 1 || (s <= a.kb / 4 && best.tiles * s <= (int64_t)cus * PER_CU); ++s) {
+    const int64_t wgs = best.tiles * s, per_cu = wgs >= (int64_t)cus * PER_CU ? PER_CU : (wgs + cus - 1) / cus;
+    const int64_t rounds = (wgs + (int64_t)cus * PER_CU - 1) / ((int64_t)cus * PER_CU);
+    const double step = PER_CU == 1 ? t.step_full : t.step_alone + (t.step_full - t.step_alone) * (per_cu - 1) / (PER_CU - 1);
+    const double work = (double)(rounds * ((a.kb + s - 1) / s)) * step;
+    const double cost = t.begin + (work > memory ? work : memory) + (s > 1 ? t.join + s * t.join_each : 0);
     if (s == 1 || cost < best.cost) {
       best.cost = cost;
       best.splits = s;
     }
   }
   return best;
+}
+
+// The same of the kernel for many tokens (f8_pp.hip): a step takes longer where all CUs work at once.
+double pp_cost(const F8Args& a, bool gated, int cus) {
+  const int64_t tiles = (int64_t)((a.tokens + 255) / 256) * ((a.n + (gated ? 127 : 255)) / (gated ? 128 : 256));
+  const double busy = tiles >= cus ? 1.0 : (double)tiles / cus;
+  return 8 + (double)((tiles + cus - 1) / cus * a.kb) * (1.15 + (busy > 0.5 ? (busy - 0.5) * 1.1 : 0.0));
 }
 
 template <int BN, int BT, int WN, int WT, int STAGES, int PER_CU, bool GATED, bool WIDE, Out O>
@@ -322,33 +391,35 @@ hipError_t launch(F8Args a, const Cut& cut, hipStream_t stream) {
 
 template <Out O>
 hipError_t plain(const F8Args& a, int cus, hipStream_t stream) {
-  if (a.tokens <= 32) return launch<128, 32, 4, 1, 3, 2, false, true, O>(a, cut_of<128, 32, 2, false>(a, cus, 1.0), stream);
-  if (a.tokens <= kF8FewTokens)
-    return launch<128, 64, 4, 1, 3, 2, false, true, O>(a, cut_of<128, 64, 2, false>(a, cus, 1.0), stream);
-  const int64_t large = (int64_t)((a.tokens + 255) / 256) * ((a.n + 255) / 256);
-  if (large >= cus) return f8_pp_launch(a, false, O == Out::F16, cus, stream);
-  const Cut small = cut_of<128, 64, 2, false>(a, cus, 1.0), middle = cut_of<128, 128, 1, false>(a, cus, 1.0);
-  return small.cost < middle.cost ? launch<128, 64, 4, 1, 3, 2, false, false, O>(a, small, stream)
-                                  : launch<128, 128, 2, 4, 4, 1, false, false, O>(a, middle, stream);
+  if (a.tokens <= 32) return launch<64, 32, 2, 2, 4, 3, false, false, O>(a, cut_of<64, 32, 3, false>(a, cus, kT64x32), stream);
+  const Cut s = cut_of<64, 64, 3, false>(a, cus, kT64x64), m = cut_of<128, 64, 2, false>(a, cus, kT128x64);
+  const Cut l = cut_of<128, 128, 1, false>(a, cus, kT128x128);
+  const double least = s.cost < m.cost ? (s.cost < l.cost ? s.cost : l.cost) : (m.cost < l.cost ? m.cost : l.cost);
+  if (pp_cost(a, false, cus) < least) return f8_pp_launch(a, false, O == Out::F16, cus, stream);
+  if (l.cost == least) return launch<128, 128, 2, 4, 4, 1, false, false, O>(a, l, stream);
+  if (m.cost == least) return launch<128, 64, 4, 1, 3, 2, false, false, O>(a, m, stream);
+  return launch<64, 64, 2, 2, 3, 3, false, false, O>(a, s, stream);
 }
 
 }  // namespace
 
 hipError_t f8_tiled_launch(const F8Args& a, bool gated, int dtype, int cus, hipStream_t stream) {
   if (!gated) return dtype ? plain<Out::F16>(a, cus, stream) : plain<Out::BF16>(a, cus, stream);
-  if (a.tokens <= kF8FewTokens)
-    return launch<256, 64, 4, 2, 3, 1, true, true, Out::BF16>(a, cut_of<256, 64, 1, true>(a, cus, 1.0), stream);
-  const int64_t large = (int64_t)((a.tokens + 255) / 256) * ((a.n + 127) / 128);
-  if (large >= cus) return f8_pp_launch(a, true, dtype, cus, stream);
-  const Cut small = cut_of<256, 64, 1, true>(a, cus, 1.0), middle = cut_of<256, 128, 1, true>(a, cus, 1.6);
-  return small.cost < middle.cost ? launch<256, 64, 4, 2, 3, 1, true, false, Out::BF16>(a, small, stream)
-                                  : launch<256, 128, 4, 2, 3, 1, true, false, Out::BF16>(a, middle, stream);
+  constexpr Out O = Out::BF16;  // (codes come out)
+  if (a.tokens <= 32) return launch<256, 32, 4, 1, 4, 1, true, true, O>(a, cut_of<256, 32, 1, true>(a, cus, kG256x32), stream);
+  if (a.tokens <= kF8WideTokens)
+    return launch<256, 64, 4, 2, 3, 1, true, true, O>(a, cut_of<256, 64, 1, true>(a, cus, kG256x64Wide), stream);
+  const Cut s = cut_of<256, 64, 1, true>(a, cus, kG256x64), l = cut_of<256, 128, 1, true>(a, cus, kG256x128);
+  const double least = s.cost < l.cost ? s.cost : l.cost;
+  if (pp_cost(a, true, cus) < least) return f8_pp_launch(a, true, dtype, cus, stream);
+  if (l.cost == least) return launch<256, 128, 4, 2, 3, 1, true, false, O>(a, l, stream);
+  return launch<256, 64, 4, 2, 3, 1, true, false, O>(a, s, stream);
 }
 
 void f8_workspace(int64_t max_tokens, int cus, uint64_t* part_bytes, uint64_t* counter_bytes) {
-  // at most two workgroups of 128 x 64, or one of 256 x 128, per CU
+  // per CU at most three workgroups of 64 x 64, two of 128 x 64, or one of 256 x 128
   *part_bytes = max_tokens > kF8OneTile ? (uint64_t)cus * (256 * 128 * 4) : 0;
-  *counter_bytes = max_tokens > kF8OneTile ? (uint64_t)cus * 2 * 4 : 0;
+  *counter_bytes = max_tokens > kF8OneTile ? (uint64_t)cus * 3 * 4 : 0;
 }
 
 }  // namespace bsg

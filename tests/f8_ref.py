@@ -11,7 +11,8 @@ U32 = 2.0 ** -24
 # Half a step of the output, relative to the value, and of its subnormal numbers.
 HALF = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11}
 TINY = {"bf16": 2.0 ** -134, "f16": 2.0 ** -25}
-FEW = 64  # tokens up to which products are of widened codes (exact, with sums in fp32)
+FEW = 16   # tokens up to which products are of widened codes (exact, with sums in fp32)
+WIDE = 64  # ... and those whose results become codes
 
 
 def blocks(n):
@@ -55,8 +56,9 @@ def weight_values(codes, scales):
 
 def sum_bound(k, few, exact_range=False):
     """How far a sum of k scaled products may be off, in units of the sum of their magnitudes: a rounding to fp32 for each
-    product at the most and three for the scales; beyond FEW tokens the matrix instruction also aligns every 8 products to
-    the largest and drops what lies 2^-13 below, 2^-10 of it for all 8, unless they span few bits (exact_range)."""
+    product at the most and three for the scales; where the codes are not widened (few) the matrix instruction also aligns
+    every 8 products to the largest and drops what lies 2^-13 below, 2^-10 of it for all 8, unless they span few bits
+    (exact_range)."""
     return (k + 4) * U32 + (0.0 if few or exact_range else 2.0 ** -10)
 
 
@@ -88,8 +90,9 @@ def _changes(h, d):
     return out
 
 
-def ffn(x, w1, w3, w2, few, exact_range=False):
+def ffn(x, w1, w3, w2, exact_range=False):
     """(the block's output, how far the kernels' may be off before it is rounded) for doubles x, w1, w3 [I][H], w2 [H][I]."""
+    few = len(x) <= WIDE
     xv = row_values(*quantize(x))
     (gate, sg), (up, su) = product(xv, w1), product(xv, w3)
     c = sum_bound(x.shape[1], few, exact_range)
@@ -101,4 +104,4 @@ def ffn(x, w1, w3, w2, few, exact_range=False):
     hv = row_values(*quantize(h))
     y, s = product(hv, w2)
     off = _changes(h, d)
-    return y, sum_bound(h.shape[1], few, exact_range) * (s + off @ np.abs(w2).T) + off @ np.abs(w2).T
+    return y, sum_bound(h.shape[1], len(x) <= FEW) * (s + off @ np.abs(w2).T) + off @ np.abs(w2).T

@@ -109,7 +109,7 @@ def test_reference_quantize_against_torch():
 def test_reference_block_against_torch():
     g = torch.Generator().manual_seed(1)
     x, w1, w3, w2 = (torch.randn(s, generator=g).double() / 8 for s in ((5, 144), (272, 144), (272, 144), (144, 272)))
-    want, off = ref.ffn(x.numpy(), w1.numpy(), w3.numpy(), w2.numpy(), few=True)
+    want, off = ref.ffn(x.numpy(), w1.numpy(), w3.numpy(), w2.numpy())
 
     def q(v):
         out = torch.empty_like(v)

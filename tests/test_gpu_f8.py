@@ -270,7 +270,7 @@ def test_feed_forward(t, hidden, inter, dtype):
     print("[f8]", label, flush=True)
     held, doubles = ffn_weights(hidden, inter, t)
     x = activations(t, hidden, dtype, t + hidden)
-    want, off = ref.ffn(x.double().numpy(), *doubles, few=t <= ref.FEW)
+    want, off = ref.ffn(x.double().numpy(), *doubles)
     check(run_ffn(x, held, hidden, inter, dtype), want, off, dtype, label)
 
 
@@ -280,9 +280,7 @@ def test_feed_forward_of_numbers_that_the_matrix_units_keep(t, hidden, inter):
     # value has one possible code
     held, doubles = ffn_weights(hidden, inter, t, narrow_codes)
     x = torch.from_numpy(ref.values(narrow_codes(np.random.default_rng(t), (t, hidden)))).bfloat16()
-    want, off = ref.ffn(x.double().numpy(), *doubles, few=False, exact_range=True)
-    hv = np.abs(ref.row_values(*ref.quantize(ref.silu(x.double().numpy() @ doubles[0].T) * (x.double().numpy() @ doubles[1].T))))
-    off = off + 2.0 ** -10 * (hv @ np.abs(doubles[2]).T)  # (the inner values are no such numbers)
+    want, off = ref.ffn(x.double().numpy(), *doubles, exact_range=True)
     check(run_ffn(x, held, hidden, inter, "bf16"), want, off, "bf16", (t, hidden, inter))
 
 
@@ -313,7 +311,7 @@ def test_feed_forward_strides_stream_and_smaller_calls():
             torch.cuda.synchronize()
             plan.run(wide[:t, 16:160], *ws, room[:t, 8:152], stream=side)
             torch.cuda.synchronize()
-            want, off = ref.ffn(wide[:t, 16:160].double().cpu().numpy(), *doubles, few=t <= ref.FEW)
+            want, off = ref.ffn(wide[:t, 16:160].double().cpu().numpy(), *doubles)
             check(room[:t, 8:152].double().cpu().numpy(), want, off, "f16", t)
             assert (room[:, :8] == 7).all() and (room[:, 152:] == 7).all() and (room[t:] == 7).all()
         plan.run(wide[:0, 16:160], *ws, room[:0, 8:152])
