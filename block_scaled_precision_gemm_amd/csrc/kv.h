@@ -13,6 +13,8 @@ struct HeadsArg {  // a bsg_heads, patched per call
   int64_t token_stride, head_stride;  // elements
 };
 
+constexpr int kForceShared = 1 << 30;  // in flags, beside BSG_KV_*: shared positions are read once wherever that can be
+
 // Kernel arguments: the plan's part is filled at plan creation, the rest per call.
 struct KvArgs {
   // plan

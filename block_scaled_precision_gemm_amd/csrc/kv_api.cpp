@@ -238,6 +238,8 @@ bsg_status bsg_kv_plan_create(const bsg_kv_problem* problem, bsg_kv_plan* out_pl
   a.rope_half = p.rope_dim / 2;
   a.window = bsg::kept_window(p.window);
   a.flags = (int)p.flags;
+  const char* force = getenv("BSG_FORCE_SHARED");
+  if (force && atoi(force)) a.flags |= bsg::kForceShared;
   a.page_stride = p.page_stride;
   a.score_mul = p.scale * p.k_scale;
   a.cap = p.softcap * 1.44269504088896341f;

@@ -172,8 +172,9 @@ __device__ __forceinline__ void soft_cap(const KvArgs& p, float mul, v4f s[N]) {
 }
 
 hipError_t kv_attend_rows_launch(const KvArgs& a, int dtype, int head_dim, int cus, hipStream_t stream);
-// All rows of the batch over the first a->shared positions; fills in where the parts are.  Whether they fit the workspace.
-bool kv_shared_fits(const KvArgs& a, int cus);
+// All rows of the batch over the first a->shared positions; fills in where the parts are.  What that costs, in
+// microseconds, or a negative number where the parts do not fit the workspace.
+double kv_shared_cost(const KvArgs& a, int head_dim, int cus);
 hipError_t kv_attend_shared_launch(KvArgs* a, int dtype, int head_dim, int cus, hipStream_t stream);
 // 2^kRowsBias P is what the many-row kernels' parts hold, relative to their maxima.
 constexpr float kRowsBias = 10.0f;

@@ -76,7 +76,7 @@ __device__ __forceinline__ Span span_of(const KvArgs& p, int b) {
 // Join a row's parts of the shared positions to its sums (four dims of the output): row `row` of the batch.
 template <int D>
 __device__ __forceinline__ void join_shared(const KvArgs& p, int h, int row, int d, v4f& y, float& top, float& sum) {
-  constexpr int AT_ONCE = 8;
+  constexpr int AT_ONCE = 16;
   const int R = p.shared_rows, block = row / R, r = row - block * R, last = p.shared_splits - 1;
   const int slot = R * (D + 2);
   const float* part = p.shared_part + (int64_t)((h + 1) * p.shared_width - 1 - block) * p.shared_splits * slot;
@@ -569,10 +569,16 @@ hipError_t launch(const KvArgs& a, int cus, hipStream_t stream) {
 }
 
 // Whether positions that all sequences share are read once for all of them, by the many-row kernel, and only what lies
-// behind them by the few-row kernel for each.
-bool shared_pays(const KvArgs& a, int cus) {
-  return a.shared > 0 && a.window == 0 && a.num_seqs > 1 && (int64_t)a.max_q * a.group <= kFewRows &&
-         (int64_t)a.num_tokens * a.group > kFewRows && kv_shared_fits(a, cus);
+// behind them by the few-row kernel for each.  That kernel reads 6 MB a microsecond for blocks of 16 rows and half as much
+// for 32; the other one costs 12 to 50 us.  Heads of 128, 32 on 8, 200 positions of their own, by one and by both kernels:
+// 64 tokens and 512 shared positions 24 and 35 us, 2048 42 and 40, 8192 106 and 54; 16 tokens and 2048 21 and 23, 8192 43
+// and 30 us.  5 tokens each, heads of 64: 16 sequences and 8192 45 and 38 us, 64 sequences and 2048 45 and 53 us.
+bool shared_pays(const KvArgs& a, int head_dim, int cus) {
+  const int64_t rows = (int64_t)a.max_q * a.group;
+  if (a.shared <= 0 || a.window > 0 || a.num_seqs < 2 || rows > kFewRows || (int64_t)a.num_tokens * a.group <= kFewRows) return false;
+  const double saved = (double)(a.num_seqs - 1) * a.kv_heads * a.shared * head_dim * (9.0 / 8);
+  const double cost = kv_shared_cost(a, head_dim, cus);
+  return cost >= 0 && ((a.flags & kForceShared) || saved > cost * (rows <= 16 ? 6e6 : 3e6));
 }
 
 // Floats of the few-row kernel's parts: two for each workgroup, of up to 32 rows.
@@ -591,7 +597,7 @@ size_t few_part_floats(int head_dim, int cus) { return (size_t)cus * kWgPerCu * 
 // us, over 1000 38 and 48 us; with 2 of each 70 and 56, 42 and 51 us).
 hipError_t kv_attend_launch(const KvArgs& args, int dtype, int head_dim, int cus, hipStream_t stream) {
   KvArgs a = args;
-  if (shared_pays(a, cus)) {
+  if (shared_pays(a, head_dim, cus)) {
     a.shared_part = a.part + few_part_floats(head_dim, cus);
     const hipError_t e = kv_attend_shared_launch(&a, dtype, head_dim, cus, stream);
     if (e != hipSuccess) return e;

@@ -132,7 +132,6 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
   };
   __shared__ Buffer sh[2];
   __shared__ int sh_nan[4];  // tile n's first position at n % 4, if it has such a NaN block (below)
-  __shared__ int sh_seen[SHARED ? WAVES : 1];
 
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int c = lane & 15, g = lane >> 4;
@@ -160,6 +159,14 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
   const int rows = min(R, q_len * G - rb * R), pos0 = len - q_len;
   const int i_first = rb * R / G, i_last = (rb * R + rows - 1) / G;
   const int lo = p.window > 0 ? max(0, pos0 + i_first - p.window + 1) : 0;
+  // Shared positions are mostly seen by every row.  Whether they are: the least of what the sequences' first new tokens
+  // see, whose loads are on their way meanwhile (see_all, below).
+  int least = 0x7FFFFFFF;
+  if constexpr (SHARED)
+    for (int i = lane; i < p.num_seqs; i += 64) {
+      const int n = seq_len(p, i), new_tokens = p.one_each ? 1 : min(max(seq_start(p, i + 1) - seq_start(p, i), 0), p.max_q);
+      least = min(least, new_tokens == 0 ? 0x7FFFFFFF : causal ? n - new_tokens : n - 1);
+    }
   const int hi = causal && !SHARED ? max(0, pos0 + i_last + 1) : len;
   const int base = lo & ~15, all = hi > base ? (hi - base + kTile - 1) / kTile : 0;
   const int per = (all + p.splits - 1) / p.splits;
@@ -176,22 +183,11 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
     v4i raw[NJ];
     load_query<D>(p, first_token, h, row, g, raw);
     convert_query<O, D>(p, raw, q[t], mul[t]);
-    pos[t] = causal ? pos0 + row / G : len - 1;
-    if constexpr (SHARED) {
-      const int i0 = (rb * R + (w_row < rows ? w_row : 0)) / G;
-      pos[t] = min(last_seen(p, i0, r < rows ? row / G : i0, lane, causal), len - 1);
-    }
+    pos[t] = causal && !SHARED ? pos0 + row / G : len - 1;
   }
   // positions that all, and any, of the wave's rows see up to
-  int w_first = causal ? pos0 + (rb * R + min(w_row, rows - 1)) / G : len - 1;
-  if constexpr (SHARED) {
-    w_first = min(pos[0], pos[1]);
-#pragma unroll
-    for (int d = 1; d < 16; d *= 2) w_first = min(w_first, __shfl_xor(w_first, d));
-    w_first = __builtin_amdgcn_readfirstlane(w_first);
-    if (lane == 0) sh_seen[wave] = w_first;
-  }
-  const int w_last = causal ? pos0 + (rb * R + min(w_row + 31, rows - 1)) / G : len - 1;
+  int w_first = causal && !SHARED ? pos0 + (rb * R + min(w_row, rows - 1)) / G : len - 1;
+  const int w_last = causal && !SHARED ? pos0 + (rb * R + min(w_row + 31, rows - 1)) / G : len - 1;
   v4f o[RT][E];
   float m[RT], l[RT];
 #pragma unroll
@@ -257,8 +253,18 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
       }
     };
     // some row of the workgroup does not see all of the tile at t0
-    int all_first = causal ? pos0 + i_first : len - 1;
-    const int any_last = causal ? pos0 + i_last : len - 1;
+    int all_first = causal && !SHARED ? pos0 + i_first : len - 1;
+    const int any_last = causal && !SHARED ? pos0 + i_last : len - 1;
+    // A sequence ends among the shared positions: every row's own last one, and no tile is taken to be seen by all.
+    auto see_all = [&] {
+      if (!__any(least < len - 1)) return;
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        const int r = w_row + 16 * t + c, i0 = (rb * R + (w_row < rows ? w_row : 0)) / G;
+        pos[t] = min(last_seen(p, i0, r < rows ? (rb * R + r) / G : i0, lane, causal), len - 1);
+      }
+      w_first = all_first = -1;
+    };
     auto partly_hidden = [&](int t0) {
       return t0 + kTile - 1 > min(all_first, t_end - 1) || (p.window > 0 && t0 <= any_last - p.window);
     };
@@ -314,12 +320,6 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
     for (int t = 0; t < RT; ++t) pt[t][0] = pt[t][1] = v8h{};
     for (int i = tid; i < 2 * E * 64; i += 64 * WAVES) (&sh[1].v[0][0][0])[i] = v4i{0, 0, 0, 0};
     __syncthreads();
-    if constexpr (SHARED) {
-      all_first = sh_seen[0];
-#pragma unroll
-      for (int w = 1; w < WAVES; ++w) all_first = min(all_first, sh_seen[w]);
-      all_first = __builtin_amdgcn_readfirstlane(all_first);
-    }
     // A tile's products: the last tile's outputs, then this tile's scores, each fragment read from LDS
     // kFly fragments before its two products.  Between them the wave decodes its part of this tile's values into
     // buffer buf and of the next tile's keys into the other, and loads the following ones: its vector operations
@@ -441,10 +441,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void rows_kernel(KvArgs p) {
     };
     auto run = [&](auto do_v, auto do_k) __attribute__((always_inline)) {
       constexpr bool late = !do_v.value;
-      if (do_v.value) {
-        load_v(t_begin);
-        mask_v(t_begin);
-      }
+      if (do_v.value) load_v(t_begin);
+      if constexpr (SHARED) see_all();
+      if (do_v.value) mask_v(t_begin);
       if (do_k.value) {
         load_k(t_begin);
 #pragma unroll
@@ -622,9 +621,16 @@ hipError_t launch_shared(KvArgs* a, int cus, hipStream_t stream) {
 
 }  // namespace
 
-bool kv_shared_fits(const KvArgs& a, int cus) {
+double kv_shared_cost(const KvArgs& a, int head_dim, int cus) {
   const int waves = rows_waves(a.num_tokens, a.group);
-  return ((int64_t)a.num_tokens * a.group + 32 * waves - 1) / (32 * waves) * a.kv_heads <= (int64_t)2 * cus * (8 / waves);
+  const int64_t rows = (int64_t)a.num_tokens * a.group, places = (rows + 32 * waves - 1) / (32 * waves) * a.kv_heads;
+  const int64_t fill = (int64_t)cus * (8 / waves), tiles = (a.shared + kTile - 1) / kTile;
+  if (places > 2 * fill) return -1;
+  const int64_t s = cheapest_splits(places, places, tiles, fill);
+  // the launch, a tile's 2.3 us for 256 rows of 128 dims, and the parts that the few-row kernel joins
+  const double tile = 2.3 * head_dim / 128 * waves / 8;
+  return (a.max_q * a.group <= 16 ? 14 : 16) + (double)((places * s + fill - 1) / fill * ((tiles + s - 1) / s)) * tile +
+         (double)(rows * a.kv_heads * s) * (head_dim + 2) * 4 / 8e6;
 }
 
 hipError_t kv_attend_shared_launch(KvArgs* a, int dtype, int head_dim, int cus, hipStream_t stream) {

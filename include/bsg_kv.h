@@ -133,7 +133,8 @@ bsg_status bsg_kv_attend(bsg_kv_plan plan, const bsg_kv_batch* batch, const bsg_
  * `pages` are the same, also where its context is shorter (only those of the first row are looked at for them).  The result
  * is bsg_kv_attend's but for the order of sums; the shared positions are read and multiplied once for the whole batch where
  * that pays: plans without a window, more than one sequence, at most 32 and together more than 32 query rows (new tokens x
- * query heads per key/value head).  Elsewhere, and with shared 0, the call is bsg_kv_attend.  Errors: as bsg_kv_attend. */
+ * query heads per key/value head), and enough positions.  Elsewhere, and with shared 0, the call is bsg_kv_attend.
+ * (BSG_FORCE_SHARED=1 in the environment when the plan is made: however few positions.)  Errors: as bsg_kv_attend. */
 bsg_status bsg_kv_attend_shared(bsg_kv_plan plan, const bsg_kv_batch* batch, int64_t shared, const bsg_heads* q,
                                 const void* cache, const bsg_heads* out, float* lse, void* stream);
 

@@ -11,6 +11,11 @@ from test_gpu_kv import DT, check, dev, filled
 pytestmark = pytest.mark.gpu
 
 
+@pytest.fixture(autouse=True)
+def small_cases_are_shared_too(monkeypatch):
+    monkeypatch.setenv("BSG_FORCE_SHARED", "1")
+
+
 def layout(new, lens, shared, P, seed):
     """q_start, pages (the first shared / P of every row the same) and the number of pages."""
     rng = np.random.default_rng(seed)
@@ -200,6 +205,37 @@ def test_a_captured_call_replays_with_growing_contexts():
             got = out.double().cpu().numpy(), lse.double().cpu().numpy()
             want, want_lse = kv_ref.attend(q.double().cpu().numpy(), c, q_start, lens.tolist(), pages, 2)
             check(*got, want, want_lse, "bf16", 4.0, step)
+
+
+@pytest.mark.parametrize("D,new,dtype", [(128, 1, "bf16"), (64, 4, "f16")])
+def test_the_choice_by_cost(monkeypatch, D, new, dtype):
+    # without the switch: a long common beginning (read once) and a short one (not), the same results but for rounding
+    monkeypatch.delenv("BSG_FORCE_SHARED")
+    gen = torch.Generator(device="cuda").manual_seed(D)
+    P, H, G, seqs = 64, 8, 4, 48
+    for shared in (8192, 128):
+        common, own = shared // P, 3
+        n_pages = common + own * seqs
+        pages = torch.cat((torch.arange(common, device="cuda").expand(seqs, common),
+                           common + torch.arange(own * seqs, device="cuda").view(seqs, own)), 1).int().contiguous()
+        lens = (shared + new + torch.arange(seqs, device="cuda") * 3 % 150).int()
+        with bsg.KVPlan(H * G, H, D, P, n_pages, seqs * new, dtype=dtype) as plan:
+            starts = torch.arange(0, seqs * new + 1, new, dtype=torch.int32, device="cuda")
+            batch = bsg.KVBatch(starts, lens, pages, seqs * new, new, int(lens.max()))
+            cache = torch.randint(0, 256, (n_pages * plan.page_bytes,), dtype=torch.uint8, device="cuda", generator=gen)
+            chunk = cache.view(n_pages, H, -1)[:, :, P * D:]
+            chunk.copy_(torch.randint(0x28, 0x40, chunk.shape, dtype=torch.uint8, device="cuda", generator=gen))  # scales
+            q = torch.randn(seqs * new, H * G, D, device="cuda", generator=gen).to(DT[dtype])
+            outs = [torch.empty_like(q) for _ in range(2)]
+            lses = [torch.empty(seqs * new, H * G, device="cuda") for _ in range(2)]
+            plan.attend(batch, q, cache, outs[0], lse=lses[0], shared=shared)
+            plan.attend(batch, q, cache, outs[1], lse=lses[1])
+            torch.cuda.synchronize()
+        # both are within check()'s bound of the exact result
+        v_max = 6 * 1.875
+        a, b = (x.double() for x in outs)
+        assert ((a - b).abs() <= 4 * (2.0 ** -8 if dtype == "bf16" else 2.0 ** -11) * b.abs() + 2.0 ** -10 * v_max + 2e-7).all(), shared
+        assert ((lses[0] - lses[1]).abs() <= 2 * (2e-5 + 2e-6 * lses[1].abs())).all(), shared
 
 
 @pytest.mark.parametrize("shared", [-16, 8, 24, 128])
