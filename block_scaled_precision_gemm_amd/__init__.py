@@ -13,6 +13,7 @@ The library is loaded on first use and a missing build raises LibraryNotBuilt: t
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import struct
 
@@ -593,6 +594,12 @@ def _f8_blocks(n: int) -> int:
     return (n + F8_BLOCK - 1) // F8_BLOCK
 
 
+@functools.cache
+def _f8_types() -> tuple:
+    import torch
+    return torch.float32, {torch.bfloat16: OUT_DTYPES["bf16"], torch.float16: OUT_DTYPES["f16"]}
+
+
 def f8_scales_shape(rows: int, cols: int) -> tuple[int, int]:
     """Shape of the float32 scales of rows [rows][cols]: [blocks of 128 columns][rows rounded up to a multiple of 4]."""
     return _f8_blocks(cols), (rows + 3) // 4 * 4
@@ -600,7 +607,7 @@ def f8_scales_shape(rows: int, cols: int) -> tuple[int, int]:
 
 def _f8_rows(t, rows: int, cols: int, what: str) -> int:
     """Bytes from row to row of a tensor of codes."""
-    if t.dim() != 2 or t.shape != (rows, cols) or t.element_size() != 1 or t.stride(1) != 1:
+    if t.shape != (rows, cols) or t.itemsize != 1 or t.stride(1) != 1:
         raise ValueError(f"{what} must be codes of one byte [{rows}][{cols}] with contiguous rows, got {t.dtype} {tuple(t.shape)} "
                          f"with strides {t.stride()}")
     return t.stride(0) if rows > 1 else _f8_round16(cols)
@@ -612,17 +619,18 @@ def _f8_round16(n: int) -> int:
 
 def _f8_scales(t, rows: int, cols: int, f32) -> int:
     """Floats from block to block of a tensor of rows' scales."""
-    if t.dim() != 2 or t.dtype != f32 or t.shape[0] != _f8_blocks(cols) or t.shape[1] < rows or t.stride(1) != 1:
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or t.dtype != f32 or shape[0] != _f8_blocks(cols) or shape[1] < rows or stride[1] != 1:
         raise ValueError(f"scales must be float32 [{_f8_blocks(cols)}][{rows} or more] with contiguous rows, got {t.dtype} "
                          f"{tuple(t.shape)} with strides {t.stride()}")
-    if t.shape[1] % 4:
+    if shape[1] % 4:
         raise BsgError(4, f"scales have {t.shape[1]} columns, not a multiple of 4 (f8_scales_shape)")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return stride[0] if shape[0] > 1 else shape[1]
 
 
 def _f8_matrix(t, rows: int, cols: int, dtypes, what: str) -> int:
     """Elements from row to row of a 16-bit tensor."""
-    if t.dim() != 2 or t.shape != (rows, cols) or t.dtype not in dtypes or t.stride(1) != 1:
+    if t.shape != (rows, cols) or t.dtype not in dtypes or t.stride(1) != 1:
         raise ValueError(f"{what} must be a 16-bit tensor [{rows}][{cols}] of the dtype asked for with contiguous rows, got "
                          f"{t.dtype} {tuple(t.shape)} with strides {t.stride()}")
     return t.stride(0) if rows > 1 else cols
@@ -630,7 +638,7 @@ def _f8_matrix(t, rows: int, cols: int, dtypes, what: str) -> int:
 
 def _f8_weights(checks, f32) -> None:
     for name, w, s, nw, ns in checks:
-        if w.element_size() != 1 or w.numel() != nw or not w.is_contiguous() or s.dtype != f32 or s.numel() != ns or not s.is_contiguous():
+        if w.itemsize != 1 or w.numel() != nw or not w.is_contiguous() or s.dtype != f32 or s.numel() != ns or not s.is_contiguous():
             raise ValueError(f"{name} must be {nw} contiguous codes of one byte with {ns} contiguous float32 scales, got "
                              f"{w.dtype} {tuple(w.shape)} and {s.dtype} {tuple(s.shape)}")
 
@@ -638,14 +646,14 @@ def _f8_weights(checks, f32) -> None:
 def f8_quantize(x, codes, scales, stream=None) -> None:
     """codes (one byte each: uint8 or float8_e4m3fn) [rows][cols] and scales (float32, f8_scales_shape) = x [rows][cols] of
     bfloat16 or float16 as E4M3 with the least power of two that fits for each 128 columns (bsg_f8_quantize)."""
-    import torch
-    if x.dtype not in (torch.bfloat16, torch.float16):
-        raise ValueError(f"x must be bfloat16 or float16, got {x.dtype}")
+    f32, dtypes = _f8_types()
+    dtype = dtypes.get(x.dtype)
+    if dtype is None or x.dim() != 2:
+        raise ValueError(f"x must be bfloat16 or float16 [rows][cols], got {x.dtype} {tuple(x.shape)}")
     rows, cols = x.shape
     _check(load_library().bsg_f8_quantize(
-        OUT_DTYPES["bf16" if x.dtype == torch.bfloat16 else "f16"], rows, cols, x.data_ptr(),
-        _f8_matrix(x, rows, cols, (x.dtype,), "x"), codes.data_ptr(), _f8_rows(codes, rows, cols, "codes"), scales.data_ptr(),
-        _f8_scales(scales, rows, cols, torch.float32), _stream(stream)))
+        dtype, rows, cols, x.data_ptr(), _f8_matrix(x, rows, cols, dtypes, "x"), codes.data_ptr(),
+        _f8_rows(codes, rows, cols, "codes"), scales.data_ptr(), _f8_scales(scales, rows, cols, f32), _stream(stream)))
 
 
 class F8Plan:

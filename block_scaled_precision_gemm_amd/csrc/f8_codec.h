@@ -101,6 +101,13 @@ __device__ __forceinline__ float f8_gated(float gate, float up) {
   return gate * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-gate * 1.44269504088896341f)) * up;
 }
 
+// The largest of a value over the 8 lanes that hold a block.
+__device__ __forceinline__ uint32_t f8_max8(uint32_t x) {
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0xB1, 0xF, 0xF, true));   // lanes 1, 0, 3, 2 of each four
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x4E, 0xF, 0xF, true));   // lanes 2, 3, 0, 1
+  return max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x141, 0xF, 0xF, true));  // of each eight, back to front
+}
+
 constexpr int kF8Nan = 0x7F7F7F7F;  // four codes of a block that holds an infinity or a NaN
 __device__ __forceinline__ bool f8_not_finite(uint32_t amax) { return amax >= 0x7F800000u; }
 

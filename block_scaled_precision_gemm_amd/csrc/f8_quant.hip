@@ -9,13 +9,6 @@ namespace {
 
 constexpr int kThreads = 256, kRows = 16, kStep = 2, kSteps = 4;
 
-// The largest of a value over the 8 lanes that hold a block.
-__device__ __forceinline__ uint32_t max8(uint32_t x) {
-  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0xB1, 0xF, 0xF, true));   // lanes 1, 0, 3, 2 of each four
-  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x4E, 0xF, 0xF, true));   // lanes 2, 3, 0, 1
-  return max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x141, 0xF, 0xF, true));  // of each eight, back to front
-}
-
 template <Src S>
 __global__ __launch_bounds__(kThreads) void quant_kernel(const uint8_t* x, int64_t x_stride, uint8_t* codes,
                                                         int64_t codes_stride, float* scales, int64_t scale_stride,
@@ -36,7 +29,7 @@ __global__ __launch_bounds__(kThreads) void quant_kernel(const uint8_t* x, int64
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) {
     const int b = b0 + kStep * i, col = b * 128 + 16 * in_block;
-    const uint32_t most = max8(v[i].amax());
+    const uint32_t most = f8_max8(v[i].amax());
     const float s = f8_scale(most);
     v4i q = v[i].codes(s);
     if (f8_not_finite(most)) q = v4i{kF8Nan, kF8Nan, kF8Nan, kF8Nan};
