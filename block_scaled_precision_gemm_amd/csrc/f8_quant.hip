@@ -1,7 +1,11 @@
 // Rows of 16-bit values to E4M3 codes with a power-of-two scale for each block of 128 (include/bsg_f8.h).
 //
 // A lane holds 16 consecutive values, so 8 lanes hold a block.  A workgroup takes 16 rows of 8 blocks, two blocks of all
-// rows at a time: a row's part is at least 512 bytes in a row, and the 16 scales of a block are neighbours in memory.
+// rows at a time: a row's part is at least 512 bytes in a row, and the 16 scales of a block are neighbours in memory.  All of a
+// lane's loads (four blocks) are on their way before the first is used.
+//
+// Bound: memory, three bytes and a little for each value: 8191 rows of 8192 in 39 to 47 us (4.3 to 5.2 TB/s; a copy of as many
+// bytes takes 40 us).  One row of 4096: 2.5 us, a launch.
 #include "f8_codec.h"
 
 namespace bsg {

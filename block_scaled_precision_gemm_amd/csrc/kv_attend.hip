@@ -24,6 +24,9 @@
 // Softmax: maximum m and sum l per row, in fp32 and base 2.  P is rounded to fp16 for its product, 2^-11 of itself at most (a
 // second product for what is left would double the work beside the loads); l sums the unrounded values.
 //
+// Where the batch's first positions are shared and read by the many-row kernel (kv_rows.hip, shared_pays below), units begin
+// behind them, and whoever finishes a unit adds the shared positions' parts, which are in the workspace by then.
+//
 // Bound: bytes of the cache (D 9/8 bytes per position and head) where contexts are long; for short ones the
 // chain of dependent trips to memory (lengths, page numbers, codes, the join), about 10 us.  Measured, heads
 // of 128: 64 tokens over up to 16384 positions, 64 heads on 8: 80 us (4.3 TB/s); one token over 131072
