@@ -596,8 +596,10 @@ def _f8_blocks(n: int) -> int:
 
 @functools.cache
 def _f8_types() -> tuple:
+    """float32, the types of values and what the library calls them, and those of codes (other 8-bit floats are none)."""
     import torch
-    return torch.float32, {torch.bfloat16: OUT_DTYPES["bf16"], torch.float16: OUT_DTYPES["f16"]}
+    return (torch.float32, {torch.bfloat16: OUT_DTYPES["bf16"], torch.float16: OUT_DTYPES["f16"]},
+            (torch.float8_e4m3fn, torch.uint8, torch.int8))
 
 
 def f8_scales_shape(rows: int, cols: int) -> tuple[int, int]:
@@ -607,8 +609,8 @@ def f8_scales_shape(rows: int, cols: int) -> tuple[int, int]:
 
 def _f8_rows(t, rows: int, cols: int, what: str) -> int:
     """Bytes from row to row of a tensor of codes."""
-    if t.shape != (rows, cols) or t.itemsize != 1 or t.stride(1) != 1:
-        raise ValueError(f"{what} must be codes of one byte [{rows}][{cols}] with contiguous rows, got {t.dtype} {tuple(t.shape)} "
+    if t.shape != (rows, cols) or t.dtype not in _f8_types()[2] or t.stride(1) != 1:
+        raise ValueError(f"{what} must be E4M3 codes or bytes [{rows}][{cols}] with contiguous rows, got {t.dtype} {tuple(t.shape)} "
                          f"with strides {t.stride()}")
     return t.stride(0) if rows > 1 else _f8_round16(cols)
 
@@ -637,16 +639,17 @@ def _f8_matrix(t, rows: int, cols: int, dtypes, what: str) -> int:
 
 
 def _f8_weights(checks, f32) -> None:
+    kinds = _f8_types()[2]
     for name, w, s, nw, ns in checks:
-        if w.itemsize != 1 or w.numel() != nw or not w.is_contiguous() or s.dtype != f32 or s.numel() != ns or not s.is_contiguous():
-            raise ValueError(f"{name} must be {nw} contiguous codes of one byte with {ns} contiguous float32 scales, got "
+        if w.dtype not in kinds or w.numel() != nw or not w.is_contiguous() or s.dtype != f32 or s.numel() != ns or not s.is_contiguous():
+            raise ValueError(f"{name} must be {nw} contiguous E4M3 codes or bytes with {ns} contiguous float32 scales, got "
                              f"{w.dtype} {tuple(w.shape)} and {s.dtype} {tuple(s.shape)}")
 
 
 def f8_quantize(x, codes, scales, stream=None) -> None:
     """codes (one byte each: uint8 or float8_e4m3fn) [rows][cols] and scales (float32, f8_scales_shape) = x [rows][cols] of
     bfloat16 or float16 as E4M3 with the least power of two that fits for each 128 columns (bsg_f8_quantize)."""
-    f32, dtypes = _f8_types()
+    f32, dtypes, _ = _f8_types()
     dtype = dtypes.get(x.dtype)
     if dtype is None or x.dim() != 2:
         raise ValueError(f"x must be bfloat16 or float16 [rows][cols], got {x.dtype} {tuple(x.shape)}")

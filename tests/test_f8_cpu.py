@@ -125,3 +125,11 @@ def test_reference_block_against_torch():
     # of a code is 9% of a value, so 0.25% of the inner values have two possible codes; 272 of them, 9% of each added up
     # without signs, against a sum of random signs, are 272 * 0.0025 * 0.09 / 272^0.5 = 0.4% of it: bf16's half step.
     assert np.median(off / np.abs(want)) < 2.0 ** -8
+
+
+@pytest.mark.parametrize("kind", [torch.float8_e5m2, torch.bool])
+def test_codes_of_other_types_are_refused(kind):
+    # E5M2 has the size of E4M3, and would be taken for other numbers
+    x, codes = torch.zeros(4, 32, dtype=torch.bfloat16), torch.zeros(4, 32, dtype=torch.uint8).view(kind)
+    with pytest.raises(ValueError, match="E4M3"):
+        bsg.f8_quantize(x, codes, torch.zeros(bsg.f8_scales_shape(4, 32)))

@@ -392,3 +392,16 @@ def test_what_the_binding_and_the_plans_refuse():
     with pytest.raises(ValueError):
         bsg.f8_quantize(h, x[:, :128], sx)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("other", [torch.float8_e5m2, torch.bool])
+def test_one_byte_types_that_are_no_codes_are_refused(other):
+    x, w = torch.zeros(4, 32, dtype=torch.uint8, device="cuda"), torch.zeros(16, 32, dtype=torch.uint8, device="cuda")
+    sx, sw, out = torch.ones(1, 4, device="cuda"), torch.ones(1, 1, device="cuda"), torch.zeros(4, 16, dtype=torch.bfloat16, device="cuda")
+    with bsg.F8Plan(16, 32, 4) as plan:
+        for kind in (torch.uint8, torch.int8, torch.float8_e4m3fn):
+            plan.run(x.view(kind), sx, w.view(kind), sw, out)
+        for args in ((x.view(other), sx, w, sw, out), (x, sx, w.view(other), sw, out)):
+            with pytest.raises(ValueError):
+                plan.run(*args)
+    torch.cuda.synchronize()
