@@ -65,12 +65,12 @@ struct Span {
   int blocks;      // its blocks of R rows
 };
 
-template <int R>
+template <int R, bool SHARED>
 __device__ __forceinline__ Span span_of(const KvArgs& p, int b) {
   Span s;
   s.len = seq_len(p, b);
   s.q_len = p.one_each ? 1 : min(max(seq_start(p, b + 1) - seq_start(p, b), 0), p.max_q);
-  s.lo = p.window > 0 ? max(0, s.len - s.q_len - p.window + 1) & ~15 : p.shared;
+  s.lo = SHARED ? p.shared : p.window > 0 ? max(0, s.len - s.q_len - p.window + 1) & ~15 : 0;
   s.tiles = max(1, (s.len - s.lo + kTile - 1) / kTile);
   s.blocks = p.mixed && s.q_len * p.group > kFewRows ? 0 : (s.q_len * p.group + R - 1) / R;
   return s;
@@ -109,7 +109,9 @@ __device__ __forceinline__ void join_shared(const KvArgs& p, int h, int row, int
   }
 }
 
-template <Out O, int D, int RT>
+// SHARED: the first p.shared positions of all sequences are in parts already.  (A kernel of its own: the ordinary one would be
+// 5% slower for long contexts and for drafted tokens, 28.7 and 30.1 us, 19.9 and 21.2.)
+template <Out O, int D, int RT, bool SHARED>
 __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
   constexpr int R = 16 * RT;
   constexpr int NG = 2, DEPTH = 2;   // groups of 16 positions in a wave's step, steps in flight
@@ -149,7 +151,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
   for (int i = 0; i < per_thread; ++i) {
     const int b = tid * per_thread + i;
     if (b < p.num_seqs) {
-      const Span s = span_of<R>(p, b);
+      const Span s = span_of<R, SHARED>(p, b);
       const int n = s.blocks * H;
       tiles += n * s.tiles;
       units += n;
@@ -166,7 +168,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
   for (int i = 0; i < per_thread; ++i) {
     const int b = tid * per_thread + i;
     if (b < p.num_seqs) {
-      const Span s = span_of<R>(p, b);
+      const Span s = span_of<R, SHARED>(p, b);
       mine += s.blocks * H * items(s);
     }
   }
@@ -179,7 +181,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
   if (before <= run0 && run0 < before + mine) {  // the one thread whose sequences hold the run's start
     int at = before, b = tid * per_thread;
     for (;; ++b) {
-      const Span s = span_of<R>(p, b);
+      const Span s = span_of<R, SHARED>(p, b);
       const int n = s.blocks * H * items(s);
       if (run0 < at + n) break;
       at += n;
@@ -192,12 +194,12 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
   int seq0 = __builtin_amdgcn_readfirstlane(sh_at[1]);  // line position of sequence b's first item
 
   for (int x = run0; x < run1;) {
-    Span s = span_of<R>(p, b);
+    Span s = span_of<R, SHARED>(p, b);
     int len = items(s);
     while (x >= seq0 + s.blocks * H * len) {
       seq0 += s.blocks * H * len;
       ++b;
-      s = span_of<R>(p, b);
+      s = span_of<R, SHARED>(p, b);
       len = items(s);
     }
     const int unit = (x - seq0) / len;
@@ -218,7 +220,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
     const int pos0 = s.len - s.q_len;  // position of the sequence's first new token
     // positions seen by some row of the block
     const int i_first = rb * R / G, i_last = (rb * R + rows - 1) / G;
-    const int lo = p.window > 0 ? max(0, pos0 + i_first - p.window + 1) : p.shared;
+    const int lo = SHARED ? p.shared : p.window > 0 ? max(0, pos0 + i_first - p.window + 1) : 0;
     const int hi = causal ? max(0, pos0 + i_last + 1) : s.len;
     const int s0 = max(s.lo + tile0 * kTile, lo & ~15), s1 = min(s.lo + tile1 * kTile, hi);
 
@@ -469,7 +471,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(KvArgs p) {
     const __amdgpu_buffer_rsrc_t parts = handoff_buffer(p.part, 2u * gridDim.x * SLOT * 4u);
     // element (row r, dims d .. d+3)
     auto store_out = [&](int r, int d, v4f y, float top, float sum) {
-      if (p.shared) join_shared<D>(p, h, first_token * G + rb * R + r, d, y, top, sum);
+      if constexpr (SHARED) join_shared<D>(p, h, first_token * G + rb * R + r, d, y, top, sum);
       const int i = (rb * R + r) / G, hq = rb * R + r - i * G;
       const float f = 256.0f / sum, gain = p.v_scale;  // (one after the other: v_scale may be near fp32's ends)
       const bool none = sum == 0.0f;                   // an empty row gives zeros
@@ -567,8 +569,9 @@ hipError_t launch(const KvArgs& a, int cus, hipStream_t stream) {
   const int64_t units = ((int64_t)a.num_tokens * a.group / R + a.num_seqs) * a.kv_heads;
   const int64_t want = units * ((tiles + kMinTiles - 1) / kMinTiles), most = (int64_t)cus * kWgPerCu;
   const dim3 grid((unsigned)(want < most ? want : most));
-  const void* fn = R == 16 ? (const void*)&few_kernel<O, D, 1> : (const void*)&few_kernel<O, D, 2>;
-  return hipLaunchKernel(fn, grid, dim3(kThreads), argv, 0, stream);
+  const void* one = a.shared ? (const void*)&few_kernel<O, D, 1, true> : (const void*)&few_kernel<O, D, 1, false>;
+  const void* two = a.shared ? (const void*)&few_kernel<O, D, 2, true> : (const void*)&few_kernel<O, D, 2, false>;
+  return hipLaunchKernel(R == 16 ? one : two, grid, dim3(kThreads), argv, 0, stream);
 }
 
 // Whether positions that all sequences share are read once for all of them, by the many-row kernel, and only what lies
