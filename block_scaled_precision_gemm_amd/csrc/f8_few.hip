@@ -17,8 +17,8 @@
 //
 // The codes are widened to fp16, which holds every E4M3 value, and multiplied by v_mfma_f32_16x16x32_f16: its products are
 // exact and its sums fp32.  The matrix instructions that take E4M3 itself align the products of a group to the largest and
-// keep 14 bits (1.4e-5 of the result, measured), which is more than what the weights' bytes leave idle here would save, and
-// would turn one in 400 of the block's inner values to a neighbouring code.
+// keep 14 bits (1.4e-5 of the result, measured), which turns one in 400 of the feed-forward block's inner values to a
+// neighbouring code; their rate is of no use here, where the matrix units wait for the weights' bytes.
 #include "epilogue.h"
 #include "f8_codec.h"
 
