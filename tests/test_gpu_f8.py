@@ -405,3 +405,29 @@ def test_one_byte_types_that_are_no_codes_are_refused(other):
             with pytest.raises(ValueError):
                 plan.run(*args)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("n", [272, 2064])
+def test_rows_whose_offsets_pass_32_bits(n):
+    """Rows 2^21 and more apart, so that the last lie beyond 2^32 bytes: the same bits as from neighbouring rows."""
+    t, k, far = 2100, 144, (1 << 21) + 16
+    x = activations(t, k, "bf16", 7).cuda()
+    w, sw = (dev(a) for a in weights(n, k, 8))
+
+    def spread(cols, dtype):
+        held = torch.empty(t * far, dtype=dtype, device="cuda").view(t, far)
+        return held[:, :cols]
+
+    results = []
+    for make in (lambda cols, dtype: torch.empty(t, cols, dtype=dtype, device="cuda"), spread):
+        a, codes, out = make(k, torch.bfloat16), make(k, torch.uint8), make(n, torch.bfloat16)
+        a.copy_(x)
+        scales = torch.ones(bsg.f8_scales_shape(t, k), device="cuda")
+        bsg.f8_quantize(a, codes, scales)
+        with bsg.F8Plan(n, k, t) as plan:
+            plan.run(codes, scales, w, sw, out)
+        torch.cuda.synchronize()
+        results.append((codes.cpu(), scales.cpu(), out.cpu()))
+    for near, distant in zip(*results):
+        assert torch.equal(near.contiguous().view(torch.uint8), distant.contiguous().view(torch.uint8))
+    torch.cuda.empty_cache()  # (13 GB)
