@@ -278,11 +278,15 @@ __global__ __launch_bounds__(THREADS, 2) void pp_kernel(F8Args p) {
         atomicMax(&sh_most[64 * ws + TT * c + j], most);
       }
       __syncthreads();
+      uint32_t of_token[TT];
+#pragma unroll
+      for (int j = 0; j < TT; ++j) of_token[j] = sh_most[64 * ws + TT * c + j];
+      __syncthreads();  // (the next tile's first copies of scales, which no other barrier precedes, go where these lay)
       const int n = n0 + 64 * grp + 16 * g;
 #pragma unroll
       for (int j = 0; j < TT; ++j) {
         const int t = 64 * ws + TT * c + j;
-        const uint32_t most = sh_most[t];
+        const uint32_t most = of_token[j];
         const float s = f8_scale(most);
         v4i q;
 #pragma unroll

@@ -284,6 +284,21 @@ def test_feed_forward_of_numbers_that_the_matrix_units_keep(t, hidden, inter):
     check(run_ffn(x, held, hidden, inter, "bf16"), want, off, "bf16", (t, hidden, inter))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_feed_forward_of_more_large_tiles_than_run_at_once(dtype):
+    """8 x 64 tiles of 256 tokens and 128 inner values, the last of both shorter: every workgroup does two, and the second
+    one's copies go where the first kept its tokens' largest magnitudes.  The reference has the tokens at the tiles' edges
+    and every 13th; tokens do not depend on each other."""
+    t, hidden, inter = 2040, 528, 8176
+    print("[f8] ffn", t, hidden, inter, dtype, flush=True)
+    held, doubles = ffn_weights(hidden, inter, 5, narrow_codes)
+    x = torch.from_numpy(ref.values(narrow_codes(np.random.default_rng(6), (t, hidden)))).to(DT[dtype])
+    got = run_ffn(x, held, hidden, inter, dtype)
+    rows = np.unique(np.concatenate([np.arange(0, t, 13), np.arange(255, t, 256), np.arange(256, t, 256), [t - 1]]))
+    want, off = ref.ffn(x[rows].double().numpy(), *doubles, exact_range=True)
+    check(got[rows], want, off, dtype, (t, hidden, inter))
+
+
 @pytest.mark.parametrize("t", [3, 40, 100])
 def test_feed_forward_infinite_and_nan_tokens_stay_in_their_rows(t):
     held, doubles = ffn_weights(144, 144, t)
