@@ -115,7 +115,7 @@ __global__ __launch_bounds__(THREADS, 2) void pp_kernel(F8Args p) {
         copy16(half ? second : first, dst + q * 8 * BK, kpos[q & 1] < left ? voff[half][q] : kOut, col);
     };
     // the scales of the wave's tokens, for itself
-    const int my_t = t0 + 64 * ws, my_tokens = (int)max((int64_t)0, min((int64_t)64, p.sx_stride - my_t));
+    const int my_t = t0 + 64 * ws, my_tokens = max(0, min(64, p.tokens - my_t));
     uint8_t* const sc_lds = lds + SCALES + wave * 256;
     auto copy_scales = [&](auto sc, int kt) __attribute__((always_inline)) {
       constexpr int stage = decltype(sc)::value;

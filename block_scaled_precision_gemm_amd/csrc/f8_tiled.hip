@@ -103,7 +103,7 @@ __global__ __launch_bounds__(64 * WN * WT, WN* WT* PER_CU / 4) void tiled_kernel
     }
   }
   const int my_t = t0 + 16 * TT * wt;
-  const int my_scales = (int)max((int64_t)0, min((int64_t)16 * TT, p.sx_stride - my_t));
+  const int my_scales = max(0, min(16 * TT, p.tokens - my_t));
   // Every step has the same number of copies: those past the last have an offset past the buffers.
   auto copy_one = [&](int i, int b, int stage) __attribute__((always_inline)) {
     const bool real = b < b1;

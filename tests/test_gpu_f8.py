@@ -232,6 +232,23 @@ def test_strided_rows_and_another_stream(t):
     check(room[:, 8:152].double().cpu().numpy(), want, ref.sum_bound(k, t <= ref.FEW) * s, "f16", "strided")
 
 
+@pytest.mark.parametrize("t,n,k", [(7, 144, 272), (20, 144, 272), (61, 144, 272), (510, 6160, 144), (1003, 6160, 400), (2042, 6160, 400)])
+def test_scales_in_the_last_columns_of_their_storage(t, n, k):
+    """A view of the scales that ends where its storage does, whose rows are shorter than a tile: nothing behind it is read,
+    and the result has the bits of a copy's."""
+    print("[f8] view of scales", t, n, k, flush=True)
+    x, sx, w, sw, _ = operands(t, n, k, t)
+    held = torch.full((ref.blocks(k), 16 + sx.shape[1]), float("nan"), device="cuda")
+    held[:, 16:16 + t] = dev(sx)[:, :t]
+    x, w, sw = dev(x), dev(w), dev(sw)
+    outs = [torch.full((t, n), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    with bsg.F8Plan(n, k, t) as plan:
+        for scales, out in zip((held[:, 16:], held[:, 16:].contiguous()), outs):
+            plan.run(x, scales, w, sw, out)
+    torch.cuda.synchronize()
+    assert torch.isfinite(outs[0]).all() and torch.equal(outs[0].view(torch.int16), outs[1].view(torch.int16))
+
+
 def test_scales_near_the_ends_of_fp32():
     x, sx, w, sw, _ = operands(3, 16, 272, 1, narrow_codes)
     for a, b in ((1e30, 1e-30), (1e-37, 1e35)):
