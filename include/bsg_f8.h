@@ -3,11 +3,14 @@
  * feed-forward block over them, on AMD MI355X (gfx950), C ABI.
  *
  * Elements are E4M3 codes (OCP 8-bit, as in bsg.h; 0x7F and 0xFF are NaN).  B(k) = ceil(k / 128) is the number
- * of blocks along k.  Two kinds of scales, both fp32 and of any value:
+ * of blocks along k.  Two kinds of scales, both fp32:
  *   rows      one for each 128 consecutive elements of a row, block by block: the scale of row t, block b is
  *             scales[b * scale_stride + t], so that the scales which a product needs at a time are neighbours;
  *   weights   one for each 128 x 128 block, [B(n)][B(k)], row-major.
  * The last block of a row, and of the weights' rows, may be shorter.
+ * Scales may have any values whose product, a row's scale times a weight's, is below 2^128: it is formed in fp32 and then
+ * multiplied by the block's sum of codes.  Where it is larger it is infinite, also for a block whose sum is zero (NaN then).
+ * Where it is below 2^-126 it is rounded to a multiple of 2^-149, which moves a block's part of an output by at most 2^-125.
  *
  * bsg_f8_quantize   codes and scales of 16-bit rows: of the elements x of a block, the scale is the least power of
  *                   two s >= 2^-126 with max|x| <= 448 s, and the codes are x / s rounded to nearest even (x / s is

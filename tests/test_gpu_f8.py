@@ -257,6 +257,40 @@ def test_scales_near_the_ends_of_fp32():
         check(got, want, ref.sum_bound(272, True) * s + 1e-40, "bf16", (a, b))
 
 
+def scales_at_the_limits(t, n, k, seed):
+    """Operands of which block 0 of k has scales of rows from 2^-120 to 2^66 and of weights from 2^-118 to 2^61, whose
+    products lie below 2^127 and may be subnormal; every other token's codes are zero there, the others' everywhere else."""
+    x, sx, w, sw, _ = operands(t, n, k, seed, narrow_codes)
+    rng = np.random.default_rng(seed)
+    sx[0, :t] = np.ldexp(1 + rng.random(t), rng.choice([-120, -100, -60, -20, 0, 40, 65], t))
+    sw[:, 0] = np.ldexp(1 + rng.random(len(sw)), rng.choice([-118, -50, 0, 40, 60], len(sw)))
+    sx[0, :4], sw[:2, 0] = [1.5 * 2.0 ** 65, 1.75 * 2.0 ** 65, 1.5, 1.25 * 2.0 ** -100], [1.25 * 2.0 ** 60, 1.75 * 2.0 ** -40]
+    x[::2, :128] = 0
+    x[1::2, 128:] = 0
+    return x, sx, w, sw
+
+
+@pytest.mark.parametrize("t,n,k", [(5, 272, 272), (16, 784, 400), (20, 784, 272), (40, 784, 400), (70, 784, 272), (510, 6160, 144),
+                                   (1003, 6160, 400), (2042, 6160, 400)])
+def test_scales_whose_products_reach_the_ends_of_fp32(t, n, k):
+    print("[f8] scales at the limits", t, n, k, flush=True)
+    x, sx, w, sw = scales_at_the_limits(t, n, k, t)
+    want, s = ref.product(ref.row_values(x, sx.astype(np.float64)), ref.weight_values(w, sw))
+    factors = sx[0, :t, None].astype(np.float64) * np.repeat(sw[:, 0].astype(np.float64), 128)[None, :n]
+    # the inputs are what they are meant to be: products of scales near both ends, with sums of zero and with others
+    assert (factors[::2] > 2.0 ** 125).any() and (factors[1::2] > 2.0 ** 125).any() and (factors[1::2] < 2.0 ** -126).any()
+    got = run_product(x, sx, w, sw, None, "bf16")
+    # beside the roundings of fp32 sums, 2^-24 or 2^-150 of subnormal ones: half a step of a subnormal product of scales, times a
+    # block's sum of at most 128 * 1.875^2 < 2^9 for these codes
+    off = ref.sum_bound(k, t <= ref.FEW, True) * s + (2.0 ** 9 + k + 4) * 2.0 ** -150
+    most = (2 - 2.0 ** -8) * 2.0 ** 127  # from here on bf16 is infinite
+    infinite = np.isinf(got)
+    assert not np.isnan(got).any() and infinite.any()
+    assert (np.abs(want) + off >= most)[infinite].all() and (np.abs(want) - off < most)[~infinite].all()
+    assert np.array_equal(np.sign(got)[infinite], np.sign(want)[infinite])
+    check(got[~infinite], want[~infinite], off[~infinite], "bf16", (t, n, k))
+
+
 # ------------------------------------------------------------------------------------------------ feed-forward block
 def ffn_weights(hidden, inter, seed, make=codes_of):
     (w1, s1), (w3, s3) = weights(inter, hidden, seed, hidden ** -0.5, make), weights(inter, hidden, seed + 1, hidden ** -0.5, make)
