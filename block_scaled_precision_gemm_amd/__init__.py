@@ -639,11 +639,14 @@ def _f8_matrix(t, rows: int, cols: int, dtypes, what: str) -> int:
 
 
 def _f8_weights(checks, f32) -> None:
+    """checks: name, codes, scales, how many of each there are, and how many in a row of each."""
     kinds = _f8_types()[2]
-    for name, w, s, nw, ns in checks:
-        if w.dtype not in kinds or w.numel() != nw or not w.is_contiguous() or s.dtype != f32 or s.numel() != ns or not s.is_contiguous():
-            raise ValueError(f"{name} must be {nw} contiguous E4M3 codes or bytes with {ns} contiguous float32 scales, got "
-                             f"{w.dtype} {tuple(w.shape)} and {s.dtype} {tuple(s.shape)}")
+    for name, w, s, nw, ns, row, s_row in checks:
+        # (beside the documented shapes: any split of the rows, and everything in one dimension)
+        if (w.dtype not in kinds or w.numel() != nw or not w.is_contiguous() or (w.dim() > 1 and w.size(-1) != row)
+                or s.dtype != f32 or s.numel() != ns or not s.is_contiguous() or (s.dim() > 1 and s.size(-1) != s_row)):
+            raise ValueError(f"{name} must be {nw // row} contiguous rows of {row} E4M3 codes or bytes with {ns // s_row} contiguous "
+                             f"rows of {s_row} float32 scales, got {w.dtype} {tuple(w.shape)} and {s.dtype} {tuple(s.shape)}")
 
 
 def f8_quantize(x, codes, scales, stream=None) -> None:
@@ -672,13 +675,13 @@ class F8Plan:
         _check(lib.bsg_f8_plan_create(ctypes.byref(prob), ctypes.byref(h)))
         self._h = h
         self._dtypes, (self._f32, _) = _dtypes(dtype), _f32_i32()
-        self._nw, self._ns = n * k, _f8_blocks(n) * _f8_blocks(k)
+        self._weights = n * k, _f8_blocks(n) * _f8_blocks(k), k, _f8_blocks(k)
 
     def run(self, x, x_scales, w, w_scales, out, bias=None, stream=None) -> None:
         """out [tokens][n] = x w^T (+ bias).  x, x_scales: as f8_quantize writes them; w: codes [n][k], w_scales: float32
         [blocks of n][blocks of k]; bias: float32 [n], where the plan has one.  x and out may be strided by rows."""
         tokens = x.shape[0]
-        _f8_weights((("w", w, w_scales, self._nw, self._ns),), self._f32)
+        _f8_weights((("w", w, w_scales, *self._weights),), self._f32)
         if self.bias and (bias is None or bias.dtype != self._f32 or bias.shape != (self.n,) or not bias.is_contiguous()):
             raise ValueError(f"the plan needs a contiguous float32 bias [{self.n}]")
         rows = F8Rows(x.data_ptr(), x_scales.data_ptr(), _f8_rows(x, tokens, self.k, "x"),
@@ -723,13 +726,14 @@ class F8FFNPlan:
         _check(lib.bsg_f8_ffn_plan_create(ctypes.byref(prob), ctypes.byref(h)))
         self._h = h
         self._dtypes, (self._f32, _) = _dtypes(dtype), _f32_i32()
-        self._n13, self._n2, self._ns = 2 * inter * hidden, inter * hidden, _f8_blocks(inter) * _f8_blocks(hidden)
+        n, ns = inter * hidden, _f8_blocks(inter) * _f8_blocks(hidden)
+        self._w13, self._w2 = (2 * n, 2 * ns, hidden, _f8_blocks(hidden)), (n, ns, inter, _f8_blocks(inter))
 
     def run(self, x, w13, s13, w2, s2, out, stream=None) -> None:
         """x, out: [tokens][hidden] (row-strided views are fine); w13: codes [2 inter][hidden], gate's rows, then up's, s13:
         float32 [2][blocks of inter][blocks of hidden]; w2: codes [hidden][inter], s2: [blocks of hidden][blocks of inter]."""
         tokens = x.shape[0]
-        _f8_weights((("w13", w13, s13, self._n13, 2 * self._ns), ("w2", w2, s2, self._n2, self._ns)), self._f32)
+        _f8_weights((("w13", w13, s13, *self._w13), ("w2", w2, s2, *self._w2)), self._f32)
         w = F8FFNWeights(ctypes.sizeof(F8FFNWeights), 0, w13.data_ptr(), s13.data_ptr(), w2.data_ptr(), s2.data_ptr())
         _check(self._lib.bsg_f8_ffn_run(self._h, tokens, x.data_ptr(), _f8_matrix(x, tokens, self.hidden, self._dtypes, "x"),
                                         ctypes.byref(w), out.data_ptr(),

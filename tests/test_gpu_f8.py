@@ -460,6 +460,30 @@ def test_what_the_binding_and_the_plans_refuse():
     torch.cuda.synchronize()
 
 
+def test_weights_laid_out_the_other_way_are_refused():
+    t, n, k = 6, 272, 144
+    x, sx = torch.zeros(t, k, dtype=torch.uint8, device="cuda"), torch.ones(bsg.f8_scales_shape(t, k), device="cuda")
+    w, sw = torch.zeros(n, k, dtype=torch.uint8, device="cuda"), torch.ones(3, 2, device="cuda")
+    out = torch.zeros(t, n, dtype=torch.bfloat16, device="cuda")
+    with bsg.F8Plan(n, k, t) as plan:
+        for good in ((w, sw), (w.view(2, n // 2, k), sw), (w.flatten(), sw.flatten())):
+            plan.run(x, sx, *good, out)
+        for bad in ((w.view(k, n), sw), (w.t().contiguous(), sw), (w, sw.t().contiguous()), (w, sw.view(6, 1))):
+            with pytest.raises(ValueError):
+                plan.run(x, sx, *bad, out)
+    h = torch.zeros(t, k, dtype=torch.bfloat16, device="cuda")
+    w13, s13 = torch.zeros(2 * n, k, dtype=torch.uint8, device="cuda"), torch.ones(2, 3, 2, device="cuda")
+    w2, s2 = torch.zeros(k, n, dtype=torch.uint8, device="cuda"), torch.ones(2, 3, device="cuda")
+    with bsg.F8FFNPlan(k, n, t) as ffn:
+        ffn.run(h, w13, s13, w2, s2, h.clone())
+        ffn.run(h, w13.view(2, n, k), s13.view(6, 2), w2, s2, h.clone())
+        for bad in ((w13.view(k, 2 * n), s13, w2, s2), (w13, s13.transpose(1, 2).contiguous(), w2, s2),
+                    (w13, s13, w2.view(n, k), s2), (w13, s13, w2, s2.view(3, 2))):
+            with pytest.raises(ValueError):
+                ffn.run(h, *bad, h.clone())
+    torch.cuda.synchronize()
+
+
 @pytest.mark.parametrize("other", [torch.float8_e5m2, torch.bool])
 def test_one_byte_types_that_are_no_codes_are_refused(other):
     x, w = torch.zeros(4, 32, dtype=torch.uint8, device="cuda"), torch.zeros(16, 32, dtype=torch.uint8, device="cuda")
