@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 import struct
 
@@ -638,15 +639,18 @@ def _f8_matrix(t, rows: int, cols: int, dtypes, what: str) -> int:
     return t.stride(0) if rows > 1 else cols
 
 
+def _f8_lies_as(t, shape) -> bool:
+    """Whether a contiguous tensor lies as one of `shape` does: the shape itself, any split of the rows, or one dimension."""
+    return t.shape == shape or (t.numel() == math.prod(shape) and (t.dim() < 2 or t.shape[-1] == shape[-1]))
+
+
 def _f8_weights(checks, f32) -> None:
-    """checks: name, codes, scales, how many of each there are, and how many in a row of each."""
     kinds = _f8_types()[2]
-    for name, w, s, nw, ns, row, s_row in checks:
-        # (beside the documented shapes: any split of the rows, and everything in one dimension)
-        if (w.dtype not in kinds or w.numel() != nw or not w.is_contiguous() or (w.dim() > 1 and w.size(-1) != row)
-                or s.dtype != f32 or s.numel() != ns or not s.is_contiguous() or (s.dim() > 1 and s.size(-1) != s_row)):
-            raise ValueError(f"{name} must be {nw // row} contiguous rows of {row} E4M3 codes or bytes with {ns // s_row} contiguous "
-                             f"rows of {s_row} float32 scales, got {w.dtype} {tuple(w.shape)} and {s.dtype} {tuple(s.shape)}")
+    for name, w, s, w_shape, s_shape in checks:
+        if not (w.dtype in kinds and _f8_lies_as(w, w_shape) and w.is_contiguous()
+                and s.dtype == f32 and _f8_lies_as(s, s_shape) and s.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous E4M3 codes or bytes {w_shape} with contiguous float32 scales {s_shape}, got "
+                             f"{w.dtype} {tuple(w.shape)} and {s.dtype} {tuple(s.shape)}")
 
 
 def f8_quantize(x, codes, scales, stream=None) -> None:
@@ -675,7 +679,7 @@ class F8Plan:
         _check(lib.bsg_f8_plan_create(ctypes.byref(prob), ctypes.byref(h)))
         self._h = h
         self._dtypes, (self._f32, _) = _dtypes(dtype), _f32_i32()
-        self._weights = n * k, _f8_blocks(n) * _f8_blocks(k), k, _f8_blocks(k)
+        self._weights = (n, k), (_f8_blocks(n), _f8_blocks(k))
 
     def run(self, x, x_scales, w, w_scales, out, bias=None, stream=None) -> None:
         """out [tokens][n] = x w^T (+ bias).  x, x_scales: as f8_quantize writes them; w: codes [n][k], w_scales: float32
@@ -726,8 +730,8 @@ class F8FFNPlan:
         _check(lib.bsg_f8_ffn_plan_create(ctypes.byref(prob), ctypes.byref(h)))
         self._h = h
         self._dtypes, (self._f32, _) = _dtypes(dtype), _f32_i32()
-        n, ns = inter * hidden, _f8_blocks(inter) * _f8_blocks(hidden)
-        self._w13, self._w2 = (2 * n, 2 * ns, hidden, _f8_blocks(hidden)), (n, ns, inter, _f8_blocks(inter))
+        bh, bi = _f8_blocks(hidden), _f8_blocks(inter)
+        self._w13, self._w2 = ((2 * inter, hidden), (2, bi, bh)), ((hidden, inter), (bh, bi))
 
     def run(self, x, w13, s13, w2, s2, out, stream=None) -> None:
         """x, out: [tokens][hidden] (row-strided views are fine); w13: codes [2 inter][hidden], gate's rows, then up's, s13:

@@ -94,15 +94,15 @@ N, K = 272, 144  # (blocks: 3 and 2)
 
 @pytest.mark.parametrize("w,s", [((N, K), (3, 2)), ((2, N // 2, K), (3, 2)), ((N * K,), (6,)), ((N * K,), (3, 2)), ((N, K), (3, 1, 2))])
 def test_weights_as_they_lie(w, s):
-    bsg._f8_weights((("w", torch.zeros(w, dtype=torch.uint8), torch.ones(s), N * K, 6, K, 2),), torch.float32)
+    bsg._f8_weights((("w", torch.zeros(w, dtype=torch.uint8), torch.ones(s), (N, K), (3, 2)),), torch.float32)
 
 
 @pytest.mark.parametrize("w,s", [((K, N), (3, 2)), ((N, K), (2, 3)), ((N, K // 2, 2), (3, 2)), ((N, K), (6, 1)), ((1, N * K), (3, 2)),
                                  ((N, K), (1, 6)), ((N, K), (3, 3)), ((N, K + 16), (3, 2))])
 def test_weights_of_another_layout_are_refused(w, s):
     # a contiguous [k][n] matrix has as many codes as [n][k], and would be multiplied as other weights
-    with pytest.raises(ValueError, match="rows of 144 E4M3 codes"):
-        bsg._f8_weights((("w", torch.zeros(w, dtype=torch.uint8), torch.ones(s), N * K, 6, K, 2),), torch.float32)
+    with pytest.raises(ValueError, match="codes or bytes .272, 144."):
+        bsg._f8_weights((("w", torch.zeros(w, dtype=torch.uint8), torch.ones(s), (N, K), (3, 2)),), torch.float32)
 
 
 # ------------------------------------------------------------------------------------------------ reference
