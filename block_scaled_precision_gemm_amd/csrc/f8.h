@@ -46,9 +46,8 @@ hipError_t f8_quantize_launch(Src src, int64_t rows, int64_t cols, const void* x
 constexpr int kF8OneTile = 16;
 hipError_t f8_few_launch(const F8Args& a, Src src, bool gated, int dtype, hipStream_t stream);
 
-// Any number of tokens, as codes.  Gated results are codes with scales, of up to kF8WideTokens tokens by products of widened
-// codes.
-constexpr int kF8WideTokens = 64;
+// Any number of tokens, as codes.  Gated results are codes with scales, of up to kF8WideTokens tokens (f8_cut.h) by products of
+// widened codes.
 hipError_t f8_tiled_launch(const F8Args& a, bool gated, int dtype, int cus, hipStream_t stream);
 // Its workspace for calls of up to max_tokens: parts, then counters.
 void f8_workspace(int64_t max_tokens, int cus, uint64_t* part_bytes, uint64_t* counter_bytes);

@@ -27,6 +27,7 @@
 
 #include "epilogue.h"
 #include "f8_codec.h"
+#include "f8_cut.h"
 #include "handoff.h"
 
 namespace bsg {
@@ -343,83 +344,39 @@ __global__ __launch_bounds__(64 * WN * WT, WN* WT* PER_CU / 4) void tiled_kernel
   }
 }
 
-// A kernel's way to do a call, and what it costs, in microseconds.
-struct Cut {
-  int64_t tiles, splits;
-  double cost;
-};
-
-// What a shape of tile takes: to begin and end, a step with one workgroup on a CU and with PER_CU, and joining parts
-// (JOIN + s JOIN_EACH).  Measured with 61 to 2048 tokens, n and k of 512 to 8192.
-struct Times {
-  double begin, step_alone, step_full, join, join_each;
-};
-constexpr Times kT64x32 = {3.4, 0.25, 0.42, 1.4, 0.5}, kT64x64 = {3.5, 0.33, 0.58, 1.6, 0.8}, kT128x64 = {4.1, 0.43, 0.73, 1.0, 1.15},
-                kT128x128 = {4.8, 0.62, 0.62, 1.8, 1.4};
-constexpr Times kG256x32 = {4.5, 0.6, 0.6, 1.2, 0.8}, kG256x64Wide = {5.0, 1.0, 1.0, 1.5, 1.2}, kG256x64 = {5.0, 0.78, 0.78, 1.5, 1.2},
-                kG256x128 = {6.0, 1.05, 1.05, 2.5, 2.5};
-constexpr double kBytesPerUs = 4.8e6;  // of weights that come from memory
-
-// The number of parts of K that takes the least time: at least four blocks a part, and all parts' workgroups run at once.
-template <int BN, int BT, int PER_CU, bool GATED>
-Cut cut_of(const F8Args& a, int cus, const Times& t) {
-  constexpr int BH = BN / (GATED ? 2 : 1);
-  Cut best = {(int64_t)((a.tokens + BT - 1) / BT) * ((a.n + BH - 1) / BH), 1, 0};
-  const double memory = (GATED ? 2.0 : 1.0) * a.n * a.k / kBytesPerUs;
-  for (int64_t s = 1; s == 1 || (s <= a.kb / 4 && best.tiles * s <= (int64_t)cus * PER_CU); ++s) {
-    const int64_t wgs = best.tiles * s, per_cu = wgs >= (int64_t)cus * PER_CU ? PER_CU : (wgs + cus - 1) / cus;
-    const int64_t rounds = (wgs + (int64_t)cus * PER_CU - 1) / ((int64_t)cus * PER_CU);
-    const double step = PER_CU == 1 ? t.step_full : t.step_alone + (t.step_full - t.step_alone) * (per_cu - 1) / (PER_CU - 1);
-    const double work = (double)(rounds * ((a.kb + s - 1) / s)) * step;
-    const double cost = t.begin + (work > memory ? work : memory) + (s > 1 ? t.join + s * t.join_each : 0);
-    if (s == 1 || cost < best.cost) {
-      best.cost = cost;
-      best.splits = s;
-    }
-  }
-  return best;
-}
-
-// The same of the kernel for many tokens (f8_pp.hip): a step takes longer where all CUs work at once.
-double pp_cost(const F8Args& a, bool gated, int cus) {
-  const int64_t tiles = (int64_t)((a.tokens + 255) / 256) * ((a.n + (gated ? 127 : 255)) / (gated ? 128 : 256));
-  const double busy = tiles >= cus ? 1.0 : (double)tiles / cus;
-  return 8 + (double)((tiles + cus - 1) / cus * a.kb) * (1.15 + (busy > 0.5 ? (busy - 0.5) * 1.1 : 0.0));
-}
-
-template <int BN, int BT, int WN, int WT, int STAGES, int PER_CU, bool GATED, bool WIDE, Out O>
-hipError_t launch(F8Args a, const Cut& cut, hipStream_t stream) {
+template <F8Way WAY, int WN, int WT, int STAGES, bool WIDE, Out O>
+hipError_t launch(F8Args a, const F8Cut& cut, hipStream_t stream) {
+  constexpr F8Shape t = f8_shape(WAY);
   a.splits = (int)cut.splits;
   void* argv[] = {&a};
-  return hipLaunchKernel((const void*)&tiled_kernel<BN, BT, WN, WT, STAGES, PER_CU, GATED, WIDE, O>,
+  return hipLaunchKernel((const void*)&tiled_kernel<t.rows, t.tokens, WN, WT, STAGES, t.per_cu, t.gated, WIDE, O>,
                          dim3((unsigned)(cut.tiles * cut.splits)), dim3(64 * WN * WT), argv, 0, stream);
 }
 
 template <Out O>
-hipError_t plain(const F8Args& a, int cus, hipStream_t stream) {
-  if (a.tokens <= 32) return launch<64, 32, 2, 2, 4, 3, false, false, O>(a, cut_of<64, 32, 3, false>(a, cus, kT64x32), stream);
-  const Cut s = cut_of<64, 64, 3, false>(a, cus, kT64x64), m = cut_of<128, 64, 2, false>(a, cus, kT128x64);
-  const Cut l = cut_of<128, 128, 1, false>(a, cus, kT128x128);
-  const double least = s.cost < m.cost ? (s.cost < l.cost ? s.cost : l.cost) : (m.cost < l.cost ? m.cost : l.cost);
-  if (pp_cost(a, false, cus) < least) return f8_pp_launch(a, false, O == Out::F16, cus, stream);
-  if (l.cost == least) return launch<128, 128, 2, 4, 4, 1, false, false, O>(a, l, stream);
-  if (m.cost == least) return launch<128, 64, 4, 1, 3, 2, false, false, O>(a, m, stream);
-  return launch<64, 64, 2, 2, 3, 3, false, false, O>(a, s, stream);
+hipError_t plain(const F8Args& a, const F8Cut& cut, hipStream_t stream) {
+  switch (cut.way) {
+    case F8Way::T64x32: return launch<F8Way::T64x32, 2, 2, 4, false, O>(a, cut, stream);
+    case F8Way::T64x64: return launch<F8Way::T64x64, 2, 2, 3, false, O>(a, cut, stream);
+    case F8Way::T128x64: return launch<F8Way::T128x64, 4, 1, 3, false, O>(a, cut, stream);
+    default: return launch<F8Way::T128x128, 2, 4, 4, false, O>(a, cut, stream);
+  }
 }
 
 }  // namespace
 
 hipError_t f8_tiled_launch(const F8Args& a, bool gated, int dtype, int cus, hipStream_t stream) {
-  if (!gated) return dtype ? plain<Out::F16>(a, cus, stream) : plain<Out::BF16>(a, cus, stream);
-  constexpr Out O = Out::BF16;  // (codes come out)
-  if (a.tokens <= 32) return launch<256, 32, 4, 1, 4, 1, true, true, O>(a, cut_of<256, 32, 1, true>(a, cus, kG256x32), stream);
-  if (a.tokens <= kF8WideTokens)
-    return launch<256, 64, 4, 2, 3, 1, true, true, O>(a, cut_of<256, 64, 1, true>(a, cus, kG256x64Wide), stream);
-  const Cut s = cut_of<256, 64, 1, true>(a, cus, kG256x64), l = cut_of<256, 128, 1, true>(a, cus, kG256x128);
-  const double least = s.cost < l.cost ? s.cost : l.cost;
-  if (pp_cost(a, true, cus) < least) return f8_pp_launch(a, true, dtype, cus, stream);
-  if (l.cost == least) return launch<256, 128, 4, 2, 3, 1, true, false, O>(a, l, stream);
-  return launch<256, 64, 4, 2, 3, 1, true, false, O>(a, s, stream);
+  const F8Cut cut = f8_cut(gated, a.tokens, a.n, a.k, cus);
+  constexpr Out C = Out::BF16;  // (gated results are codes)
+  switch (cut.way) {
+    case F8Way::T256x256:
+    case F8Way::G256x256: return f8_pp_launch(a, gated, dtype, cus, stream);
+    case F8Way::G256x32Wide: return launch<F8Way::G256x32Wide, 4, 1, 4, true, C>(a, cut, stream);
+    case F8Way::G256x64Wide: return launch<F8Way::G256x64Wide, 4, 2, 3, true, C>(a, cut, stream);
+    case F8Way::G256x64: return launch<F8Way::G256x64, 4, 2, 3, false, C>(a, cut, stream);
+    case F8Way::G256x128: return launch<F8Way::G256x128, 4, 2, 3, false, C>(a, cut, stream);
+    default: return dtype ? plain<Out::F16>(a, cut, stream) : plain<Out::BF16>(a, cut, stream);
+  }
 }
 
 void f8_workspace(int64_t max_tokens, int cus, uint64_t* part_bytes, uint64_t* counter_bytes) {

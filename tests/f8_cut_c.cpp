@@ -1,0 +1,13 @@
+// The choice of csrc/f8_cut.h for tests, built for the host.
+#include "f8_cut.h"
+
+extern "C" {
+int cut(int gated, int64_t tokens, int64_t n, int64_t k, int cus, int64_t out[3], double* cost) {
+  const bsg::F8Cut c = bsg::f8_cut(gated, tokens, n, k, cus);
+  out[0] = (int)c.way;
+  out[1] = c.tiles;
+  out[2] = c.splits;
+  *cost = c.cost;
+  return 0;
+}
+}

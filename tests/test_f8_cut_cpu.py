@@ -1,0 +1,72 @@
+"""Which kernel takes an E4M3 product and in how many parts (csrc/f8_cut.h), built for the host."""
+import ctypes
+import os
+import random
+import shutil
+import subprocess
+
+import pytest
+
+import f8_cases
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+CSRC = os.path.join(os.path.dirname(HERE), "block_scaled_precision_gemm_amd", "csrc")
+PER_CU = {"T64x32": 3, "T64x64": 3, "T128x64": 2, "T128x128": 1}  # workgroups that run on one CU; others: 1
+SHAPE = {w: tuple(int(n) for n in w[1:].removesuffix("Wide").split("x")) for w in f8_cases.WAYS}
+
+
+@pytest.fixture(scope="module")
+def cut(tmp_path_factory):
+    if not shutil.which("g++"):
+        pytest.skip("no g++")
+    lib, i64 = str(tmp_path_factory.mktemp("cut") / "cut.so"), ctypes.c_int64
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-shared", "-fPIC", f"-I{CSRC}", os.path.join(HERE, "f8_cut_c.cpp"), "-o", lib],
+                   check=True, timeout=120)
+    lib = ctypes.CDLL(lib)
+    lib.cut.argtypes = [ctypes.c_int, i64, i64, i64, ctypes.c_int, i64 * 3, ctypes.POINTER(ctypes.c_double)]
+
+    def choose(gated, tokens, n, k, cus=f8_cases.CUS):
+        out, cost = (i64 * 3)(), ctypes.c_double()
+        lib.cut(gated, tokens, n, k, cus, out, ctypes.byref(cost))
+        return f8_cases.WAYS[out[0]], out[1], out[2], cost.value
+    return choose
+
+
+def test_the_cases_reach_what_they_are_for(cut):
+    for gated, cases in ((0, f8_cases.PRODUCTS), (1, f8_cases.GATED)):
+        for t, n, k, way, parts in cases:
+            assert cut(gated, t, n, k)[::2] == (way, parts), (t, n, k)
+    ways = {c[3] for c in f8_cases.PRODUCTS + f8_cases.GATED}
+    assert ways == set(f8_cases.WAYS)
+    for way in f8_cases.WAYS:  # each with parts, where it has them, and with weights' scales that are loaded again
+        mine = [c for c in f8_cases.PRODUCTS + f8_cases.GATED if c[3] == way]
+        assert any(-(-c[2] // 128) > 64 * c[4] for c in mine), way
+        assert way.endswith("256x256") or any(c[4] > 1 for c in mine), way
+    for way in ("T256x256", "G256x256"):
+        mine = [c for c in f8_cases.PRODUCTS + f8_cases.GATED if c[3] == way]
+        assert any(-(-c[0] // 256) * -(-c[1] // (256 if way[0] == "T" else 128)) > f8_cases.CUS for c in mine)
+        assert {-(-c[2] // 128) % 2 for c in mine} == {0, 1}
+    for t, inter, hidden in f8_cases.FEW_GATED:
+        assert t <= 16 and t * -(-max(inter, hidden) // 128) > 512
+
+
+def test_a_cut_fits_the_device_and_the_call(cut):
+    rng = random.Random(0)
+    for _ in range(5000):
+        gated, t = rng.randint(0, 1), rng.choice([17, 32, 33, 64, 65, rng.randint(17, 300), rng.randint(17, 20000)])
+        n, k, cus = 16 * rng.randint(1, 1000), 16 * rng.choice([1, rng.randint(1, 100), rng.randint(1, 16384)]), rng.choice([256, 64, 304])
+        way, tiles, parts, cost = cut(gated, t, n, k, cus)
+        rows, cols = SHAPE[way]
+        assert way[0] == "TG"[gated] and cost > 0
+        assert tiles == -(-t // cols) * -(-n // (rows // 2 if gated else rows))
+        # the workspace holds the parts of as many workgroups as run at once, and a part is worth a workgroup's start
+        assert parts == 1 or (not way.endswith("256x256") and tiles * parts <= cus * PER_CU.get(way, 1) and parts * 4 <= -(-k // 128))
+        # gate and up of up to 64 tokens are products of widened codes, of more they are not
+        assert not gated or way.endswith("Wide") == (t <= 64)
+        assert cols >= min(t, 32)
+
+
+def test_equal_costs_and_the_smallest_calls(cut):
+    assert cut(0, 17, 16, 16)[0] == "T64x32" and cut(0, 33, 16, 16)[0] == "T64x64"
+    assert cut(0, 1 << 24, 1 << 18, 1 << 18)[0] == "T256x256" and cut(1, 1 << 24, 1 << 18, 1 << 18)[0] == "G256x256"
+    assert cut(1, 17, 16, 16)[:3] == ("G256x32Wide", 1, 1)

@@ -1,0 +1,107 @@
+"""Every kernel of the E4M3 products on calls that reach all parts of its loops (f8_cases), on numbers of which no sum is
+rounded: codes of +-1 .. 1.875, and products of scales that are powers of two from 2^-2 to 2^2.  All sums then have steps of 2^-8,
+and random signs keep them below 2^15: 23 bits.  So outputs of products are the exact sums rounded once, whatever the kernel,
+the order and the parts."""
+import numpy as np
+import pytest
+import torch
+
+import block_scaled_precision_gemm_amd as bsg
+import f8_cases
+import f8_ref as ref
+from test_gpu_f8 import DT, check
+
+pytestmark = pytest.mark.gpu
+
+ONE = 7 << 3
+
+
+def generator(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def narrow(shape, g):
+    """Codes of +-1 .. 1.875."""
+    r = torch.randint(0, 16, shape, dtype=torch.uint8, device="cuda", generator=g)
+    return (r & 8) << 4 | ONE | r & 7
+
+
+def powers(shape, g, middle=0):
+    return torch.ldexp(torch.ones(shape, device="cuda"), torch.randint(middle - 1, middle + 2, shape, device="cuda", generator=g))
+
+
+def exact(x, sx, w, sw):
+    """The sums in 64 bits: x codes [t][k], sx [blocks][t or more], w codes [n][k], sw [blocks of n][blocks of k]."""
+    table = torch.from_numpy(ref.values(np.arange(256))).cuda()
+    out = torch.zeros(len(x), len(w), dtype=torch.float64, device="cuda")
+    for a in range(0, x.shape[1], 8192):
+        b = slice(a // 128, a // 128 + 64)
+        xs = sx[b, :len(x)].t().double().repeat_interleave(128, 1)[:, :x[:, a:a + 8192].shape[1]]
+        ws = sw[:, b].double().repeat_interleave(128, 0)[:len(w)].repeat_interleave(128, 1)[:, :xs.shape[1]]
+        out += (table[x[:, a:a + 8192].int()] * xs) @ (table[w[:, a:a + 8192].int()] * ws).t()
+    assert out.abs().max() < 2.0 ** 15  # with steps of 2^-8: 23 bits
+    return out
+
+
+def devices_cus():
+    return torch.cuda.get_device_properties(0).multi_processor_count
+
+
+@pytest.mark.parametrize("case", f8_cases.PRODUCTS + f8_cases.FEW_PRODUCTS, ids=str)
+def test_products_are_exact_sums(case):
+    t, n, k = case[:3]
+    dtype = "f16" if t % 2 == 0 else "bf16"
+    print("[f8] exact product", *case, dtype, flush=True)
+    assert devices_cus() == f8_cases.CUS, "the cases are for such a device"
+    g = generator(t + n + k)
+    x, sx, w, sw = narrow((t, k), g), powers((ref.blocks(k), (t + 3) // 4 * 4), g), narrow((n, k), g), powers((ref.blocks(n), ref.blocks(k)), g)
+    sx[:, t:] = float("nan")
+    want = exact(x, sx, w, sw).float().to(DT[dtype])
+    out = torch.full((t + 2, n), 7.0, dtype=DT[dtype], device="cuda")
+    with bsg.F8Plan(n, k, t, dtype=dtype) as plan:
+        for _ in range(2):
+            out[:t] = -7.0
+            plan.run(x, sx, w, sw, out[:t])
+            torch.cuda.synchronize()
+            wrong = (out[:t] != want).nonzero()
+            assert len(wrong) == 0, (len(wrong), wrong[:5].tolist())
+    assert (out[t:] == 7).all()
+
+
+@pytest.mark.parametrize("case", f8_cases.GATED + f8_cases.FEW_GATED, ids=str)
+def test_gate_and_up_are_exact_sums(case):
+    """The second product picks inner values, one for each output: out[j] is the quantised value at pick[j]."""
+    t, inter, hidden = case[:3]
+    dtype = "f16" if t % 2 == 0 else "bf16"
+    print("[f8] exact gate and up", *case, dtype, flush=True)
+    assert devices_cus() == f8_cases.CUS, "the cases are for such a device"
+    g = generator(t + inter + hidden)
+    bi, bh = ref.blocks(inter), ref.blocks(hidden)
+    x, w13 = narrow((t, hidden), g), narrow((2 * inter, hidden), g)
+    s13 = powers((2, bi, bh), g, -1 - round(np.log2(hidden) / 2))  # sums of about 1
+    pick = torch.randperm(inter, device="cuda", generator=g).repeat(-(-hidden // inter))[:hidden]
+    pick[:2] = torch.tensor([0, inter - 1], device="cuda")
+    w2 = torch.zeros((hidden, inter), dtype=torch.uint8, device="cuda")
+    w2[torch.arange(hidden, device="cuda"), pick] = ONE
+    s2 = torch.ones((bh, bi), device="cuda")
+    values = torch.from_numpy(ref.values(np.arange(256))).cuda()[x.int()]
+    out = torch.full((t + 1, hidden), 7.0, dtype=DT[dtype], device="cuda")
+    with bsg.F8FFNPlan(hidden, inter, t, dtype=dtype) as plan:
+        plan.run(values.to(DT[dtype]), w13, s13, w2, s2, out[:t])
+        torch.cuda.synchronize()
+        first = out.clone()
+        plan.run(values.to(DT[dtype]), w13, s13, w2, s2, out[:t])
+        torch.cuda.synchronize()
+        assert torch.equal(out.view(torch.int16), first.view(torch.int16)), "not deterministic"
+    assert (out[t:] == 7).all()
+    # tokens at the tiles' edges and every 13th (the reference's bounds take a while)
+    rows = np.arange(t) if t <= 128 else np.unique(np.concatenate([np.arange(0, t, 13), np.arange(255, t, 256), np.arange(256, t, 256), [t - 1]]))
+    ones = torch.ones((bh, len(rows)), device="cuda")  # (x itself: its scales are powers of two, its codes narrow)
+    gate, up = (exact(x[torch.from_numpy(rows).cuda()], ones, w, s).cpu().numpy() for w, s in zip(w13.view(2, inter, hidden), s13))
+    h = ref.silu(gate) * up
+    # the exponential, the sum and the reciprocal of SiLU cost 8 roundings and the exponent's own, |gate| of them, the products two
+    d = np.abs(h) * (10 + np.abs(gate)) * ref.U32 + 1e-38
+    held, off = ref.row_values(*ref.quantize(h)), ref._changes(h, d)
+    at = pick.cpu().numpy()
+    check(out[:t].double().cpu().numpy()[rows], held[:, at], off[:, at], dtype, case)
+    assert np.median(off) == 0  # nearly every inner value has one possible code
