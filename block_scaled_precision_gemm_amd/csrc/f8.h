@@ -49,8 +49,6 @@ hipError_t f8_few_launch(const F8Args& a, Src src, bool gated, int dtype, hipStr
 // Any number of tokens, as codes.  Gated results are codes with scales, of up to kF8WideTokens tokens (f8_cut.h) by products of
 // widened codes.
 hipError_t f8_tiled_launch(const F8Args& a, bool gated, int dtype, int cus, hipStream_t stream);
-// Its workspace for calls of up to max_tokens: parts, then counters.
-void f8_workspace(int64_t max_tokens, int cus, uint64_t* part_bytes, uint64_t* counter_bytes);
 
 // The same, in tiles of 256 x 256 (gated: 128 outputs).
 hipError_t f8_pp_launch(const F8Args& a, bool gated, int dtype, int cus, hipStream_t stream);

@@ -7,6 +7,7 @@
 #include <new>
 
 #include "f8.h"
+#include "f8_cut.h"
 #include "plan.h"
 
 struct bsg_f8_plan_s {
@@ -160,8 +161,8 @@ bsg_status bsg_f8_plan_create(const bsg_f8_problem* problem, bsg_f8_plan* out_pl
   plan->cus = cus;
   plan->dtype = problem->dtype == BSG_OUT_F16;
   plan->log_level = log_level();
-  uint64_t part = 0, counters = 0;
-  bsg::f8_workspace(problem->max_tokens, cus, &part, &counters);
+  const bsg::F8Parts parts = bsg::f8_parts(false, problem->max_tokens, problem->n, problem->k, cus);
+  const uint64_t part = 4 * (uint64_t)parts.floats, counters = 4 * (uint64_t)parts.counters;
   plan->workspace_bytes = part + counters;
   if (plan->workspace_bytes) {
     st = bsg::device_alloc(dev, plan->workspace_bytes, &plan->workspace);
@@ -274,8 +275,11 @@ bsg_status bsg_f8_ffn_plan_create(const bsg_f8_ffn_problem* problem, bsg_f8_ffn_
   plan->dtype = problem->dtype == BSG_OUT_F16;
   plan->log_level = log_level();
   const int64_t t = problem->max_tokens, few = t < bsg::kF8OneTile ? t : bsg::kF8OneTile;
-  uint64_t at = 0, part_bytes = 0, counter_bytes = 0;
-  bsg::f8_workspace(t, cus, &part_bytes, &counter_bytes);
+  const bsg::F8Parts up = bsg::f8_parts(true, t, problem->inter, problem->hidden, cus);
+  const bsg::F8Parts down = bsg::f8_parts(false, t, problem->hidden, problem->inter, cus);
+  const uint64_t part_bytes = 4 * (uint64_t)(up.floats > down.floats ? up.floats : down.floats);
+  const uint64_t counter_bytes = 4 * (uint64_t)(up.counters > down.counters ? up.counters : down.counters);
+  uint64_t at = 0;
   auto take = [&](uint64_t bytes) {
     const uint64_t here = at;
     at += (bytes + 255) / 256 * 256;

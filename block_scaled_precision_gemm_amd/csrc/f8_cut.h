@@ -80,4 +80,28 @@ inline F8Cut f8_cut(bool gated, int64_t tokens, int64_t n, int64_t k, int cus) {
   return best;
 }
 
+// What calls of up to max_tokens may need for parts of K, in floats, and how many tiles they count.
+struct F8Parts {
+  int64_t floats, counters;
+};
+inline F8Parts f8_parts(bool gated, int64_t max_tokens, int64_t n, int64_t k, int cus) {
+  F8Parts most = {0, 0};
+  if (max_tokens <= 16) return most;
+  const int64_t pieces = (k + 127) / 128 / 4;
+  const int first = gated ? (int)F8Way::G256x32Wide : (int)F8Way::T64x32, last = gated ? (int)F8Way::G256x128 : (int)F8Way::T128x128;
+  for (int way = first; way <= last; ++way) {
+    const F8Shape& t = kF8Shapes[way];
+    const int64_t limit = way == first ? 32 : way == (int)F8Way::G256x64Wide ? kF8WideTokens : max_tokens;
+    for (int64_t tokens = 1; tokens <= max_tokens && tokens <= limit; tokens += t.tokens) {  // row after row of tiles
+      const int64_t tiles = f8_tiles(t.rows, t.tokens, gated, tokens, n), fit = (int64_t)cus * t.per_cu / tiles;
+      const int64_t splits = fit < pieces ? fit : pieces;
+      if (splits < 2) break;  // (more tiles have no more)
+      const int64_t floats = tiles * splits * t.rows * t.tokens;
+      if (floats > most.floats) most.floats = floats;
+      if (tiles > most.counters) most.counters = tiles;
+    }
+  }
+  return most;
+}
+
 }  // namespace bsg

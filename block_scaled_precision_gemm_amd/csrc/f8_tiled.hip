@@ -379,10 +379,4 @@ hipError_t f8_tiled_launch(const F8Args& a, bool gated, int dtype, int cus, hipS
   }
 }
 
-void f8_workspace(int64_t max_tokens, int cus, uint64_t* part_bytes, uint64_t* counter_bytes) {
-  // per CU at most three workgroups of 64 x 64, two of 128 x 64, or one of 256 x 128
-  *part_bytes = max_tokens > kF8OneTile ? (uint64_t)cus * (256 * 128 * 4) : 0;
-  *counter_bytes = max_tokens > kF8OneTile ? (uint64_t)cus * 3 * 4 : 0;
-}
-
 }  // namespace bsg

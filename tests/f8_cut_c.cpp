@@ -10,4 +10,9 @@ int cut(int gated, int64_t tokens, int64_t n, int64_t k, int cus, int64_t out[3]
   *cost = c.cost;
   return 0;
 }
+void parts(int gated, int64_t max_tokens, int64_t n, int64_t k, int cus, int64_t out[2]) {
+  const bsg::F8Parts p = bsg::f8_parts(gated, max_tokens, n, k, cus);
+  out[0] = p.floats;
+  out[1] = p.counters;
+}
 }

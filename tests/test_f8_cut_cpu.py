@@ -29,6 +29,13 @@ def cut(tmp_path_factory):
         out, cost = (i64 * 3)(), ctypes.c_double()
         lib.cut(gated, tokens, n, k, cus, out, ctypes.byref(cost))
         return f8_cases.WAYS[out[0]], out[1], out[2], cost.value
+
+    def parts(gated, max_tokens, n, k, cus=f8_cases.CUS):
+        out = (i64 * 2)()
+        lib.parts(gated, max_tokens, n, k, cus, out)
+        return tuple(out)
+    lib.parts.argtypes = [ctypes.c_int, i64, i64, i64, ctypes.c_int, i64 * 2]
+    choose.parts = parts
     return choose
 
 
@@ -70,3 +77,25 @@ def test_equal_costs_and_the_smallest_calls(cut):
     assert cut(0, 17, 16, 16)[0] == "T64x32" and cut(0, 33, 16, 16)[0] == "T64x64"
     assert cut(0, 1 << 24, 1 << 18, 1 << 18)[0] == "T256x256" and cut(1, 1 << 24, 1 << 18, 1 << 18)[0] == "G256x256"
     assert cut(1, 17, 16, 16)[:3] == ("G256x32Wide", 1, 1)
+
+
+def test_a_workspace_holds_the_parts_of_every_call_and_little_more(cut):
+    rng = random.Random(1)
+    for _ in range(300):
+        gated, cus, most = rng.randint(0, 1), rng.choice([256, 64]), rng.choice([17, 33, 64, 65, 200, 5000])
+        n, k = 16 * rng.choice([rng.randint(1, 40), rng.randint(1, 1000)]), 16 * rng.choice([rng.randint(1, 63), rng.randint(64, 16384)])
+        floats, counters = cut.parts(gated, most, n, k, cus)
+        # never more than the workgroups that run at once have, and nothing where K cannot be split
+        assert floats <= cus * 256 * 128 and counters <= cus * 3 // 2
+        assert k > 7 * 128 or floats == counters == 0
+        for t in {17, most, *(rng.randint(17, most) for _ in range(40))}:
+            way, tiles, parts, _ = cut(gated, t, n, k, cus)
+            rows, cols = SHAPE[way]
+            assert parts == 1 or (tiles * parts * rows * cols <= floats and tiles <= counters), (gated, t, n, k, cus)
+
+
+def test_workspaces_of_some_plans(cut):
+    assert cut.parts(0, 16, 8192, 8192) == cut.parts(1, 16, 8192, 8192) == (0, 0)
+    assert cut.parts(0, 8192, 4096, 896) == (0, 0)                # seven blocks
+    assert cut.parts(0, 8192, 1 << 18, 8192) == (0, 0)            # more tiles than run at once
+    assert cut.parts(0, 64, 16, 1024) == (2 * 128 * 128, 1)       # one tile of 128 x 128 in two parts

@@ -105,3 +105,16 @@ def test_gate_and_up_are_exact_sums(case):
     at = pick.cpu().numpy()
     check(out[:t].double().cpu().numpy()[rows], held[:, at], off[:, at], dtype, case)
     assert np.median(off) == 0  # nearly every inner value has one possible code
+
+
+def test_workspaces_are_those_of_the_plans_sizes():
+    def bytes_of(plan):
+        with plan:
+            return plan.workspace_bytes()
+
+    assert bytes_of(bsg.F8Plan(4096, 896, 8192)) == 0             # seven blocks of K are not split
+    assert bytes_of(bsg.F8Plan(262144, 8192, 8192)) == 0          # nor is K where tiles alone fill the device
+    assert 0 < bytes_of(bsg.F8Plan(16, 1024, 64)) <= 2 * 128 * 128 * 4 + 64
+    assert bytes_of(bsg.F8Plan(8192, 8192, 8192)) <= f8_cases.CUS * (256 * 128 * 4 + 12)
+    small = bytes_of(bsg.F8FFNPlan(128, 128, 64))                 # codes, scales, inner values of 16 tokens
+    assert small <= 64 * (128 + 128) + 2 * 4 * 64 + 16 * 128 * 4 + 7 * 256
