@@ -621,8 +621,10 @@ hipError_t kv_attend_launch(const KvArgs& args, int dtype, int head_dim, int cus
 
 void kv_workspace(const bsg_kv_problem& p, int cus, size_t* part_floats, size_t* counters, size_t* group_counters) {
   const size_t slots = (size_t)cus * kWgPerCu * 2;
-  // the few-row kernel's parts, then the many-row kernel's of shared positions (others begin where the former do)
-  *part_floats = few_part_floats(p.head_dim, cus) + kv_rows_part_floats(p, cus);
+  // The few-row kernel's parts, then the many-row kernel's of shared positions; its others begin where the former do.  With
+  // a window no positions are shared.
+  const size_t few = few_part_floats(p.head_dim, cus), rows = kv_rows_part_floats(p, cus);
+  *part_floats = kept_window(p.window) > 0 ? (few > rows ? few : rows) : few + rows;
   *counters = slots + (size_t)p.max_tokens * p.q_heads;
   *group_counters = slots;
 }

@@ -246,3 +246,16 @@ def test_refused_counts(shared):
         with pytest.raises(bsg.BsgError) as e:
             plan.attend(batch, z, torch.zeros(9 * plan.page_bytes, dtype=torch.uint8, device="cuda"), z.clone(), shared=shared)
         assert e.value.status_name == "BSG_ERR_SHAPE"
+
+
+def test_plans_with_a_window_have_no_room_for_shared_parts():
+    """Positions are never shared under a window: such plans hold what either kernel needs, others both.  A window that no
+    context reaches is none."""
+    def bytes_of(**kw):
+        with bsg.KVPlan(32, 8, 128, 16, 64, 512, **kw) as plan:
+            return plan.info()["workspace_bytes"]
+
+    few, rows = 512 * 2 * 32 * (128 + 4) * 4, 2 * 256 * 256 * (128 + 2) * 4  # parts on 256 CUs
+    both, windowed = bytes_of(), bytes_of(window=1000)
+    assert both - windowed == few and rows <= windowed < both
+    assert bytes_of(window=(1 << 31) - 1) == both
