@@ -24,6 +24,7 @@ struct F8Args {
   float* part;
   int* arrived;          // one for each tile, zero between calls
   int splits;
+  int exact;             // (host) products of widened codes, however many tokens
 };
 
 // How token rows come: codes with scales, or values of 16 or 32 bits.

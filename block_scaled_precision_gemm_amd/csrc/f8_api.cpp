@@ -146,7 +146,7 @@ bsg_status bsg_f8_plan_create(const bsg_f8_problem* problem, bsg_f8_plan* out_pl
     set_error("bsg_f8_problem.struct_size is %u, expected %zu", problem->struct_size, sizeof(bsg_f8_problem));
     return BSG_ERR_ABI;
   }
-  bsg_status st = check_common(problem->dtype, problem->flags, BSG_F8_BIAS, "n", problem->n, "k", problem->k, problem->max_tokens);
+  bsg_status st = check_common(problem->dtype, problem->flags, BSG_F8_BIAS | BSG_F8_EXACT, "n", problem->n, "k", problem->k, problem->max_tokens);
   if (st != BSG_OK) return st;
   int dev = -1, cus = 0;
   if ((st = bsg::resolve_device(problem->device, &dev, &cus)) != BSG_OK) return st;
@@ -161,7 +161,7 @@ bsg_status bsg_f8_plan_create(const bsg_f8_problem* problem, bsg_f8_plan* out_pl
   plan->cus = cus;
   plan->dtype = problem->dtype == BSG_OUT_F16;
   plan->log_level = log_level();
-  const bsg::F8Parts parts = bsg::f8_parts(false, problem->max_tokens, problem->n, problem->k, cus);
+  const bsg::F8Parts parts = bsg::f8_parts(false, problem->flags & BSG_F8_EXACT, problem->max_tokens, problem->n, problem->k, cus);
   const uint64_t part = 4 * (uint64_t)parts.floats, counters = 4 * (uint64_t)parts.counters;
   plan->workspace_bytes = part + counters;
   if (plan->workspace_bytes) {
@@ -241,6 +241,7 @@ bsg_status bsg_f8_run(bsg_f8_plan plan, int64_t tokens, const bsg_f8_rows* x, co
   a.out_stride = out_stride;
   a.part = plan->part;
   a.arrived = plan->arrived;
+  a.exact = (p.flags & BSG_F8_EXACT) != 0;
   if (plan->log_level >= 2) fprintf(stderr, "bsg: f8 run tokens=%lld stream=%p\n", (long long)tokens, stream);
   const hipStream_t s = (hipStream_t)stream;
   return launched(tokens <= bsg::kF8OneTile ? bsg::f8_few_launch(a, bsg::Src::CODES, false, plan->dtype, s)
@@ -258,7 +259,7 @@ bsg_status bsg_f8_ffn_plan_create(const bsg_f8_ffn_problem* problem, bsg_f8_ffn_
     set_error("bsg_f8_ffn_problem.struct_size is %u, expected %zu", problem->struct_size, sizeof(bsg_f8_ffn_problem));
     return BSG_ERR_ABI;
   }
-  bsg_status st = check_common(problem->dtype, problem->flags, 0, "hidden", problem->hidden, "inter", problem->inter,
+  bsg_status st = check_common(problem->dtype, problem->flags, BSG_F8_EXACT, "hidden", problem->hidden, "inter", problem->inter,
                                problem->max_tokens);
   if (st != BSG_OK) return st;
   int dev = -1, cus = 0;
@@ -275,8 +276,9 @@ bsg_status bsg_f8_ffn_plan_create(const bsg_f8_ffn_problem* problem, bsg_f8_ffn_
   plan->dtype = problem->dtype == BSG_OUT_F16;
   plan->log_level = log_level();
   const int64_t t = problem->max_tokens, few = t < bsg::kF8OneTile ? t : bsg::kF8OneTile;
-  const bsg::F8Parts up = bsg::f8_parts(true, t, problem->inter, problem->hidden, cus);
-  const bsg::F8Parts down = bsg::f8_parts(false, t, problem->hidden, problem->inter, cus);
+  const bool exact = problem->flags & BSG_F8_EXACT;
+  const bsg::F8Parts up = bsg::f8_parts(true, exact, t, problem->inter, problem->hidden, cus);
+  const bsg::F8Parts down = bsg::f8_parts(false, exact, t, problem->hidden, problem->inter, cus);
   const uint64_t part_bytes = 4 * (uint64_t)(up.floats > down.floats ? up.floats : down.floats);
   const uint64_t counter_bytes = 4 * (uint64_t)(up.counters > down.counters ? up.counters : down.counters);
   uint64_t at = 0;
@@ -394,6 +396,7 @@ bsg_status bsg_f8_ffn_run(bsg_f8_ffn_plan plan, int64_t tokens, const void* x, i
   b.out_stride = out_stride;
   a.part = b.part = plan->part;
   a.arrived = b.arrived = plan->arrived;
+  a.exact = b.exact = (p.flags & BSG_F8_EXACT) != 0;
   hipError_t e = hipSuccess;
   if (tokens <= bsg::kF8OneTile) {  // both products quantise what they read
     a.x = (const uint8_t*)x;

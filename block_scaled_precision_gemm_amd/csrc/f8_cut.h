@@ -6,9 +6,12 @@
 
 namespace bsg {
 
-// The kernels' shapes of tiles: weight rows x tokens.  Gated ones hold gate's and up's rows of half as many outputs.  WIDE:
+// The kernels' shapes of tiles: weight rows x tokens.  Gated ones hold gate's and up's rows of half as many outputs.  Wide:
 // products of widened codes.
-enum class F8Way : int { T64x32, T64x64, T128x64, T128x128, G256x32Wide, G256x64Wide, G256x64, G256x128, T256x256, G256x256 };
+enum class F8Way : int {
+  T64x32, T64x64, T128x64, T128x128, G256x32Wide, G256x64Wide, G256x64, G256x128, T64x32Wide, T64x64Wide, T128x128Wide,
+  T256x256, G256x256
+};
 
 // What a shape of tile takes, in microseconds: to begin and end, a step with one workgroup on a CU and with per_cu, and joining
 // parts (join + s join_each).  Measured with 61 to 2048 tokens, n and k of 512 to 8192.
@@ -22,6 +25,8 @@ constexpr F8Shape kF8Shapes[] = {
     {128, 64, 2, false, 4.1, 0.43, 0.73, 1.0, 1.15},  {128, 128, 1, false, 4.8, 0.62, 0.62, 1.8, 1.4},
     {256, 32, 1, true, 4.5, 0.6, 0.6, 1.2, 0.8},      {256, 64, 1, true, 5.0, 1.0, 1.0, 1.5, 1.2},
     {256, 64, 1, true, 5.0, 0.78, 0.78, 1.5, 1.2},    {256, 128, 1, true, 6.0, 1.05, 1.05, 2.5, 2.5},
+    {64, 32, 3, false, 3.4, 0.40, 0.65, 1.4, 0.5},    {64, 64, 3, false, 3.5, 0.52, 0.95, 1.6, 0.8},
+    {128, 128, 1, false, 4.8, 1.15, 1.15, 1.8, 1.4},
 };
 constexpr const F8Shape& f8_shape(F8Way way) { return kF8Shapes[(int)way]; }  // (all but the last two)
 constexpr double kF8BytesPerUs = 4.8e6;  // of weights that come from memory
@@ -65,15 +70,19 @@ inline F8Cut f8_cut_large(bool gated, int64_t tokens, int64_t n, int64_t k, int 
           8 + (double)((tiles + cus - 1) / cus * kb) * (1.15 + (busy > 0.5 ? (busy - 0.5) * 1.1 : 0.0))};
 }
 
-// The way of a call of more than 16 tokens.
-inline F8Cut f8_cut(bool gated, int64_t tokens, int64_t n, int64_t k, int cus) {
+// The way of a call of more than 16 tokens.  exact: by products of widened codes, however many tokens.
+inline F8Cut f8_cut(bool gated, bool exact, int64_t tokens, int64_t n, int64_t k, int cus) {
   auto of = [&](F8Way way) { return f8_cut_of(way, tokens, n, k, cus); };
-  if (tokens <= 32) return of(gated ? F8Way::G256x32Wide : F8Way::T64x32);
-  if (gated && tokens <= kF8WideTokens) return of(F8Way::G256x64Wide);
-  F8Cut best = of(gated ? F8Way::G256x64 : F8Way::T64x64);
+  if (tokens <= 32) return of(gated ? F8Way::G256x32Wide : exact ? F8Way::T64x32Wide : F8Way::T64x32);
+  if (gated && (exact || tokens <= kF8WideTokens)) return of(F8Way::G256x64Wide);
+  F8Cut best = of(gated ? F8Way::G256x64 : exact ? F8Way::T64x64Wide : F8Way::T64x64);
   auto take = [&](const F8Cut& c, bool even) {  // (a larger tile also where it takes as long)
     if (c.cost < best.cost || (even && c.cost == best.cost)) best = c;
   };
+  if (exact) {
+    take(of(F8Way::T128x128Wide), true);
+    return best;
+  }
   if (!gated) take(of(F8Way::T128x64), true);
   take(of(gated ? F8Way::G256x128 : F8Way::T128x128), true);
   take(f8_cut_large(gated, tokens, n, k, cus), false);
@@ -84,14 +93,15 @@ inline F8Cut f8_cut(bool gated, int64_t tokens, int64_t n, int64_t k, int cus) {
 struct F8Parts {
   int64_t floats, counters;
 };
-inline F8Parts f8_parts(bool gated, int64_t max_tokens, int64_t n, int64_t k, int cus) {
+inline F8Parts f8_parts(bool gated, bool exact, int64_t max_tokens, int64_t n, int64_t k, int cus) {
   F8Parts most = {0, 0};
   if (max_tokens <= 16) return most;
   const int64_t pieces = (k + 127) / 128 / 4;
-  const int first = gated ? (int)F8Way::G256x32Wide : (int)F8Way::T64x32, last = gated ? (int)F8Way::G256x128 : (int)F8Way::T128x128;
-  for (int way = first; way <= last; ++way) {
+  const F8Way first = gated ? F8Way::G256x32Wide : exact ? F8Way::T64x32Wide : F8Way::T64x32;
+  const F8Way last = gated ? exact ? F8Way::G256x64Wide : F8Way::G256x128 : exact ? F8Way::T128x128Wide : F8Way::T128x128;
+  for (int way = (int)first; way <= (int)last; ++way) {
     const F8Shape& t = kF8Shapes[way];
-    const int64_t limit = way == first ? 32 : way == (int)F8Way::G256x64Wide ? kF8WideTokens : max_tokens;
+    const int64_t limit = way == (int)first ? 32 : way == (int)F8Way::G256x64Wide && !exact ? kF8WideTokens : max_tokens;
     for (int64_t tokens = 1; tokens <= max_tokens && tokens <= limit; tokens += t.tokens) {  // row after row of tiles
       const int64_t tiles = f8_tiles(t.rows, t.tokens, gated, tokens, n), fit = (int64_t)cus * t.per_cu / tiles;
       const int64_t splits = fit < pieces ? fit : pieces;

@@ -41,6 +41,13 @@ def test_a_feed_forward_plan_has_no_flags():
     assert create(bsg.F8FFNProblem, "bsg_f8_ffn_plan_create", FFN | dict(flags=1)) == "BSG_ERR_ABI"
 
 
+@pytest.mark.parametrize("flags", [3, 5, 8, 12, 1 << 31])
+def test_unknown_flags(flags):
+    if flags != 5:  # (5: a bias and exact products)
+        assert create(bsg.F8Problem, "bsg_f8_plan_create", PLAN | dict(flags=flags)) == "BSG_ERR_ABI"
+    assert create(bsg.F8FFNProblem, "bsg_f8_ffn_plan_create", FFN | dict(flags=flags)) == "BSG_ERR_ABI"
+
+
 GOOD = dict(dtype=1, rows=3, cols=144, x=4096, x_stride=144, codes=8192, codes_stride=144, scales=16384, scale_stride=4)
 
 

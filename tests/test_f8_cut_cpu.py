@@ -11,7 +11,7 @@ import f8_cases
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(os.path.dirname(HERE), "block_scaled_precision_gemm_amd", "csrc")
-PER_CU = {"T64x32": 3, "T64x64": 3, "T128x64": 2, "T128x128": 1}  # workgroups that run on one CU; others: 1
+PER_CU = {"T64x32": 3, "T64x64": 3, "T128x64": 2, "T64x32Wide": 3, "T64x64Wide": 3}  # workgroups that run on one CU; others: 1
 SHAPE = {w: tuple(int(n) for n in w[1:].removesuffix("Wide").split("x")) for w in f8_cases.WAYS}
 
 
@@ -40,13 +40,13 @@ def cut(tmp_path_factory):
 
 
 def test_the_cases_reach_what_they_are_for(cut):
-    for gated, cases in ((0, f8_cases.PRODUCTS), (1, f8_cases.GATED)):
+    for gated, cases in ((0, f8_cases.PRODUCTS), (1, f8_cases.GATED), (2, f8_cases.EXACT_PRODUCTS), (3, f8_cases.EXACT_GATED)):
         for t, n, k, way, parts in cases:
             assert cut(gated, t, n, k)[::2] == (way, parts), (t, n, k)
-    ways = {c[3] for c in f8_cases.PRODUCTS + f8_cases.GATED}
-    assert ways == set(f8_cases.WAYS)
+    everything = f8_cases.PRODUCTS + f8_cases.GATED + f8_cases.EXACT_PRODUCTS + f8_cases.EXACT_GATED
+    assert {c[3] for c in everything} == set(f8_cases.WAYS)
     for way in f8_cases.WAYS:  # each with parts, where it has them, and with weights' scales that are loaded again
-        mine = [c for c in f8_cases.PRODUCTS + f8_cases.GATED if c[3] == way]
+        mine = [c for c in everything if c[3] == way]
         assert any(-(-c[2] // 128) > 64 * c[4] for c in mine), way
         assert way.endswith("256x256") or any(c[4] > 1 for c in mine), way
     for way in ("T256x256", "G256x256"):
@@ -60,16 +60,16 @@ def test_the_cases_reach_what_they_are_for(cut):
 def test_a_cut_fits_the_device_and_the_call(cut):
     rng = random.Random(0)
     for _ in range(5000):
-        gated, t = rng.randint(0, 1), rng.choice([17, 32, 33, 64, 65, rng.randint(17, 300), rng.randint(17, 20000)])
+        gated, exact, t = rng.randint(0, 1), rng.randint(0, 1), rng.choice([17, 32, 33, 64, 65, rng.randint(17, 300), rng.randint(17, 20000)])
         n, k, cus = 16 * rng.randint(1, 1000), 16 * rng.choice([1, rng.randint(1, 100), rng.randint(1, 16384)]), rng.choice([256, 64, 304])
-        way, tiles, parts, cost = cut(gated, t, n, k, cus)
+        way, tiles, parts, cost = cut(gated + 2 * exact, t, n, k, cus)
         rows, cols = SHAPE[way]
         assert way[0] == "TG"[gated] and cost > 0
         assert tiles == -(-t // cols) * -(-n // (rows // 2 if gated else rows))
         # the workspace holds the parts of as many workgroups as run at once, and a part is worth a workgroup's start
         assert parts == 1 or (not way.endswith("256x256") and tiles * parts <= cus * PER_CU.get(way, 1) and parts * 4 <= -(-k // 128))
-        # gate and up of up to 64 tokens are products of widened codes, of more they are not
-        assert not gated or way.endswith("Wide") == (t <= 64)
+        # exact products are of widened codes, others in gate and up of up to 64 tokens
+        assert way.endswith("Wide") == bool(exact or (gated and t <= 64))
         assert cols >= min(t, 32)
 
 
@@ -82,7 +82,7 @@ def test_equal_costs_and_the_smallest_calls(cut):
 def test_a_workspace_holds_the_parts_of_every_call_and_little_more(cut):
     rng = random.Random(1)
     for _ in range(300):
-        gated, cus, most = rng.randint(0, 1), rng.choice([256, 64]), rng.choice([17, 33, 64, 65, 200, 5000])
+        gated, cus, most = rng.randint(0, 3), rng.choice([256, 64]), rng.choice([17, 33, 64, 65, 200, 5000])
         n, k = 16 * rng.choice([rng.randint(1, 40), rng.randint(1, 1000)]), 16 * rng.choice([rng.randint(1, 63), rng.randint(64, 16384)])
         floats, counters = cut.parts(gated, most, n, k, cus)
         # never more than the workgroups that run at once have, and nothing where K cannot be split
@@ -91,6 +91,7 @@ def test_a_workspace_holds_the_parts_of_every_call_and_little_more(cut):
         for t in {17, most, *(rng.randint(17, most) for _ in range(40))}:
             way, tiles, parts, _ = cut(gated, t, n, k, cus)
             rows, cols = SHAPE[way]
+            # (gated: 1, and 2 for exact products)
             assert parts == 1 or (tiles * parts * rows * cols <= floats and tiles <= counters), (gated, t, n, k, cus)
 
 

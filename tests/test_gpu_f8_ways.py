@@ -9,7 +9,7 @@ import torch
 import block_scaled_precision_gemm_amd as bsg
 import f8_cases
 import f8_ref as ref
-from test_gpu_f8 import DT, check
+from test_gpu_f8 import DT, activations, check, dev, ffn_weights, operands
 
 pytestmark = pytest.mark.gpu
 
@@ -49,6 +49,15 @@ def devices_cus():
 
 @pytest.mark.parametrize("case", f8_cases.PRODUCTS + f8_cases.FEW_PRODUCTS, ids=str)
 def test_products_are_exact_sums(case):
+    check_product(case, False)
+
+
+@pytest.mark.parametrize("case", f8_cases.EXACT_PRODUCTS + f8_cases.FEW_PRODUCTS, ids=str)
+def test_exact_products_are_exact_sums(case):
+    check_product(case, True)
+
+
+def check_product(case, of_exact_plan):
     t, n, k = case[:3]
     dtype = "f16" if t % 2 == 0 else "bf16"
     print("[f8] exact product", *case, dtype, flush=True)
@@ -58,7 +67,7 @@ def test_products_are_exact_sums(case):
     sx[:, t:] = float("nan")
     want = exact(x, sx, w, sw).float().to(DT[dtype])
     out = torch.full((t + 2, n), 7.0, dtype=DT[dtype], device="cuda")
-    with bsg.F8Plan(n, k, t, dtype=dtype) as plan:
+    with bsg.F8Plan(n, k, t, dtype=dtype, exact=of_exact_plan) as plan:
         for _ in range(2):
             out[:t] = -7.0
             plan.run(x, sx, w, sw, out[:t])
@@ -70,6 +79,15 @@ def test_products_are_exact_sums(case):
 
 @pytest.mark.parametrize("case", f8_cases.GATED + f8_cases.FEW_GATED, ids=str)
 def test_gate_and_up_are_exact_sums(case):
+    check_gated(case, False)
+
+
+@pytest.mark.parametrize("case", f8_cases.EXACT_GATED, ids=str)
+def test_exact_gate_and_up_are_exact_sums(case):
+    check_gated(case, True)
+
+
+def check_gated(case, of_exact_plan):
     """The second product picks inner values, one for each output: out[j] is the quantised value at pick[j]."""
     t, inter, hidden = case[:3]
     dtype = "f16" if t % 2 == 0 else "bf16"
@@ -86,7 +104,7 @@ def test_gate_and_up_are_exact_sums(case):
     s2 = torch.ones((bh, bi), device="cuda")
     values = torch.from_numpy(ref.values(np.arange(256))).cuda()[x.int()]
     out = torch.full((t + 1, hidden), 7.0, dtype=DT[dtype], device="cuda")
-    with bsg.F8FFNPlan(hidden, inter, t, dtype=dtype) as plan:
+    with bsg.F8FFNPlan(hidden, inter, t, dtype=dtype, exact=of_exact_plan) as plan:
         plan.run(values.to(DT[dtype]), w13, s13, w2, s2, out[:t])
         torch.cuda.synchronize()
         first = out.clone()
@@ -105,6 +123,60 @@ def test_gate_and_up_are_exact_sums(case):
     at = pick.cpu().numpy()
     check(out[:t].double().cpu().numpy()[rows], held[:, at], off[:, at], dtype, case)
     assert np.median(off) == 0  # nearly every inner value has one possible code
+
+
+@pytest.mark.parametrize("dtype,bias", [("bf16", False), ("f16", True)])
+@pytest.mark.parametrize("t,n,k", [(9, 144, 400), (17, 144, 1040), (32, 272, 16), (33, 144, 2064), (65, 400, 1040), (130, 528, 2064),
+                                   (700, 272, 400), (1003, 2064, 528)])
+def test_exact_products_of_any_codes(t, n, k, dtype, bias):
+    """No more than fp32's roundings off, for codes of which the other kernels drop bits."""
+    print("[f8] exact plan", t, n, k, dtype, flush=True)
+    x, sx, w, sw, b = operands(t, n, k, t + n)
+    want, s = ref.product(ref.row_values(x, sx.astype(np.float64)), ref.weight_values(w, sw), b if bias else None)
+    with bsg.F8Plan(n, k, t, dtype=dtype, bias=bias, exact=True) as plan:
+        out = torch.full((t + 1, n), 7.0, dtype=DT[dtype], device="cuda")
+        plan.run(dev(x), dev(sx), dev(w), dev(sw), out[:t], bias=dev(b) if bias else None)
+        torch.cuda.synchronize()
+    assert (out[t:] == 7).all()
+    check(out[:t].double().cpu().numpy(), want, ref.sum_bound(k, True) * s, dtype, (t, n, k))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("t,hidden,inter", [(5, 144, 272), (33, 272, 400), (65, 400, 528), (300, 528, 272), (1100, 272, 1040)])
+def test_exact_feed_forward_of_any_numbers(monkeypatch, t, hidden, inter, dtype):
+    monkeypatch.setattr(ref, "FEW", 1 << 30)  # (the reference's bounds for exact products)
+    monkeypatch.setattr(ref, "WIDE", 1 << 30)
+    print("[f8] exact feed-forward", t, hidden, inter, dtype, flush=True)
+    held, doubles = ffn_weights(hidden, inter, t)
+    x = activations(t, hidden, dtype, t + hidden)
+    out = torch.full((t + 1, hidden), 7.0, dtype=DT[dtype], device="cuda")
+    with bsg.F8FFNPlan(hidden, inter, t, dtype=dtype, exact=True) as plan:
+        plan.run(x.cuda(), *(dev(a) for a in held), out[:t])
+        torch.cuda.synchronize()
+    assert (out[t:] == 7).all()
+    check(out[:t].double().cpu().numpy(), *ref.ffn(x.double().numpy(), *doubles), dtype, (t, hidden, inter))
+
+
+def test_exact_plans_refuse_and_replay_as_others():
+    t, n, k = 100, 144, 272
+    x, sx, w, sw, _ = (dev(a) for a in operands(t, n, k, 1))
+    out, side = torch.empty(t, n, dtype=torch.bfloat16, device="cuda"), torch.cuda.Stream()
+    with bsg.F8Plan(n, k, t, exact=True) as plan:
+        with pytest.raises(ValueError):
+            plan.run(x[:, :128], sx, w, sw, out)
+        plan.run(x, sx, w, sw, out)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            plan.run(x, sx, w, sw, out)
+        for i in range(3):
+            x.copy_(dev(operands(t, n, k, 10 + i)[0]))
+            graph.replay()
+            torch.cuda.synchronize()
+            got = out.clone()
+            plan.run(x, sx, w, sw, out)
+            torch.cuda.synchronize()
+            assert torch.equal(got.view(torch.int16), out.view(torch.int16))
 
 
 def test_workspaces_are_those_of_the_plans_sizes():
