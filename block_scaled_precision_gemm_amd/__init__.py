@@ -667,19 +667,50 @@ def f8_quantize(x, codes, scales, stream=None) -> None:
         _f8_rows(codes, rows, cols, "codes"), scales.data_ptr(), _f8_scales(scales, rows, cols, f32), _stream(stream)))
 
 
-class F8Plan:
+class _F8Handle:
+    """What both kinds of plans have: a handle of the library, whose functions begin with _PREFIX."""
+    _PREFIX = ""
+
+    def _create(self, problem) -> None:
+        self._h = None
+        self._lib = load_library()
+        h = _VP()
+        _check(getattr(self._lib, self._PREFIX + "_create")(ctypes.byref(problem), ctypes.byref(h)))
+        self._h = h
+
+    def workspace_bytes(self) -> int:
+        n = ctypes.c_uint64()
+        _check(getattr(self._lib, self._PREFIX + "_workspace")(self._h, ctypes.byref(n)))
+        return n.value
+
+    def close(self) -> None:
+        if self._h is not None and self._h.value:
+            _check(getattr(self._lib, self._PREFIX + "_destroy")(self._h))
+        self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+
+class F8Plan(_F8Handle):
     """A plan of products of E4M3 rows of k with a scale for each 128 of them and weights [n][k] with a scale for each
     128 x 128 of them, outputs of `dtype` (bsg_f8.h).  exact: no bits of a product are dropped before it is summed in fp32,
     also beyond 16 tokens, where that takes 1.1 (some) to 2.7 (thousands of tokens) times as long."""
+    _PREFIX = "bsg_f8_plan"
 
     def __init__(self, n: int, k: int, max_tokens: int, dtype: str = "bf16", bias: bool = False, device: int = -1, exact: bool = False):
-        self._h = None
-        self._lib = lib = load_library()
         self.n, self.k, self.bias = n, k, bias
-        prob = F8Problem(ctypes.sizeof(F8Problem), OUT_DTYPES[dtype], (F8_BIAS if bias else 0) | (F8_EXACT if exact else 0), device, n, k, max_tokens)
-        h = _VP()
-        _check(lib.bsg_f8_plan_create(ctypes.byref(prob), ctypes.byref(h)))
-        self._h = h
+        flags = (F8_BIAS if bias else 0) | (F8_EXACT if exact else 0)
+        self._create(F8Problem(ctypes.sizeof(F8Problem), OUT_DTYPES[dtype], flags, device, n, k, max_tokens))
         self._dtypes, (self._f32, _) = _dtypes(dtype), _f32_i32()
         self._weights = (n, k), (_f8_blocks(n), _f8_blocks(k))
 
@@ -696,41 +727,16 @@ class F8Plan:
                                     bias.data_ptr() if self.bias else None, out.data_ptr(),
                                     _f8_matrix(out, tokens, self.n, self._dtypes, "out"), _stream(stream)))
 
-    def workspace_bytes(self) -> int:
-        n = ctypes.c_uint64()
-        _check(self._lib.bsg_f8_plan_workspace(self._h, ctypes.byref(n)))
-        return n.value
 
-    def close(self) -> None:
-        if self._h is not None and self._h.value:
-            _check(self._lib.bsg_f8_plan_destroy(self._h))
-        self._h = None
-
-    def __del__(self):
-        try:
-            self.close()
-        except Exception:
-            pass
-
-    def __enter__(self):
-        return self
-
-    def __exit__(self, *exc):
-        self.close()
-
-
-class F8FFNPlan:
+class F8FFNPlan(_F8Handle):
     """A plan of the gated feed-forward block over such weights: out = quantize(SiLU(x w1^T) * (x w3^T)) w2^T, x quantised
     on the way in (bsg_f8.h).  exact: as for F8Plan."""
+    _PREFIX = "bsg_f8_ffn_plan"
 
     def __init__(self, hidden: int, inter: int, max_tokens: int, dtype: str = "bf16", device: int = -1, exact: bool = False):
-        self._h = None
-        self._lib = lib = load_library()
         self.hidden, self.inter = hidden, inter
-        prob = F8FFNProblem(ctypes.sizeof(F8FFNProblem), OUT_DTYPES[dtype], F8_EXACT if exact else 0, device, hidden, inter, max_tokens)
-        h = _VP()
-        _check(lib.bsg_f8_ffn_plan_create(ctypes.byref(prob), ctypes.byref(h)))
-        self._h = h
+        flags = F8_EXACT if exact else 0
+        self._create(F8FFNProblem(ctypes.sizeof(F8FFNProblem), OUT_DTYPES[dtype], flags, device, hidden, inter, max_tokens))
         self._dtypes, (self._f32, _) = _dtypes(dtype), _f32_i32()
         bh, bi = _f8_blocks(hidden), _f8_blocks(inter)
         self._w13, self._w2 = ((2 * inter, hidden), (2, bi, bh)), ((hidden, inter), (bh, bi))
@@ -744,28 +750,6 @@ class F8FFNPlan:
         _check(self._lib.bsg_f8_ffn_run(self._h, tokens, x.data_ptr(), _f8_matrix(x, tokens, self.hidden, self._dtypes, "x"),
                                         ctypes.byref(w), out.data_ptr(),
                                         _f8_matrix(out, tokens, self.hidden, self._dtypes, "out"), _stream(stream)))
-
-    def workspace_bytes(self) -> int:
-        n = ctypes.c_uint64()
-        _check(self._lib.bsg_f8_ffn_plan_workspace(self._h, ctypes.byref(n)))
-        return n.value
-
-    def close(self) -> None:
-        if self._h is not None and self._h.value:
-            _check(self._lib.bsg_f8_ffn_plan_destroy(self._h))
-        self._h = None
-
-    def __del__(self):
-        try:
-            self.close()
-        except Exception:
-            pass
-
-    def __enter__(self):
-        return self
-
-    def __exit__(self, *exc):
-        self.close()
 
 
 def rope_table(rows: int, rope_dim: int, base: float = 10000.0, scaling: tuple | None = None):

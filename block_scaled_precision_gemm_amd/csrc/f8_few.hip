@@ -21,13 +21,12 @@
 // neighbouring code; their rate is of no use here, where the matrix units wait for the weights' bytes.
 #include "epilogue.h"
 #include "f8_codec.h"
+#include "f8_copy.h"
 
 namespace bsg {
 namespace {
 
 constexpr int kWaves = 8, kThreads = 64 * kWaves;
-constexpr int kOut = (int)0x80000000u;  // an offset past any buffer: zeros, no traffic
-constexpr int kRaw = 0x00020000;
 constexpr int kHeld = 512;              // blocks of tokens held in LDS at a time
 
 __device__ __forceinline__ v4i load16(__amdgpu_buffer_rsrc_t b, int voff, int soff) {

@@ -25,6 +25,7 @@
 
 #include "epilogue.h"
 #include "f8_codec.h"
+#include "f8_copy.h"
 
 namespace bsg {
 namespace {
@@ -34,16 +35,6 @@ constexpr int TILE = 256 * BK;                // bytes of one operand's stage
 constexpr int SCALES = 4 * TILE;               // LDS: weights' stages, tokens' stages, then tokens' scales
 constexpr int SCALE_STAGE = WAVES * 64 * 4;   // each wave's own 64
 constexpr int CPW = 4;                        // copy instructions of a wave in a memory phase
-constexpr int kOut = (int)0x80000000u;        // an offset past any buffer
-constexpr int kRaw = 0x00020000;
-typedef __attribute__((address_space(3))) void lds_void;
-
-__device__ __forceinline__ void copy16(__amdgpu_buffer_rsrc_t b, uint8_t* dst, int voff, int soff) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_void*)dst, 16, voff, soff, 0, 0);
-}
-__device__ __forceinline__ void copy4(__amdgpu_buffer_rsrc_t b, uint8_t* dst, int voff, int soff) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_void*)dst, 4, voff, soff, 0, 0);
-}
 
 __device__ __forceinline__ void barrier_only() { asm volatile("s_barrier" ::: "memory"); }
 

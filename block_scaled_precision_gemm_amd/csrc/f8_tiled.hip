@@ -29,23 +29,12 @@
 
 #include "epilogue.h"
 #include "f8_codec.h"
+#include "f8_copy.h"
 #include "f8_cut.h"
 #include "handoff.h"
 
 namespace bsg {
 namespace {
-
-constexpr int kOut = (int)0x80000000u;  // an offset past any buffer: zeros, no traffic
-constexpr int kRaw = 0x00020000;
-typedef __attribute__((address_space(3))) void lds_void;
-
-// 16 or 4 bytes per lane from memory to LDS at dst (uniform), lane after lane.
-__device__ __forceinline__ void copy16(__amdgpu_buffer_rsrc_t b, uint8_t* dst, int voff, int soff) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_void*)dst, 16, voff, soff, 0, 0);
-}
-__device__ __forceinline__ void copy4(__amdgpu_buffer_rsrc_t b, uint8_t* dst, int voff, int soff) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_void*)dst, 4, voff, soff, 0, 0);
-}
 
 // Tile and part of a workgroup.  Workgroups go to the 8 XCDs in turn; each XCD gets a contiguous range of tiles, token
 // tiles first in groups of 8, so that those that share weights share an L2.
