@@ -9,16 +9,18 @@
 // Tokens that come as 16- or 32-bit values are quantised on the way (the feed-forward block of few tokens has no launch of its
 // own for that): the workgroup puts their codes into LDS while its first weights are on their way.  Read by every wave for
 // its own blocks, the values would be most of the load instructions, as one token fills one column of 16 (block of one
-// token, hidden 2048, inter 4096: 12.7 us so, 11.6 us from LDS; hidden 4096, inter 8192: 28.1 and 25.2 us).  Codes are read by
-// the waves (two blocks in flight, one token x 4096 x 4096: 5.5 us, 6.1 us from LDS; 16 tokens 6.4 and 8.3 us).
+// token, hidden 2048, inter 4096: 12.7 us so, 11.6 us from LDS; hidden 4096, inter 8192: 28.1 and 25.2 us).  16 tokens,
+// also quantised by every workgroup: hidden 4096, inter 8192 36 to 39 us.  Codes are read by the waves: one token
+// x 4096 x 4096 takes 5.2 to 5.6 us, 16 tokens 6.3, 16 x 8192 x 8192 18.9 (by way of LDS, with two blocks in flight, one token
+// took 6.1 us for 5.5 and 16 tokens 8.3 for 6.4).
 //
 // The next block is asked for when the last is computed, and the machine's other waves (two workgroups a CU, and all CUs) fill
 // the rest: with two blocks in flight 5.6 us for 5.2, with four 5.9 (one token x 8192 x 8192: 13.4 and 14.3 for 12.5 us).
 //
 // The codes are widened to fp16, which holds every E4M3 value, and multiplied by v_mfma_f32_16x16x32_f16: its products are
-// exact and its sums fp32.  The matrix instructions that take E4M3 itself align the products of 8 elements to the largest
-// and drop what lies 2^-13 below (2e-6 of the sum of magnitudes for Gaussian elements), which turns one in 400 of the feed-forward block's inner values to a
-// neighbouring code; their rate is of no use here, where the matrix units wait for the weights' bytes.
+// exact and its sums fp32.  The matrix instructions that take E4M3 itself align the products of 8 elements to the largest and
+// drop what lies 2^-13 below (2e-6 of the sum of magnitudes for Gaussian elements), which turns one in 400 of the feed-forward
+// block's inner values to a neighbouring code; their rate is of no use here, where the matrix units wait for the weights' bytes.
 #include "epilogue.h"
 #include "f8_codec.h"
 #include "f8_copy.h"

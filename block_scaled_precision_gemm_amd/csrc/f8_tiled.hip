@@ -22,9 +22,11 @@
 //   of a tile adds them in the order of the parts, so that the order of every sum is fixed.
 //
 // Bound: few tokens, the weights' bytes, and beside them a fixed 5 us (the launch, the first copies, the parts' join): 61 tokens
-// x 8192 x 8192 in 16.8 us (4.0 TB/s), 33 tokens x 8192 x 4096 with 4 parts 12.7 to 15.7 us.  Some hundred tokens, what a CU can
-// take in from the L2s: three workgroups of 64 x 64 ask for 48 KB a step, and take 0.58 us for it (83 GB/s a CU, 21 TB/s on all);
-// larger tiles ask for less, but there are fewer than CUs.  1003 tokens x 2064 x 4112: 26 to 28 us (610 to 650 TFLOP/s).
+// x 8192 x 8192 in 17 to 18 us (3.8 to 4.0 TB/s), 33 tokens x 8192 x 4096 with 4 parts 11.8 to 15.7 us.  Some hundred tokens, the
+// copies: 1003 tokens x 2064 x 4112 take 28.3 us (600 TFLOP/s) with 528 tiles of 64 x 64, the loop's copies alone 27.0, without
+// copies 16.1, the products alone 12.9 and neither, a barrier a step, 6.9.  Of the copies' 27.0 us 7 go to lines that no L2 holds
+// yet (19.9 with one block of K copied again and again), though the L2s answer 92% of the requests, in 291 cycles on average.
+// Larger tiles ask for less, but there are fewer than CUs.
 #include <type_traits>
 
 #include "epilogue.h"

@@ -578,7 +578,12 @@ hipError_t launch(const KvArgs& a, int cus, hipStream_t stream) {
 // behind them by the few-row kernel for each.  That kernel reads 6 MB a microsecond for blocks of 16 rows and half as much
 // for 32; the other one costs 12 to 50 us.  Heads of 128, 32 on 8, 200 positions of their own, by one and by both kernels:
 // 64 tokens and 512 shared positions 24 and 35 us, 2048 42 and 40, 8192 106 and 54; 16 tokens and 2048 21 and 23, 8192 43
-// and 30 us.  5 tokens each, heads of 64: 16 sequences and 8192 45 and 38 us, 64 sequences and 2048 45 and 53 us.
+// and 30 us.  5 tokens each, heads of 64: 16 sequences and 8192 45 and 38 us, which the rule leaves to the one kernel, 64
+// sequences and 2048 45 and 53 us: it sees 2.6 and 3.0 MB saved for a microsecond of cost, the wrong way round.
+//
+// Never: under a window; 32 rows and fewer in all, for whose plans there is no room for the many-row kernel's parts; sequences of
+// more than 32 rows, which that kernel does itself and would have to begin behind the shared positions.  They read the
+// shared positions once for each sequence.
 bool shared_pays(const KvArgs& a, int head_dim, int cus) {
   const int64_t rows = (int64_t)a.max_q * a.group;
   if (a.shared <= 0 || a.window > 0 || a.num_seqs < 2 || rows > kFewRows || (int64_t)a.num_tokens * a.group <= kFewRows) return false;
