@@ -89,6 +89,12 @@ inline F8Cut f8_cut(bool gated, bool exact, int64_t tokens, int64_t n, int64_t k
   return best;
 }
 
+// Tokens that one grid of such tiles can take: whole tiles, of which there are no more than 2^31 threads' worth.
+inline int64_t f8_tokens_at_once(F8Way way, int64_t n, int threads) {
+  const F8Shape& t = f8_shape(way);
+  return ((int64_t)1 << 31) / threads / f8_tiles(t.rows, t.tokens, t.gated, 1, n) * t.tokens;
+}
+
 // What calls of up to max_tokens may need for parts of K, in floats, and how many tiles they count.
 struct F8Parts {
   int64_t floats, counters;

@@ -337,13 +337,25 @@ __global__ __launch_bounds__(64 * WN * WT, WN* WT* PER_CU / 4) void tiled_kernel
   }
 }
 
+// More tiles than a grid may have (its threads are below 2^32; K is then not split) are done a range of tokens at a time.
 template <F8Way WAY, int WN, int WT, int STAGES, bool WIDE, Out O>
 hipError_t launch(F8Args a, const F8Cut& cut, hipStream_t stream) {
   constexpr F8Shape t = f8_shape(WAY);
+  constexpr int THREADS = 64 * WN * WT;
+  const int64_t tokens = a.tokens, at_once = f8_tokens_at_once(WAY, a.n, THREADS);
   a.splits = (int)cut.splits;
-  void* argv[] = {&a};
-  return hipLaunchKernel((const void*)&tiled_kernel<t.rows, t.tokens, WN, WT, STAGES, t.per_cu, t.gated, WIDE, O>,
-                         dim3((unsigned)(cut.tiles * cut.splits)), dim3(64 * WN * WT), argv, 0, stream);
+  for (int64_t first = 0;; first += at_once) {
+    a.tokens = (int)(tokens - first < at_once ? tokens - first : at_once);
+    const int64_t tiles = f8_tiles(t.rows, t.tokens, t.gated, a.tokens, a.n);
+    void* argv[] = {&a};
+    const hipError_t e = hipLaunchKernel((const void*)&tiled_kernel<t.rows, t.tokens, WN, WT, STAGES, t.per_cu, t.gated, WIDE, O>,
+                                         dim3((unsigned)(tiles * cut.splits)), dim3(THREADS), argv, 0, stream);
+    if (e != hipSuccess || first + at_once >= tokens) return e;
+    a.x += at_once * a.x_stride;
+    a.sx += at_once;
+    a.out += at_once * a.out_stride * (t.gated ? 1 : 2);
+    if (t.gated) a.so += at_once;
+  }
 }
 
 template <Out O>

@@ -10,6 +10,7 @@ int cut(int gated, int64_t tokens, int64_t n, int64_t k, int cus, int64_t out[3]
   *cost = c.cost;
   return 0;
 }
+int64_t tokens_at_once(int way, int64_t n, int threads) { return bsg::f8_tokens_at_once((bsg::F8Way)way, n, threads); }
 void parts(int gated, int64_t max_tokens, int64_t n, int64_t k, int cus, int64_t out[2]) {
   const bsg::F8Parts p = bsg::f8_parts(gated & 1, gated >> 1, max_tokens, n, k, cus);
   out[0] = p.floats;

@@ -35,7 +35,8 @@ def cut(tmp_path_factory):
         lib.parts(gated, max_tokens, n, k, cus, out)
         return tuple(out)
     lib.parts.argtypes = [ctypes.c_int, i64, i64, i64, ctypes.c_int, i64 * 2]
-    choose.parts = parts
+    lib.tokens_at_once.argtypes, lib.tokens_at_once.restype = [ctypes.c_int, i64, ctypes.c_int], i64
+    choose.parts, choose.tokens_at_once = parts, lib.tokens_at_once
     return choose
 
 
@@ -100,3 +101,16 @@ def test_workspaces_of_some_plans(cut):
     assert cut.parts(0, 8192, 4096, 896) == (0, 0)                # seven blocks
     assert cut.parts(0, 8192, 1 << 18, 8192) == (0, 0)            # more tiles than run at once
     assert cut.parts(0, 64, 16, 1024) == (2 * 128 * 128, 1)       # one tile of 128 x 128 in two parts
+
+
+def test_grids_of_many_tiles_stay_below_32_bits_of_threads(cut):
+    for way in f8_cases.WAYS[:-2]:
+        rows, cols = SHAPE[way]
+        for n in (16, 8192, 1 << 18):
+            tiles_n = -(-n // (rows // 2 if way[0] == "G" else rows))
+            most = cut.tokens_at_once(f8_cases.WAYS.index(way), n, 512)
+            assert most > 0 and most % cols == 0 and most // cols * tiles_n * 512 <= 1 << 31 < (most // cols + 1) * tiles_n * 512
+    # calls that a device of 288 GB can hold and a grid cannot: inner codes of 69 GB, outputs of 137 GB
+    for gated, t, n, k in ((3, 1 << 20, 65536, 16), (2, (1 << 19) + 128, 1 << 17, 16)):
+        way, tiles, parts, _ = cut(gated, t, n, k)
+        assert parts == 1 and tiles * 512 > 1 << 31 and cut.tokens_at_once(f8_cases.WAYS.index(way), n, 512) < t

@@ -179,6 +179,48 @@ def test_exact_plans_refuse_and_replay_as_others():
             assert torch.equal(got.view(torch.int16), out.view(torch.int16))
 
 
+def test_exact_products_of_more_tiles_than_a_grid_has():
+    """Outputs of 137 GB: 4098 x 1024 tiles of 512 threads.  Tokens around the end of a range, and every 4099th, against the exact
+    sums."""
+    t, n, k, g = (1 << 19) + 200, 1 << 17, 16, generator(1)
+    torch.cuda.empty_cache()
+    print("[f8] exact product of", t, n, k, flush=True)
+    x, sx, w, sw = narrow((t, k), g), powers((1, t), g), narrow((n, k), g), powers((ref.blocks(n), 1), g)
+    out = torch.empty(t, n, dtype=torch.bfloat16, device="cuda")
+    rows = torch.cat([torch.arange(0, t, 4099), torch.arange((1 << 19) - 130, t)]).unique().cuda()
+    out[rows] = -7.0
+    with bsg.F8Plan(n, k, t, exact=True) as plan:
+        plan.run(x, sx, w, sw, out)
+        torch.cuda.synchronize()
+    for some in rows.split(128):
+        assert torch.equal(out[some], exact(x[some], sx[:, some], w, sw).bfloat16())
+    del out
+    torch.cuda.empty_cache()
+
+
+def test_exact_gate_and_up_of_more_tiles_than_a_grid_has():
+    """Inner codes of 69 GB: 16384 x 512 tiles of 512 threads, two ranges of tokens, against calls with some of the tokens."""
+    t, hidden, inter, g = 1 << 20, 16, 1 << 16, generator(2)
+    torch.cuda.empty_cache()
+    print("[f8] exact feed-forward of", t, hidden, inter, flush=True)
+    x = torch.randn(t, hidden, device="cuda", generator=g).bfloat16()
+    w13, s13 = narrow((2 * inter, hidden), g), powers((2, inter // 128, 1), g, -2)
+    w2 = torch.zeros((hidden, inter), dtype=torch.uint8, device="cuda")
+    w2[torch.arange(hidden, device="cuda"), torch.randperm(inter, device="cuda", generator=g)[:hidden]] = ONE  # (picks inner values)
+    held = w13, s13, w2, torch.ones((1, inter // 128), device="cuda")
+    out = torch.full((t, hidden), 7.0, dtype=torch.bfloat16, device="cuda")
+    with bsg.F8FFNPlan(hidden, inter, t, exact=True) as plan:
+        plan.run(x, *held, out)
+        torch.cuda.synchronize()
+    with bsg.F8FFNPlan(hidden, inter, 4096, exact=True) as plan:
+        for a in [*range(0, t, 1 << 17), (t >> 1) - 2048, t - 4096]:
+            some = torch.empty(4096, hidden, dtype=torch.bfloat16, device="cuda")
+            plan.run(x[a:a + 4096], *held, some)
+            torch.cuda.synchronize()
+            assert torch.equal(out[a:a + 4096].view(torch.int16), some.view(torch.int16)), a
+    torch.cuda.empty_cache()
+
+
 def test_workspaces_are_those_of_the_plans_sizes():
     def bytes_of(plan):
         with plan:
